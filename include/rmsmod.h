@@ -313,6 +313,52 @@ int conv_bias_epilogue(const void* x, const void* bias, int bias_is_fp32, const 
                        void* out, int64_t pixels, int64_t C, rmsmod_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 4-bit rows (MXFP4) and their product: a block's projections on
+ * the rows that the operations above produce.
+ *
+ *   A row of K values (K a multiple of 32, up to RMSMOD_MXFP4_MAX_K) is cut
+ *   into blocks of 32.  Block: 32 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and
+ *   a sign) under one e8m0 scale 2^(byte - 127), byte 255 = NaN.
+ *     packed  [rows, K / 2] bytes, the even element in the low four bits
+ *     scales  mxfp4_scale_bytes(rows, K) bytes: tiles of 128 rows by 4 blocks
+ *             (128 values), tile (i, j) at 512 * (i * ceil(K / 128) + j); in
+ *             a tile row r, block k at byte (r % 32) * 16 + (r / 32) * 4 + k.
+ *             Bytes of blocks past K have to be zero (mxfp4_quantize writes
+ *             every byte of the tiles, zeros for what the matrix lacks).
+ *   dtype: RMSMOD_BF16 or RMSMOD_F16, the type of values, bias, gate,
+ *   residual and out.  All pointers 16-byte aligned.
+ * ---------------------------------------------------------------------- */
+enum { RMSMOD_BF16 = 0, RMSMOD_F16 = 1 };
+#define RMSMOD_MXFP4_MAX_K 1048576
+
+/* Bytes of the tiled scales of a [rows, K] matrix; 0 if unsupported. */
+size_t mxfp4_scale_bytes(int64_t rows, int64_t K);
+
+/* mxfp4_quantize: scale 2^e, the least power of two with max|x| <= 6 * 2^e
+ * (no value saturates; e >= -127), code = x * 2^-e to nearest, ties to the
+ * even code.  A block that holds Inf or NaN gets the NaN scale; a block of
+ * zeros scale byte 0. */
+int mxfp4_quantize(const void* x, void* packed, void* scales, int64_t rows, int64_t K, int dtype,
+                   rmsmod_stream_t stream);
+
+/* mxfp4_dequantize: the values that the codes stand for, rounded to dtype
+ * (exact but for bf16 subnormals, and fp16's range). */
+int mxfp4_dequantize(const void* packed, const void* scales, void* out, int64_t rows, int64_t K,
+                     int dtype, rmsmod_stream_t stream);
+
+/* mxfp4_matmul: for every row m = b * S + s of a and row n of b
+ *     acc       = sum_k a[m, k] * b[n, k]                (fp32)
+ *     out[m, n] = R(f(residual[m, n]) + f(gate_b[n]) * (acc + f(bias[n])))
+ *   in fp32 with one rounding; bias, gate and residual are nullable (no add,
+ *   no product).  a [B*S, K], b [N, K] packed with their scales; N a multiple
+ *   of 8; gate rows at gate + b * gate_bstride (elements, a multiple of 8);
+ *   residual, out [B*S, N], out may equal residual.  One launch. */
+int mxfp4_matmul(const void* a, const void* a_scales, const void* b, const void* b_scales,
+                 const void* bias, const void* gate, int64_t gate_bstride, const void* residual,
+                 void* out, int64_t B, int64_t S, int64_t N, int64_t K, int dtype,
+                 rmsmod_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Predicates and diagnostics
  * ---------------------------------------------------------------------- */
 

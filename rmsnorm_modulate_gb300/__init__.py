@@ -17,6 +17,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple
 
 import torch
 
@@ -25,7 +26,8 @@ __all__ = [
     "ln_modulate_backward", "ln_modulate_backward_static", "backward_workspace_bytes",
     "rmsnorm_modulate",
     "gated_rmsnorm_modulate", "qk_layernorm", "rmsnorm_silu_cl", "modulate_scale_shift",
-    "residual_gate_add", "conv_bias_epilogue", "supported", "status_string", "device_status",
+    "residual_gate_add", "conv_bias_epilogue", "Mxfp4", "mxfp4_quantize", "mxfp4_dequantize",
+    "mxfp4_scale_bytes", "mxfp4_linear", "supported", "status_string", "device_status",
     "selftest_wait_timeout",
     "OP_LN_MODULATE", "OP_RMSNORM_MODULATE", "OP_GATED_RMSNORM_MODULATE",
     "OP_QK_LAYERNORM", "OP_RMSNORM_SILU_CL", "OP_LN_MODULATE_FOLDED",
@@ -83,6 +85,9 @@ def library() -> ctypes.CDLL:
             "modulate_scale_shift": [P, P, P, P, I, I, I, I, P],
             "residual_gate_add": [P, P, P, I, P, I, I, I, P],
             "conv_bias_epilogue": [P, P, C, P, P, I, I, P],
+            "mxfp4_quantize": [P, P, P, I, I, C, P],
+            "mxfp4_dequantize": [P, P, P, I, I, C, P],
+            "mxfp4_matmul": [P, P, P, P, P, P, I, P, P, I, I, I, I, C, P],
             "rmsmod_supported": [C, I, ctypes.POINTER(P), C],
             "rmsmod_status_string": [C],
             "rmsmod_version": [],
@@ -94,6 +99,8 @@ def library() -> ctypes.CDLL:
             fn.argtypes = args
             fn.restype = ctypes.c_int
         lib.rmsmod_status_string.restype = ctypes.c_char_p
+        lib.mxfp4_scale_bytes.argtypes = [I, I]
+        lib.mxfp4_scale_bytes.restype = ctypes.c_size_t
         _lib = lib
         return lib
 
@@ -116,6 +123,25 @@ def _stream(stream):
     if stream is None:
         stream = torch.cuda.current_stream()
     return ctypes.c_void_p(stream.cuda_stream)
+
+
+def _call_on(device, name, *args, stream=None) -> None:
+    """_call on the tensors' own device, with `stream` (default: that device's current one) as the
+    last argument."""
+    if device.index == torch.cuda.current_device():
+        _call(name, *args, _stream(stream))
+    else:
+        with torch.cuda.device(device):
+            _call(name, *args, _stream(stream))
+
+
+def _scratch(stream, n, device):
+    """`n` bytes that only work on `stream` uses: they come from that stream's own pool, so that
+    nothing on another stream can be given them before that work is done."""
+    if stream is None:
+        return torch.empty(n, dtype=torch.uint8, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(n, dtype=torch.uint8, device=device)
 
 
 def _bf16(t, name, dtype=torch.bfloat16):
@@ -480,6 +506,140 @@ def conv_bias_epilogue(x, bias, h=None, out=None, stream=None):
     is32 = 1 if bias.dtype == torch.float32 else 0
     _call("conv_bias_epilogue", _ptr(x), _ptr(bias), is32, _ptr(h), _ptr(out), pixels, C,
           _stream(stream))
+    return out
+
+
+class Mxfp4(NamedTuple):
+    """A microscaled 4-bit matrix: `packed` uint8 [..., K / 2] (two e2m1 codes a byte, the even
+    element in the low half) and `scales` uint8, the tiled e8m0 scale bytes of its rows
+    (mxfp4_scale_bytes(rows, K) of them; layout in include/rmsmod.h)."""
+
+    packed: torch.Tensor
+    scales: torch.Tensor
+
+
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def mxfp4_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the tiled scales of a [rows, K] 4-bit matrix (0 if the size is unsupported)."""
+    return int(library().mxfp4_scale_bytes(rows, K))
+
+
+def _half(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    return _dense(t, name, t.dtype)
+
+
+def _codes(q, name, device=None):
+    """-> (rows, K) of a checked Mxfp4."""
+    if not isinstance(q, Mxfp4):
+        raise TypeError(f"{name} must be an Mxfp4")
+    for t, n in ((q.packed, f"{name}.packed"), (q.scales, f"{name}.scales")):
+        _dense(t, n, torch.uint8)
+        if device is not None and t.device != device:
+            raise ValueError(f"{n} must be on {device}")
+    K = 2 * q.packed.shape[-1] if q.packed.dim() else 0
+    if K == 0 or K % 32:
+        raise ValueError(f"{name}.packed must hold rows of a multiple of 32 values")
+    rows = 2 * q.packed.numel() // K
+    if q.scales.numel() != mxfp4_scale_bytes(rows, K):
+        raise ValueError(f"{name}.scales must hold {mxfp4_scale_bytes(rows, K)} bytes")
+    return rows, K
+
+
+def mxfp4_quantize(x, out=None, stream=None) -> Mxfp4:
+    """Rows of x [..., K] (bfloat16 or float16, K a multiple of 32) in blocks of 32 e2m1 codes
+    under the least power-of-two scale that holds the block without saturation."""
+    _half(x, "x")
+    K = x.shape[-1] if x.dim() else 0
+    if K == 0 or K % 32:
+        raise ValueError("x must hold rows of a multiple of 32 values")
+    rows = x.numel() // K
+    if out is None:
+        out = Mxfp4(torch.empty(*x.shape[:-1], K // 2, dtype=torch.uint8, device=x.device),
+                    torch.empty(mxfp4_scale_bytes(rows, K), dtype=torch.uint8, device=x.device))
+    elif _codes(out, "out", x.device) != (rows, K):
+        raise ValueError("out must match x")
+    _call_on(x.device, "mxfp4_quantize", _ptr(x), _ptr(out.packed), _ptr(out.scales), rows, K,
+             _DTYPES[x.dtype], stream=stream)
+    return out
+
+
+def mxfp4_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that q stands for, as bfloat16 or float16 [..., K]."""
+    rows, K = _codes(q, "q")
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    if out is None:
+        out = torch.empty(*q.packed.shape[:-1], K, dtype=dtype, device=q.packed.device)
+    else:
+        _dense(out, "out", dtype)
+        if out.shape != (*q.packed.shape[:-1], K) or out.device != q.packed.device:
+            raise ValueError("out must match q")
+    _call_on(out.device, "mxfp4_dequantize", _ptr(q.packed), _ptr(q.scales), _ptr(out), rows, K,
+             _DTYPES[dtype], stream=stream)
+    return out
+
+
+def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None, stream=None):
+    """x w^T in 4 bits, its bias, and a block's gated residual add in the epilogue:
+    R(residual + gate * (x w^T + bias)), one rounding.
+
+    x [..., K]: bfloat16 or float16 (quantised here) or an Mxfp4 (then `dtype`, default
+    bfloat16, is the result's type); w: an Mxfp4 [N, K], laid out once.  bias [N]; gate rows [N]
+    or [B, 1, N] (for x [B, S, K]); residual [..., N], all of the result's type.  out may be
+    residual."""
+    if isinstance(x, Mxfp4):
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in _DTYPES:
+            raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+        width = _codes(x, "x")[1]
+        lead, device = x.packed.shape[:-1], x.packed.device
+    else:
+        _half(x, "x")
+        if dtype is not None and dtype != x.dtype:
+            raise TypeError(f"dtype must be x's, {x.dtype}")
+        dtype, lead, device = x.dtype, x.shape[:-1], x.device
+        width = x.shape[-1] if x.dim() else 0
+    N, K = _codes(w, "w", device)
+    if w.packed.dim() != 2 or N % 8:
+        raise ValueError("w must be [N, K], N a multiple of 8")
+    if len(lead) == 0 or width != K:
+        raise ValueError(f"x must hold rows of K={K} values")
+    B = lead[0] if len(lead) > 1 else 1
+    M = 1
+    for n in lead:
+        M *= n
+    S = M // B if B else 0
+    if bias is not None:
+        _dense(bias, "bias", dtype)
+        if bias.numel() != N:
+            raise ValueError("bias must have N elements")
+    gs = 0 if gate is None else _mod_rows(gate, B, N, "gate", dtype)
+    if residual is not None:
+        _dense(residual, "residual", dtype)
+        if residual.shape != (*lead, N):
+            raise ValueError("residual must match the result")
+    if out is None:
+        out = torch.empty(*lead, N, dtype=dtype, device=device)
+    else:
+        _dense(out, "out", dtype)
+        if out.shape != (*lead, N):
+            raise ValueError("out must match the result")
+    for t, n in ((bias, "bias"), (gate, "gate"), (residual, "residual"), (out, "out")):
+        if t is not None and t.device != device:
+            raise ValueError(f"{n} must be on {device}")
+    if not isinstance(x, Mxfp4):
+        codes = M * (K // 2)
+        q = _scratch(stream, codes + mxfp4_scale_bytes(M, K), device)
+        x = mxfp4_quantize(x, Mxfp4(q[:codes].view(*lead, K // 2), q[codes:]), stream)
+    _call_on(device, "mxfp4_matmul", _ptr(x.packed), _ptr(x.scales), _ptr(w.packed),
+             _ptr(w.scales), _ptr(bias), _ptr(gate), gs, _ptr(residual), _ptr(out), B, S, N, K,
+             _DTYPES[dtype], stream=stream)
     return out
 
 

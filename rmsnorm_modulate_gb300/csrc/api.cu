@@ -10,6 +10,7 @@
 
 #include "../../include/rmsmod.h"
 #include "launch.h"
+#include "mxfp4.h"
 #include "selftest.h"
 
 #define RMSMOD_EXPORT extern "C" __attribute__((visibility("default")))
@@ -135,16 +136,17 @@ RMSMOD_EXPORT int rmsmod_device_status(unsigned int* bits, int clear)
 {
     if (!bits)
         return RMSMOD_ERR_NULL;
-    unsigned a = 0, b = 0, c = 0, d = 0, e = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
     if (rmsmod::row_kernels_error(&a, clear != 0) != cudaSuccess ||
         rmsmod::qk_kernel_error(&b, clear != 0) != cudaSuccess ||
         rmsmod::wan_kernel_error(&c, clear != 0) != cudaSuccess ||
         rmsmod::backward_error(&d, clear != 0) != cudaSuccess ||
-        rmsmod::selftest_error(&e, clear != 0) != cudaSuccess) {
+        rmsmod::selftest_error(&e, clear != 0) != cudaSuccess ||
+        rmsmod::mxfp4_matmul_error(&f, clear != 0) != cudaSuccess) {
         cudaGetLastError();
         return RMSMOD_ERR_CUDA;
     }
-    *bits = a | b | c | d | e;
+    *bits = a | b | c | d | e | f;
     return RMSMOD_OK;
 }
 
@@ -751,4 +753,134 @@ RMSMOD_EXPORT int conv_bias_epilogue(const void* x, const void* bias, int bias_i
     a.S = 1;
     a.Dv = static_cast<int>(C / 8);
     return launch_status(rmsmod::launch_elementwise(rmsmod::kEwBias, a, dev, stream));
+}
+
+// ---- microscaled 4-bit rows and their product ----------------------------
+
+namespace {
+
+// Sizes of a 4-bit matrix of `rows` rows of K values; false if unsupported.
+struct Mxfp4Size {
+    int64_t block_tiles, row_tiles, packed_bytes, scale_bytes;
+};
+
+bool mxfp4_size(int64_t rows, int64_t K, Mxfp4Size& z)
+{
+    if (rows < 0 || K <= 0 || K % 32 != 0 || K > RMSMOD_MXFP4_MAX_K || rows > (int64_t{1} << 31) - 256)
+        return false;
+    z.block_tiles = (K + 127) / 128;
+    z.row_tiles = (rows + 127) / 128;
+    // the row kernels count 128-value units with 32-bit integers
+    if (z.row_tiles * 128 * z.block_tiles > (int64_t{1} << 32) - 256)
+        return false;
+    z.packed_bytes = rows * (K / 2);
+    z.scale_bytes = z.row_tiles * z.block_tiles * 512;
+    return true;
+}
+
+bool dtype_ok(int dtype) { return dtype == RMSMOD_BF16 || dtype == RMSMOD_F16; }
+
+int mxfp4_rows(bool quantize, const void* values, const void* packed, const void* scales,
+               int64_t rows, int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    Mxfp4Size z;
+    if (!mxfp4_size(rows, K, z))
+        return RMSMOD_ERR_SHAPE;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    if (rows == 0)
+        return RMSMOD_OK;
+    if (!values || !packed || !scales)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(values, 16) || !aligned(packed, 16) || !aligned(scales, 16))
+        return RMSMOD_ERR_ALIGN;
+    const int64_t bytes = rows * K * 2;
+    if (overlap(values, bytes, packed, z.packed_bytes) ||
+        overlap(values, bytes, scales, z.scale_bytes) ||
+        overlap(packed, z.packed_bytes, scales, z.scale_bytes))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    int st;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    rmsmod::Mxfp4RowsArgs a{};
+    a.values = const_cast<void*>(values);
+    a.packed = const_cast<void*>(packed);
+    a.scales = const_cast<void*>(scales);
+    a.rows = static_cast<uint32_t>(rows);
+    a.rows_padded = static_cast<uint32_t>(z.row_tiles * 128);
+    a.Kv = static_cast<uint32_t>(K / 8);
+    a.by_tiles = rmsmod::FastDiv::make(static_cast<uint32_t>(z.block_tiles));
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_mxfp4_rows(quantize, a, stream));
+}
+
+}  // namespace
+
+RMSMOD_EXPORT size_t mxfp4_scale_bytes(int64_t rows, int64_t K)
+{
+    Mxfp4Size z;
+    return mxfp4_size(rows, K, z) ? static_cast<size_t>(z.scale_bytes) : 0;
+}
+
+RMSMOD_EXPORT int mxfp4_quantize(const void* x, void* packed, void* scales, int64_t rows,
+                                 int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    return mxfp4_rows(true, x, packed, scales, rows, K, dtype, stream);
+}
+
+RMSMOD_EXPORT int mxfp4_dequantize(const void* packed, const void* scales, void* out, int64_t rows,
+                                   int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    return mxfp4_rows(false, out, packed, scales, rows, K, dtype, stream);
+}
+
+RMSMOD_EXPORT int mxfp4_matmul(const void* a, const void* a_scales, const void* b,
+                               const void* b_scales, const void* bias, const void* gate,
+                               int64_t gate_bstride, const void* residual, void* out, int64_t B,
+                               int64_t S, int64_t N, int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    if (B < 0 || S < 0 || (B != 0 && S > INT64_MAX / B) || N < 0 || N % 8 != 0)
+        return RMSMOD_ERR_SHAPE;
+    const int64_t M = B * S;
+    Mxfp4Size za, zb;
+    if (!mxfp4_size(M, K, za) || !mxfp4_size(N, K, zb) || N > (int64_t{1} << 23))
+        return RMSMOD_ERR_SHAPE;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    int st;
+    if ((st = check_bstride(gate_bstride)) != RMSMOD_OK)
+        return st;
+    if (M == 0 || N == 0)
+        return RMSMOD_OK;
+    if (!a || !a_scales || !b || !b_scales || !out)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(b, 16) || !aligned(b_scales, 16) ||
+        !aligned(bias, 16) || !aligned(gate, 16) || !aligned(residual, 16) || !aligned(out, 16))
+        return RMSMOD_ERR_ALIGN;
+    const int64_t bytes = M * N * 2;
+    if (bad_alias(out, residual, bytes, true) || overlap(out, bytes, a, za.packed_bytes) ||
+        overlap(out, bytes, a_scales, za.scale_bytes) || overlap(out, bytes, b, zb.packed_bytes) ||
+        overlap(out, bytes, b_scales, zb.scale_bytes) || overlap(out, bytes, bias, 2 * N) ||
+        overlap(out, bytes, gate, 2 * ((B - 1) * gate_bstride + N)))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    rmsmod::Mxfp4MatmulArgs g{};
+    g.a = a;
+    g.a_scales = a_scales;
+    g.b = b;
+    g.b_scales = b_scales;
+    g.bias = bias;
+    g.gate = gate;
+    g.gate_bstride = gate_bstride;
+    g.residual = residual;
+    g.out = out;
+    g.M = M;
+    g.S = S;
+    g.N = N;
+    g.K = K;
+    g.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_mxfp4_matmul(g, dev, stream));
 }
