@@ -313,6 +313,93 @@ int conv_bias_epilogue(const void* x, const void* bias, int bias_is_fp32, const 
                        void* out, int64_t pixels, int64_t C, rmsmod_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * sandwich_rmsnorm_modulate -- the norm after a block with its gate and
+ * residual scale, the residual add, and the norm before the next block:
+ *
+ *     u    = f(update);  rp = 1 / sqrt(mean(u^2) + post_eps)
+ *     v    = update_scale * f(post_weight) * f(gate_b)
+ *     res  = R(residual_scale * f(residual) + (u * rp) * v)
+ *     r    = 1 / sqrt(mean(f(res)^2) + eps)      (over res as stored)
+ *     out  = R((f(res) * r) * (f(weight) * (1 + f(scale_b))) + f(shift_b))
+ *
+ *   A single-rounding tier: fp32 throughout (products and sums may be fused),
+ *   one rounding per stored value.  The statistics are fp32 sums in an order
+ *   that D alone fixes (batch-invariant), good to a few 2^-24; rows whose
+ *   squares leave fp32's range are summed again at unit size.
+ *
+ *   residual, update, res_out, out  [B*S*D] of `dtype` (RMSMOD_BF16 or
+ *   RMSMOD_F16), res_out may equal residual; out nullable (then no norm after
+ *   the add).  post_weight, weight nullable [D]; gate, scale, shift nullable
+ *   rows at base + b * bstride (0 = one row for every batch): a missing
+ *   factor is 1, a missing shift 0.  post_rstd_out, rstd_out nullable fp32
+ *   [B*S] (rp and r, what the backward pass takes).
+ * ---------------------------------------------------------------------- */
+enum { RMSMOD_BF16 = 0, RMSMOD_F16 = 1 };
+
+int sandwich_rmsnorm_modulate(const void* residual, const void* update, const void* post_weight,
+                              const void* gate, int64_t gate_bstride, const void* weight,
+                              const void* scale, const void* shift, int64_t mod_bstride,
+                              void* res_out, void* out, int64_t B, int64_t S, int64_t D,
+                              float residual_scale, float update_scale, float post_eps, float eps,
+                              float* post_rstd_out, float* rstd_out, int dtype,
+                              rmsmod_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * sandwich_rmsnorm_modulate_backward -- gradients of the above, roundings
+ * passed straight through; rp, r: the forward's statistics; go, gr: the
+ * gradients of out and of res (either may be NULL: no such term).
+ *
+ *     hh = f(res) * r;  uh = f(update) * rp;  m = f(weight) * (1 + f(scale_b))
+ *     dh            = r * (go * m - hh * mean(go * m * hh)) + gr
+ *     grad_residual = R(residual_scale * dh)
+ *     grad_update   = R(rp * (dh * v - uh * mean(dh * v * uh)))
+ *   and over the tokens of a batch
+ *     grad_shift = sum go;  grad_scale = f(weight) * sum go * hh
+ *     grad_gate  = update_scale * f(post_weight) * sum dh * uh
+ *   and over all batches
+ *     grad_weight      = sum go * hh * (1 + f(scale_b))
+ *     grad_post_weight = update_scale * sum dh * uh * f(gate_b)
+ *
+ *   grad_residual, grad_update  nullable [B*S*D] of `dtype`
+ *   grad_post_weight, grad_weight  nullable fp32 [D]
+ *   grad_gate, grad_scale, grad_shift  nullable fp32 [B, D], or [1, D] where
+ *     the row's bstride is 0 (the sum over the batches)
+ *   Without grad_out: res, rstd unused; grad_weight, grad_scale, grad_shift
+ *   must be NULL.  The token sums are fp32 in an order that S and D fix.
+ *   Without rows the sums are zeros.  No output may overlap an input or
+ *   another output.
+ *   workspace  256-byte aligned device memory of at least
+ *     sandwich_rmsnorm_modulate_backward_workspace_bytes(B, S, D) bytes,
+ *     needed where a row vector's gradient is wanted; in use until the call's
+ *     work on `stream` is done.  Two launches (one without row vectors).
+ * ---------------------------------------------------------------------- */
+size_t sandwich_rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S, int64_t D);
+
+int sandwich_rmsnorm_modulate_backward(
+    const void* update, const void* res, const void* post_weight, const void* gate,
+    int64_t gate_bstride, const void* weight, const void* scale, int64_t mod_bstride,
+    const void* grad_res, const void* grad_out, const float* post_rstd, const float* rstd,
+    int64_t B, int64_t S, int64_t D, float residual_scale, float update_scale,
+    void* grad_residual, void* grad_update, float* grad_post_weight, float* grad_gate,
+    float* grad_weight, float* grad_scale, float* grad_shift, void* workspace,
+    size_t workspace_bytes, int dtype, rmsmod_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * rmsnorm_modulate_backward -- gradients of rmsnorm_modulate (bf16), roundings
+ * passed straight through; rstd: the forward's.  grad_x = dh above with
+ * f(x) in res's place and grad_res (nullable: the gradient that reaches x on
+ * the residual stream) as gr; grad_weight, grad_scale, grad_shift, workspace
+ * (rmsnorm_modulate_backward_workspace_bytes) and errors as above.
+ * ---------------------------------------------------------------------- */
+size_t rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S, int64_t D);
+
+int rmsnorm_modulate_backward(const void* x, const void* weight, const void* scale,
+                              int64_t mod_bstride, const void* grad_out, const void* grad_res,
+                              const float* rstd, int64_t B, int64_t S, int64_t D, void* grad_x,
+                              float* grad_weight, float* grad_scale, float* grad_shift,
+                              void* workspace, size_t workspace_bytes, rmsmod_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Microscaled 4-bit rows (MXFP4) and their product: a block's projections on
  * the rows that the operations above produce.
  *
@@ -328,7 +415,6 @@ int conv_bias_epilogue(const void* x, const void* bias, int bias_is_fp32, const 
  *   dtype: RMSMOD_BF16 or RMSMOD_F16, the type of values, bias, gate,
  *   residual and out.  All pointers 16-byte aligned.
  * ---------------------------------------------------------------------- */
-enum { RMSMOD_BF16 = 0, RMSMOD_F16 = 1 };
 #define RMSMOD_MXFP4_MAX_K 1048576
 
 /* Bytes of the tiled scales of a [rows, K] matrix; 0 if unsupported. */

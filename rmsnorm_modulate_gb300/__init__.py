@@ -26,7 +26,8 @@ __all__ = [
     "ln_modulate_backward", "ln_modulate_backward_static", "backward_workspace_bytes",
     "rmsnorm_modulate",
     "gated_rmsnorm_modulate", "qk_layernorm", "rmsnorm_silu_cl", "modulate_scale_shift",
-    "residual_gate_add", "conv_bias_epilogue", "Mxfp4", "mxfp4_quantize", "mxfp4_dequantize",
+    "residual_gate_add", "conv_bias_epilogue", "sandwich_rmsnorm_modulate",
+    "sandwich_rmsnorm_modulate_backward", "SandwichGrads", "rmsnorm_modulate_backward", "Mxfp4", "mxfp4_quantize", "mxfp4_dequantize",
     "mxfp4_scale_bytes", "mxfp4_linear", "supported", "status_string", "device_status",
     "selftest_wait_timeout",
     "OP_LN_MODULATE", "OP_RMSNORM_MODULATE", "OP_GATED_RMSNORM_MODULATE",
@@ -85,6 +86,13 @@ def library() -> ctypes.CDLL:
             "modulate_scale_shift": [P, P, P, P, I, I, I, I, P],
             "residual_gate_add": [P, P, P, I, P, I, I, I, P],
             "conv_bias_epilogue": [P, P, C, P, P, I, I, P],
+            "sandwich_rmsnorm_modulate": [P, P, P, P, I, P, P, P, I, P, P, I, I, I, F, F, F, F, P,
+                                          P, C, P],
+            "sandwich_rmsnorm_modulate_backward": [P, P, P, P, I, P, P, I, P, P, P, P, I, I, I, F,
+                                                   F, P, P, P, P, P, P, P, P, ctypes.c_size_t, C,
+                                                   P],
+            "rmsnorm_modulate_backward": [P, P, P, I, P, P, P, I, I, I, P, P, P, P, P,
+                                          ctypes.c_size_t, P],
             "mxfp4_quantize": [P, P, P, I, I, C, P],
             "mxfp4_dequantize": [P, P, P, I, I, C, P],
             "mxfp4_matmul": [P, P, P, P, P, P, I, P, P, I, I, I, I, C, P],
@@ -99,6 +107,10 @@ def library() -> ctypes.CDLL:
             fn.argtypes = args
             fn.restype = ctypes.c_int
         lib.rmsmod_status_string.restype = ctypes.c_char_p
+        for name in ("sandwich_rmsnorm_modulate_backward_workspace_bytes",
+                     "rmsnorm_modulate_backward_workspace_bytes"):
+            getattr(lib, name).argtypes = [I, I, I]
+            getattr(lib, name).restype = ctypes.c_size_t
         lib.mxfp4_scale_bytes.argtypes = [I, I]
         lib.mxfp4_scale_bytes.restype = ctypes.c_size_t
         _lib = lib
@@ -509,6 +521,214 @@ def conv_bias_epilogue(x, bias, h=None, out=None, stream=None):
     return out
 
 
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
+
+
+def _half(t, name):
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _DTYPES:
+        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
+    return _dense(t, name, t.dtype)
+
+
+def _same_device(device, **tensors):
+    for name, t in tensors.items():
+        if t is not None and t.device != device:
+            raise ValueError(f"{name} must be on {device}")
+
+
+def _like(t, x, name):
+    """An input of x's shape and type, or None."""
+    if t is not None:
+        _dense(t, name, x.dtype)
+        if t.shape != x.shape:
+            raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(x.shape)}")
+    return t
+
+
+def _vector(t, D, name, dtype):
+    if t is not None:
+        _dense(t, name, dtype)
+        if t.numel() != D:
+            raise ValueError(f"{name} must have D elements")
+    return t
+
+
+def _modulation(scale, shift, B, D, dtype):
+    """Batch stride of the nullable scale and shift rows."""
+    strides = [_mod_rows(t, B, D, n, dtype) for t, n in ((scale, "scale"), (shift, "shift"))
+               if t is not None]
+    if len(set(strides)) > 1:
+        raise ValueError("scale and shift must share one batch stride")
+    return strides[0] if strides else 0
+
+
+def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, weight=None,
+                              scale=None, shift=None, eps: float = 1e-6, post_eps=None,
+                              residual_scale: float = 1.0, update_scale: float = 1.0,
+                              need_out=True, res_out=None, out=None, post_rstd_out=None,
+                              rstd_out=None, stream=None):
+    """The norm after a block with its gate and residual scale, the residual add, and the norm
+    before the next block:
+
+        res = R(residual_scale * residual + update_scale * gate * RMSNorm(update) * post_weight)
+        out = R(RMSNorm(res) * weight * (1 + scale) + shift)
+
+    -> (res, out); out is None without need_out.  bfloat16 or float16, one rounding per value.
+    A missing post_weight, gate, weight or scale is a factor of 1, a missing shift 0; post_eps
+    defaults to eps.  post_rstd_out / rstd_out: fp32 [B * S] for the backward pass."""
+    _half(residual, "residual")
+    dt = residual.dtype
+    B, S, D = _bsd(residual, "residual", dt)
+    if update is None:
+        raise TypeError("update must be a torch.Tensor")
+    _like(update, residual, "update")
+    _vector(post_weight, D, "post_weight", dt)
+    gs = 0 if gate is None else _mod_rows(gate, B, D, "gate", dt)
+    if not need_out and (out is not None or rstd_out is not None):
+        raise ValueError("out and rstd_out need need_out")
+    _vector(weight, D, "weight", dt)
+    bs = _modulation(scale, shift, B, D, dt)
+    res_out = _out_like(res_out, residual, "res_out")
+    out = _out_like(out, residual) if need_out else None
+    _f32_out(post_rstd_out, B * S, "post_rstd_out", residual.device)
+    _f32_out(rstd_out, B * S, "rstd_out", residual.device)
+    _same_device(residual.device, update=update, post_weight=post_weight, gate=gate,
+                 weight=weight, scale=scale, shift=shift, res_out=res_out, out=out,
+                 post_rstd_out=post_rstd_out, rstd_out=rstd_out)
+    _call_on(residual.device, "sandwich_rmsnorm_modulate", _ptr(residual), _ptr(update),
+             _ptr(post_weight), _ptr(gate), gs, _ptr(weight), _ptr(scale), _ptr(shift), bs,
+             _ptr(res_out), _ptr(out), B, S, D, residual_scale, update_scale,
+             eps if post_eps is None else post_eps, eps, _ptr(post_rstd_out), _ptr(rstd_out),
+             _DTYPES[dt], stream=stream)
+    return res_out, out
+
+
+class SandwichGrads(NamedTuple):
+    """Gradients of sandwich_rmsnorm_modulate by its inputs: residual and update of their type,
+    the row vectors in fp32 ([D]; gate, scale and shift [B, D], or [1, D] where one row is shared
+    by the batches); None for an input that took no part."""
+
+    residual: torch.Tensor
+    update: torch.Tensor
+    post_weight: torch.Tensor
+    gate: torch.Tensor
+    weight: torch.Tensor
+    scale: torch.Tensor
+    shift: torch.Tensor
+
+
+def _row_grads(wanted, stride, B, D, device):
+    if not wanted:
+        return None
+    return torch.empty(B if stride else 1, D, dtype=torch.float32, device=device)
+
+
+def _vector_grad(wanted, D, device):
+    return torch.empty(D, dtype=torch.float32, device=device) if wanted else None
+
+
+def _need_stats(t, n, name, device):
+    if t is None:
+        raise ValueError(f"{name} (the forward's statistics) is required")
+    _f32_out(t, n, name, device)
+
+
+def _backward_workspace(name, workspace, wanted, B, S, D, device, stream):
+    if not wanted:
+        return None, 0
+    need = int(getattr(library(), name + "_workspace_bytes")(B, S, D))
+    if workspace is None:
+        workspace = _scratch(stream, max(need, 1), device)
+    elif workspace.device != device or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be contiguous and on {device}")
+    wbytes = workspace.numel() * workspace.element_size()
+    if wbytes < need:
+        raise ValueError(f"workspace holds fewer than the {need} bytes needed")
+    return workspace, wbytes
+
+
+def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, scale, grad_res,
+                                       grad_out, post_rstd, rstd, residual_scale: float = 1.0,
+                                       update_scale: float = 1.0, need_x=True, need_mod=True,
+                                       workspace=None, stream=None) -> SandwichGrads:
+    """Gradients of sandwich_rmsnorm_modulate.  update, post_weight, gate, weight, scale and the
+    two factors as in the forward, res and the statistics as it left them; grad_res, grad_out: the
+    gradients of res and out (grad_res may be None; without grad_out, which drops the second norm,
+    grad_res is needed and res, weight, scale and rstd are not).  need_x: residual and update;
+    need_mod: the row vectors, whose token sums (in an order that S and D fix) take a workspace,
+    allocated here unless one is passed.  A gradient of shift comes with that of scale."""
+    _half(update, "update")
+    dt, device = update.dtype, update.device
+    B, S, D = _bsd(update, "update", dt)
+    _like(grad_res, update, "grad_res")
+    _like(grad_out, update, "grad_out")
+    if grad_res is None and grad_out is None:
+        raise ValueError("grad_res or grad_out is required")
+    _vector(post_weight, D, "post_weight", dt)
+    gs = 0 if gate is None else _mod_rows(gate, B, D, "gate", dt)
+    bs = 0
+    _need_stats(post_rstd, B * S, "post_rstd", device)
+    if grad_out is not None:
+        if res is None:
+            raise ValueError("res is required with grad_out")
+        _like(res, update, "res")
+        _vector(weight, D, "weight", dt)
+        bs = _modulation(scale, None, B, D, dt)
+        _need_stats(rstd, B * S, "rstd", device)
+    else:
+        res = weight = scale = rstd = None
+    _same_device(device, res=res, post_weight=post_weight, gate=gate, weight=weight, scale=scale,
+                 grad_res=grad_res, grad_out=grad_out, post_rstd=post_rstd, rstd=rstd)
+    g = SandwichGrads(
+        torch.empty_like(update) if need_x else None,
+        torch.empty_like(update) if need_x else None,
+        _vector_grad(need_mod and post_weight is not None, D, device),
+        _row_grads(need_mod and gate is not None, gs, B, D, device),
+        _vector_grad(need_mod and weight is not None, D, device),
+        _row_grads(need_mod and scale is not None, bs, B, D, device),
+        _row_grads(need_mod and scale is not None, bs, B, D, device))
+    workspace, wbytes = _backward_workspace("sandwich_rmsnorm_modulate_backward", workspace,
+                                            need_mod, B, S, D, device, stream)
+    _call_on(device, "sandwich_rmsnorm_modulate_backward", _ptr(update), _ptr(res),
+             _ptr(post_weight), _ptr(gate), gs, _ptr(weight), _ptr(scale), bs, _ptr(grad_res),
+             _ptr(grad_out), _ptr(post_rstd), _ptr(rstd), B, S, D, residual_scale, update_scale,
+             _ptr(g.residual), _ptr(g.update), _ptr(g.post_weight), _ptr(g.gate), _ptr(g.weight),
+             _ptr(g.scale), _ptr(g.shift), _ptr(workspace), wbytes, _DTYPES[dt], stream=stream)
+    return g
+
+
+def rmsnorm_modulate_backward(x, weight, scale, grad_out, rstd, grad_res=None, need_x=True,
+                              need_mod=True, workspace=None, stream=None):
+    """Gradients of rmsnorm_modulate (bfloat16; x, weight, scale as in the forward, rstd its
+    statistics) -> (grad_x, grad_weight, grad_scale, grad_shift).  grad_res: a gradient that
+    reaches x on the residual stream, added to grad_x before its rounding.  grad_weight fp32 [D];
+    grad_scale, grad_shift fp32 [B, D] ([1, D] where one row is shared); scale may be None (no
+    modulation: no such gradients).  Workspace as in sandwich_rmsnorm_modulate_backward."""
+    B, S, D = _bsd(x)
+    if grad_out is None:
+        raise TypeError("grad_out must be a torch.Tensor")
+    _like(grad_out, x, "grad_out")
+    _like(grad_res, x, "grad_res")
+    _vector(weight, D, "weight", x.dtype)
+    bs = _modulation(scale, None, B, D, x.dtype)
+    _need_stats(rstd, B * S, "rstd", x.device)
+    _same_device(x.device, weight=weight, scale=scale, grad_out=grad_out, rstd=rstd,
+                 grad_res=grad_res)
+    grad_x = torch.empty_like(x) if need_x else None
+    grad_weight = _vector_grad(need_mod and weight is not None, D, x.device)
+    grad_scale = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
+    grad_shift = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
+    workspace, wbytes = _backward_workspace("rmsnorm_modulate_backward", workspace, need_mod, B,
+                                            S, D, x.device, stream)
+    _call_on(x.device, "rmsnorm_modulate_backward", _ptr(x), _ptr(weight), _ptr(scale), bs,
+             _ptr(grad_out), _ptr(grad_res), _ptr(rstd), B, S, D, _ptr(grad_x),
+             _ptr(grad_weight), _ptr(grad_scale), _ptr(grad_shift), _ptr(workspace), wbytes,
+             stream=stream)
+    return grad_x, grad_weight, grad_scale, grad_shift
+
+
 class Mxfp4(NamedTuple):
     """A microscaled 4-bit matrix: `packed` uint8 [..., K / 2] (two e2m1 codes a byte, the even
     element in the low half) and `scales` uint8, the tiled e8m0 scale bytes of its rows
@@ -518,20 +738,9 @@ class Mxfp4(NamedTuple):
     scales: torch.Tensor
 
 
-_DTYPES = {torch.bfloat16: 0, torch.float16: 1}
-
-
 def mxfp4_scale_bytes(rows: int, K: int) -> int:
     """Bytes of the tiled scales of a [rows, K] 4-bit matrix (0 if the size is unsupported)."""
     return int(library().mxfp4_scale_bytes(rows, K))
-
-
-def _half(t, name):
-    if not isinstance(t, torch.Tensor):
-        raise TypeError(f"{name} must be a torch.Tensor")
-    if t.dtype not in _DTYPES:
-        raise TypeError(f"{name} must be torch.bfloat16 or torch.float16, got {t.dtype}")
-    return _dense(t, name, t.dtype)
 
 
 def _codes(q, name, device=None):
@@ -630,9 +839,7 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
         _dense(out, "out", dtype)
         if out.shape != (*lead, N):
             raise ValueError("out must match the result")
-    for t, n in ((bias, "bias"), (gate, "gate"), (residual, "residual"), (out, "out")):
-        if t is not None and t.device != device:
-            raise ValueError(f"{n} must be on {device}")
+    _same_device(device, bias=bias, gate=gate, residual=residual, out=out)
     if not isinstance(x, Mxfp4):
         codes = M * (K // 2)
         q = _scratch(stream, codes + mxfp4_scale_bytes(M, K), device)

@@ -11,6 +11,7 @@
 #include "../../include/rmsmod.h"
 #include "launch.h"
 #include "mxfp4.h"
+#include "sandwich.h"
 #include "selftest.h"
 
 #define RMSMOD_EXPORT extern "C" __attribute__((visibility("default")))
@@ -136,17 +137,18 @@ RMSMOD_EXPORT int rmsmod_device_status(unsigned int* bits, int clear)
 {
     if (!bits)
         return RMSMOD_ERR_NULL;
-    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0;
     if (rmsmod::row_kernels_error(&a, clear != 0) != cudaSuccess ||
         rmsmod::qk_kernel_error(&b, clear != 0) != cudaSuccess ||
         rmsmod::wan_kernel_error(&c, clear != 0) != cudaSuccess ||
         rmsmod::backward_error(&d, clear != 0) != cudaSuccess ||
         rmsmod::selftest_error(&e, clear != 0) != cudaSuccess ||
-        rmsmod::mxfp4_matmul_error(&f, clear != 0) != cudaSuccess) {
+        rmsmod::mxfp4_matmul_error(&f, clear != 0) != cudaSuccess ||
+        rmsmod::sandwich_error(&g, clear != 0) != cudaSuccess) {
         cudaGetLastError();
         return RMSMOD_ERR_CUDA;
     }
-    *bits = a | b | c | d | e | f;
+    *bits = a | b | c | d | e | f | g;
     return RMSMOD_OK;
 }
 
@@ -755,6 +757,272 @@ RMSMOD_EXPORT int conv_bias_epilogue(const void* x, const void* bias, int bias_i
     return launch_status(rmsmod::launch_elementwise(rmsmod::kEwBias, a, dev, stream));
 }
 
+// ---- the norms after and before a block, and their gradients --------------
+
+namespace {
+
+bool dtype_ok(int dtype) { return dtype == RMSMOD_BF16 || dtype == RMSMOD_F16; }
+
+struct Span {
+    const void* p;
+    int64_t n;
+};
+
+// No output overlaps an input or another output.
+template <int NI, int NO>
+bool apart(const Span (&in)[NI], const Span (&out)[NO])
+{
+    for (int i = 0; i < NO; ++i) {
+        for (int j = 0; j < NI; ++j)
+            if (overlap(out[i].p, out[i].n, in[j].p, in[j].n))
+                return false;
+        for (int j = i + 1; j < NO; ++j)
+            if (overlap(out[i].p, out[i].n, out[j].p, out[j].n))
+                return false;
+    }
+    return true;
+}
+
+// Bytes from the first to the last of B 16-bit rows of D values.
+int64_t rows_span(int64_t B, int64_t bstride, int64_t D) { return ((B - 1) * bstride + D) * 2; }
+
+int check_bstride_span(int64_t B, int64_t s)
+{
+    const int st = check_bstride(s);
+    if (st != RMSMOD_OK)
+        return st;
+    return s != 0 && B > INT64_MAX / 4 / s ? RMSMOD_ERR_STRIDE : RMSMOD_OK;
+}
+
+}  // namespace
+
+RMSMOD_EXPORT int sandwich_rmsnorm_modulate(
+    const void* residual, const void* update, const void* post_weight, const void* gate,
+    int64_t gate_bstride, const void* weight, const void* scale, const void* shift,
+    int64_t mod_bstride, void* res_out, void* out, int64_t B, int64_t S, int64_t D,
+    float residual_scale, float update_scale, float post_eps, float eps, float* post_rstd_out,
+    float* rstd_out, int dtype, rmsmod_stream_t stream)
+{
+    int st = check_bsd(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    if ((st = check_bstride_span(B, mod_bstride)) != RMSMOD_OK ||
+        (st = check_bstride_span(B, gate_bstride)) != RMSMOD_OK)
+        return st;
+    const int64_t rows = B * S;
+    if (rows == 0)
+        return RMSMOD_OK;
+    if (!residual || !update || !res_out)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(residual, 16) || !aligned(update, 16) || !aligned(post_weight, 16) ||
+        !aligned(gate, 16) || !aligned(weight, 16) || !aligned(scale, 16) || !aligned(shift, 16) ||
+        !aligned(res_out, 16) || !aligned(out, 16) || !aligned(post_rstd_out, 4) ||
+        !aligned(rstd_out, 4))
+        return RMSMOD_ERR_ALIGN;
+    const int64_t bytes = tensor_bytes(rows, D);
+    const int64_t mod_bytes = rows_span(B, mod_bstride, D);
+    const Span in[] = {{update, bytes}, {post_weight, 2 * D}, {gate, rows_span(B, gate_bstride, D)},
+                       {weight, 2 * D}, {scale, mod_bytes}, {shift, mod_bytes}};
+    const Span outs[] = {{res_out, bytes}, {out, bytes}, {post_rstd_out, 4 * rows},
+                         {rstd_out, 4 * rows}};
+    if (!apart(in, outs) || bad_alias(res_out, residual, bytes, true) ||
+        overlap(out, bytes, residual, bytes) || overlap(post_rstd_out, 4 * rows, residual, bytes) ||
+        overlap(rstd_out, 4 * rows, residual, bytes))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    rmsmod::SandwichArgs a{};
+    a.residual = residual;
+    a.update = update;
+    a.post_weight = post_weight;
+    a.gate = gate;
+    a.gate_bstride = gate_bstride / 8;
+    a.weight = weight;
+    a.scale = scale;
+    a.shift = shift;
+    a.mod_bstride = mod_bstride / 8;
+    a.res_out = res_out;
+    a.out = out;
+    a.post_rstd_out = post_rstd_out;
+    a.rstd_out = rstd_out;
+    a.rows = rows;
+    a.S = S;
+    a.Dv = static_cast<int>(D / 8);
+    a.n = static_cast<float>(D);
+    a.post_eps = post_eps;
+    a.eps = eps;
+    a.residual_scale = residual_scale;
+    a.update_scale = update_scale;
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_sandwich(a, dev, stream));
+}
+
+RMSMOD_EXPORT size_t sandwich_rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S,
+                                                                        int64_t D)
+{
+    if (check_bsd(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
+        return 0;
+    return rmsmod::sandwich_backward_workspace_bytes(B, S, D, 3);
+}
+
+RMSMOD_EXPORT size_t rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S, int64_t D)
+{
+    if (check_bsd(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
+        return 0;
+    return rmsmod::sandwich_backward_workspace_bytes(B, S, D, 2);
+}
+
+// update null: the gradient of rmsnorm_modulate.
+static int norm_backward(const void* update, const void* res, const void* post_weight,
+                         const void* gate, int64_t gate_bstride, const void* weight,
+                         const void* scale, int64_t mod_bstride, const void* grad_res,
+                         const void* grad_out, const float* post_rstd, const float* rstd,
+                         int64_t B, int64_t S, int64_t D, float residual_scale,
+                         float update_scale, void* grad_residual, void* grad_update,
+                         float* grad_post_weight, float* grad_gate, float* grad_weight,
+                         float* grad_scale, float* grad_shift, void* workspace,
+                         size_t workspace_bytes, int dtype, rmsmod_stream_t stream)
+{
+    int st;
+    const int64_t rows = B * S;
+    const int parts = (update ? 1 : 0) + (grad_out ? 2 : 0);
+    const bool sums = grad_post_weight || grad_gate || grad_weight || grad_scale || grad_shift;
+    if (!grad_residual && !grad_update && !sums)
+        return RMSMOD_OK;
+    const size_t need =
+        rows && sums ? rmsmod::sandwich_backward_workspace_bytes(B, S, D, parts) : 0;
+    if (need && !workspace)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(update, 16) || !aligned(res, 16) || !aligned(post_weight, 16) ||
+        !aligned(gate, 16) || !aligned(weight, 16) || !aligned(scale, 16) ||
+        !aligned(grad_res, 16) || !aligned(grad_out, 16) || !aligned(post_rstd, 4) ||
+        !aligned(rstd, 4) || !aligned(grad_residual, 16) || !aligned(grad_update, 16) ||
+        !aligned(grad_post_weight, 16) || !aligned(grad_gate, 16) || !aligned(grad_weight, 16) ||
+        !aligned(grad_scale, 16) || !aligned(grad_shift, 16) || !aligned(workspace, 256))
+        return RMSMOD_ERR_ALIGN;
+    if (need && workspace_bytes < need)
+        return RMSMOD_ERR_SHAPE;
+    const int64_t bytes = tensor_bytes(rows, D);
+    const int64_t gate_rows = gate_bstride ? B : 1, mod_rows = mod_bstride ? B : 1;
+    const Span in[] = {{update, bytes},
+                       {res, bytes},
+                       {grad_res, bytes},
+                       {grad_out, bytes},
+                       {post_weight, 2 * D},
+                       {weight, 2 * D},
+                       {gate, rows_span(B, gate_bstride, D)},
+                       {scale, rows_span(B, mod_bstride, D)},
+                       {post_rstd, 4 * rows},
+                       {rstd, 4 * rows}};
+    const Span outs[] = {{grad_residual, bytes},
+                         {grad_update, bytes},
+                         {grad_post_weight, 4 * D},
+                         {grad_gate, 4 * D * gate_rows},
+                         {grad_weight, 4 * D},
+                         {grad_scale, 4 * D * mod_rows},
+                         {grad_shift, 4 * D * mod_rows},
+                         {need ? workspace : nullptr, static_cast<int64_t>(need)}};
+    if (!apart(in, outs))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    if (rows == 0) {  // sums over no tokens
+        for (int i = 2; i < 7; ++i)
+            if (outs[i].p && outs[i].n > 0 &&
+                cudaMemsetAsync(const_cast<void*>(outs[i].p), 0,
+                                static_cast<size_t>(outs[i].n), stream) != cudaSuccess) {
+                cudaGetLastError();
+                return RMSMOD_ERR_CUDA;
+            }
+        return RMSMOD_OK;
+    }
+    rmsmod::SandwichBwdArgs a{};
+    a.update = update;
+    a.res = res;
+    a.post_weight = post_weight;
+    a.gate = gate;
+    a.gate_bstride = gate_bstride / 8;
+    a.weight = weight;
+    a.scale = scale;
+    a.mod_bstride = mod_bstride / 8;
+    a.grad_res = grad_res;
+    a.grad_out = grad_out;
+    a.post_rstd = post_rstd;
+    a.rstd = rstd;
+    a.grad_residual = grad_residual;
+    a.grad_update = grad_update;
+    a.grad_post_weight = grad_post_weight;
+    a.grad_gate = grad_gate;
+    a.grad_weight = grad_weight;
+    a.grad_scale = grad_scale;
+    a.grad_shift = grad_shift;
+    a.sums = sums;
+    a.partials = static_cast<float*>(workspace);
+    a.B = B;
+    a.S = S;
+    a.Dv = static_cast<int>(D / 8);
+    a.n = static_cast<float>(D);
+    a.residual_scale = residual_scale;
+    a.update_scale = update_scale;
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_sandwich_backward(a, dev, stream));
+}
+
+RMSMOD_EXPORT int sandwich_rmsnorm_modulate_backward(
+    const void* update, const void* res, const void* post_weight, const void* gate,
+    int64_t gate_bstride, const void* weight, const void* scale, int64_t mod_bstride,
+    const void* grad_res, const void* grad_out, const float* post_rstd, const float* rstd,
+    int64_t B, int64_t S, int64_t D, float residual_scale, float update_scale,
+    void* grad_residual, void* grad_update, float* grad_post_weight, float* grad_gate,
+    float* grad_weight, float* grad_scale, float* grad_shift, void* workspace,
+    size_t workspace_bytes, int dtype, rmsmod_stream_t stream)
+{
+    int st = check_bsd(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    if ((st = check_bstride_span(B, mod_bstride)) != RMSMOD_OK ||
+        (st = check_bstride_span(B, gate_bstride)) != RMSMOD_OK)
+        return st;
+    if (B * S != 0 && (!update || !post_rstd || (!grad_out && !grad_res) ||
+                       (grad_out && (!res || !rstd))))
+        return RMSMOD_ERR_NULL;
+    // a gradient by something that took no part
+    if (B * S != 0 && !grad_out && (grad_weight || grad_scale || grad_shift))
+        return RMSMOD_ERR_UNSUPPORTED;
+    return norm_backward(update, res, post_weight, gate, gate_bstride, weight, scale, mod_bstride,
+                         grad_res, grad_out, post_rstd, rstd, B, S, D, residual_scale,
+                         update_scale, grad_residual, grad_update, grad_post_weight, grad_gate,
+                         grad_weight, grad_scale, grad_shift, workspace, workspace_bytes, dtype,
+                         stream);
+}
+
+RMSMOD_EXPORT int rmsnorm_modulate_backward(const void* x, const void* weight, const void* scale,
+                                            int64_t mod_bstride, const void* grad_out,
+                                            const void* grad_res, const float* rstd, int64_t B,
+                                            int64_t S, int64_t D, void* grad_x,
+                                            float* grad_weight, float* grad_scale,
+                                            float* grad_shift, void* workspace,
+                                            size_t workspace_bytes, rmsmod_stream_t stream)
+{
+    int st = check_bsd(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    if ((st = check_bstride_span(B, mod_bstride)) != RMSMOD_OK)
+        return st;
+    if (B * S != 0 && (!x || !grad_out || !rstd))
+        return RMSMOD_ERR_NULL;
+    return norm_backward(nullptr, x, nullptr, nullptr, 0, weight, scale, mod_bstride, grad_res,
+                         grad_out, nullptr, rstd, B, S, D, 1.0f, 1.0f, grad_x, nullptr, nullptr,
+                         nullptr, grad_weight, grad_scale, grad_shift, workspace, workspace_bytes,
+                         RMSMOD_BF16, stream);
+}
+
 // ---- microscaled 4-bit rows and their product ----------------------------
 
 namespace {
@@ -777,8 +1045,6 @@ bool mxfp4_size(int64_t rows, int64_t K, Mxfp4Size& z)
     z.scale_bytes = z.row_tiles * z.block_tiles * 512;
     return true;
 }
-
-bool dtype_ok(int dtype) { return dtype == RMSMOD_BF16 || dtype == RMSMOD_F16; }
 
 int mxfp4_rows(bool quantize, const void* values, const void* packed, const void* scales,
                int64_t rows, int64_t K, int dtype, rmsmod_stream_t stream)

@@ -11,44 +11,15 @@
 //   scales   tiles of 128 rows by 4 blocks, 512 bytes each, [row tile][block tile]; in a tile row r
 //            and block k stand at byte (r % 32) * 16 + (r / 32) * 4 + k.  Bytes of rows and blocks
 //            that the matrix does not have are zero.
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
 
 #include "device_common.cuh"
+#include "half_types.cuh"
 #include "launch.h"
 #include "mxfp4.h"
 
 namespace rmsmod {
 
 namespace {
-
-// Two stored values of a word as fp32.
-template <typename T>
-__device__ __forceinline__ float2 widen2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w)
-{
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-template <>
-__device__ __forceinline__ float2 widen2<__half>(uint32_t w)
-{
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-
-template <typename T>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float lo, float hi)
-{
-    return pack_bf2(lo, hi);
-}
-template <>
-__device__ __forceinline__ uint32_t narrow2<__half>(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
-}
 
 // Eight e2m1 codes of eight fp32 (nearest, ties to even), element 0 in the lowest four bits.
 __device__ __forceinline__ uint32_t e2m1x8(const float (&v)[8])

@@ -8,12 +8,10 @@
 // issuing thread copies the scales into tensor memory and starts four products of 64 values each;
 // four warps read the accumulators back and finish the rows.
 #include <cuda.h>
-#include <cuda_bf16.h>
-#include <cuda_fp16.h>
-
 #include <mutex>
 
 #include "device_common.cuh"
+#include "half_types.cuh"
 #include "launch.h"
 #include "mxfp4.h"
 
@@ -109,32 +107,6 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
           "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]),
           "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(addr));
-}
-
-template <typename T>
-__device__ __forceinline__ float2 widen2(uint32_t w);
-template <>
-__device__ __forceinline__ float2 widen2<__nv_bfloat16>(uint32_t w)
-{
-    return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
-}
-template <>
-__device__ __forceinline__ float2 widen2<__half>(uint32_t w)
-{
-    return __half22float2(*reinterpret_cast<const __half2*>(&w));
-}
-template <typename T>
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi);
-template <>
-__device__ __forceinline__ uint32_t narrow2<__nv_bfloat16>(float lo, float hi)
-{
-    return pack_bf2(lo, hi);
-}
-template <>
-__device__ __forceinline__ uint32_t narrow2<__half>(float lo, float hi)
-{
-    const __half2 h = __floats2half2_rn(lo, hi);
-    return *reinterpret_cast<const uint32_t*>(&h);
 }
 
 struct Maps {
