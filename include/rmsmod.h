@@ -325,7 +325,7 @@ int conv_bias_epilogue(const void* x, const void* bias, int bias_is_fp32, const 
  *   A single-rounding tier: fp32 throughout (products and sums may be fused),
  *   one rounding per stored value.  The statistics are fp32 sums in an order
  *   that D alone fixes (batch-invariant), good to a few 2^-24; rows whose
- *   squares leave fp32's range are summed again at unit size.
+ *   squares leave fp32's range are summed again at unit size.  B * S < 2^31.
  *
  *   residual, update, res_out, out  [B*S*D] of `dtype` (RMSMOD_BF16 or
  *   RMSMOD_F16), res_out may equal residual; out nullable (then no norm after

@@ -15,6 +15,8 @@ rows may be strided views (adaLN chunk views of one projection output).
 from __future__ import annotations
 
 import ctypes
+import functools
+import math
 import os
 import threading
 from typing import NamedTuple
@@ -137,14 +139,33 @@ def _stream(stream):
     return ctypes.c_void_p(stream.cuda_stream)
 
 
+_entries = {}  # the library's functions by name, once looked up
+
+
+def _entry(name):
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(library(), name)
+    return fn
+
+
 def _call_on(device, name, *args, stream=None) -> None:
-    """_call on the tensors' own device, with `stream` (default: that device's current one) as the
-    last argument."""
-    if device.index == torch.cuda.current_device():
-        _call(name, *args, _stream(stream))
+    """Call `name` on the tensors' own device, with `stream` (default: that device's current one)
+    as the last argument.  Pointers are passed as integers (_at): half of a small call's time would
+    otherwise go into ctypes objects."""
+    index = device.index
+    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
+    if index == torch._C._cuda_getDevice():
+        st = _entry(name)(*args, raw)
     else:
         with torch.cuda.device(device):
-            _call(name, *args, _stream(stream))
+            st = _entry(name)(*args, raw)
+    if st != 0:
+        raise RmsmodError(st, name)
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
 
 
 def _scratch(stream, n, device):
@@ -186,10 +207,7 @@ def _mod_rows(t, B, D, name, dtype=torch.bfloat16):
     _bf16(t, name, dtype)
     if t.shape[-1] != D or t.stride(-1) != 1:
         raise ValueError(f"{name} must end in a unit-stride dimension of size {D}")
-    lead = [s for s in t.shape[:-1]]
-    rows = 1
-    for s in lead:
-        rows *= s
+    rows = t.numel() // D if D else math.prod(t.shape[:-1])
     if rows == 1:
         return 0
     if rows != B:
@@ -597,10 +615,10 @@ def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, wei
     _same_device(residual.device, update=update, post_weight=post_weight, gate=gate,
                  weight=weight, scale=scale, shift=shift, res_out=res_out, out=out,
                  post_rstd_out=post_rstd_out, rstd_out=rstd_out)
-    _call_on(residual.device, "sandwich_rmsnorm_modulate", _ptr(residual), _ptr(update),
-             _ptr(post_weight), _ptr(gate), gs, _ptr(weight), _ptr(scale), _ptr(shift), bs,
-             _ptr(res_out), _ptr(out), B, S, D, residual_scale, update_scale,
-             eps if post_eps is None else post_eps, eps, _ptr(post_rstd_out), _ptr(rstd_out),
+    _call_on(residual.device, "sandwich_rmsnorm_modulate", _at(residual), _at(update),
+             _at(post_weight), _at(gate), gs, _at(weight), _at(scale), _at(shift), bs,
+             _at(res_out), _at(out), B, S, D, residual_scale, update_scale,
+             eps if post_eps is None else post_eps, eps, _at(post_rstd_out), _at(rstd_out),
              _DTYPES[dt], stream=stream)
     return res_out, out
 
@@ -635,10 +653,15 @@ def _need_stats(t, n, name, device):
     _f32_out(t, n, name, device)
 
 
+@functools.lru_cache(maxsize=256)
+def _workspace_bytes(name, B, S, D):
+    return int(getattr(library(), name + "_workspace_bytes")(B, S, D))
+
+
 def _backward_workspace(name, workspace, wanted, B, S, D, device, stream):
     if not wanted:
         return None, 0
-    need = int(getattr(library(), name + "_workspace_bytes")(B, S, D))
+    need = _workspace_bytes(name, B, S, D)
     if workspace is None:
         workspace = _scratch(stream, max(need, 1), device)
     elif workspace.device != device or not workspace.is_contiguous():
@@ -691,11 +714,11 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
         _row_grads(need_mod and scale is not None, bs, B, D, device))
     workspace, wbytes = _backward_workspace("sandwich_rmsnorm_modulate_backward", workspace,
                                             need_mod, B, S, D, device, stream)
-    _call_on(device, "sandwich_rmsnorm_modulate_backward", _ptr(update), _ptr(res),
-             _ptr(post_weight), _ptr(gate), gs, _ptr(weight), _ptr(scale), bs, _ptr(grad_res),
-             _ptr(grad_out), _ptr(post_rstd), _ptr(rstd), B, S, D, residual_scale, update_scale,
-             _ptr(g.residual), _ptr(g.update), _ptr(g.post_weight), _ptr(g.gate), _ptr(g.weight),
-             _ptr(g.scale), _ptr(g.shift), _ptr(workspace), wbytes, _DTYPES[dt], stream=stream)
+    _call_on(device, "sandwich_rmsnorm_modulate_backward", _at(update), _at(res),
+             _at(post_weight), _at(gate), gs, _at(weight), _at(scale), bs, _at(grad_res),
+             _at(grad_out), _at(post_rstd), _at(rstd), B, S, D, residual_scale, update_scale,
+             _at(g.residual), _at(g.update), _at(g.post_weight), _at(g.gate), _at(g.weight),
+             _at(g.scale), _at(g.shift), _at(workspace), wbytes, _DTYPES[dt], stream=stream)
     return g
 
 
@@ -722,9 +745,9 @@ def rmsnorm_modulate_backward(x, weight, scale, grad_out, rstd, grad_res=None, n
     grad_shift = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
     workspace, wbytes = _backward_workspace("rmsnorm_modulate_backward", workspace, need_mod, B,
                                             S, D, x.device, stream)
-    _call_on(x.device, "rmsnorm_modulate_backward", _ptr(x), _ptr(weight), _ptr(scale), bs,
-             _ptr(grad_out), _ptr(grad_res), _ptr(rstd), B, S, D, _ptr(grad_x),
-             _ptr(grad_weight), _ptr(grad_scale), _ptr(grad_shift), _ptr(workspace), wbytes,
+    _call_on(x.device, "rmsnorm_modulate_backward", _at(x), _at(weight), _at(scale), bs,
+             _at(grad_out), _at(grad_res), _at(rstd), B, S, D, _at(grad_x),
+             _at(grad_weight), _at(grad_scale), _at(grad_shift), _at(workspace), wbytes,
              stream=stream)
     return grad_x, grad_weight, grad_scale, grad_shift
 
@@ -738,6 +761,7 @@ class Mxfp4(NamedTuple):
     scales: torch.Tensor
 
 
+@functools.lru_cache(maxsize=256)
 def mxfp4_scale_bytes(rows: int, K: int) -> int:
     """Bytes of the tiled scales of a [rows, K] 4-bit matrix (0 if the size is unsupported)."""
     return int(library().mxfp4_scale_bytes(rows, K))
@@ -773,7 +797,7 @@ def mxfp4_quantize(x, out=None, stream=None) -> Mxfp4:
                     torch.empty(mxfp4_scale_bytes(rows, K), dtype=torch.uint8, device=x.device))
     elif _codes(out, "out", x.device) != (rows, K):
         raise ValueError("out must match x")
-    _call_on(x.device, "mxfp4_quantize", _ptr(x), _ptr(out.packed), _ptr(out.scales), rows, K,
+    _call_on(x.device, "mxfp4_quantize", _at(x), _at(out.packed), _at(out.scales), rows, K,
              _DTYPES[x.dtype], stream=stream)
     return out
 
@@ -789,7 +813,7 @@ def mxfp4_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
         _dense(out, "out", dtype)
         if out.shape != (*q.packed.shape[:-1], K) or out.device != q.packed.device:
             raise ValueError("out must match q")
-    _call_on(out.device, "mxfp4_dequantize", _ptr(q.packed), _ptr(q.scales), _ptr(out), rows, K,
+    _call_on(out.device, "mxfp4_dequantize", _at(q.packed), _at(q.scales), _at(out), rows, K,
              _DTYPES[dtype], stream=stream)
     return out
 
@@ -844,8 +868,8 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
         codes = M * (K // 2)
         q = _scratch(stream, codes + mxfp4_scale_bytes(M, K), device)
         x = mxfp4_quantize(x, Mxfp4(q[:codes].view(*lead, K // 2), q[codes:]), stream)
-    _call_on(device, "mxfp4_matmul", _ptr(x.packed), _ptr(x.scales), _ptr(w.packed),
-             _ptr(w.scales), _ptr(bias), _ptr(gate), gs, _ptr(residual), _ptr(out), B, S, N, K,
+    _call_on(device, "mxfp4_matmul", _at(x.packed), _at(x.scales), _at(w.packed),
+             _at(w.scales), _at(bias), _at(gate), gs, _at(residual), _at(out), B, S, N, K,
              _DTYPES[dtype], stream=stream)
     return out
 

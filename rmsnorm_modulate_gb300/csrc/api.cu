@@ -794,6 +794,15 @@ int check_bstride_span(int64_t B, int64_t s)
     return s != 0 && B > INT64_MAX / 4 / s ? RMSMOD_ERR_STRIDE : RMSMOD_OK;
 }
 
+// check_bsd, and rows that 31 bits count.
+int check_rows31(int64_t B, int64_t S, int64_t D)
+{
+    const int st = check_bsd(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    return B * S > (int64_t{1} << 31) - 1 ? RMSMOD_ERR_SHAPE : RMSMOD_OK;
+}
+
 }  // namespace
 
 RMSMOD_EXPORT int sandwich_rmsnorm_modulate(
@@ -803,7 +812,7 @@ RMSMOD_EXPORT int sandwich_rmsnorm_modulate(
     float residual_scale, float update_scale, float post_eps, float eps, float* post_rstd_out,
     float* rstd_out, int dtype, rmsmod_stream_t stream)
 {
-    int st = check_bsd(B, S, D);
+    int st = check_rows31(B, S, D);
     if (st != RMSMOD_OK)
         return st;
     if (!dtype_ok(dtype))
@@ -863,14 +872,14 @@ RMSMOD_EXPORT int sandwich_rmsnorm_modulate(
 RMSMOD_EXPORT size_t sandwich_rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S,
                                                                         int64_t D)
 {
-    if (check_bsd(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
+    if (check_rows31(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
         return 0;
     return rmsmod::sandwich_backward_workspace_bytes(B, S, D, 3);
 }
 
 RMSMOD_EXPORT size_t rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S, int64_t D)
 {
-    if (check_bsd(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
+    if (check_rows31(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
         return 0;
     return rmsmod::sandwich_backward_workspace_bytes(B, S, D, 2);
 }
@@ -981,7 +990,7 @@ RMSMOD_EXPORT int sandwich_rmsnorm_modulate_backward(
     float* grad_weight, float* grad_scale, float* grad_shift, void* workspace,
     size_t workspace_bytes, int dtype, rmsmod_stream_t stream)
 {
-    int st = check_bsd(B, S, D);
+    int st = check_rows31(B, S, D);
     if (st != RMSMOD_OK)
         return st;
     if (!dtype_ok(dtype))
@@ -1010,7 +1019,7 @@ RMSMOD_EXPORT int rmsnorm_modulate_backward(const void* x, const void* weight, c
                                             float* grad_shift, void* workspace,
                                             size_t workspace_bytes, rmsmod_stream_t stream)
 {
-    int st = check_bsd(B, S, D);
+    int st = check_rows31(B, S, D);
     if (st != RMSMOD_OK)
         return st;
     if ((st = check_bstride_span(B, mod_bstride)) != RMSMOD_OK)

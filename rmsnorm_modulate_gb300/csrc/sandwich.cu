@@ -71,29 +71,38 @@ __device__ __forceinline__ void row_barrier()
         __syncthreads();
 }
 
-// Where the warps of a row leave their partial values: [value][warp of the row].
+// Where the warps of a row leave their partial values: [value][warp of the row, the other CTA's
+// after this one's places]; zeros where the row has no warp.
+constexpr int kMaxWarps = kMaxThreads / 32;
+
 template <int N>
-struct Exchange {
-    float v[N][2 * kMaxThreads / 32];
+struct __align__(16) Exchange {
+    float v[N][2 * kMaxWarps];
 };
 
-// N sums (or maxima) over all threads of the row, in an order that the row's length fixes; every
-// thread gets them.  One barrier: the same exchange may be used again after one more.
+template <int N>
+__device__ __forceinline__ void clear(Exchange<N>& ex)
+{
+    for (int i = threadIdx.x; i < N * 2 * kMaxWarps; i += blockDim.x)
+        ex.v[0][i] = 0.0f;
+}
+
+// N sums (or maxima of magnitudes) over all threads of the row, in an order that the row's length
+// fixes; every thread gets them.  One barrier: the same exchange may be used again after one more.
 template <int N, bool CL, bool MAX = false>
 __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, int warp, int lane,
                                            int warps, uint32_t rank)
 {
+    auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : __fadd_rn(a, b); };
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            const float o = __shfl_xor_sync(kFullMask, x[i], off);
-            x[i] = MAX ? fmaxf(x[i], o) : __fadd_rn(x[i], o);
-        }
+        for (int i = 0; i < N; ++i)
+            x[i] = join(x[i], __shfl_xor_sync(kFullMask, x[i], off));
     if (!CL && warps == 1)
         return;
     if (lane == 0) {
-        const int at = static_cast<int>(rank) * (kMaxThreads / 32) + warp;
+        const int at = static_cast<int>(rank) * kMaxWarps + warp;
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             ex.v[i][at] = x[i];
@@ -102,17 +111,17 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, int w
         }
     }
     row_barrier<CL>();
+    // four warps' values a load
+    const int quads = CL ? 2 * kMaxWarps / 4 : (warps + 3) / 4;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        float t = ex.v[i][0];
-        for (int w = 1; w < warps; ++w)
-            t = MAX ? fmaxf(t, ex.v[i][w]) : __fadd_rn(t, ex.v[i][w]);
-        if (CL)
-            for (int w = 0; w < warps; ++w) {
-                const float o = ex.v[i][kMaxThreads / 32 + w];
-                t = MAX ? fmaxf(t, o) : __fadd_rn(t, o);
-            }
-        x[i] = t;
+        const float4* q = reinterpret_cast<const float4*>(ex.v[i]);
+        float4 t = q[0];
+        for (int k = 1; k < quads; ++k) {
+            const float4 o = q[k];
+            t = make_float4(join(t.x, o.x), join(t.y, o.y), join(t.z, o.z), join(t.w, o.w));
+        }
+        x[i] = join(join(t.x, t.y), join(t.z, t.w));
     }
 }
 
@@ -167,14 +176,18 @@ __device__ __noinline__ float rstd_scaled(const uint4 (&x)[kV], float sum, float
 }
 
 template <typename T, bool CL>
-__device__ __forceinline__ float rstd_of(const uint4 (&x)[kV], float sum, float n, float eps,
-                                         Exchange<1> (&slow)[2], int warp, int lane, int warps,
+__device__ __forceinline__ float rstd_of(const uint4 (&x)[kV], float sum, float n, float inv_n,
+                                         float eps, Exchange<1> (&slow)[2], int warp, int lane, int warps,
                                          uint32_t rank)
 {
     // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
     if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f))
         return rstd_scaled<T, CL>(x, sum, n, eps, slow[0], slow[1], warp, lane, warps, rank);
-    return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps)));
+    // the approximate root and one Newton step: within 2 * 2^-24 of the root, in a tenth of the
+    // instructions of a division and a square root, which every warp of a row repeats
+    const float ms = __fmaf_rn(sum, inv_n, eps);
+    const float y = rsqrtf(ms);
+    return __fmaf_rn(__fmul_rn(0.5f, y), __fmaf_rn(__fmul_rn(-ms, y), y, 1.0f), y);
 }
 
 // ---------------------------------------------------------------------------
@@ -182,29 +195,31 @@ __device__ __forceinline__ float rstd_of(const uint4 (&x)[kV], float sum, float 
 // ---------------------------------------------------------------------------
 
 struct Items {
-    int64_t per_batch;
-    int64_t chunk;
-    int64_t count;
+    FastDiv per_batch;
+    uint32_t chunk;
+    uint32_t count;
+    uint32_t S;
     int stages;
 };
 
 struct Cursor {
-    int64_t item, row, end;
+    uint32_t item, batch, row, end;
 
-    __device__ __forceinline__ void open(const Items& it, int64_t S)
+    __device__ __forceinline__ void open(const Items& it)
     {
-        const int64_t b = item / it.per_batch;
-        row = b * S + (item - b * it.per_batch) * it.chunk;
-        end = row + it.chunk < (b + 1) * S ? row + it.chunk : (b + 1) * S;
+        batch = it.per_batch.div(item);
+        row = batch * it.S + (item - batch * it.per_batch.d) * it.chunk;
+        const uint32_t left = (batch + 1) * it.S - row;
+        end = row + (it.chunk < left ? it.chunk : left);
     }
     __device__ __forceinline__ bool valid(const Items& it) const { return item < it.count; }
-    __device__ __forceinline__ void advance(const Items& it, int64_t S, int64_t step)
+    __device__ __forceinline__ void advance(const Items& it, uint32_t step)
     {
         if (++row < end)
             return;
         item += step;
         if (item < it.count)
-            open(it, S);
+            open(it);
     }
 };
 
@@ -226,8 +241,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int warps = blockDim.x >> 5;
     const uint32_t rank = CL ? cluster_rank() : 0u;
-    const int64_t step = CL ? gridDim.x / 2 : gridDim.x;
-    const int64_t first = CL ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t step = CL ? gridDim.x / 2 : gridDim.x;
+    const uint32_t first = CL ? blockIdx.x / 2 : blockIdx.x;
     // this CTA's vectors of a row
     const int half = CL ? (a.Dv + 1) / 2 : a.Dv;
     const int v0 = static_cast<int>(rank) * half;
@@ -239,6 +254,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
             mbar_init(smem_addr(&full[s]), 1u);
         mbar_init_fence();
     }
+    clear(ex[0]);
+    clear(ex[1]);
+    clear(slow[0]);
+    clear(slow[1]);
     row_barrier<CL>();
     grid_dependency_sync();
 
@@ -248,7 +267,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
     uint4* res_out = static_cast<uint4*>(a.res_out) + v0;
     uint4* out = static_cast<uint4*>(a.out) + v0;
 
-    Cursor ahead{first, 0, 0};
+    Cursor ahead{first, 0, 0, 0};
     int put = 0;
     auto issue = [&]() {  // thread 0
         if (!ahead.valid(items))
@@ -257,15 +276,15 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
         const uint32_t dst = smem_addr(ring + static_cast<size_t>(put) * 2 * half);
         fence_proxy_async();
         mbar_expect_tx(bar, 2 * bytes);
-        bulk_g2s(dst, update + ahead.row * a.Dv, bytes, bar);
-        bulk_g2s(dst + half * 16, residual + ahead.row * a.Dv, bytes, bar);
+        bulk_g2s(dst, update + static_cast<int64_t>(ahead.row) * a.Dv, bytes, bar);
+        bulk_g2s(dst + half * 16, residual + static_cast<int64_t>(ahead.row) * a.Dv, bytes, bar);
         put = put + 1 == items.stages ? 0 : put + 1;
-        ahead.advance(items, a.S, step);
+        ahead.advance(items, step);
     };
-    Cursor at{first, 0, 0};
+    Cursor at{first, 0, 0, 0};
     if (at.valid(items)) {
-        at.open(items, a.S);
-        ahead.open(items, a.S);
+        at.open(items);
+        ahead.open(items);
     }
     if (threadIdx.x == 0)
         for (int s = 0; s < items.stages; ++s)
@@ -273,11 +292,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
 
     u64 v[kV][4], m[kV][4], sh[kV][4];
     const u64 rs2 = f2_splat(a.residual_scale);
-    int64_t batch = -1;
+    const float inv_n = __fdiv_rn(1.0f, a.n);
+    uint32_t batch = 0xFFFFFFFFu;
     int get = 0;
     uint32_t phase = 0;
-    for (; at.valid(items); at.advance(items, a.S, step)) {
-        const int64_t b = at.item / items.per_batch;
+    for (; at.valid(items); at.advance(items, step)) {
+        const uint32_t b = at.batch;
         if (b != batch) {  // the row vectors of this batch
             batch = b;
 #pragma unroll
@@ -328,9 +348,10 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
             __syncwarp();
         if (threadIdx.x == 0)
             issue();
-        const float rp = rstd_of<T, CL>(u, s[0], a.n, a.post_eps, slow, warp, lane, warps, rank);
+        const float rp = rstd_of<T, CL>(u, s[0], a.n, inv_n, a.post_eps, slow, warp, lane,
+                                         warps, rank);
         const u64 rp2 = f2_splat(rp);
-        const int64_t base = at.row * a.Dv;
+        const int64_t base = static_cast<int64_t>(at.row) * a.Dv;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = j * blockDim.x + threadIdx.x;
@@ -349,7 +370,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
         if (a.out) {
             s[0] = sum_squares<T>(x);
             row_reduce<1, CL>(s, ex[1], warp, lane, warps, rank);
-            const float r = rstd_of<T, CL>(x, s[0], a.n, a.eps, slow, warp, lane, warps, rank);
+            const float r = rstd_of<T, CL>(x, s[0], a.n, inv_n, a.eps, slow, warp, lane,
+                                            warps, rank);
             const u64 r2 = f2_splat(r);
 #pragma unroll
             for (int j = 0; j < kV; ++j) {
@@ -394,8 +416,8 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int warps = blockDim.x >> 5;
     const uint32_t rank = CL ? cluster_rank() : 0u;
-    const int64_t step = CL ? gridDim.x / 2 : gridDim.x;
-    const int64_t first = CL ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t step = CL ? gridDim.x / 2 : gridDim.x;
+    const uint32_t first = CL ? blockIdx.x / 2 : blockIdx.x;
     const int half = CL ? (a.Dv + 1) / 2 : a.Dv;
     const int v0 = static_cast<int>(rank) * half;
     const int nv = a.Dv - v0 < half ? a.Dv - v0 : half;
@@ -410,18 +432,20 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
             mbar_init(smem_addr(&full[s]), 1u);
         mbar_init_fence();
     }
+    clear(ex[0]);
+    clear(ex[1]);
     row_barrier<CL>();
     grid_dependency_sync();
 
     bool broken = false;
-    Cursor ahead{first, 0, 0};
+    Cursor ahead{first, 0, 0, 0};
     int put = 0;
     auto issue = [&]() {  // thread 0
         if (!ahead.valid(items))
             return;
         const uint32_t bar = smem_addr(&full[put]);
         const uint32_t dst = smem_addr(ring + static_cast<size_t>(put) * rows * half);
-        const int64_t from = ahead.row * a.Dv + v0;
+        const int64_t from = static_cast<int64_t>(ahead.row) * a.Dv + v0;
         auto bring = [&](int k, const void* p) {
             bulk_g2s(dst + k * half * 16, static_cast<const uint4*>(p) + from, bytes, bar);
         };
@@ -436,12 +460,12 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
         if (has_gr)
             bring(k_gr, a.grad_res);
         put = put + 1 == items.stages ? 0 : put + 1;
-        ahead.advance(items, a.S, step);
+        ahead.advance(items, step);
     };
-    Cursor at{first, 0, 0};
+    Cursor at{first, 0, 0, 0};
     if (at.valid(items)) {
-        at.open(items, a.S);
-        ahead.open(items, a.S);
+        at.open(items);
+        ahead.open(items);
     }
     // one slot less than the ring holds: a slot is refilled after the next row's barrier
     if (threadIdx.x == 0)
@@ -451,15 +475,16 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
     constexpr int kParts = (OUT ? 2 : 0) + (POST ? 1 : 0);
     u64 v[kV][4], m[kV][4];
     u64 sum_go[kV][4], sum_gh[kV][4], sum_du[kV][4];
-    auto clear = [&]() {
+    auto restart = [&]() {
 #pragma unroll
         for (int j = 0; j < kV; ++j)
 #pragma unroll
             for (int i = 0; i < 4; ++i)
                 sum_go[j][i] = sum_gh[j][i] = sum_du[j][i] = 0ull;
     };
-    clear();
-    int64_t batch = -1;
+    restart();
+    const float inv_n = __fdiv_rn(1.0f, a.n);
+    uint32_t batch = 0xFFFFFFFFu;
     int get = 0, par = 0;
     uint32_t phase = 0;
     float r = 0.0f, rp = 0.0f;
@@ -468,7 +493,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
         rp = POST ? a.post_rstd[at.row] : 0.0f;
     }
     while (at.valid(items)) {
-        const int64_t b = at.item / items.per_batch;
+        const uint32_t b = at.batch;
         if (b != batch) {
             batch = b;
 #pragma unroll
@@ -561,18 +586,18 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
             issue();
         // the next row's statistics, on their way during this row's second half
         Cursor next = at;
-        next.advance(items, a.S, step);
+        next.advance(items, step);
         float r_next = 0.0f, rp_next = 0.0f;
         if (next.valid(items)) {
             r_next = OUT ? a.rstd[next.row] : 0.0f;
             rp_next = POST ? a.post_rstd[next.row] : 0.0f;
         }
-        const float rc = __fmul_rn(r, __fdiv_rn(s[0], a.n));
-        const float c_upd = __fdiv_rn(__fmaf_rn(-rc, s[2], s[1]), a.n);
+        const float rc = __fmul_rn(r, __fmul_rn(s[0], inv_n));
+        const float c_upd = __fmul_rn(__fmaf_rn(-rc, s[2], s[1]), inv_n);
         const u64 nrc2 = f2_splat(-rc), ncu2 = f2_splat(-c_upd);
         const u64 rs2 = f2_splat(a.residual_scale);
         // ---- the gradients of the row
-        const int64_t base = at.row * a.Dv + v0;
+        const int64_t base = static_cast<int64_t>(at.row) * a.Dv + v0;
 #pragma unroll
         for (int j = 0; j < kV; ++j) {
             const int c = j * blockDim.x + threadIdx.x;
@@ -615,13 +640,14 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
             get = 0;
             phase ^= 1u;
         }
-        const int64_t item = at.item;
+        const uint32_t item = at.item;
         at = next;
         r = r_next;
         rp = rp_next;
         if (at.item != item) {  // the item's partial sums
             if (a.sums) {
-                float4* to = reinterpret_cast<float4*>(a.partials) + item * kParts * a.Dv * 2;
+                float4* to = reinterpret_cast<float4*>(a.partials) +
+                             static_cast<int64_t>(item) * kParts * a.Dv * 2;
 #pragma unroll
                 for (int j = 0; j < kV; ++j) {
                     const int c = j * blockDim.x + threadIdx.x;
@@ -644,7 +670,7 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
                         leave(kParts - 1, sum_du[j]);
                 }
             }
-            clear();
+            restart();
         }
     }
     if (broken)
@@ -788,7 +814,7 @@ cudaError_t launch_rows(K kern, const A& a, const Items& items, const Shape& s, 
     if (e != cudaSuccess)
         return e;
     const int64_t cap = static_cast<int64_t>(dev.sms) * ctas_per_sm(s) / (s.cluster ? 2 : 1);
-    const int64_t groups = items.count < cap ? items.count : cap;
+    const int64_t groups = static_cast<int64_t>(items.count) < cap ? items.count : cap;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(groups * (s.cluster ? 2 : 1)));
     cfg.blockDim = dim3(static_cast<unsigned>(s.threads));
@@ -806,17 +832,24 @@ cudaError_t launch_rows(K kern, const A& a, const Items& items, const Shape& s, 
     return cudaLaunchKernelEx(&cfg, kern, a, items);
 }
 
+Items items_of(int64_t B, int64_t S, int64_t chunk)
+{
+    Items it;
+    const int64_t per_batch = (S + chunk - 1) / chunk;
+    it.per_batch = FastDiv::make(static_cast<uint32_t>(per_batch));
+    it.chunk = static_cast<uint32_t>(chunk);
+    it.count = static_cast<uint32_t>(B * per_batch);
+    it.S = static_cast<uint32_t>(S);
+    it.stages = 2;
+    return it;
+}
+
 // Rows of a batch in items that spread over the GPU.
 Items spread(int64_t B, int64_t S, int64_t cap)
 {
-    Items it;
     int64_t per = cap / B;
     per = per < 1 ? 1 : (per > S ? S : per);
-    it.chunk = (S + per - 1) / per;
-    it.per_batch = (S + it.chunk - 1) / it.chunk;
-    it.count = B * it.per_batch;
-    it.stages = 2;
-    return it;
+    return items_of(B, S, (S + per - 1) / per);
 }
 
 template <typename T, int MAXT, bool CL>
@@ -847,13 +880,8 @@ Items backward_items(int64_t B, int64_t S, int Dv)
 {
     const Shape s = shape_of(Dv);
     const int64_t spread_over = 152 * ctas_per_sm(s) / (s.cluster ? 2 : 1);
-    Items it;
-    it.chunk = (S + spread_over - 1) / spread_over;
-    it.chunk = it.chunk < 1 ? 1 : (it.chunk > 64 ? 64 : it.chunk);
-    it.per_batch = (S + it.chunk - 1) / it.chunk;
-    it.count = B * it.per_batch;
-    it.stages = 2;
-    return it;
+    const int64_t chunk = (S + spread_over - 1) / spread_over;
+    return items_of(B, S, chunk > 64 ? 64 : chunk);
 }
 
 template <typename T, int MAXT, bool CL, bool POST, bool OUT>
@@ -885,7 +913,7 @@ cudaError_t launch_columns(const SandwichBwdArgs& a, const Items& it, cudaStream
     const int parts = (a.grad_out ? 2 : 0) + (a.update ? 1 : 0);
     const int grid = (a.Dv * 8 + 31) / 32;
     return launch_dependent(sandwich_columns_kernel<T>, grid, 32 * kColWarps, 0, stream, a,
-                            it.per_batch, parts);
+                            static_cast<int64_t>(it.per_batch.d), parts);
 }
 
 template <typename T>
