@@ -15,11 +15,12 @@
 // All in fp32 with one rounding per stored value.  Sums run in an order that D (and, over tokens,
 // S) alone fixes, so a result does not depend on the batch it stands in.
 //
-// Both are bound by HBM: 8 and 12 bytes per value.  A CTA takes a row at a time, two 16-byte vectors
-// a thread; the rows come through a ring of bulk copies (TMA) that stays ahead of the arithmetic,
-// the row vectors' products stay in registers for all rows of a batch.  Rows of more than 8192
-// values are shared by a cluster of two CTAs, which exchange their partial sums through distributed
-// shared memory.
+// Both are bound by HBM: 8 and 12 bytes per value.  One CTA of up to 16 warps per SM; its warps form
+// groups that take a row each, four (forward) or two (backward) 16-byte vectors a thread, and every
+// group has a ring of bulk copies (TMA) that stays ahead of the arithmetic.  The products of a
+// batch's row vectors lie in shared memory for all groups.  A row's values are in registers when its
+// slot is refilled, before its sums are known.  Rows of more than 8192 values are shared by a
+// cluster of two CTAs, which exchange their partial sums through distributed shared memory.
 #include "device_common.cuh"
 #include "half_types.cuh"
 #include "launch.h"
@@ -31,11 +32,11 @@ namespace {
 
 __device__ unsigned int g_error;
 
-constexpr int kV = 2;              // 16-byte vectors per thread
-constexpr int kMaxStages = 8;
-constexpr int kMaxThreads = 512;
-constexpr int kMaxDvPerCta = kMaxThreads * kV;
-constexpr int kSmemPerSm = 216 * 1024;
+constexpr int kMaxWarps = 16;      // of a CTA
+constexpr int kMaxThreads = 32 * kMaxWarps;
+constexpr int kMaxDvPerCta = 1024; // vectors of a row that one CTA takes
+constexpr int kMaxStages = 4;      // of a group's ring
+constexpr int kSmemBytes = 222 * 1024;
 
 // ---------------------------------------------------------------------------
 // sums over a row
@@ -62,60 +63,97 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t rank, float v)
                  : "memory");
 }
 
+// The threads of a CTA that share rows.
+struct Group {
+    int warps;       // of a group
+    int index;       // of this group in its CTA
+    int warp;        // of this thread in its group
+    int lane;
+    uint32_t rank;   // of the CTA in its cluster
+
+    __device__ __forceinline__ bool leader() const { return warp == 0 && lane == 0; }
+    __device__ __forceinline__ int at(int j) const { return (j * warps + warp) * 32 + lane; }
+};
+
 template <bool CL>
-__device__ __forceinline__ void row_barrier()
+__device__ __forceinline__ void group_barrier(const Group& g)
 {
     if (CL)
         cluster_barrier();
+    else if (g.warps == 1)
+        __syncwarp();
     else
-        __syncthreads();
+        asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.warps * 32) : "memory");
 }
 
-// Where the warps of a row leave their partial values: [value][warp of the row, the other CTA's
-// after this one's places]; zeros where the row has no warp.
-constexpr int kMaxWarps = kMaxThreads / 32;
-
+// Where the warps of a row leave their partial values: per value 32 places, a group's warps from a
+// multiple of four on (in a cluster the two CTAs' warps from 0 and 16 on); zeros where there is no
+// warp.
 template <int N>
 struct __align__(16) Exchange {
-    float v[N][2 * kMaxWarps];
+    float v[N][32];
 };
 
 template <int N>
 __device__ __forceinline__ void clear(Exchange<N>& ex)
 {
-    for (int i = threadIdx.x; i < N * 2 * kMaxWarps; i += blockDim.x)
+    for (int i = threadIdx.x; i < N * 32; i += blockDim.x)
         ex.v[0][i] = 0.0f;
 }
 
 // N sums (or maxima of magnitudes) over all threads of the row, in an order that the row's length
 // fixes; every thread gets them.  One barrier: the same exchange may be used again after one more.
 template <int N, bool CL, bool MAX = false>
-__device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, int warp, int lane,
-                                           int warps, uint32_t rank)
+__device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const Group& g)
 {
     auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : __fadd_rn(a, b); };
+    const int first = CL ? 0 : g.index * ((g.warps + 3) & ~3);
+    if constexpr (N == 3) {
+        // three sums in six exchanges: each step halves the values that a lane still carries, so
+        // lanes 0-7, 8-15 and 16-23 end with one sum each
+        const bool up = g.lane & 16, odd = g.lane & 8;
+        float a = join(up ? x[2] : x[0], __shfl_xor_sync(kFullMask, up ? x[0] : x[2], 16));
+        const float b = join(up ? 0.0f : x[1], __shfl_xor_sync(kFullMask, up ? x[1] : 0.0f, 16));
+        a = join(odd ? b : a, __shfl_xor_sync(kFullMask, odd ? a : b, 8));
 #pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i)
-            x[i] = join(x[i], __shfl_xor_sync(kFullMask, x[i], off));
-    if (!CL && warps == 1)
-        return;
-    if (lane == 0) {
-        const int at = static_cast<int>(rank) * kMaxWarps + warp;
-#pragma unroll
-        for (int i = 0; i < N; ++i) {
-            ex.v[i][at] = x[i];
+        for (int off = 4; off > 0; off >>= 1)
+            a = join(a, __shfl_xor_sync(kFullMask, a, off));
+        if (!CL && g.warps == 1) {
+            x[0] = __shfl_sync(kFullMask, a, 0);
+            x[1] = __shfl_sync(kFullMask, a, 8);
+            x[2] = __shfl_sync(kFullMask, a, 16);
+            return;
+        }
+        if ((g.lane & 7) == 0 && g.lane < 24) {
+            float* to = &ex.v[g.lane >> 3][(CL ? static_cast<int>(g.rank) * 16 : first) + g.warp];
+            *to = a;
             if (CL)
-                st_peer(smem_addr(&ex.v[i][at]), rank ^ 1u, x[i]);
+                st_peer(smem_addr(to), g.rank ^ 1u, a);
+        }
+    } else {
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+#pragma unroll
+            for (int i = 0; i < N; ++i)
+                x[i] = join(x[i], __shfl_xor_sync(kFullMask, x[i], off));
+        if (!CL && g.warps == 1)
+            return;
+        if (g.lane == 0) {
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                float* to = &ex.v[i][(CL ? static_cast<int>(g.rank) * 16 : first) + g.warp];
+                *to = x[i];
+                if (CL)
+                    st_peer(smem_addr(to), g.rank ^ 1u, x[i]);
+            }
         }
     }
-    row_barrier<CL>();
+    group_barrier<CL>(g);
     // four warps' values a load
-    const int quads = CL ? 2 * kMaxWarps / 4 : (warps + 3) / 4;
+    const int quads = CL ? 8 : (g.warps + 3) / 4;
 #pragma unroll
     for (int i = 0; i < N; ++i) {
-        const float4* q = reinterpret_cast<const float4*>(ex.v[i]);
+        const float4* q = reinterpret_cast<const float4*>(&ex.v[i][first]);
         float4 t = q[0];
         for (int k = 1; k < quads; ++k) {
             const float4 o = q[k];
@@ -125,64 +163,74 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, int w
     }
 }
 
-template <typename T>
-__device__ __forceinline__ float sum_squares(const uint4 (&x)[kV])
+template <typename T, int V>
+__device__ __forceinline__ float sum_squares(const uint4 (&x)[V])
 {
-    u64 s = 0ull;
+    u64 s[2] = {0ull, 0ull};
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const u64 p = widen<T>(word(x[j], i));
-            s = f2_fma(p, p, s);
+            s[i & 1] = f2_fma(p, p, s[i & 1]);
         }
     float lo, hi;
-    f2_unpack(s, lo, hi);
+    f2_unpack(f2_add(s[0], s[1]), lo, hi);
     return __fadd_rn(lo, hi);
 }
 
+// Vectors handed to a function that is not inlined: by value, so that the caller's stay in registers
+// (a reference would keep them in local memory for every row).
+template <int V>
+struct Vectors {
+    uint4 v[V];
+};
+
 // 1 / sqrt of a row whose fp32 sum of squares left fp32's comfortable range although its values are
 // finite: squares of the values over the power of two of the largest, joined in fp64.
-template <typename T, bool CL>
-__device__ __noinline__ float rstd_scaled(const uint4 (&x)[kV], float sum, float n, float eps,
-                                          Exchange<1>& e0, Exchange<1>& e1, int warp, int lane,
-                                          int warps, uint32_t rank)
+template <typename T, int V, bool CL>
+__device__ __noinline__ float rstd_scaled(const Vectors<V> x, float sum, float n, float eps,
+                                          Exchange<1>& e0, Exchange<1>& e1, const Group g)
 {
     float top[1] = {0.0f};
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 p = widen2<T>(word(x[j], i));
+            const float2 p = widen2<T>(word(x.v[j], i));
             top[0] = fmaxf(top[0], fmaxf(fabsf(p.x), fabsf(p.y)));
         }
-    row_reduce<1, CL, true>(top, e0, warp, lane, warps, rank);
+    row_reduce<1, CL, true>(top, e0, g);
     // Inf, or nothing but zeros: the sum says it all.  (A NaN never gets here.)
     if (!(top[0] <= 3.4028235e38f) || top[0] == 0.0f)
         return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps)));
     const int e = ilogbf(top[0]);
     float s[1] = {0.0f};
 #pragma unroll
-    for (int j = 0; j < kV; ++j)
+    for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 p = widen2<T>(word(x[j], i));
+            const float2 p = widen2<T>(word(x.v[j], i));
             const float a = scalbnf(p.x, -e), b = scalbnf(p.y, -e);
             s[0] = __fadd_rn(s[0], __fadd_rn(__fmul_rn(a, a), __fmul_rn(b, b)));
         }
-    row_reduce<1, CL>(s, e1, warp, lane, warps, rank);
+    row_reduce<1, CL>(s, e1, g);
     const double ms = scalbn(static_cast<double>(s[0]) / static_cast<double>(n), 2 * e);
     return static_cast<float>(1.0 / sqrt(ms + static_cast<double>(eps)));
 }
 
-template <typename T, bool CL>
-__device__ __forceinline__ float rstd_of(const uint4 (&x)[kV], float sum, float n, float inv_n,
-                                         float eps, Exchange<1> (&slow)[2], int warp, int lane, int warps,
-                                         uint32_t rank)
+template <typename T, int V, bool CL>
+__device__ __forceinline__ float rstd_of(const uint4 (&x)[V], float sum, float n, float inv_n,
+                                         float eps, Exchange<1> (&slow)[2], const Group& g)
 {
     // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
-    if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f))
-        return rstd_scaled<T, CL>(x, sum, n, eps, slow[0], slow[1], warp, lane, warps, rank);
+    if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f)) {
+        Vectors<V> copy;
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+            copy.v[j] = x[j];
+        return rstd_scaled<T, V, CL>(copy, sum, n, eps, slow[0], slow[1], g);
+    }
     // the approximate root and one Newton step: within 2 * 2^-24 of the root, in a tenth of the
     // instructions of a division and a square root, which every warp of a row repeats
     const float ms = __fmaf_rn(sum, inv_n, eps);
@@ -191,74 +239,167 @@ __device__ __forceinline__ float rstd_of(const uint4 (&x)[kV], float sum, float 
 }
 
 // ---------------------------------------------------------------------------
-// rows of a CTA (or cluster): items blockIdx, blockIdx + grid, ... of `chunk` rows of one batch
+// rows of a CTA (or cluster): items blockIdx, blockIdx + grid, ... of `chunk` rows of one batch,
+// dealt to its groups in turn
 // ---------------------------------------------------------------------------
 
-struct Items {
+struct Plan {
     FastDiv per_batch;
     uint32_t chunk;
     uint32_t count;
     uint32_t S;
-    int stages;
+    int groups;
+    int warps;   // of a group
+    int stages;  // of a group's ring
 };
 
-struct Cursor {
-    uint32_t item, batch, row, end;
+struct Span {  // an item
+    uint32_t batch, begin, end;
 
-    __device__ __forceinline__ void open(const Items& it)
+    __device__ __forceinline__ Span(const Plan& p, uint32_t item)
     {
-        batch = it.per_batch.div(item);
-        row = batch * it.S + (item - batch * it.per_batch.d) * it.chunk;
-        const uint32_t left = (batch + 1) * it.S - row;
-        end = row + (it.chunk < left ? it.chunk : left);
+        batch = p.per_batch.div(item);
+        begin = batch * p.S + (item - batch * p.per_batch.d) * p.chunk;
+        const uint32_t left = (batch + 1) * p.S - begin;
+        end = begin + (p.chunk < left ? p.chunk : left);
     }
-    __device__ __forceinline__ bool valid(const Items& it) const { return item < it.count; }
-    __device__ __forceinline__ void advance(const Items& it, uint32_t step)
+};
+
+// The rows of one group ahead of its arithmetic, in the ring's order.
+struct Ahead {
+    uint32_t item, row, end;
+    int put;
+
+    __device__ __forceinline__ void seek(const Plan& p, uint32_t step, int group)
     {
-        if (++row < end)
+        for (; item < p.count; item += step) {
+            const Span s(p, item);
+            row = s.begin + group;
+            end = s.end;
+            if (row < end)
+                return;
+        }
+    }
+    __device__ __forceinline__ void start(const Plan& p, uint32_t first, uint32_t step, int group)
+    {
+        item = first;
+        put = 0;
+        seek(p, step, group);
+    }
+    __device__ __forceinline__ void advance(const Plan& p, uint32_t step, int group)
+    {
+        put = put + 1 == p.stages ? 0 : put + 1;
+        row += p.groups;
+        if (row < end)
             return;
         item += step;
-        if (item < it.count)
-            open(it);
+        seek(p, step, group);
     }
 };
 
-template <int MAXT>
-constexpr int min_blocks() { return kMaxThreads / MAXT; }
+// Shared memory: per vector of the CTA's part of a row the fp32 products of the row vectors in two
+// halves of four values (so that neighbouring lanes read neighbouring 16 bytes), then the rings.
+__device__ __forceinline__ void put_pairs(float4* lo, float4* hi, const u64 (&t)[4])
+{
+    float4 f;
+    f2_unpack(t[0], f.x, f.y);
+    f2_unpack(t[1], f.z, f.w);
+    *lo = f;
+    f2_unpack(t[2], f.x, f.y);
+    f2_unpack(t[3], f.z, f.w);
+    *hi = f;
+}
+
+__device__ __forceinline__ void get_pairs(const float4* lo, const float4* hi, u64 (&t)[4])
+{
+    const float4 a = *lo, b = *hi;
+    t[0] = f2_pack(a.x, a.y);
+    t[1] = f2_pack(a.z, a.w);
+    t[2] = f2_pack(b.x, b.y);
+    t[3] = f2_pack(b.z, b.w);
+}
+
+// Product of a constant and up to two nullable row vectors at vector c.
+template <typename T>
+__device__ __forceinline__ void product(u64 (&t)[4], float k, const void* p, const void* q,
+                                        int64_t q_at, int c)
+{
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        t[i] = f2_splat(k);
+    if (p) {
+        const uint4 w = ld_cached(static_cast<const uint4*>(p) + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = f2_mul(t[i], widen<T>(word(w, i)));
+    }
+    if (q) {
+        const uint4 w = ld_cached(static_cast<const uint4*>(q) + q_at + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = f2_mul(t[i], widen<T>(word(w, i)));
+    }
+}
+
+// weight * (1 + scale)
+template <typename T>
+__device__ __forceinline__ void multiplier(u64 (&t)[4], const void* weight, const void* scale,
+                                           int64_t scale_at, int c)
+{
+    product<T>(t, 1.0f, weight, nullptr, 0, c);
+    if (scale) {
+        const uint4 w = ld_cached(static_cast<const uint4*>(scale) + scale_at + c);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            t[i] = f2_mul(t[i], f2_add(f2_splat(1.0f), widen<T>(word(w, i))));
+    }
+}
 
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
 
-template <typename T, int MAXT, bool CL>
-__global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
-    sandwich_kernel(const SandwichArgs a, const Items items)
+constexpr int kFwdVectorBytes = 80;  // v and m in fp32, shift as stored
+
+template <typename T, int V, bool CL>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    sandwich_kernel(const SandwichArgs a, const Plan plan)
 {
-    extern __shared__ __align__(128) uint4 ring[];
-    __shared__ __align__(8) unsigned long long full[kMaxStages];
+    extern __shared__ __align__(128) uint4 smem[];
+    __shared__ __align__(8) unsigned long long full[kMaxWarps][kMaxStages];
     __shared__ Exchange<1> ex[2], slow[2];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int warps = blockDim.x >> 5;
-    const uint32_t rank = CL ? cluster_rank() : 0u;
+    Group g;
+    g.warps = plan.warps;
+    g.index = (threadIdx.x >> 5) / plan.warps;
+    g.warp = (threadIdx.x >> 5) - g.index * plan.warps;
+    g.lane = threadIdx.x & 31;
+    g.rank = CL ? cluster_rank() : 0u;
     const uint32_t step = CL ? gridDim.x / 2 : gridDim.x;
     const uint32_t first = CL ? blockIdx.x / 2 : blockIdx.x;
     // this CTA's vectors of a row
     const int half = CL ? (a.Dv + 1) / 2 : a.Dv;
-    const int v0 = static_cast<int>(rank) * half;
+    const int v0 = static_cast<int>(g.rank) * half;
     const int nv = a.Dv - v0 < half ? a.Dv - v0 : half;
     const uint32_t bytes = static_cast<uint32_t>(nv) * 16u;
+    float4* v_lo = reinterpret_cast<float4*>(smem);
+    float4 *v_hi = v_lo + half, *m_lo = v_lo + 2 * half, *m_hi = v_lo + 3 * half;
+    uint4* sh = smem + 4 * half;
+    uint4* ring = smem + 5 * half + static_cast<size_t>(g.index) * plan.stages * 2 * half;
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < items.stages; ++s)
-            mbar_init(smem_addr(&full[s]), 1u);
+    if (g.leader()) {
+        for (int s = 0; s < plan.stages; ++s)
+            mbar_init(smem_addr(&full[g.index][s]), 1u);
         mbar_init_fence();
     }
     clear(ex[0]);
     clear(ex[1]);
     clear(slow[0]);
     clear(slow[1]);
-    row_barrier<CL>();
+    if (CL)
+        cluster_barrier();
+    else
+        __syncthreads();
     grid_dependency_sync();
 
     bool broken = false;
@@ -266,132 +407,119 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
     const uint4* __restrict__ update = static_cast<const uint4*>(a.update) + v0;
     uint4* res_out = static_cast<uint4*>(a.res_out) + v0;
     uint4* out = static_cast<uint4*>(a.out) + v0;
+    const float inv_n = __fdiv_rn(1.0f, a.n);
+    const u64 rs2 = f2_splat(a.residual_scale);
 
-    Cursor ahead{first, 0, 0, 0};
-    int put = 0;
-    auto issue = [&]() {  // thread 0
-        if (!ahead.valid(items))
+    Ahead ahead{};
+    auto issue = [&]() {  // the group's leader
+        if (ahead.item >= plan.count)
             return;
-        const uint32_t bar = smem_addr(&full[put]);
-        const uint32_t dst = smem_addr(ring + static_cast<size_t>(put) * 2 * half);
+        const uint32_t bar = smem_addr(&full[g.index][ahead.put]);
+        const uint32_t dst = smem_addr(ring + static_cast<size_t>(ahead.put) * 2 * half);
+        const int64_t from = static_cast<int64_t>(ahead.row) * a.Dv;
         fence_proxy_async();
         mbar_expect_tx(bar, 2 * bytes);
-        bulk_g2s(dst, update + static_cast<int64_t>(ahead.row) * a.Dv, bytes, bar);
-        bulk_g2s(dst + half * 16, residual + static_cast<int64_t>(ahead.row) * a.Dv, bytes, bar);
-        put = put + 1 == items.stages ? 0 : put + 1;
-        ahead.advance(items, step);
+        bulk_g2s(dst, update + from, bytes, bar);
+        bulk_g2s(dst + half * 16, residual + from, bytes, bar);
+        ahead.advance(plan, step, g.index);
     };
-    Cursor at{first, 0, 0, 0};
-    if (at.valid(items)) {
-        at.open(items);
-        ahead.open(items);
-    }
-    if (threadIdx.x == 0)
-        for (int s = 0; s < items.stages; ++s)
+    if (g.leader()) {
+        ahead.start(plan, first, step, g.index);
+        for (int s = 0; s < plan.stages; ++s)
             issue();
+    }
 
-    u64 v[kV][4], m[kV][4], sh[kV][4];
-    const u64 rs2 = f2_splat(a.residual_scale);
-    const float inv_n = __fdiv_rn(1.0f, a.n);
-    uint32_t batch = 0xFFFFFFFFu;
+    uint32_t batch = 0xFFFFFFFFu, phase = 0;
     int get = 0;
-    uint32_t phase = 0;
-    for (; at.valid(items); at.advance(items, step)) {
-        const uint32_t b = at.batch;
-        if (b != batch) {  // the row vectors of this batch
-            batch = b;
+    for (uint32_t item = first; item < plan.count; item += step) {
+        const Span span(plan, item);
+        if (span.batch != batch) {  // the row vectors of this batch
+            __syncthreads();
+            batch = span.batch;
+            for (int c = threadIdx.x; c < nv; c += blockDim.x) {
+                u64 t[4];
+                product<T>(t, a.update_scale, a.post_weight, a.gate, batch * a.gate_bstride,
+                           v0 + c);
+                put_pairs(v_lo + c, v_hi + c, t);
+                multiplier<T>(t, a.weight, a.scale, batch * a.mod_bstride, v0 + c);
+                put_pairs(m_lo + c, m_hi + c, t);
+                sh[c] = a.shift ? ld_cached(static_cast<const uint4*>(a.shift) +
+                                            batch * a.mod_bstride + v0 + c)
+                                : make_uint4(0u, 0u, 0u, 0u);
+            }
+            __syncthreads();
+        }
+        for (uint32_t row = span.begin + g.index; row < span.end; row += plan.groups) {
+            if (!broken && !mbar_wait(smem_addr(&full[g.index][get]), phase, kWaitLimitNs)) {
+                broken = true;
+                atomicOr(&g_error, kErrCopyTimeout);
+            }
+            const uint4* slot = ring + static_cast<size_t>(get) * 2 * half;
+            if (++get == plan.stages) {
+                get = 0;
+                phase ^= 1u;
+            }
+            uint4 u[V], x[V];
 #pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const int c = j * blockDim.x + threadIdx.x;
-                const bool in = c < nv;
-                auto load = [&](const void* p, int64_t row) {
-                    return in && p ? ld_cached(static_cast<const uint4*>(p) + row + v0 + c)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                };
-                const uint4 wp = load(a.post_weight, 0), g = load(a.gate, b * a.gate_bstride);
-                const uint4 w = load(a.weight, 0), sc = load(a.scale, b * a.mod_bstride);
-                const uint4 sf = load(a.shift, b * a.mod_bstride);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const u64 one = f2_splat(1.0f);
-                    u64 t = f2_splat(a.update_scale);
-                    if (a.post_weight)
-                        t = f2_mul(t, widen<T>(word(wp, i)));
-                    if (a.gate)
-                        t = f2_mul(t, widen<T>(word(g, i)));
-                    v[j][i] = t;
-                    t = a.weight ? widen<T>(word(w, i)) : one;
-                    m[j][i] = a.scale ? f2_mul(t, f2_add(one, widen<T>(word(sc, i)))) : t;
-                    sh[j][i] = widen<T>(word(sf, i));
+            for (int j = 0; j < V; ++j) {
+                const int c = g.at(j);
+                u[j] = x[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < nv) {
+                    u[j] = slot[c];
+                    x[j] = slot[half + c];
                 }
             }
-        }
-        if (!broken && !mbar_wait(smem_addr(&full[get]), phase, kWaitLimitNs)) {
-            broken = true;
-            atomicOr(&g_error, kErrCopyTimeout);
-        }
-        const uint4* slot = ring + static_cast<size_t>(get) * 2 * half;
-        uint4 u[kV], x[kV];
+            float s[1] = {sum_squares<T, V>(u)};
+            row_reduce<1, CL>(s, ex[0], g);
+            // a barrier has passed (or a warp's exchange, for a group of one): the slot is read
+            if (!CL && g.warps == 1)
+                __syncwarp();
+            if (g.leader())
+                issue();
+            const float rp = rstd_of<T, V, CL>(u, s[0], a.n, inv_n, a.post_eps, slow, g);
+            const u64 rp2 = f2_splat(rp);
+            const int64_t base = static_cast<int64_t>(row) * a.Dv;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int c = j * blockDim.x + threadIdx.x;
-            u[j] = x[j] = make_uint4(0u, 0u, 0u, 0u);
-            if (c < nv) {
-                u[j] = slot[c];
-                x[j] = slot[half + c];
+            for (int j = 0; j < V; ++j) {
+                const int c = g.at(j);
+                if (c < nv) {
+                    u64 t[4];
+                    get_pairs(v_lo + c, v_hi + c, t);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        word(x[j], i) = narrow<T>(
+                            f2_fma(widen<T>(word(x[j], i)), rs2,
+                                   f2_mul(f2_mul(widen<T>(word(u[j], i)), rp2), t[i])));
+                    st_stream(res_out + base + c, x[j]);
+                }
             }
-        }
-        float s[1] = {sum_squares<T>(u)};
-        row_reduce<1, CL>(s, ex[0], warp, lane, warps, rank);
-        // a barrier has passed (or this is the only warp): the slot has been read
-        if (!CL && warps == 1)
-            __syncwarp();
-        if (threadIdx.x == 0)
-            issue();
-        const float rp = rstd_of<T, CL>(u, s[0], a.n, inv_n, a.post_eps, slow, warp, lane,
-                                         warps, rank);
-        const u64 rp2 = f2_splat(rp);
-        const int64_t base = static_cast<int64_t>(at.row) * a.Dv;
+            if (g.leader() && g.rank == 0 && a.post_rstd_out)
+                a.post_rstd_out[row] = rp;
+            if (a.out) {
+                s[0] = sum_squares<T, V>(x);
+                row_reduce<1, CL>(s, ex[1], g);
+                const float r = rstd_of<T, V, CL>(x, s[0], a.n, inv_n, a.eps, slow, g);
+                const u64 r2 = f2_splat(r);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int c = j * blockDim.x + threadIdx.x;
+                for (int j = 0; j < V; ++j) {
+                    const int c = g.at(j);
+                    if (c < nv) {
+                        u64 t[4];
+                        get_pairs(m_lo + c, m_hi + c, t);
+                        const uint4 sf = sh[c];
+                        uint4 o;
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                word(x[j], i) = narrow<T>(
-                    f2_fma(widen<T>(word(x[j], i)), rs2,
-                           f2_mul(f2_mul(widen<T>(word(u[j], i)), rp2), v[j][i])));
-            if (c < nv)
-                st_stream(res_out + base + c, x[j]);
-            else
-                x[j] = make_uint4(0u, 0u, 0u, 0u);
-        }
-        if (threadIdx.x == 0 && rank == 0 && a.post_rstd_out)
-            a.post_rstd_out[at.row] = rp;
-        if (a.out) {
-            s[0] = sum_squares<T>(x);
-            row_reduce<1, CL>(s, ex[1], warp, lane, warps, rank);
-            const float r = rstd_of<T, CL>(x, s[0], a.n, inv_n, a.eps, slow, warp, lane,
-                                            warps, rank);
-            const u64 r2 = f2_splat(r);
-#pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const int c = j * blockDim.x + threadIdx.x;
-                uint4 o;
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    word(o, i) = narrow<T>(
-                        f2_fma(f2_mul(widen<T>(word(x[j], i)), r2), m[j][i], sh[j][i]));
-                if (c < nv)
-                    st_stream(out + base + c, o);
+                        for (int i = 0; i < 4; ++i)
+                            word(o, i) = narrow<T>(f2_fma(f2_mul(widen<T>(word(x[j], i)), r2),
+                                                          t[i], widen<T>(word(sf, i))));
+                        st_stream(out + base + c, o);
+                    }
+                }
+                if (g.leader() && g.rank == 0 && a.rstd_out)
+                    a.rstd_out[row] = r;
+            } else {
+                group_barrier<CL>(g);  // between two uses of ex[0]
             }
-            if (threadIdx.x == 0 && rank == 0 && a.rstd_out)
-                a.rstd_out[at.row] = r;
-        } else {
-            row_barrier<CL>();  // between two uses of ex[0]
-        }
-        if (++get == items.stages) {
-            get = 0;
-            phase ^= 1u;
         }
     }
     if (broken)
@@ -404,47 +532,62 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
 // backward
 // ---------------------------------------------------------------------------
 
+constexpr int kBwdVectorBytes = 64;  // v and m in fp32
+
 // POST: the block's post norm takes part (update), OUT: the norm after the add does (grad_out).
-template <typename T, int MAXT, bool CL, bool POST, bool OUT>
-__global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
-    sandwich_bwd_kernel(const SandwichBwdArgs a, const Items items)
+template <typename T, int V, bool CL, bool POST, bool OUT>
+__global__ void __launch_bounds__(kMaxThreads, 1)
+    sandwich_bwd_kernel(const SandwichBwdArgs a, const Plan plan)
 {
-    extern __shared__ __align__(128) uint4 ring[];
-    __shared__ __align__(8) unsigned long long full[kMaxStages];
+    extern __shared__ __align__(128) uint4 smem[];
+    __shared__ __align__(8) unsigned long long full[kMaxWarps][kMaxStages];
     __shared__ Exchange<3> ex[2];
 
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int warps = blockDim.x >> 5;
-    const uint32_t rank = CL ? cluster_rank() : 0u;
+    Group g;
+    g.warps = plan.warps;
+    g.index = (threadIdx.x >> 5) / plan.warps;
+    g.warp = (threadIdx.x >> 5) - g.index * plan.warps;
+    g.lane = threadIdx.x & 31;
+    g.rank = CL ? cluster_rank() : 0u;
     const uint32_t step = CL ? gridDim.x / 2 : gridDim.x;
     const uint32_t first = CL ? blockIdx.x / 2 : blockIdx.x;
     const int half = CL ? (a.Dv + 1) / 2 : a.Dv;
-    const int v0 = static_cast<int>(rank) * half;
+    const int v0 = static_cast<int>(g.rank) * half;
     const int nv = a.Dv - v0 < half ? a.Dv - v0 : half;
     const uint32_t bytes = static_cast<uint32_t>(nv) * 16u;
     const bool has_gr = a.grad_res != nullptr;
     // rows of a slot: update, res, grad_out, grad_res
     const int k_res = POST ? 1 : 0, k_go = k_res + 1, k_gr = (POST ? 1 : 0) + (OUT ? 2 : 0);
     const int rows = k_gr + (has_gr ? 1 : 0);
+    float4* v_lo = reinterpret_cast<float4*>(smem);
+    float4 *v_hi = v_lo + half, *m_lo = v_lo + 2 * half, *m_hi = v_lo + 3 * half;
+    uint4* ring = smem + 4 * half + static_cast<size_t>(g.index) * plan.stages * rows * half;
+    // where groups hand their sums on: a place for every two of them, behind the rings
+    float4* handed = reinterpret_cast<float4*>(
+        smem + 4 * half + static_cast<size_t>(plan.groups) * plan.stages * rows * half);
 
-    if (threadIdx.x == 0) {
-        for (int s = 0; s < items.stages; ++s)
-            mbar_init(smem_addr(&full[s]), 1u);
+    if (g.leader()) {
+        for (int s = 0; s < plan.stages; ++s)
+            mbar_init(smem_addr(&full[g.index][s]), 1u);
         mbar_init_fence();
     }
     clear(ex[0]);
     clear(ex[1]);
-    row_barrier<CL>();
+    if (CL)
+        cluster_barrier();
+    else
+        __syncthreads();
     grid_dependency_sync();
 
     bool broken = false;
-    Cursor ahead{first, 0, 0, 0};
-    int put = 0;
-    auto issue = [&]() {  // thread 0
-        if (!ahead.valid(items))
+    const float inv_n = __fdiv_rn(1.0f, a.n);
+    const u64 rs2 = f2_splat(a.residual_scale);
+    Ahead ahead{};
+    auto issue = [&]() {  // the group's leader
+        if (ahead.item >= plan.count)
             return;
-        const uint32_t bar = smem_addr(&full[put]);
-        const uint32_t dst = smem_addr(ring + static_cast<size_t>(put) * rows * half);
+        const uint32_t bar = smem_addr(&full[g.index][ahead.put]);
+        const uint32_t dst = smem_addr(ring + static_cast<size_t>(ahead.put) * rows * half);
         const int64_t from = static_cast<int64_t>(ahead.row) * a.Dv + v0;
         auto bring = [&](int k, const void* p) {
             bulk_g2s(dst + k * half * 16, static_cast<const uint4*>(p) + from, bytes, bar);
@@ -459,219 +602,219 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
         }
         if (has_gr)
             bring(k_gr, a.grad_res);
-        put = put + 1 == items.stages ? 0 : put + 1;
-        ahead.advance(items, step);
+        ahead.advance(plan, step, g.index);
     };
-    Cursor at{first, 0, 0, 0};
-    if (at.valid(items)) {
-        at.open(items);
-        ahead.open(items);
-    }
-    // one slot less than the ring holds: a slot is refilled after the next row's barrier
-    if (threadIdx.x == 0)
-        for (int s = 0; s + 1 < items.stages; ++s)
+    if (g.leader()) {
+        ahead.start(plan, first, step, g.index);
+        for (int s = 0; s < plan.stages; ++s)
             issue();
+    }
 
     constexpr int kParts = (OUT ? 2 : 0) + (POST ? 1 : 0);
-    u64 v[kV][4], m[kV][4];
-    u64 sum_go[kV][4], sum_gh[kV][4], sum_du[kV][4];
-    auto restart = [&]() {
-#pragma unroll
-        for (int j = 0; j < kV; ++j)
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-                sum_go[j][i] = sum_gh[j][i] = sum_du[j][i] = 0ull;
-    };
-    restart();
-    const float inv_n = __fdiv_rn(1.0f, a.n);
-    uint32_t batch = 0xFFFFFFFFu;
+    u64 sums[V][kParts][4];  // go, go * hh (OUT), dh * uh (POST)
+    uint32_t batch = 0xFFFFFFFFu, phase = 0;
     int get = 0, par = 0;
-    uint32_t phase = 0;
-    float r = 0.0f, rp = 0.0f;
-    if (at.valid(items)) {
-        r = OUT ? a.rstd[at.row] : 0.0f;
-        rp = POST ? a.post_rstd[at.row] : 0.0f;
-    }
-    while (at.valid(items)) {
-        const uint32_t b = at.batch;
-        if (b != batch) {
-            batch = b;
-#pragma unroll
-            for (int j = 0; j < kV; ++j) {
-                const int c = j * blockDim.x + threadIdx.x;
-                const bool in = c < nv;
-                auto load = [&](const void* p, int64_t row) {
-                    return in && p ? ld_cached(static_cast<const uint4*>(p) + row + v0 + c)
-                                   : make_uint4(0u, 0u, 0u, 0u);
-                };
-                const u64 one = f2_splat(1.0f);
+    for (uint32_t item = first; item < plan.count; item += step) {
+        const Span span(plan, item);
+        if (span.batch != batch) {
+            __syncthreads();
+            batch = span.batch;
+            for (int c = threadIdx.x; c < nv; c += blockDim.x) {
+                u64 t[4];
                 if (POST) {
-                    const uint4 wp = load(a.post_weight, 0), g = load(a.gate, b * a.gate_bstride);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        u64 t = f2_splat(a.update_scale);
-                        if (a.post_weight)
-                            t = f2_mul(t, widen<T>(word(wp, i)));
-                        if (a.gate)
-                            t = f2_mul(t, widen<T>(word(g, i)));
-                        v[j][i] = t;
-                    }
+                    product<T>(t, a.update_scale, a.post_weight, a.gate, batch * a.gate_bstride,
+                               v0 + c);
+                    put_pairs(v_lo + c, v_hi + c, t);
                 }
                 if (OUT) {
-                    const uint4 w = load(a.weight, 0), sc = load(a.scale, b * a.mod_bstride);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const u64 t = a.weight ? widen<T>(word(w, i)) : one;
-                        m[j][i] = a.scale ? f2_mul(t, f2_add(one, widen<T>(word(sc, i)))) : t;
-                    }
+                    multiplier<T>(t, a.weight, a.scale, batch * a.mod_bstride, v0 + c);
+                    put_pairs(m_lo + c, m_hi + c, t);
                 }
             }
+            __syncthreads();
         }
-        if (!broken && !mbar_wait(smem_addr(&full[get]), phase, kWaitLimitNs)) {
-            broken = true;
-            atomicOr(&g_error, kErrCopyTimeout);
+#pragma unroll
+        for (int j = 0; j < V; ++j)
+#pragma unroll
+            for (int p = 0; p < kParts; ++p)
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    sums[j][p][i] = 0ull;
+        uint32_t row = span.begin + g.index;
+        float r = 0.0f, rp = 0.0f;
+        if (row < span.end) {
+            r = OUT ? a.rstd[row] : 0.0f;
+            rp = POST ? a.post_rstd[row] : 0.0f;
         }
-        const uint4* slot = ring + static_cast<size_t>(get) * rows * half;
-        const u64 r2 = f2_splat(r), rp2 = f2_splat(rp);
-        // ---- the row's sums: s0 = sum go m hh, s1 = sum q p, s2 = sum hh p with p = v uh, from
-        //      which both means follow (dh = q - r c hh)
-        float s[3] = {0.0f, 0.0f, 0.0f};
-        u64 t0 = 0ull, t1 = 0ull, t2 = 0ull;
+        while (row < span.end) {
+            if (!broken && !mbar_wait(smem_addr(&full[g.index][get]), phase, kWaitLimitNs)) {
+                broken = true;
+                atomicOr(&g_error, kErrCopyTimeout);
+            }
+            const uint4* slot = ring + static_cast<size_t>(get) * rows * half;
+            if (++get == plan.stages) {
+                get = 0;
+                phase ^= 1u;
+            }
+            const u64 r2 = f2_splat(r), rp2 = f2_splat(rp);
+            // ---- the row's sums: s0 = sum go m hh, s1 = sum q p, s2 = sum hh p with p = v uh, from
+            //      which both means follow (dh = q - r c hh)
+            u64 q[V][4];
+            uint4 x[V], u[V];
+            u64 t0 = 0ull, t1 = 0ull, t2 = 0ull;
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int c = j * blockDim.x + threadIdx.x;
-            if (c < nv) {
-                uint4 uu, hh, go, gr;
-                if (POST)
-                    uu = slot[c];
-                if (OUT) {
-                    hh = slot[k_res * half + c];
-                    go = slot[k_go * half + c];
-                }
-                if (POST && has_gr)
-                    gr = slot[k_gr * half + c];
+            for (int j = 0; j < V; ++j) {
+                const int c = g.at(j);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u64 q = POST && has_gr ? widen<T>(word(gr, i)) : 0ull;
-                    u64 h = 0ull;
+                for (int i = 0; i < 4; ++i)
+                    q[j][i] = 0ull;
+                x[j] = u[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (c < nv) {
+                    if (has_gr) {
+                        const uint4 w = slot[k_gr * half + c];
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            q[j][i] = widen<T>(word(w, i));
+                    }
                     if (OUT) {
-                        h = f2_mul(widen<T>(word(hh, i)), r2);
-                        const u64 d = f2_mul(widen<T>(word(go, i)), m[j][i]);
-                        t0 = f2_fma(d, h, t0);
-                        if (POST)
-                            q = f2_fma(d, r2, q);
-                    }
-                    if (POST) {
-                        const u64 p = f2_mul(f2_mul(widen<T>(word(uu, i)), rp2), v[j][i]);
-                        t1 = f2_fma(q, p, t1);
-                        if (OUT)
-                            t2 = f2_fma(h, p, t2);
-                    }
-                }
-            }
-        }
-        float lo, hi;
-        f2_unpack(t0, lo, hi);
-        s[0] = __fadd_rn(lo, hi);
-        f2_unpack(t1, lo, hi);
-        s[1] = __fadd_rn(lo, hi);
-        f2_unpack(t2, lo, hi);
-        s[2] = __fadd_rn(lo, hi);
-        row_reduce<3, CL>(s, ex[par], warp, lane, warps, rank);
-        par ^= 1;
-        // every thread is past the previous row: its slot takes the next copies
-        if (!CL && warps == 1)
-            __syncwarp();
-        if (threadIdx.x == 0)
-            issue();
-        // the next row's statistics, on their way during this row's second half
-        Cursor next = at;
-        next.advance(items, step);
-        float r_next = 0.0f, rp_next = 0.0f;
-        if (next.valid(items)) {
-            r_next = OUT ? a.rstd[next.row] : 0.0f;
-            rp_next = POST ? a.post_rstd[next.row] : 0.0f;
-        }
-        const float rc = __fmul_rn(r, __fmul_rn(s[0], inv_n));
-        const float c_upd = __fmul_rn(__fmaf_rn(-rc, s[2], s[1]), inv_n);
-        const u64 nrc2 = f2_splat(-rc), ncu2 = f2_splat(-c_upd);
-        const u64 rs2 = f2_splat(a.residual_scale);
-        // ---- the gradients of the row
-        const int64_t base = static_cast<int64_t>(at.row) * a.Dv + v0;
+                        const uint4 go = slot[k_go * half + c];
+                        x[j] = slot[k_res * half + c];
+                        u64 m[4];
+                        get_pairs(m_lo + c, m_hi + c, m);
 #pragma unroll
-        for (int j = 0; j < kV; ++j) {
-            const int c = j * blockDim.x + threadIdx.x;
-            if (c < nv) {
-                uint4 uu, hh, go, gr, ox, ou;
-                if (POST)
-                    uu = slot[c];
-                if (OUT) {
-                    hh = slot[k_res * half + c];
-                    go = slot[k_go * half + c];
-                }
-                if (has_gr)
-                    gr = slot[k_gr * half + c];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    u64 dh = has_gr ? widen<T>(word(gr, i)) : 0ull;
-                    if (OUT) {
-                        const u64 g = widen<T>(word(go, i));
-                        const u64 h = f2_mul(widen<T>(word(hh, i)), r2);
-                        dh = f2_fma(f2_mul(g, m[j][i]), r2, dh);
-                        dh = f2_fma(h, nrc2, dh);
-                        sum_go[j][i] = f2_add(sum_go[j][i], g);
-                        sum_gh[j][i] = f2_fma(g, h, sum_gh[j][i]);
-                    }
-                    word(ox, i) = narrow<T>(POST ? f2_mul(dh, rs2) : dh);
-                    if (POST) {
-                        const u64 uh = f2_mul(widen<T>(word(uu, i)), rp2);
-                        sum_du[j][i] = f2_fma(dh, uh, sum_du[j][i]);
-                        word(ou, i) = narrow<T>(
-                            f2_mul(f2_fma(uh, ncu2, f2_mul(dh, v[j][i])), rp2));
-                    }
-                }
-                if (a.grad_residual)
-                    st_stream(static_cast<uint4*>(a.grad_residual) + base + c, ox);
-                if (POST && a.grad_update)
-                    st_stream(static_cast<uint4*>(a.grad_update) + base + c, ou);
-            }
-        }
-        if (++get == items.stages) {
-            get = 0;
-            phase ^= 1u;
-        }
-        const uint32_t item = at.item;
-        at = next;
-        r = r_next;
-        rp = rp_next;
-        if (at.item != item) {  // the item's partial sums
-            if (a.sums) {
-                float4* to = reinterpret_cast<float4*>(a.partials) +
-                             static_cast<int64_t>(item) * kParts * a.Dv * 2;
-#pragma unroll
-                for (int j = 0; j < kV; ++j) {
-                    const int c = j * blockDim.x + threadIdx.x;
-                    if (c >= nv)
-                        continue;
-                    auto leave = [&](int part, const u64 (&t)[4]) {
-                        float4 f;
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            f2_unpack(t[2 * h], f.x, f.y);
-                            f2_unpack(t[2 * h + 1], f.z, f.w);
-                            to[(static_cast<int64_t>(part) * a.Dv + v0 + c) * 2 + h] = f;
+                        for (int i = 0; i < 4; ++i) {
+                            const u64 y = widen<T>(word(go, i));
+                            const u64 h = f2_mul(widen<T>(word(x[j], i)), r2);
+                            const u64 d = f2_mul(y, m[i]);
+                            t0 = f2_fma(d, h, t0);
+                            q[j][i] = f2_fma(d, r2, q[j][i]);
+                            sums[j][0][i] = f2_add(sums[j][0][i], y);
+                            sums[j][1][i] = f2_fma(y, h, sums[j][1][i]);
                         }
-                    };
-                    if (OUT) {
-                        leave(0, sum_go[j]);
-                        leave(1, sum_gh[j]);
                     }
-                    if (POST)
-                        leave(kParts - 1, sum_du[j]);
+                    if (POST) {
+                        u[j] = slot[c];
+                        u64 v[4];
+                        get_pairs(v_lo + c, v_hi + c, v);
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const u64 p = f2_mul(f2_mul(widen<T>(word(u[j], i)), rp2), v[i]);
+                            t1 = f2_fma(q[j][i], p, t1);
+                            if (OUT)
+                                t2 = f2_fma(f2_mul(widen<T>(word(x[j], i)), r2), p, t2);
+                        }
+                    }
                 }
             }
-            restart();
+            float s[3], hi;
+            f2_unpack(t0, s[0], hi);
+            s[0] = __fadd_rn(s[0], hi);
+            f2_unpack(t1, s[1], hi);
+            s[1] = __fadd_rn(s[1], hi);
+            f2_unpack(t2, s[2], hi);
+            s[2] = __fadd_rn(s[2], hi);
+            row_reduce<3, CL>(s, ex[par], g);
+            par ^= 1;
+            // the row is in registers everywhere: its slot takes the next copies
+            if (!CL && g.warps == 1)
+                __syncwarp();
+            if (g.leader())
+                issue();
+            const int64_t base = static_cast<int64_t>(row) * a.Dv + v0;
+            const float rc = __fmul_rn(r, __fmul_rn(s[0], inv_n));
+            const float c_upd = __fmul_rn(__fmaf_rn(-rc, s[2], s[1]), inv_n);
+            // the next row's statistics, on their way during this row's second half
+            row += plan.groups;
+            float r_next = 0.0f, rp_next = 0.0f;
+            if (row < span.end) {
+                r_next = OUT ? a.rstd[row] : 0.0f;
+                rp_next = POST ? a.post_rstd[row] : 0.0f;
+            }
+            // hh and uh once more from the stored values: held in fp32 they would not fit the registers
+            const u64 nrc2 = f2_splat(-rc), ncu2 = f2_splat(-c_upd);
+            // ---- the gradients of the row
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = g.at(j);
+                if (c < nv) {
+                    uint4 ox, ou;
+                    u64 v[4];
+                    if (POST)
+                        get_pairs(v_lo + c, v_hi + c, v);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const u64 dh =
+                            OUT ? f2_fma(f2_mul(widen<T>(word(x[j], i)), r2), nrc2, q[j][i])
+                                : q[j][i];
+                        word(ox, i) = narrow<T>(POST ? f2_mul(dh, rs2) : dh);
+                        if (POST) {
+                            const u64 uh = f2_mul(widen<T>(word(u[j], i)), rp2);
+                            sums[j][kParts - 1][i] = f2_fma(dh, uh, sums[j][kParts - 1][i]);
+                            word(ou, i) =
+                                narrow<T>(f2_mul(f2_fma(uh, ncu2, f2_mul(dh, v[i])), rp2));
+                        }
+                    }
+                    if (a.grad_residual)
+                        st_stream(static_cast<uint4*>(a.grad_residual) + base + c, ox);
+                    if (POST && a.grad_update)
+                        st_stream(static_cast<uint4*>(a.grad_update) + base + c, ou);
+                }
+            }
+            r = r_next;
+            rp = rp_next;
         }
+        if (!a.sums)
+            continue;
+        // ---- the item's sums: groups hand theirs on in pairs, the first one stores the total
+        for (int apart = 1; apart < plan.groups; apart *= 2) {
+            const bool gives = (g.index & (2 * apart - 1)) == apart;
+            const bool takes = (g.index & (2 * apart - 1)) == 0 && g.index + apart < plan.groups;
+            float4* place = handed + static_cast<size_t>((gives ? g.index : g.index + apart) >> 1) *
+                                         kParts * 2 * half;
+            if (gives) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int c = g.at(j);
+                    if (c < nv)
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p)
+                            put_pairs(place + 2 * p * half + c, place + (2 * p + 1) * half + c,
+                                      sums[j][p]);
+                }
+            }
+            __syncthreads();
+            if (takes) {
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    const int c = g.at(j);
+                    if (c < nv)
+#pragma unroll
+                        for (int p = 0; p < kParts; ++p) {
+                            u64 t[4];
+                            get_pairs(place + 2 * p * half + c, place + (2 * p + 1) * half + c, t);
+#pragma unroll
+                            for (int i = 0; i < 4; ++i)
+                                sums[j][p][i] = f2_add(sums[j][p][i], t[i]);
+                        }
+                }
+            }
+        }
+        if (g.index == 0) {
+            float4* to = reinterpret_cast<float4*>(a.partials) +
+                         static_cast<int64_t>(item) * kParts * a.Dv * 2;
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                const int c = g.at(j);
+                if (c < nv)
+#pragma unroll
+                    for (int p = 0; p < kParts; ++p) {
+                        float4* at = to + (static_cast<int64_t>(p) * a.Dv + v0 + c) * 2;
+                        put_pairs(at, at + 1, sums[j][p]);
+                    }
+            }
+        }
+        if (plan.groups > 1)
+            __syncthreads();  // the places are free for the next item
     }
     if (broken)
         drain_pause();
@@ -679,68 +822,78 @@ __global__ void __launch_bounds__(MAXT, min_blocks<MAXT>())
         cluster_barrier();
 }
 
-// The gradients of the row vectors from the items' partial sums: 32 columns a CTA, the items of a
-// batch dealt to its warps in turn and joined in the warps' order; batches in order.
-constexpr int kColWarps = 8;
+// The gradients of the row vectors from the items' partial sums: 32 columns a CTA, four a thread;
+// the items of a batch are dealt to 32 threads in turn and joined in their order; batches in order.
+constexpr int kColSlices = 32;
 
 template <typename T>
-__global__ void __launch_bounds__(32 * kColWarps)
-    sandwich_columns_kernel(const SandwichBwdArgs a, int64_t per_batch, int parts)
+__global__ void __launch_bounds__(8 * kColSlices)
+    sandwich_columns_kernel(const SandwichBwdArgs a, uint32_t per_batch, int parts)
 {
     grid_dependency_sync();
-    __shared__ float part[3][kColWarps][32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    __shared__ float4 part[3][kColSlices][8];
+    const int quad = threadIdx.x & 7, slice = threadIdx.x >> 3;
     const int64_t D = static_cast<int64_t>(a.Dv) * 8;
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;
-    const bool in = d < D;
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + quad;  // quad of columns
+    const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;  // the column it ends
     const bool out_on = a.grad_out != nullptr, post_on = a.update != nullptr;
+    const bool ends = threadIdx.x < 32 && d < D;
     auto value = [&](const void* p, int64_t at, float none) {
-        return p && in ? static_cast<float>(static_cast<const T*>(p)[at + d]) : none;
+        return p && ends ? static_cast<float>(static_cast<const T*>(p)[at + d]) : none;
     };
     const float w = value(a.weight, 0, 1.0f);
     const float wp = __fmul_rn(value(a.post_weight, 0, 1.0f), a.update_scale);
     float g_w = 0.0f, g_wp = 0.0f, g_scale = 0.0f, g_shift = 0.0f, g_gate = 0.0f;
     for (int64_t b = 0; b < a.B; ++b) {
-        float s[3] = {0.0f, 0.0f, 0.0f};
-        if (in) {
-            const float* from = a.partials + b * per_batch * parts * D + d;
-#pragma unroll 4
-            for (int64_t k = warp; k < per_batch; k += kColWarps)
+        float4 s[3];
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            s[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        if (q * 4 < D) {
+            const float4* from = reinterpret_cast<const float4*>(a.partials) +
+                                 b * per_batch * parts * (D / 4) + q;
+#pragma unroll 5
+            for (uint32_t k = slice; k < per_batch; k += kColSlices)
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
-                    if (p < parts)
-                        s[p] = __fadd_rn(s[p], __ldcs(from + (k * parts + p) * D));
+                    if (p < parts) {
+                        const float4 f = __ldcs(from + (static_cast<int64_t>(k) * parts + p) * (D / 4));
+                        s[p] = make_float4(__fadd_rn(s[p].x, f.x), __fadd_rn(s[p].y, f.y),
+                                           __fadd_rn(s[p].z, f.z), __fadd_rn(s[p].w, f.w));
+                    }
         }
 #pragma unroll
         for (int p = 0; p < 3; ++p)
-            part[p][warp][lane] = s[p];
+            part[p][slice][quad] = s[p];
         __syncthreads();
-        if (warp == 0 && in) {
+        if (ends) {
+            float t[3];
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
-                s[p] = part[p][0][lane];
+                const float* at = reinterpret_cast<const float*>(&part[p][0][0]) + threadIdx.x;
+                t[p] = at[0];
 #pragma unroll
-                for (int k = 1; k < kColWarps; ++k)
-                    s[p] = __fadd_rn(s[p], part[p][k][lane]);
+                for (int k = 1; k < kColSlices; ++k)
+                    t[p] = __fadd_rn(t[p], at[k * 32]);
             }
             if (out_on) {
                 const float one = __fadd_rn(1.0f, value(a.scale, b * a.mod_bstride * 8, 0.0f));
-                g_w = __fmaf_rn(s[1], one, g_w);
-                const float gs = __fmul_rn(s[1], w);
+                g_w = __fmaf_rn(t[1], one, g_w);
+                const float gs = __fmul_rn(t[1], w);
                 if (a.mod_bstride != 0) {
                     if (a.grad_shift)
-                        a.grad_shift[b * D + d] = s[0];
+                        a.grad_shift[b * D + d] = t[0];
                     if (a.grad_scale)
                         a.grad_scale[b * D + d] = gs;
                 } else {
-                    g_shift = __fadd_rn(g_shift, s[0]);
+                    g_shift = __fadd_rn(g_shift, t[0]);
                     g_scale = __fadd_rn(g_scale, gs);
                 }
             }
             if (post_on) {
-                const float du = out_on ? s[2] : s[0];
-                const float g = value(a.gate, b * a.gate_bstride * 8, 1.0f);
-                g_wp = __fmaf_rn(du, __fmul_rn(g, a.update_scale), g_wp);
+                const float du = out_on ? t[2] : t[0];
+                const float gt = value(a.gate, b * a.gate_bstride * 8, 1.0f);
+                g_wp = __fmaf_rn(du, __fmul_rn(gt, a.update_scale), g_wp);
                 const float gg = __fmul_rn(du, wp);
                 if (a.gate_bstride != 0) {
                     if (a.grad_gate)
@@ -752,7 +905,7 @@ __global__ void __launch_bounds__(32 * kColWarps)
         }
         __syncthreads();
     }
-    if (warp != 0 || !in)
+    if (!ends)
         return;
     if (a.grad_weight)
         a.grad_weight[d] = g_w;
@@ -772,53 +925,66 @@ __global__ void __launch_bounds__(32 * kColWarps)
 // launches
 // ---------------------------------------------------------------------------
 
+// How a CTA's warps share rows of Dv vectors, V a thread.
 struct Shape {
     bool cluster;
-    int threads;
-    int row_bytes;  // of one CTA's part of a row
+    int nv;      // vectors of a CTA's part of a row
+    int warps;   // of a group
+    int groups;
 };
 
-Shape shape_of(int Dv)
+Shape shape_of(int Dv, int V)
 {
     Shape s;
     s.cluster = Dv > kMaxDvPerCta;
-    const int nv = s.cluster ? (Dv + 1) / 2 : Dv;
-    s.threads = (nv + 32 * kV - 1) / (32 * kV) * 32;
-    s.row_bytes = nv * 16;
+    s.nv = s.cluster ? (Dv + 1) / 2 : Dv;
+    s.warps = (s.nv + 32 * V - 1) / (32 * V);
+    s.groups = s.cluster ? 1 : kMaxWarps / s.warps;
     return s;
 }
 
-// CTAs that share an SM: as many as 512 threads make up.
-int ctas_per_sm(const Shape& s)
+// Rows of one 16-byte vector a lane or two need no more registers than that.
+int forward_vectors(int Dv) { return Dv <= 32 ? 1 : (Dv <= 64 ? 2 : 4); }
+int backward_vectors(int Dv) { return Dv <= 32 ? 1 : 2; }
+
+Plan plan_of(int64_t B, int64_t S, int64_t chunk, const Shape& s)
 {
-    const int n = kMaxThreads / s.threads;
-    return n > 16 ? 16 : n;
+    Plan p;
+    const int64_t per_batch = (S + chunk - 1) / chunk;
+    p.per_batch = FastDiv::make(static_cast<uint32_t>(per_batch));
+    p.chunk = static_cast<uint32_t>(chunk);
+    p.count = static_cast<uint32_t>(B * per_batch);
+    p.S = static_cast<uint32_t>(S);
+    p.groups = chunk < s.groups ? static_cast<int>(chunk) : s.groups;
+    p.warps = s.warps;
+    p.stages = 1;
+    return p;
 }
 
-int ring_stages(const Shape& s, int rows_per_slot)
-{
-    const int budget = kSmemPerSm / ctas_per_sm(s) - 2048;
-    const int n = budget / (s.row_bytes * rows_per_slot);
-    return n > kMaxStages ? kMaxStages : (n < 2 ? 2 : n);
-}
-
+// `fixed` bytes of shared memory beside the rings, slots of `slot` bytes.
 template <typename K, typename A>
-cudaError_t launch_rows(K kern, const A& a, const Items& items, const Shape& s, int rows_per_slot,
+cudaError_t launch_rows(K kern, const A& a, Plan p, const Shape& s, int fixed, int slot,
                         PerDeviceInt& ready, const DeviceInfo& dev, cudaStream_t stream)
 {
     int v = 0;
     cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
         n = 1;
-        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemPerSm);
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, kSmemBytes);
     });
     if (e != cudaSuccess)
         return e;
-    const int64_t cap = static_cast<int64_t>(dev.sms) * ctas_per_sm(s) / (s.cluster ? 2 : 1);
-    const int64_t groups = static_cast<int64_t>(items.count) < cap ? items.count : cap;
+    // rings no longer than the rows of a group in an item need
+    const int rows = static_cast<int>((p.chunk + p.groups - 1) / p.groups);
+    p.stages = (kSmemBytes - fixed) / (slot * p.groups);
+    p.stages = p.stages > kMaxStages ? kMaxStages : p.stages;
+    if (p.count <= static_cast<uint32_t>(dev.sms) && rows < p.stages)
+        p.stages = rows;
+    const int64_t cap = s.cluster ? dev.sms / 2 : dev.sms;
+    const int64_t clusters = static_cast<int64_t>(p.count) < cap ? p.count : cap;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(static_cast<unsigned>(groups * (s.cluster ? 2 : 1)));
-    cfg.blockDim = dim3(static_cast<unsigned>(s.threads));
-    cfg.dynamicSmemBytes = static_cast<size_t>(items.stages) * rows_per_slot * s.row_bytes;
+    cfg.gridDim = dim3(static_cast<unsigned>(clusters * (s.cluster ? 2 : 1)));
+    cfg.blockDim = dim3(static_cast<unsigned>(32 * p.warps * p.groups));
+    cfg.dynamicSmemBytes = static_cast<size_t>(fixed) + static_cast<size_t>(p.stages) * p.groups * slot;
     cfg.stream = stream;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -829,100 +995,93 @@ cudaError_t launch_rows(K kern, const A& a, const Items& items, const Shape& s, 
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = s.cluster ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, a, items);
+    return cudaLaunchKernelEx(&cfg, kern, a, p);
 }
 
-Items items_of(int64_t B, int64_t S, int64_t chunk)
-{
-    Items it;
-    const int64_t per_batch = (S + chunk - 1) / chunk;
-    it.per_batch = FastDiv::make(static_cast<uint32_t>(per_batch));
-    it.chunk = static_cast<uint32_t>(chunk);
-    it.count = static_cast<uint32_t>(B * per_batch);
-    it.S = static_cast<uint32_t>(S);
-    it.stages = 2;
-    return it;
-}
-
-// Rows of a batch in items that spread over the GPU.
-Items spread(int64_t B, int64_t S, int64_t cap)
-{
-    int64_t per = cap / B;
-    per = per < 1 ? 1 : (per > S ? S : per);
-    return items_of(B, S, (S + per - 1) / per);
-}
-
-template <typename T, int MAXT, bool CL>
+template <typename T, int V, bool CL>
 cudaError_t launch_fwd(const SandwichArgs& a, const Shape& s, const DeviceInfo& dev,
                        cudaStream_t stream)
 {
     static PerDeviceInt ready;
-    Items it = spread(a.rows / a.S, a.S,
-                      static_cast<int64_t>(dev.sms) * ctas_per_sm(s) / (CL ? 2 : 1));
-    it.stages = ring_stages(s, 2);
-    return launch_rows(sandwich_kernel<T, MAXT, CL>, a, it, s, 2, ready, dev, stream);
+    // items that spread over the GPU
+    const int64_t B = a.rows / a.S;
+    int64_t per = (CL ? dev.sms / 2 : dev.sms) / B;
+    per = per < 1 ? 1 : (per > a.S ? a.S : per);
+    const Plan p = plan_of(B, a.S, (a.S + per - 1) / per, s);
+    return launch_rows(sandwich_kernel<T, V, CL>, a, p, s, s.nv * kFwdVectorBytes, s.nv * 32, ready,
+                       dev, stream);
 }
 
 template <typename T>
 cudaError_t launch_fwd_t(const SandwichArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
-    const Shape s = shape_of(a.Dv);
+    const Shape s = shape_of(a.Dv, forward_vectors(a.Dv));
     if (s.cluster)
-        return launch_fwd<T, 512, true>(a, s, dev, stream);
-    if (s.threads > 256)
-        return launch_fwd<T, 512, false>(a, s, dev, stream);
-    return launch_fwd<T, 256, false>(a, s, dev, stream);
+        return launch_fwd<T, 4, true>(a, s, dev, stream);
+    switch (forward_vectors(a.Dv)) {
+    case 1:
+        return launch_fwd<T, 1, false>(a, s, dev, stream);
+    case 2:
+        return launch_fwd<T, 2, false>(a, s, dev, stream);
+    default:
+        return launch_fwd<T, 4, false>(a, s, dev, stream);
+    }
 }
 
 // Items of the backward pass: their rows depend on S and D alone, so that the token sums do not
-// depend on the batch.  152 SMs.
-Items backward_items(int64_t B, int64_t S, int Dv)
+// depend on the batch.  At least a row for each group; 152 SMs.
+Plan backward_plan(int64_t B, int64_t S, int Dv)
 {
-    const Shape s = shape_of(Dv);
-    const int64_t spread_over = 152 * ctas_per_sm(s) / (s.cluster ? 2 : 1);
-    const int64_t chunk = (S + spread_over - 1) / spread_over;
-    return items_of(B, S, chunk > 64 ? 64 : chunk);
+    const Shape s = shape_of(Dv, backward_vectors(Dv));
+    const int64_t over = s.cluster ? 76 : 152;
+    int64_t chunk = (S + over - 1) / over;
+    chunk = chunk < s.groups ? s.groups : (chunk > 64 ? 64 : chunk);
+    return plan_of(B, S, chunk < S ? chunk : S, s);
 }
 
-template <typename T, int MAXT, bool CL, bool POST, bool OUT>
-cudaError_t launch_bwd(const SandwichBwdArgs& a, const Shape& s, Items it, const DeviceInfo& dev,
-                       cudaStream_t stream)
+template <typename T, int V, bool CL, bool POST, bool OUT>
+cudaError_t launch_bwd(const SandwichBwdArgs& a, const Shape& s, const Plan& p,
+                       const DeviceInfo& dev, cudaStream_t stream)
 {
     static PerDeviceInt ready;
     const int rows = (POST ? 1 : 0) + (OUT ? 2 : 0) + (a.grad_res ? 1 : 0);
-    it.stages = ring_stages(s, rows);
-    return launch_rows(sandwich_bwd_kernel<T, MAXT, CL, POST, OUT>, a, it, s, rows, ready, dev,
+    const int parts = (OUT ? 2 : 0) + (POST ? 1 : 0);
+    const int handed = a.sums ? p.groups / 2 * parts * 32 : 0;
+    // an odd number of groups: the last one's place too
+    const int odd = a.sums && p.groups > 1 && p.groups % 2 ? parts * 32 : 0;
+    return launch_rows(sandwich_bwd_kernel<T, V, CL, POST, OUT>, a, p, s,
+                       s.nv * (kBwdVectorBytes + handed + odd), s.nv * 16 * rows, ready, dev,
                        stream);
 }
 
 template <typename T, bool POST, bool OUT>
-cudaError_t launch_bwd_t(const SandwichBwdArgs& a, const Items& it, const DeviceInfo& dev,
+cudaError_t launch_bwd_t(const SandwichBwdArgs& a, const Plan& p, const DeviceInfo& dev,
                          cudaStream_t stream)
 {
-    const Shape s = shape_of(a.Dv);
+    const Shape s = shape_of(a.Dv, backward_vectors(a.Dv));
     if (s.cluster)
-        return launch_bwd<T, 512, true, POST, OUT>(a, s, it, dev, stream);
-    if (s.threads > 256)
-        return launch_bwd<T, 512, false, POST, OUT>(a, s, it, dev, stream);
-    return launch_bwd<T, 256, false, POST, OUT>(a, s, it, dev, stream);
+        return launch_bwd<T, 2, true, POST, OUT>(a, s, p, dev, stream);
+    if (backward_vectors(a.Dv) == 1)
+        return launch_bwd<T, 1, false, POST, OUT>(a, s, p, dev, stream);
+    return launch_bwd<T, 2, false, POST, OUT>(a, s, p, dev, stream);
 }
 
 template <typename T>
-cudaError_t launch_columns(const SandwichBwdArgs& a, const Items& it, cudaStream_t stream)
+cudaError_t launch_columns(const SandwichBwdArgs& a, const Plan& p, cudaStream_t stream)
 {
     const int parts = (a.grad_out ? 2 : 0) + (a.update ? 1 : 0);
     const int grid = (a.Dv * 8 + 31) / 32;
-    return launch_dependent(sandwich_columns_kernel<T>, grid, 32 * kColWarps, 0, stream, a,
-                            static_cast<int64_t>(it.per_batch.d), parts);
+    return launch_dependent(sandwich_columns_kernel<T>, grid, 8 * kColSlices, 0, stream, a,
+                            p.per_batch.d, parts);
 }
 
 template <typename T>
-cudaError_t launch_sandwich_t(const SandwichBwdArgs& a, const Items& it, const DeviceInfo& dev,
+cudaError_t launch_sandwich_t(const SandwichBwdArgs& a, const Plan& p, const DeviceInfo& dev,
                               cudaStream_t stream)
 {
-    const cudaError_t e = a.grad_out ? launch_bwd_t<T, true, true>(a, it, dev, stream)
-                                     : launch_bwd_t<T, true, false>(a, it, dev, stream);
-    return e == cudaSuccess && a.sums ? launch_columns<T>(a, it, stream) : e;
+    const cudaError_t e = a.grad_out ? launch_bwd_t<T, true, true>(a, p, dev, stream)
+                                     : launch_bwd_t<T, true, false>(a, p, dev, stream);
+    return e == cudaSuccess && a.sums ? launch_columns<T>(a, p, stream) : e;
 }
 
 }  // namespace
@@ -935,20 +1094,20 @@ cudaError_t launch_sandwich(const SandwichArgs& a, const DeviceInfo& dev, cudaSt
 
 size_t sandwich_backward_workspace_bytes(int64_t B, int64_t S, int64_t D, int parts)
 {
-    return static_cast<size_t>(backward_items(B, S, static_cast<int>(D / 8)).count) * parts * D *
+    return static_cast<size_t>(backward_plan(B, S, static_cast<int>(D / 8)).count) * parts * D *
            sizeof(float);
 }
 
 cudaError_t launch_sandwich_backward(const SandwichBwdArgs& a, const DeviceInfo& dev,
                                      cudaStream_t stream)
 {
-    const Items it = backward_items(a.B, a.S, a.Dv);
+    const Plan p = backward_plan(a.B, a.S, a.Dv);
     if (a.update)
-        return a.f16 ? launch_sandwich_t<__half>(a, it, dev, stream)
-                     : launch_sandwich_t<__nv_bfloat16>(a, it, dev, stream);
+        return a.f16 ? launch_sandwich_t<__half>(a, p, dev, stream)
+                     : launch_sandwich_t<__nv_bfloat16>(a, p, dev, stream);
     // the norm alone: rmsnorm_modulate is bf16
-    const cudaError_t e = launch_bwd_t<__nv_bfloat16, false, true>(a, it, dev, stream);
-    return e == cudaSuccess && a.sums ? launch_columns<__nv_bfloat16>(a, it, stream) : e;
+    const cudaError_t e = launch_bwd_t<__nv_bfloat16, false, true>(a, p, dev, stream);
+    return e == cudaSuccess && a.sums ? launch_columns<__nv_bfloat16>(a, p, stream) : e;
 }
 
 cudaError_t sandwich_error(unsigned* bits, bool clear)
