@@ -163,74 +163,63 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
     }
 }
 
-template <typename T, int V>
-__device__ __forceinline__ float sum_squares(const uint4 (&x)[V])
+template <int V>
+__device__ __forceinline__ float sum_squares(const u64 (&x)[V][4])
 {
     u64 s[2] = {0ull, 0ull};
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const u64 p = widen<T>(word(x[j], i));
-            s[i & 1] = f2_fma(p, p, s[i & 1]);
-        }
+        for (int i = 0; i < 4; ++i)
+            s[i & 1] = f2_fma(x[j][i], x[j][i], s[i & 1]);
     float lo, hi;
     f2_unpack(f2_add(s[0], s[1]), lo, hi);
     return __fadd_rn(lo, hi);
 }
 
-// Vectors handed to a function that is not inlined: by value, so that the caller's stay in registers
-// (a reference would keep them in local memory for every row).
-template <int V>
-struct Vectors {
-    uint4 v[V];
-};
-
 // 1 / sqrt of a row whose fp32 sum of squares left fp32's comfortable range although its values are
-// finite: squares of the values over the power of two of the largest, joined in fp64.
-template <typename T, int V, bool CL>
-__device__ __noinline__ float rstd_scaled(const Vectors<V> x, float sum, float n, float eps,
-                                          Exchange<1>& e0, Exchange<1>& e1, const Group g)
+// finite: squares of the values over the power of two of the largest, joined in fp64.  The thread's
+// vectors are read again from `from`, so that the callers' registers need not outlive the sum.
+template <typename T, bool CL>
+__device__ __noinline__ float rstd_scaled(const uint4* from, int nv, int vectors, float sum, float n,
+                                          float eps, Exchange<1>* slow, const Group g)
 {
     float top[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 p = widen2<T>(word(x.v[j], i));
-            top[0] = fmaxf(top[0], fmaxf(fabsf(p.x), fabsf(p.y)));
+    for (int j = 0; j < vectors; ++j)
+        if (g.at(j) < nv) {
+            const uint4 x = from[g.at(j)];
+            for (int i = 0; i < 4; ++i) {
+                const float2 p = widen2<T>(word(x, i));
+                top[0] = fmaxf(top[0], fmaxf(fabsf(p.x), fabsf(p.y)));
+            }
         }
-    row_reduce<1, CL, true>(top, e0, g);
+    row_reduce<1, CL, true>(top, slow[0], g);
     // Inf, or nothing but zeros: the sum says it all.  (A NaN never gets here.)
     if (!(top[0] <= 3.4028235e38f) || top[0] == 0.0f)
         return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps)));
     const int e = ilogbf(top[0]);
     float s[1] = {0.0f};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 p = widen2<T>(word(x.v[j], i));
-            const float a = scalbnf(p.x, -e), b = scalbnf(p.y, -e);
-            s[0] = __fadd_rn(s[0], __fadd_rn(__fmul_rn(a, a), __fmul_rn(b, b)));
+    for (int j = 0; j < vectors; ++j)
+        if (g.at(j) < nv) {
+            const uint4 x = from[g.at(j)];
+            for (int i = 0; i < 4; ++i) {
+                const float2 p = widen2<T>(word(x, i));
+                const float a = scalbnf(p.x, -e), b = scalbnf(p.y, -e);
+                s[0] = __fadd_rn(s[0], __fadd_rn(__fmul_rn(a, a), __fmul_rn(b, b)));
+            }
         }
-    row_reduce<1, CL>(s, e1, g);
+    row_reduce<1, CL>(s, slow[1], g);
     const double ms = scalbn(static_cast<double>(s[0]) / static_cast<double>(n), 2 * e);
     return static_cast<float>(1.0 / sqrt(ms + static_cast<double>(eps)));
 }
 
-template <typename T, int V, bool CL>
-__device__ __forceinline__ float rstd_of(const uint4 (&x)[V], float sum, float n, float inv_n,
-                                         float eps, Exchange<1> (&slow)[2], const Group& g)
+template <typename T, bool CL>
+__device__ __forceinline__ float rstd_of(const uint4* from, int nv, int vectors, float sum, float n,
+                                         float inv_n, float eps, Exchange<1>* slow, const Group& g)
 {
     // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
-    if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f)) {
-        Vectors<V> copy;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-            copy.v[j] = x[j];
-        return rstd_scaled<T, V, CL>(copy, sum, n, eps, slow[0], slow[1], g);
-    }
+    if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f))
+        return rstd_scaled<T, CL>(from, nv, vectors, sum, n, eps, slow, g);
     // the approximate root and one Newton step: within 2 * 2^-24 of the root, in a tenth of the
     // instructions of a division and a square root, which every warp of a row repeats
     const float ms = __fmaf_rn(sum, inv_n, eps);
@@ -459,24 +448,30 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 get = 0;
                 phase ^= 1u;
             }
-            uint4 u[V], x[V];
+            u64 f[V][4];  // update, then res, in fp32: widened once each
+            uint4 x[V];
 #pragma unroll
             for (int j = 0; j < V; ++j) {
                 const int c = g.at(j);
-                u[j] = x[j] = make_uint4(0u, 0u, 0u, 0u);
+                uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                x[j] = u;
                 if (c < nv) {
-                    u[j] = slot[c];
+                    u = slot[c];
                     x[j] = slot[half + c];
                 }
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    f[j][i] = widen<T>(word(u, i));
             }
-            float s[1] = {sum_squares<T, V>(u)};
+            float s[1] = {sum_squares<V>(f)};
             row_reduce<1, CL>(s, ex[0], g);
+            const float rp =
+                rstd_of<T, CL>(slot, nv, V, s[0], a.n, inv_n, a.post_eps, slow, g);
             // a barrier has passed (or a warp's exchange, for a group of one): the slot is read
             if (!CL && g.warps == 1)
                 __syncwarp();
             if (g.leader())
                 issue();
-            const float rp = rstd_of<T, V, CL>(u, s[0], a.n, inv_n, a.post_eps, slow, g);
             const u64 rp2 = f2_splat(rp);
             const int64_t base = static_cast<int64_t>(row) * a.Dv;
 #pragma unroll
@@ -486,19 +481,22 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                     u64 t[4];
                     get_pairs(v_lo + c, v_hi + c, t);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i)
-                        word(x[j], i) = narrow<T>(
-                            f2_fma(widen<T>(word(x[j], i)), rs2,
-                                   f2_mul(f2_mul(widen<T>(word(u[j], i)), rp2), t[i])));
+                    for (int i = 0; i < 4; ++i) {
+                        const uint32_t w = narrow<T>(f2_fma(widen<T>(word(x[j], i)), rs2,
+                                                            f2_mul(f2_mul(f[j][i], rp2), t[i])));
+                        word(x[j], i) = w;
+                        f[j][i] = widen<T>(w);
+                    }
                     st_stream(res_out + base + c, x[j]);
                 }
             }
             if (g.leader() && g.rank == 0 && a.post_rstd_out)
                 a.post_rstd_out[row] = rp;
             if (a.out) {
-                s[0] = sum_squares<T, V>(x);
+                s[0] = sum_squares<V>(f);
                 row_reduce<1, CL>(s, ex[1], g);
-                const float r = rstd_of<T, V, CL>(x, s[0], a.n, inv_n, a.eps, slow, g);
+                const float r =
+                    rstd_of<T, CL>(res_out + base, nv, V, s[0], a.n, inv_n, a.eps, slow, g);
                 const u64 r2 = f2_splat(r);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -510,8 +508,8 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                         uint4 o;
 #pragma unroll
                         for (int i = 0; i < 4; ++i)
-                            word(o, i) = narrow<T>(f2_fma(f2_mul(widen<T>(word(x[j], i)), r2),
-                                                          t[i], widen<T>(word(sf, i))));
+                            word(o, i) = narrow<T>(f2_fma(f2_mul(f[j][i], r2), t[i],
+                                                          widen<T>(word(sf, i))));
                         st_stream(out + base + c, o);
                     }
                 }
@@ -1007,7 +1005,10 @@ cudaError_t launch_fwd(const SandwichArgs& a, const Shape& s, const DeviceInfo& 
     const int64_t B = a.rows / a.S;
     int64_t per = (CL ? dev.sms / 2 : dev.sms) / B;
     per = per < 1 ? 1 : (per > a.S ? a.S : per);
-    const Plan p = plan_of(B, a.S, (a.S + per - 1) / per, s);
+    Plan p = plan_of(B, a.S, (a.S + per - 1) / per, s);
+    // groups without a row help to stage the row vectors: a lone group's threads would take several
+    // rounds of loads (3 us of a call of four rows of 4096 values)
+    p.groups = s.groups;
     return launch_rows(sandwich_kernel<T, V, CL>, a, p, s, s.nv * kFwdVectorBytes, s.nv * 32, ready,
                        dev, stream);
 }
