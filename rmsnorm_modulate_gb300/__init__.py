@@ -541,6 +541,9 @@ def conv_bias_epilogue(x, bias, h=None, out=None, stream=None):
 
 _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
+# Checks of the calls below.  They take most of a small call's time, so each reads an attribute once
+# and leaves the wording of an error to the end.
+
 
 def _half(t, name):
     if not isinstance(t, torch.Tensor):
@@ -550,36 +553,67 @@ def _half(t, name):
     return _dense(t, name, t.dtype)
 
 
-def _same_device(device, **tensors):
-    for name, t in tensors.items():
-        if t is not None and t.device != device:
-            raise ValueError(f"{name} must be on {device}")
+def _input(t, name, dtype, device, shape):
+    """A required contiguous tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.shape != shape:
+        raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(shape)}")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _like(t, x, name):
-    """An input of x's shape and type, or None."""
-    if t is not None:
-        _dense(t, name, x.dtype)
-        if t.shape != x.shape:
-            raise ValueError(f"{name} shape {tuple(t.shape)} != {tuple(x.shape)}")
-    return t
+def _vector(t, name, dtype, device, D):
+    """A nullable vector of D elements."""
+    if t is None:
+        return
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype is not dtype:
+        raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+    if t.numel() != D:
+        raise ValueError(f"{name} must have {D} elements")
+    if t.device != device:
+        raise ValueError(f"{name} must be on {device}")
+    if not t.is_contiguous():
+        raise ValueError(f"{name} must be contiguous")
 
 
-def _vector(t, D, name, dtype):
-    if t is not None:
-        _dense(t, name, dtype)
-        if t.numel() != D:
-            raise ValueError(f"{name} must have D elements")
-    return t
+def _rows(t, name, dtype, device, B, D):
+    """Batch stride of a nullable modulation row (0 = shared by every batch)."""
+    if t is None:
+        return 0
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.device == device:
+        shape = t.shape
+        if len(shape) == 3 and shape[0] == B and shape[1] == 1 and shape[2] == D:
+            stride = t.stride()
+            if stride[2] == 1:
+                return stride[0] if B > 1 else 0
+    elif isinstance(t, torch.Tensor) and t.dtype is dtype:
+        raise ValueError(f"{name} must be on {device}")
+    return _mod_rows(t, B, D, name, dtype)
 
 
-def _modulation(scale, shift, B, D, dtype):
+def _modulation(scale, shift, dtype, device, B, D):
     """Batch stride of the nullable scale and shift rows."""
-    strides = [_mod_rows(t, B, D, n, dtype) for t, n in ((scale, "scale"), (shift, "shift"))
-               if t is not None]
-    if len(set(strides)) > 1:
-        raise ValueError("scale and shift must share one batch stride")
-    return strides[0] if strides else 0
+    bs = _rows(scale, "scale", dtype, device, B, D)
+    if shift is not None:
+        if scale is None:
+            return _rows(shift, "shift", dtype, device, B, D)
+        if _rows(shift, "shift", dtype, device, B, D) != bs:
+            raise ValueError("scale and shift must share one batch stride")
+    return bs
+
+
+def _stats(t, name, device, n):
+    """Nullable fp32 statistics of n rows."""
+    if t is not None and (t.dtype is not torch.float32 or t.numel() != n or t.device != device or
+                          not t.is_contiguous()):
+        raise ValueError(f"{name} must be a contiguous float32 tensor of {n} elements on {device}")
 
 
 def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, weight=None,
@@ -597,29 +631,29 @@ def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, wei
     A missing post_weight, gate, weight or scale is a factor of 1, a missing shift 0; post_eps
     defaults to eps.  post_rstd_out / rstd_out: fp32 [B * S] for the backward pass."""
     _half(residual, "residual")
-    dt = residual.dtype
-    B, S, D = _bsd(residual, "residual", dt)
-    if update is None:
-        raise TypeError("update must be a torch.Tensor")
-    _like(update, residual, "update")
-    _vector(post_weight, D, "post_weight", dt)
-    gs = 0 if gate is None else _mod_rows(gate, B, D, "gate", dt)
+    dt, device, shape = residual.dtype, residual.device, residual.shape
+    B, S, D = shape if len(shape) == 3 else _bsd(residual, "residual", dt)
+    _input(update, "update", dt, device, shape)
+    _vector(post_weight, "post_weight", dt, device, D)
+    gs = _rows(gate, "gate", dt, device, B, D)
     if not need_out and (out is not None or rstd_out is not None):
         raise ValueError("out and rstd_out need need_out")
-    _vector(weight, D, "weight", dt)
-    bs = _modulation(scale, shift, B, D, dt)
-    res_out = _out_like(res_out, residual, "res_out")
-    out = _out_like(out, residual) if need_out else None
-    _f32_out(post_rstd_out, B * S, "post_rstd_out", residual.device)
-    _f32_out(rstd_out, B * S, "rstd_out", residual.device)
-    _same_device(residual.device, update=update, post_weight=post_weight, gate=gate,
-                 weight=weight, scale=scale, shift=shift, res_out=res_out, out=out,
-                 post_rstd_out=post_rstd_out, rstd_out=rstd_out)
-    _call_on(residual.device, "sandwich_rmsnorm_modulate", _at(residual), _at(update),
-             _at(post_weight), _at(gate), gs, _at(weight), _at(scale), _at(shift), bs,
-             _at(res_out), _at(out), B, S, D, residual_scale, update_scale,
-             eps if post_eps is None else post_eps, eps, _at(post_rstd_out), _at(rstd_out),
-             _DTYPES[dt], stream=stream)
+    _vector(weight, "weight", dt, device, D)
+    bs = _modulation(scale, shift, dt, device, B, D)
+    if res_out is None:
+        res_out = torch.empty_like(residual)
+    else:
+        _input(res_out, "res_out", dt, device, shape)
+    if out is not None:
+        _input(out, "out", dt, device, shape)
+    elif need_out:
+        out = torch.empty_like(residual)
+    _stats(post_rstd_out, "post_rstd_out", device, B * S)
+    _stats(rstd_out, "rstd_out", device, B * S)
+    _call_on(device, "sandwich_rmsnorm_modulate", _at(residual), _at(update), _at(post_weight),
+             _at(gate), gs, _at(weight), _at(scale), _at(shift), bs, _at(res_out), _at(out), B, S, D,
+             residual_scale, update_scale, eps if post_eps is None else post_eps, eps,
+             _at(post_rstd_out), _at(rstd_out), _DTYPES[dt], stream=stream)
     return res_out, out
 
 
@@ -647,10 +681,10 @@ def _vector_grad(wanted, D, device):
     return torch.empty(D, dtype=torch.float32, device=device) if wanted else None
 
 
-def _need_stats(t, n, name, device):
+def _need_stats(t, name, device, n):
     if t is None:
         raise ValueError(f"{name} (the forward's statistics) is required")
-    _f32_out(t, n, name, device)
+    _stats(t, name, device, n)
 
 
 @functools.lru_cache(maxsize=256)
@@ -683,27 +717,26 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
     need_mod: the row vectors, whose token sums (in an order that S and D fix) take a workspace,
     allocated here unless one is passed.  A gradient of shift comes with that of scale."""
     _half(update, "update")
-    dt, device = update.dtype, update.device
-    B, S, D = _bsd(update, "update", dt)
-    _like(grad_res, update, "grad_res")
-    _like(grad_out, update, "grad_out")
-    if grad_res is None and grad_out is None:
+    dt, device, shape = update.dtype, update.device, update.shape
+    B, S, D = shape if len(shape) == 3 else _bsd(update, "update", dt)
+    if grad_res is not None:
+        _input(grad_res, "grad_res", dt, device, shape)
+    elif grad_out is None:
         raise ValueError("grad_res or grad_out is required")
-    _vector(post_weight, D, "post_weight", dt)
-    gs = 0 if gate is None else _mod_rows(gate, B, D, "gate", dt)
+    _vector(post_weight, "post_weight", dt, device, D)
+    gs = _rows(gate, "gate", dt, device, B, D)
     bs = 0
-    _need_stats(post_rstd, B * S, "post_rstd", device)
+    _need_stats(post_rstd, "post_rstd", device, B * S)
     if grad_out is not None:
+        _input(grad_out, "grad_out", dt, device, shape)
         if res is None:
             raise ValueError("res is required with grad_out")
-        _like(res, update, "res")
-        _vector(weight, D, "weight", dt)
-        bs = _modulation(scale, None, B, D, dt)
-        _need_stats(rstd, B * S, "rstd", device)
+        _input(res, "res", dt, device, shape)
+        _vector(weight, "weight", dt, device, D)
+        bs = _rows(scale, "scale", dt, device, B, D)
+        _need_stats(rstd, "rstd", device, B * S)
     else:
         res = weight = scale = rstd = None
-    _same_device(device, res=res, post_weight=post_weight, gate=gate, weight=weight, scale=scale,
-                 grad_res=grad_res, grad_out=grad_out, post_rstd=post_rstd, rstd=rstd)
     g = SandwichGrads(
         torch.empty_like(update) if need_x else None,
         torch.empty_like(update) if need_x else None,
@@ -729,16 +762,15 @@ def rmsnorm_modulate_backward(x, weight, scale, grad_out, rstd, grad_res=None, n
     reaches x on the residual stream, added to grad_x before its rounding.  grad_weight fp32 [D];
     grad_scale, grad_shift fp32 [B, D] ([1, D] where one row is shared); scale may be None (no
     modulation: no such gradients).  Workspace as in sandwich_rmsnorm_modulate_backward."""
-    B, S, D = _bsd(x)
-    if grad_out is None:
-        raise TypeError("grad_out must be a torch.Tensor")
-    _like(grad_out, x, "grad_out")
-    _like(grad_res, x, "grad_res")
-    _vector(weight, D, "weight", x.dtype)
-    bs = _modulation(scale, None, B, D, x.dtype)
-    _need_stats(rstd, B * S, "rstd", x.device)
-    _same_device(x.device, weight=weight, scale=scale, grad_out=grad_out, rstd=rstd,
-                 grad_res=grad_res)
+    _dense(x, "x", torch.bfloat16)
+    dt, device, shape = x.dtype, x.device, x.shape
+    B, S, D = shape if len(shape) == 3 else _bsd(x)
+    _input(grad_out, "grad_out", dt, device, shape)
+    if grad_res is not None:
+        _input(grad_res, "grad_res", dt, device, shape)
+    _vector(weight, "weight", dt, device, D)
+    bs = _rows(scale, "scale", dt, device, B, D)
+    _need_stats(rstd, "rstd", device, B * S)
     grad_x = torch.empty_like(x) if need_x else None
     grad_weight = _vector_grad(need_mod and weight is not None, D, x.device)
     grad_scale = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
@@ -771,15 +803,17 @@ def _codes(q, name, device=None):
     """-> (rows, K) of a checked Mxfp4."""
     if not isinstance(q, Mxfp4):
         raise TypeError(f"{name} must be an Mxfp4")
-    for t, n in ((q.packed, f"{name}.packed"), (q.scales, f"{name}.scales")):
-        _dense(t, n, torch.uint8)
-        if device is not None and t.device != device:
-            raise ValueError(f"{n} must be on {device}")
-    K = 2 * q.packed.shape[-1] if q.packed.dim() else 0
+    packed, scales = q
+    _dense(packed, f"{name}.packed", torch.uint8)
+    _dense(scales, f"{name}.scales", torch.uint8)
+    if packed.device != scales.device or (device is not None and packed.device != device):
+        raise ValueError(f"{name} must be on {packed.device if device is None else device}")
+    shape = packed.shape
+    K = 2 * shape[-1] if shape else 0
     if K == 0 or K % 32:
         raise ValueError(f"{name}.packed must hold rows of a multiple of 32 values")
-    rows = 2 * q.packed.numel() // K
-    if q.scales.numel() != mxfp4_scale_bytes(rows, K):
+    rows = 2 * packed.numel() // K
+    if scales.numel() != mxfp4_scale_bytes(rows, K):
         raise ValueError(f"{name}.scales must hold {mxfp4_scale_bytes(rows, K)} bytes")
     return rows, K
 
@@ -848,29 +882,26 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
     for n in lead:
         M *= n
     S = M // B if B else 0
-    if bias is not None:
-        _dense(bias, "bias", dtype)
-        if bias.numel() != N:
-            raise ValueError("bias must have N elements")
-    gs = 0 if gate is None else _mod_rows(gate, B, N, "gate", dtype)
+    _vector(bias, "bias", dtype, device, N)
+    gs = _rows(gate, "gate", dtype, device, B, N)
+    shape = (*lead, N)
     if residual is not None:
-        _dense(residual, "residual", dtype)
-        if residual.shape != (*lead, N):
-            raise ValueError("residual must match the result")
+        _input(residual, "residual", dtype, device, shape)
     if out is None:
-        out = torch.empty(*lead, N, dtype=dtype, device=device)
+        out = torch.empty(shape, dtype=dtype, device=device)
     else:
-        _dense(out, "out", dtype)
-        if out.shape != (*lead, N):
-            raise ValueError("out must match the result")
-    _same_device(device, bias=bias, gate=gate, residual=residual, out=out)
-    if not isinstance(x, Mxfp4):
-        codes = M * (K // 2)
+        _input(out, "out", dtype, device, shape)
+    code = _DTYPES[dtype]
+    if isinstance(x, Mxfp4):
+        packed, scales = _at(x.packed), _at(x.scales)
+    else:
+        codes = M * (K // 2)  # a multiple of 16
         q = _scratch(stream, codes + mxfp4_scale_bytes(M, K), device)
-        x = mxfp4_quantize(x, Mxfp4(q[:codes].view(*lead, K // 2), q[codes:]), stream)
-    _call_on(device, "mxfp4_matmul", _at(x.packed), _at(x.scales), _at(w.packed),
-             _at(w.scales), _at(bias), _at(gate), gs, _at(residual), _at(out), B, S, N, K,
-             _DTYPES[dtype], stream=stream)
+        packed = _at(q)
+        scales = packed + codes
+        _call_on(device, "mxfp4_quantize", _at(x), packed, scales, M, K, code, stream=stream)
+    _call_on(device, "mxfp4_matmul", packed, scales, _at(w.packed), _at(w.scales), _at(bias),
+             _at(gate), gs, _at(residual), _at(out), B, S, N, K, code, stream=stream)
     return out
 
 

@@ -228,8 +228,8 @@ __device__ __forceinline__ float rstd_of(const uint4* from, int nv, int vectors,
 }
 
 // ---------------------------------------------------------------------------
-// rows of a CTA (or cluster): items blockIdx, blockIdx + grid, ... of `chunk` rows of one batch,
-// dealt to its groups in turn
+// rows of a CTA (or cluster): a range of items of `chunk` rows of one batch (neighbours, so that the
+// row vectors change as seldom as they can), dealt to its groups in turn
 // ---------------------------------------------------------------------------
 
 struct Plan {
@@ -241,6 +241,13 @@ struct Plan {
     int warps;   // of a group
     int stages;  // of a group's ring
 };
+
+// The items of worker `w` of `workers`: their counts differ by one at most.
+__device__ __forceinline__ uint32_t first_item(const Plan& p, uint32_t w, uint32_t workers)
+{
+    const uint32_t each = p.count / workers, more = p.count - each * workers;
+    return w * each + (w < more ? w : more);
+}
 
 struct Span {  // an item
     uint32_t batch, begin, end;
@@ -256,12 +263,13 @@ struct Span {  // an item
 
 // The rows of one group ahead of its arithmetic, in the ring's order.
 struct Ahead {
-    uint32_t item, row, end;
+    uint32_t item, last, row, end;
     int put;
 
-    __device__ __forceinline__ void seek(const Plan& p, uint32_t step, int group)
+    __device__ __forceinline__ bool any() const { return item < last; }
+    __device__ __forceinline__ void seek(const Plan& p, int group)
     {
-        for (; item < p.count; item += step) {
+        for (; item < last; ++item) {
             const Span s(p, item);
             row = s.begin + group;
             end = s.end;
@@ -269,20 +277,14 @@ struct Ahead {
                 return;
         }
     }
-    __device__ __forceinline__ void start(const Plan& p, uint32_t first, uint32_t step, int group)
-    {
-        item = first;
-        put = 0;
-        seek(p, step, group);
-    }
-    __device__ __forceinline__ void advance(const Plan& p, uint32_t step, int group)
+    __device__ __forceinline__ void advance(const Plan& p, int group)
     {
         put = put + 1 == p.stages ? 0 : put + 1;
         row += p.groups;
         if (row < end)
             return;
-        item += step;
-        seek(p, step, group);
+        ++item;
+        seek(p, group);
     }
 };
 
@@ -364,8 +366,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     g.warp = (threadIdx.x >> 5) - g.index * plan.warps;
     g.lane = threadIdx.x & 31;
     g.rank = CL ? cluster_rank() : 0u;
-    const uint32_t step = CL ? gridDim.x / 2 : gridDim.x;
-    const uint32_t first = CL ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t worker = CL ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t workers = CL ? gridDim.x / 2 : gridDim.x;
+    const uint32_t first = first_item(plan, worker, workers);
+    const uint32_t last = first_item(plan, worker + 1, workers);
     // this CTA's vectors of a row
     const int half = CL ? (a.Dv + 1) / 2 : a.Dv;
     const int v0 = static_cast<int>(g.rank) * half;
@@ -399,9 +403,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     const float inv_n = __fdiv_rn(1.0f, a.n);
     const u64 rs2 = f2_splat(a.residual_scale);
 
-    Ahead ahead{};
+    Ahead ahead{first, last, 0u, 0u, 0};
     auto issue = [&]() {  // the group's leader
-        if (ahead.item >= plan.count)
+        if (!ahead.any())
             return;
         const uint32_t bar = smem_addr(&full[g.index][ahead.put]);
         const uint32_t dst = smem_addr(ring + static_cast<size_t>(ahead.put) * 2 * half);
@@ -410,17 +414,17 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         mbar_expect_tx(bar, 2 * bytes);
         bulk_g2s(dst, update + from, bytes, bar);
         bulk_g2s(dst + half * 16, residual + from, bytes, bar);
-        ahead.advance(plan, step, g.index);
+        ahead.advance(plan, g.index);
     };
     if (g.leader()) {
-        ahead.start(plan, first, step, g.index);
+        ahead.seek(plan, g.index);
         for (int s = 0; s < plan.stages; ++s)
             issue();
     }
 
     uint32_t batch = 0xFFFFFFFFu, phase = 0;
     int get = 0;
-    for (uint32_t item = first; item < plan.count; item += step) {
+    for (uint32_t item = first; item < last; ++item) {
         const Span span(plan, item);
         if (span.batch != batch) {  // the row vectors of this batch
             __syncthreads();
@@ -547,8 +551,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     g.warp = (threadIdx.x >> 5) - g.index * plan.warps;
     g.lane = threadIdx.x & 31;
     g.rank = CL ? cluster_rank() : 0u;
-    const uint32_t step = CL ? gridDim.x / 2 : gridDim.x;
-    const uint32_t first = CL ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t worker = CL ? blockIdx.x / 2 : blockIdx.x;
+    const uint32_t workers = CL ? gridDim.x / 2 : gridDim.x;
+    const uint32_t first = first_item(plan, worker, workers);
+    const uint32_t last = first_item(plan, worker + 1, workers);
     const int half = CL ? (a.Dv + 1) / 2 : a.Dv;
     const int v0 = static_cast<int>(g.rank) * half;
     const int nv = a.Dv - v0 < half ? a.Dv - v0 : half;
@@ -580,9 +586,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     bool broken = false;
     const float inv_n = __fdiv_rn(1.0f, a.n);
     const u64 rs2 = f2_splat(a.residual_scale);
-    Ahead ahead{};
+    Ahead ahead{first, last, 0u, 0u, 0};
     auto issue = [&]() {  // the group's leader
-        if (ahead.item >= plan.count)
+        if (!ahead.any())
             return;
         const uint32_t bar = smem_addr(&full[g.index][ahead.put]);
         const uint32_t dst = smem_addr(ring + static_cast<size_t>(ahead.put) * rows * half);
@@ -600,10 +606,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         }
         if (has_gr)
             bring(k_gr, a.grad_res);
-        ahead.advance(plan, step, g.index);
+        ahead.advance(plan, g.index);
     };
     if (g.leader()) {
-        ahead.start(plan, first, step, g.index);
+        ahead.seek(plan, g.index);
         for (int s = 0; s < plan.stages; ++s)
             issue();
     }
@@ -612,7 +618,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     u64 sums[V][kParts][4];  // go, go * hh (OUT), dh * uh (POST)
     uint32_t batch = 0xFFFFFFFFu, phase = 0;
     int get = 0, par = 0;
-    for (uint32_t item = first; item < plan.count; item += step) {
+    for (uint32_t item = first; item < last; ++item) {
         const Span span(plan, item);
         if (span.batch != batch) {
             __syncthreads();
@@ -820,103 +826,116 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
         cluster_barrier();
 }
 
-// The gradients of the row vectors from the items' partial sums: 32 columns a CTA, four a thread;
-// the items of a batch are dealt to 32 threads in turn and joined in their order; batches in order.
-constexpr int kColSlices = 32;
+// The gradients of the row vectors from the items' partial sums.  A CTA has 32 columns, a thread four
+// of them in one of 64 slices: `ks` slices share the items of a batch (a power of two that the
+// number of items fixes, 4 to 32), so 64 / ks batches are summed at a time.  A warp then joins a
+// batch's slices in order, and the warps their batches.
+constexpr int kColSlices = 64;
+constexpr int kColWarps = kColSlices / 4;
 
 template <typename T>
 __global__ void __launch_bounds__(8 * kColSlices)
-    sandwich_columns_kernel(const SandwichBwdArgs a, uint32_t per_batch, int parts)
+    sandwich_columns_kernel(const SandwichBwdArgs a, uint32_t per_batch, int parts, int ks)
 {
     grid_dependency_sync();
     __shared__ float4 part[3][kColSlices][8];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int quad = threadIdx.x & 7, slice = threadIdx.x >> 3;
+    const int at_once = kColSlices / ks;
     const int64_t D = static_cast<int64_t>(a.Dv) * 8;
-    const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + quad;  // quad of columns
-    const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + threadIdx.x;  // the column it ends
+    const int64_t q = static_cast<int64_t>(blockIdx.x) * 8 + quad;     // this thread's four columns
+    const int64_t d = static_cast<int64_t>(blockIdx.x) * 32 + lane;    // the one it joins
     const bool out_on = a.grad_out != nullptr, post_on = a.update != nullptr;
-    const bool ends = threadIdx.x < 32 && d < D;
+    const bool joins = warp < at_once && d < D;
     auto value = [&](const void* p, int64_t at, float none) {
-        return p && ends ? static_cast<float>(static_cast<const T*>(p)[at + d]) : none;
+        return p && joins ? static_cast<float>(static_cast<const T*>(p)[at + d]) : none;
     };
     const float w = value(a.weight, 0, 1.0f);
     const float wp = __fmul_rn(value(a.post_weight, 0, 1.0f), a.update_scale);
-    float g_w = 0.0f, g_wp = 0.0f, g_scale = 0.0f, g_shift = 0.0f, g_gate = 0.0f;
-    for (int64_t b = 0; b < a.B; ++b) {
+    float g[5] = {0.0f, 0.0f, 0.0f, 0.0f, 0.0f};  // weight, post weight, scale, shift, gate
+    for (int64_t b0 = 0; b0 < a.B; b0 += at_once) {
+        const int64_t mine = b0 + slice / ks, b = b0 + warp;
         float4 s[3];
 #pragma unroll
         for (int p = 0; p < 3; ++p)
             s[p] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        if (q * 4 < D) {
+        if (q * 4 < D && mine < a.B) {
             const float4* from = reinterpret_cast<const float4*>(a.partials) +
-                                 b * per_batch * parts * (D / 4) + q;
+                                 mine * per_batch * parts * (D / 4) + q;
 #pragma unroll 5
-            for (uint32_t k = slice; k < per_batch; k += kColSlices)
+            for (uint32_t k = slice & (ks - 1); k < per_batch; k += ks)
 #pragma unroll
                 for (int p = 0; p < 3; ++p)
                     if (p < parts) {
-                        const float4 f = __ldcs(from + (static_cast<int64_t>(k) * parts + p) * (D / 4));
+                        const float4 f =
+                            __ldcs(from + (static_cast<int64_t>(k) * parts + p) * (D / 4));
                         s[p] = make_float4(__fadd_rn(s[p].x, f.x), __fadd_rn(s[p].y, f.y),
                                            __fadd_rn(s[p].z, f.z), __fadd_rn(s[p].w, f.w));
                     }
         }
+        const bool on = joins && b < a.B;
+        const float one = on ? __fadd_rn(1.0f, value(a.scale, b * a.mod_bstride * 8, 0.0f)) : 0.0f;
+        const float gt = on ? value(a.gate, b * a.gate_bstride * 8, 1.0f) : 0.0f;
 #pragma unroll
         for (int p = 0; p < 3; ++p)
             part[p][slice][quad] = s[p];
         __syncthreads();
-        if (ends) {
+        if (on) {
             float t[3];
 #pragma unroll
             for (int p = 0; p < 3; ++p) {
-                const float* at = reinterpret_cast<const float*>(&part[p][0][0]) + threadIdx.x;
+                const float* at = reinterpret_cast<const float*>(&part[p][warp * ks][0]) + lane;
                 t[p] = at[0];
-#pragma unroll
-                for (int k = 1; k < kColSlices; ++k)
+#pragma unroll 4
+                for (int k = 1; k < ks; ++k)
                     t[p] = __fadd_rn(t[p], at[k * 32]);
             }
             if (out_on) {
-                const float one = __fadd_rn(1.0f, value(a.scale, b * a.mod_bstride * 8, 0.0f));
-                g_w = __fmaf_rn(t[1], one, g_w);
                 const float gs = __fmul_rn(t[1], w);
-                if (a.mod_bstride != 0) {
-                    if (a.grad_shift)
-                        a.grad_shift[b * D + d] = t[0];
+                g[0] = __fmaf_rn(t[1], one, g[0]);
+                if (a.mod_bstride == 0) {
+                    g[2] = __fadd_rn(g[2], gs);
+                    g[3] = __fadd_rn(g[3], t[0]);
+                } else {
                     if (a.grad_scale)
                         a.grad_scale[b * D + d] = gs;
-                } else {
-                    g_shift = __fadd_rn(g_shift, t[0]);
-                    g_scale = __fadd_rn(g_scale, gs);
+                    if (a.grad_shift)
+                        a.grad_shift[b * D + d] = t[0];
                 }
             }
             if (post_on) {
                 const float du = out_on ? t[2] : t[0];
-                const float gt = value(a.gate, b * a.gate_bstride * 8, 1.0f);
-                g_wp = __fmaf_rn(du, __fmul_rn(gt, a.update_scale), g_wp);
                 const float gg = __fmul_rn(du, wp);
-                if (a.gate_bstride != 0) {
-                    if (a.grad_gate)
-                        a.grad_gate[b * D + d] = gg;
-                } else {
-                    g_gate = __fadd_rn(g_gate, gg);
-                }
+                g[1] = __fmaf_rn(du, __fmul_rn(gt, a.update_scale), g[1]);
+                if (a.gate_bstride == 0)
+                    g[4] = __fadd_rn(g[4], gg);
+                else if (a.grad_gate)
+                    a.grad_gate[b * D + d] = gg;
             }
         }
         __syncthreads();
     }
-    if (!ends)
+    // the warps' batches, in the warps' order
+    float* join = reinterpret_cast<float*>(&part[0][0][0]);
+    const int warps = a.B < at_once ? static_cast<int>(a.B) : at_once;
+    if (warp < warps)
+#pragma unroll
+        for (int i = 0; i < 5; ++i)
+            join[(i * kColWarps + warp) * 32 + lane] = g[i];
+    __syncthreads();
+    if (warp >= 5 || d >= D)
         return;
-    if (a.grad_weight)
-        a.grad_weight[d] = g_w;
-    if (a.grad_post_weight)
-        a.grad_post_weight[d] = g_wp;
-    if (a.mod_bstride == 0) {
-        if (a.grad_shift)
-            a.grad_shift[d] = g_shift;
-        if (a.grad_scale)
-            a.grad_scale[d] = g_scale;
-    }
-    if (a.gate_bstride == 0 && a.grad_gate)
-        a.grad_gate[d] = g_gate;
+    float* to = warp == 0 ? a.grad_weight
+                          : (warp == 1 ? a.grad_post_weight
+                                       : (warp == 2 ? a.grad_scale
+                                                    : (warp == 3 ? a.grad_shift : a.grad_gate)));
+    const bool shared = warp < 2 || (warp < 4 ? a.mod_bstride : a.gate_bstride) == 0;
+    if (!to || !shared)
+        return;
+    float t = join[warp * kColWarps * 32 + lane];
+    for (int k = 1; k < warps; ++k)
+        t = __fadd_rn(t, join[(warp * kColWarps + k) * 32 + lane]);
+    to[d] = t;
 }
 
 // ---------------------------------------------------------------------------
@@ -1030,13 +1049,17 @@ cudaError_t launch_fwd_t(const SandwichArgs& a, const DeviceInfo& dev, cudaStrea
 }
 
 // Items of the backward pass: their rows depend on S and D alone, so that the token sums do not
-// depend on the batch.  At least a row for each group; 152 SMs.
+// depend on the batch.  152 SMs.
 Plan backward_plan(int64_t B, int64_t S, int Dv)
 {
     const Shape s = shape_of(Dv, backward_vectors(Dv));
+    // whole rounds of items, of at most 256 rows (whose sums stay within a few 2^-24); of at least
+    // eight, and two for each group, so that the partial sums stay under an eighth of the rows' bytes
     const int64_t over = s.cluster ? 76 : 152;
-    int64_t chunk = (S + over - 1) / over;
-    chunk = chunk < s.groups ? s.groups : (chunk > 64 ? 64 : chunk);
+    const int64_t rounds = (S + 256 * over - 1) / (256 * over);
+    int64_t chunk = (S + rounds * over - 1) / (rounds * over);
+    const int64_t least = s.groups > 4 ? 2 * s.groups : 8;
+    chunk = chunk < least ? least : chunk;
     return plan_of(B, S, chunk < S ? chunk : S, s);
 }
 
@@ -1072,8 +1095,11 @@ cudaError_t launch_columns(const SandwichBwdArgs& a, const Plan& p, cudaStream_t
 {
     const int parts = (a.grad_out ? 2 : 0) + (a.update ? 1 : 0);
     const int grid = (a.Dv * 8 + 31) / 32;
+    int ks = 4;
+    while (ks < 32 && static_cast<uint32_t>(ks) < p.per_batch.d)
+        ks *= 2;
     return launch_dependent(sandwich_columns_kernel<T>, grid, 8 * kColSlices, 0, stream, a,
-                            p.per_batch.d, parts);
+                            p.per_batch.d, parts, ks);
 }
 
 template <typename T>
