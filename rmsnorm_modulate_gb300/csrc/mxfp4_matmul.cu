@@ -3,10 +3,19 @@
 //   acc[m, n] = sum_k a[m, k] * b[n, k]          (fp32 accumulators in tensor memory)
 //   out       = R(residual + gate_b * (acc + bias)),  one rounding
 //
-// One CTA per 128 x 256 tile of the output.  A producer warp brings 128 bytes (256 values) of
-// every row of a and b per step by TMA (128-byte swizzle), and the scale tiles as they lie; the
-// issuing thread copies the scales into tensor memory and starts four products of 64 values each;
-// four warps read the accumulators back and finish the rows.
+// A step is 256 values (128 bytes) of every row of a tile, brought by TMA (128-byte swizzle), and two
+// scale tiles for each 128 rows; one thread copies the scales to tensor memory and starts four
+// products of 64 values.
+//
+// pair_kernel (more than 128 rows of a): two CTAs of a cluster share a 256 x BN tile
+// (cta_group::2), each with its 128 rows of a and half of b's rows, so that a step takes 32 KB
+// per SM from L2 where a CTA of its own would take 48: at this type's rate the products ask for more
+// than an SM's share of L2 otherwise.  Persistent; eight warps take a finished accumulator into
+// registers, free it for the next tile's products and finish their rows beside them.
+//
+// few_kernel (up to 128 rows of a, where reading b is what counts): b's rows take the 128-row side of
+// the instruction, a's rows the other.  A cluster of up to eight CTAs splits K, and joins its parts in
+// the CTAs' order through distributed shared memory.
 #include <cuda.h>
 #include <mutex>
 
@@ -21,21 +30,16 @@ namespace {
 
 __device__ unsigned int g_error;
 
-constexpr int kBM = 128;
-constexpr int kBN = 256;
-constexpr int kStepBytes = 128;  // of a row per step
-constexpr int kStepK = 256;      // values per step
-constexpr int kStages = 4;
-constexpr int kABytes = kBM * kStepBytes;
-constexpr int kBBytes = kBN * kStepBytes;
-constexpr int kSfaBytes = 1024;                // 128 rows x 8 blocks
-constexpr int kSfbBytes = kBN / 128 * 1024;
-constexpr int kStageBytes = kABytes + kBBytes + kSfaBytes + kSfbBytes;
-constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-constexpr int kThreads = 192;    // four epilogue warps, producer, issuer
-constexpr uint32_t kTmemCols = 512;
-constexpr uint32_t kSfaCol = 256;  // accumulators in columns 0..255
-constexpr uint32_t kSfbCol = kSfaCol + 8;
+constexpr int kStepBytes = 128;   // of a row per step
+constexpr int kStepK = 256;       // values per step
+constexpr int kTileBytes = 128 * kStepBytes;
+constexpr int kScaleBytes = 1024;  // a step's scales of 128 rows
+constexpr uint32_t kPairTmemCols = 512, kFewTmemCols = 256;
+constexpr int kSmemMax = 227 * 1024;
+
+// ---------------------------------------------------------------------------
+// instructions
+// ---------------------------------------------------------------------------
 
 __device__ __forceinline__ bool elect_one()
 {
@@ -45,15 +49,70 @@ __device__ __forceinline__ bool elect_one()
     return p != 0;
 }
 
-// Tile of a 2-D tensor map into shared memory.
-__device__ __forceinline__ void tma_tile(uint32_t dst, const CUtensorMap* map, int x, int y,
-                                         uint32_t bar)
+__device__ __forceinline__ uint32_t cluster_rank()
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
-        "l"(map), "r"(x), "r"(y), "r"(bar)
-        : "memory");
+    uint32_t r;
+    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+    return r;
+}
+
+__device__ __forceinline__ void cluster_barrier()
+{
+    asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// A shared-memory address of this CTA in CTA `rank` of the cluster.
+__device__ __forceinline__ uint32_t in_cta(uint32_t addr, uint32_t rank)
+{
+    uint32_t r;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(addr), "r"(rank));
+    return r;
+}
+
+__device__ __forceinline__ void arrive_remote(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar)
+                 : "memory");
+}
+
+// mbar_wait that also orders what the other CTA did before its arrival.
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(ok)
+            : "r"(bar), "r"(parity)
+            : "memory");
+        if (ok)
+            return true;
+        if (global_ns() - t0 > kWaitLimitNs)
+            return false;
+    }
+}
+
+// Box of a 2-D tensor map into this CTA's shared memory.  PAIR: the barrier may be the other CTA's.
+template <bool PAIR>
+__device__ __forceinline__ void tma_box(uint32_t dst, const CUtensorMap* map, int x, int y,
+                                        uint32_t bar)
+{
+    if (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.mbarrier::complete_tx"
+            "::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst),
+            "l"(map), "r"(x), "r"(y), "r"(bar)
+            : "memory");
 }
 
 // Shared-memory matrix descriptors.  Operand tiles: rows of 128 bytes, swizzled, eight rows
@@ -71,31 +130,91 @@ __device__ __forceinline__ uint64_t scale_desc(uint32_t addr)
 }
 
 // 512 bytes of scales to 32 lanes x 4 columns, repeated for the four groups of lanes.
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
-                 : "memory");
+    if (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                     : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc)
+                     : "memory");
 }
 
+template <bool PAIR>
 __device__ __forceinline__ void mma_mxf4(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t sfa, uint32_t sfb, bool accumulate)
 {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
-        "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
-        : "memory");
+    if (PAIR)
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::2.kind::mxf4.block_scale.scale_vec::2X "
+            "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+            : "memory");
+    else
+        asm volatile(
+            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
+            "tcgen05.mma.cta_group::1.kind::mxf4.block_scale.scale_vec::2X "
+            "[%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d),
+            "l"(a), "l"(b), "r"(idesc), "r"(sfa), "r"(sfb), "r"(accumulate ? 1u : 0u)
+            : "memory");
 }
 
+// Arrives on `bar` (in both CTAs of a pair) when what this thread has started is done.
+template <bool PAIR>
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::
-                     "r"(bar)
-                 : "memory");
+    if (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster"
+            ".b64 [%0], %1;" ::"r"(bar),
+            "h"(static_cast<uint16_t>(3))
+            : "memory");
+    else
+        asm volatile(
+            "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar)
+            : "memory");
 }
 
-__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
+template <bool PAIR>
+__device__ __forceinline__ void tmem_alloc(uint32_t to)
+{
+    if (PAIR) {
+        asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to),
+                     "r"(kPairTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+    } else {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(to),
+                     "r"(kFewTmemCols)
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+}
+
+template <bool PAIR>
+__device__ __forceinline__ void tmem_free(uint32_t tmem)
+{
+    if (PAIR)
+        asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kPairTmemCols));
+    else
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
+                     "r"(kFewTmemCols));
+}
+
+__device__ __forceinline__ void before_sync()
+{
+    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void after_sync()
+{
+    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+}
+
+__device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t* r)
 {
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -109,43 +228,337 @@ __device__ __forceinline__ void tmem_load32(uint32_t addr, uint32_t (&r)[32])
         : "r"(addr));
 }
 
+__device__ __forceinline__ void tmem_load16(uint32_t addr, uint32_t* r)
+{
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]),
+          "=r"(r[14]), "=r"(r[15])
+        : "r"(addr));
+}
+
+__device__ __forceinline__ void tmem_loads_done()
+{
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+}
+
+// Instruction descriptor: e2m1 operands, e8m0 scales, K = 64.
+__host__ __device__ constexpr uint32_t instruction(int M, int N)
+{
+    return (1u << 7) | (1u << 10) | (static_cast<uint32_t>(N / 8) << 17) | (1u << 23) |
+           (static_cast<uint32_t>(M / 16) << 24);
+}
+
+// The products of one step.  Scales: two tiles (of four blocks each) for each 128 rows; a product
+// takes two of a column's four scales.
+template <bool PAIR, int B_TILES>
+__device__ __forceinline__ void step_products(uint32_t acc, uint32_t sfa_col, uint32_t sfb_col,
+                                              uint32_t sa, uint32_t sb, uint32_t sfa, uint32_t sfb,
+                                              uint32_t idesc, int parts, bool first)
+{
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        if (2 * h < parts) {
+            copy_scales<PAIR>(sfa_col + h * 4, scale_desc(sfa + h * 512));
+#pragma unroll
+            for (int i = 0; i < B_TILES; ++i)
+                copy_scales<PAIR>(sfb_col + h * (4 * B_TILES) + i * 4,
+                                  scale_desc(sfb + i * kScaleBytes + h * 512));
+        }
+#pragma unroll
+    for (int p = 0; p < 4; ++p)
+        if (p < parts) {
+            const uint32_t id = (p & 1) * 2u;
+            mma_mxf4<PAIR>(acc, operand_desc(sa + p * 32), operand_desc(sb + p * 32),
+                           idesc | (id << 4) | (id << 29), sfa_col + (p >> 1) * 4,
+                           sfb_col + (p >> 1) * (4 * B_TILES), !first || p > 0);
+        }
+}
+
+// Products that the last step has: 64 values each.
+__device__ __forceinline__ int parts_of(int64_t K, int t)
+{
+    const int64_t left = K - static_cast<int64_t>(t) * kStepK;
+    return left >= kStepK ? 4 : static_cast<int>((left + 63) / 64);
+}
+
 struct Maps {
-    CUtensorMap a, b;
+    CUtensorMap a, a_scales, b, b_scales;
+};
+
+// ---------------------------------------------------------------------------
+// more than 128 rows
+// ---------------------------------------------------------------------------
+
+template <int BN>
+struct Pair {
+    static constexpr int kBBytes = BN / 2 * kStepBytes;
+    static constexpr int kBTiles = BN / 128;
+    static constexpr int kStageBytes = kTileBytes + kBBytes + kScaleBytes * (1 + kBTiles);
+    static constexpr int kStages = (kSmemMax - 2048) / kStageBytes;
+    static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
+    static constexpr int kAccs = BN == 256 ? 1 : 2;  // accumulators that fit beside the scales
+    static constexpr uint32_t kSfaCol = 256;
+    static constexpr uint32_t kSfbCol = kSfaCol + 8;
+    static constexpr int kCols = BN / 2;  // of an accumulator row in one epilogue thread
+    static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
+};
+
+constexpr int kEpilogueWarps = 8;
+constexpr int kPairThreads = 64 + 32 * kEpilogueWarps;  // producer, issuer, epilogue
+
+// Eight columns of one row.
+template <typename T>
+__device__ __forceinline__ uint4 finish8(const uint32_t* acc, const uint4* bias, const uint4* gate,
+                                         const uint4* residual, const uint4& bv, const uint4& gv,
+                                         const uint4& rv)
+{
+    uint4 o;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float lo = __uint_as_float(acc[2 * j]), hi = __uint_as_float(acc[2 * j + 1]);
+        if (bias) {
+            const float2 v = widen2<T>(word(bv, j));
+            lo += v.x;
+            hi += v.y;
+        }
+        if (gate) {
+            const float2 v = widen2<T>(word(gv, j));
+            lo *= v.x;
+            hi *= v.y;
+        }
+        if (residual) {
+            const float2 v = widen2<T>(word(rv, j));
+            lo += v.x;
+            hi += v.y;
+        }
+        word(o, j) = narrow2<T>(lo, hi);
+    }
+    return o;
+}
+
+template <typename T, int BN>
+__global__ void __launch_bounds__(kPairThreads, 1)
+    pair_kernel(const Mxfp4MatmulArgs a, const __grid_constant__ Maps maps, int tiles_m, int tiles)
+{
+    using P = Pair<BN>;
+    extern __shared__ uint8_t raw[];
+    __shared__ __align__(8) unsigned long long full[P::kStages], empty[P::kStages];
+    __shared__ __align__(8) unsigned long long acc_full[P::kAccs], acc_empty[P::kAccs];
+    __shared__ uint32_t tmem_base;
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const uint32_t rank = cluster_rank();
+    const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
+    const int steps = static_cast<int>((a.K + kStepK - 1) / kStepK);
+    const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < P::kStages; ++s) {
+            mbar_init(smem_addr(&full[s]), 1u);
+            mbar_init(smem_addr(&empty[s]), 1u);
+        }
+        for (int s = 0; s < P::kAccs; ++s) {
+            mbar_init(smem_addr(&acc_full[s]), 1u);
+            mbar_init(smem_addr(&acc_empty[s]), 2u * kEpilogueWarps);
+        }
+        mbar_init_fence();
+    }
+    if (warp == 1)
+        tmem_alloc<true>(smem_addr(&tmem_base));
+    before_sync();
+    cluster_barrier();
+    after_sync();
+    grid_dependency_sync();
+    const uint32_t tmem = tmem_base;
+
+    bool broken = false;
+    auto gave_up = [&](bool ok) {
+        if (!ok && !broken) {
+            broken = true;
+            atomicOr(&g_error, kErrCopyTimeout);
+        }
+    };
+
+    if (warp == 0) {
+        if (elect_one()) {
+            // both CTAs' copies are counted on the first one's barriers
+            const int block_tiles = static_cast<int>((a.K + 127) / 128);
+            int s = 0;
+            uint32_t phase = 1;
+            for (int tile = pair; tile < tiles; tile += pairs) {
+                const int m0 = tile % tiles_m * 256 + static_cast<int>(rank) * 128;
+                const int n0 = tile / tiles_m * BN;
+                for (int t = 0; t < steps; ++t) {
+                    if (!broken)
+                        gave_up(mbar_wait_cluster(smem_addr(&empty[s]), phase));
+                    const uint32_t bar = in_cta(smem_addr(&full[s]), 0);
+                    const uint32_t dst = ring + s * P::kStageBytes;
+                    if (rank == 0)
+                        mbar_expect_tx(smem_addr(&full[s]), 2 * P::kStageBytes);
+                    tma_box<true>(dst, &maps.a, t * kStepBytes, m0, bar);
+                    tma_box<true>(dst + kTileBytes, &maps.b, t * kStepBytes,
+                                  n0 + static_cast<int>(rank) * (BN / 2), bar);
+                    const uint32_t sf = dst + kTileBytes + P::kBBytes;
+                    tma_box<true>(sf, &maps.a_scales, 0, 2 * (m0 / 128 * block_tiles + 2 * t), bar);
+#pragma unroll
+                    for (int i = 0; i < P::kBTiles; ++i)
+                        tma_box<true>(sf + (1 + i) * kScaleBytes, &maps.b_scales, 0,
+                                      2 * ((n0 / 128 + i) * block_tiles + 2 * t), bar);
+                    if (++s == P::kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+            }
+            // no arrival is left on its way when this CTA's shared memory goes
+            for (int i = 0; i < P::kStages; ++i) {
+                if (!broken)
+                    gave_up(mbar_wait_cluster(smem_addr(&empty[s]), phase));
+                if (++s == P::kStages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
+            }
+        }
+    } else if (warp == 1) {
+        if (rank == 0 && elect_one()) {
+            constexpr uint32_t kIdesc = instruction(256, BN);
+            int s = 0, acc = 0;
+            uint32_t phase = 0, acc_phase = 1;
+            for (int tile = pair; tile < tiles; tile += pairs) {
+                if (!broken)
+                    gave_up(mbar_wait_cluster(smem_addr(&acc_empty[acc]), acc_phase));
+                after_sync();
+                for (int t = 0; t < steps; ++t) {
+                    if (!broken)
+                        gave_up(mbar_wait_cluster(smem_addr(&full[s]), phase));
+                    after_sync();
+                    const uint32_t sa = ring + s * P::kStageBytes, sb = sa + kTileBytes;
+                    const uint32_t sfa = sb + P::kBBytes, sfb = sfa + kScaleBytes;
+                    step_products<true, P::kBTiles>(tmem + acc * BN, tmem + P::kSfaCol,
+                                                    tmem + P::kSfbCol, sa, sb, sfa, sfb, kIdesc,
+                                                    parts_of(a.K, t), t == 0);
+                    commit<true>(smem_addr(&empty[s]));
+                    if (++s == P::kStages) {
+                        s = 0;
+                        phase ^= 1u;
+                    }
+                }
+                commit<true>(smem_addr(&acc_full[acc]));
+                if (++acc == P::kAccs) {
+                    acc = 0;
+                    acc_phase ^= 1u;
+                }
+            }
+        }
+    } else {
+        // a warp reads the 32 lanes of tensor memory that its index selects, half of the columns
+        const int quarter = warp & 3, half = (warp - 2) >> 2;
+        const uint4* __restrict__ bias = static_cast<const uint4*>(a.bias);
+        const uint4* __restrict__ gate = static_cast<const uint4*>(a.gate);
+        const uint4* __restrict__ residual = static_cast<const uint4*>(a.residual);
+        const int64_t Nv = a.N / 8;
+        int acc = 0;
+        uint32_t phase = 0;
+        for (int tile = pair; tile < tiles; tile += pairs) {
+            if (!broken)
+                gave_up(mbar_wait_cluster(smem_addr(&acc_full[acc]), phase));
+            __syncwarp();
+            after_sync();
+            uint32_t v[P::kCols];
+#pragma unroll
+            for (int c = 0; c < P::kCols; c += 32)
+                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN +
+                                half * P::kCols + c,
+                            v + c);
+            tmem_loads_done();
+            before_sync();
+            __syncwarp();
+            // the accumulator may take the next tile
+            if (lane == 0)
+                arrive_remote(in_cta(smem_addr(&acc_empty[acc]), 0));
+            if (++acc == P::kAccs) {
+                acc = 0;
+                phase ^= 1u;
+            }
+            const int64_t m = static_cast<int64_t>(tile % tiles_m) * 256 + rank * 128 +
+                              quarter * 32 + lane;
+            const int64_t n0 = static_cast<int64_t>(tile / tiles_m) * BN + half * P::kCols;
+            if (m >= a.M)
+                continue;
+            const int64_t gate_at = (gate ? m / a.S * a.gate_bstride : 0) / 8;
+#pragma unroll
+            for (int c = 0; c < P::kCols / 8; ++c) {
+                const int64_t n = n0 / 8 + c;
+                if (n < Nv) {
+                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 bv = bias ? ld_cached(bias + n) : zero;
+                    const uint4 gv = gate ? ld_cached(gate + gate_at + n) : zero;
+                    const uint4 rv = residual ? ld_stream(residual + m * Nv + n) : zero;
+                    st_stream(static_cast<uint4*>(a.out) + m * Nv + n,
+                              finish8<T>(v + 8 * c, bias, gate, residual, bv, gv, rv));
+                }
+            }
+        }
+    }
+    // after a timeout: a bounded pause for the copies still in flight
+    if (broken)
+        drain_pause();
+    before_sync();
+    cluster_barrier();
+    after_sync();
+    if (warp == 1)
+        tmem_free<true>(tmem);
+}
+
+// ---------------------------------------------------------------------------
+// up to 128 rows
+// ---------------------------------------------------------------------------
+
+constexpr int kFewThreads = 192;  // four epilogue warps, producer, issuer
+constexpr int kFewMaxStages = 10;
+constexpr uint32_t kFewSfwCol = 128;            // accumulators in columns 0..127
+constexpr uint32_t kFewSfxCol = kFewSfwCol + 8;
+
+struct Few {
+    int NX;           // a's rows as the instruction takes them: 16, 32, 64 or 128
+    int stages;
+    int stage_bytes;
+    int split;        // CTAs of a cluster, each with a range of the steps
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads)
-    matmul_kernel(const Mxfp4MatmulArgs a, const __grid_constant__ Maps maps)
+__global__ void __launch_bounds__(kFewThreads, 1)
+    few_kernel(const Mxfp4MatmulArgs a, const __grid_constant__ Maps maps, const Few f)
 {
     extern __shared__ uint8_t raw[];
-    __shared__ __align__(8) unsigned long long full[kStages], empty[kStages], done;
+    __shared__ __align__(8) unsigned long long full[kFewMaxStages], empty[kFewMaxStages], done;
     __shared__ uint32_t tmem_base;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
-    const int64_t m0 = static_cast<int64_t>(blockIdx.x) * kBM;
-    const int64_t n0 = static_cast<int64_t>(blockIdx.y) * kBN;
-    const int steps = static_cast<int>((a.K + kStepK - 1) / kStepK);
-    const int64_t block_tiles = (a.K + 127) / 128;
+    const uint32_t rank = f.split > 1 ? cluster_rank() : 0u;
+    const int n0 = static_cast<int>(blockIdx.x) / f.split * 128;
+    const int all = static_cast<int>((a.K + kStepK - 1) / kStepK);
+    const int begin = static_cast<int>(static_cast<int64_t>(all) * rank / f.split);
+    const int end = static_cast<int>(static_cast<int64_t>(all) * (rank + 1) / f.split);
 
     if (threadIdx.x == 0) {
-        for (int s = 0; s < kStages; ++s) {
+        for (int s = 0; s < f.stages; ++s) {
             mbar_init(smem_addr(&full[s]), 1u);
             mbar_init(smem_addr(&empty[s]), 1u);
         }
         mbar_init(smem_addr(&done), 1u);
         mbar_init_fence();
     }
-    if (warp == 5) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
-                         smem_addr(&tmem_base)),
-                     "r"(kTmemCols)
-                     : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-    }
-    asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
+    if (warp == 5)
+        tmem_alloc<false>(smem_addr(&tmem_base));
+    before_sync();
     __syncthreads();
-    asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
+    after_sync();
     grid_dependency_sync();
     const uint32_t tmem = tmem_base;
 
@@ -159,120 +572,118 @@ __global__ void __launch_bounds__(kThreads)
 
     if (warp == 4) {
         if (elect_one()) {
-            // row tiles of b's scales that exist under this tile
-            const int64_t b_tiles = (a.N + 127) / 128;
-            const int sfb_tiles = static_cast<int>(b_tiles - n0 / 128 < kBN / 128
-                                                       ? b_tiles - n0 / 128 : kBN / 128);
-            const uint8_t* sfa = static_cast<const uint8_t*>(a.a_scales) +
-                                 blockIdx.x * block_tiles * 512;
-            const uint8_t* sfb = static_cast<const uint8_t*>(a.b_scales) +
-                                 n0 / 128 * block_tiles * 512;
-            for (int t = 0; t < steps; ++t) {
-                const int s = t % kStages;
-                if (t >= kStages)
-                    wait(smem_addr(&empty[s]), ((t / kStages) & 1) ^ 1);
+            const int block_tiles = static_cast<int>((a.K + 127) / 128);
+            int s = 0;
+            uint32_t phase = 1;
+            for (int t = begin; t < end; ++t) {
+                wait(smem_addr(&empty[s]), phase);
                 const uint32_t bar = smem_addr(&full[s]);
-                const uint32_t dst = ring + s * kStageBytes;
-                const uint32_t sf_bytes = block_tiles - 2 * t >= 2 ? 1024u : 512u;
-                mbar_expect_tx(bar, kABytes + kBBytes + sf_bytes * (1 + sfb_tiles));
-                tma_tile(dst, &maps.a, t * kStepBytes, static_cast<int>(m0), bar);
-                tma_tile(dst + kABytes, &maps.b, t * kStepBytes, static_cast<int>(n0), bar);
-                bulk_g2s(dst + kABytes + kBBytes, sfa + t * 1024, sf_bytes, bar);
-                for (int i = 0; i < sfb_tiles; ++i)
-                    bulk_g2s(dst + kABytes + kBBytes + kSfaBytes + i * 1024,
-                             sfb + i * block_tiles * 512 + t * 1024, sf_bytes, bar);
+                const uint32_t dst = ring + s * f.stage_bytes;
+                mbar_expect_tx(bar, f.stage_bytes);
+                tma_box<false>(dst, &maps.b, t * kStepBytes, n0, bar);
+                tma_box<false>(dst + kTileBytes, &maps.b_scales, 0,
+                               2 * (n0 / 128 * block_tiles + 2 * t), bar);
+                tma_box<false>(dst + kTileBytes + kScaleBytes, &maps.a_scales, 0, 4 * t, bar);
+                tma_box<false>(dst + kTileBytes + 2 * kScaleBytes, &maps.a, t * kStepBytes, 0, bar);
+                if (++s == f.stages) {
+                    s = 0;
+                    phase ^= 1u;
+                }
             }
         }
     } else if (warp == 5) {
         if (elect_one()) {
-            // e2m1 operands, e8m0 scales, M = 128, N = 256
-            constexpr uint32_t kIdesc = (1u << 7) | (1u << 10) | ((kBN / 8) << 17) | (1u << 23) |
-                                        ((kBM / 16) << 24);
-            for (int t = 0; t < steps; ++t) {
-                const int s = t % kStages;
-                wait(smem_addr(&full[s]), (t / kStages) & 1);
-                asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-                const uint32_t sa = ring + s * kStageBytes, sb = sa + kABytes;
-                const uint32_t sfa = sb + kBBytes, sfb = sfa + kSfaBytes;
-                const int64_t left = a.K - static_cast<int64_t>(t) * kStepK;
-                const int parts = left >= kStepK ? 4 : static_cast<int>((left + 63) / 64);
-                // a step's scales: two tiles of four blocks for each 128 rows
-                for (int h = 0; h < (parts + 1) / 2; ++h) {
-                    copy_scales(tmem + kSfaCol + h * 4, scale_desc(sfa + h * 512));
-                    for (int i = 0; i < kBN / 128; ++i)
-                        copy_scales(tmem + kSfbCol + h * (kBN / 32) + i * 4,
-                                    scale_desc(sfb + i * 1024 + h * 512));
+            const uint32_t idesc = instruction(128, f.NX);
+            int s = 0;
+            uint32_t phase = 0;
+            for (int t = begin; t < end; ++t) {
+                wait(smem_addr(&full[s]), phase);
+                after_sync();
+                const uint32_t sw = ring + s * f.stage_bytes, sfw = sw + kTileBytes;
+                step_products<false, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, sw,
+                                        sfw + 2 * kScaleBytes, sfw, sfw + kScaleBytes, idesc,
+                                        parts_of(a.K, t), t == begin);
+                commit<false>(smem_addr(&empty[s]));
+                if (++s == f.stages) {
+                    s = 0;
+                    phase ^= 1u;
                 }
-                for (int p = 0; p < parts; ++p) {
-                    const uint32_t id = (p & 1) * 2u;  // which two of a column's four scales
-                    mma_mxf4(tmem, operand_desc(sa + p * 32), operand_desc(sb + p * 32),
-                             kIdesc | (id << 4) | (id << 29), tmem + kSfaCol + (p >> 1) * 4,
-                             tmem + kSfbCol + (p >> 1) * (kBN / 32), t > 0 || p > 0);
-                }
-                commit(smem_addr(&empty[s]));
             }
-            commit(smem_addr(&done));
+            commit<false>(smem_addr(&done));
         }
-    } else {
-        wait(smem_addr(&done), 0);
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        const int64_t m = m0 + warp * 32 + lane;
-        const uint4* __restrict__ bias = static_cast<const uint4*>(a.bias);
-        const uint4* __restrict__ gate = static_cast<const uint4*>(a.gate);
-        const uint4* __restrict__ residual = static_cast<const uint4*>(a.residual);
-        const int64_t gate_row = (m < a.M ? m / a.S : 0) * (a.gate_bstride / 8);
-        for (int c = 0; c < kBN; c += 32) {
-            if (n0 + c >= a.N)
-                break;
-            uint32_t acc[32];
-            __syncwarp();
-            tmem_load32(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, acc);
-            asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const int64_t n = n0 + c + q * 8;
-                if (m >= a.M || n >= a.N)
-                    continue;
-                const uint4 bv = bias ? ld_cached(bias + n / 8) : make_uint4(0u, 0u, 0u, 0u);
-                const uint4 gv = gate ? ld_cached(gate + gate_row + n / 8) : bv;
-                const uint4 rv = residual ? ld_stream(residual + (m * a.N + n) / 8) : bv;
-                uint4 o;
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    float lo = __uint_as_float(acc[q * 8 + 2 * j]);
-                    float hi = __uint_as_float(acc[q * 8 + 2 * j + 1]);
-                    if (bias) {
-                        const float2 v = widen2<T>(word(bv, j));
-                        lo += v.x;
-                        hi += v.y;
-                    }
-                    if (gate) {
-                        const float2 v = widen2<T>(word(gv, j));
-                        lo *= v.x;
-                        hi *= v.y;
-                    }
-                    if (residual) {
-                        const float2 v = widen2<T>(word(rv, j));
-                        lo += v.x;
-                        hi += v.y;
-                    }
-                    word(o, j) = narrow2<T>(lo, hi);
-                }
-                st_stream(static_cast<uint4*>(a.out) + (m * a.N + n) / 8, o);
-            }
-        }
-        asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
     }
-    // after a timeout: a bounded pause for the copies still in flight
+    // ---- lane n of tensor memory, column m
+    const int n_in = warp * 32 + lane;
+    const int64_t n = n0 + n_in;
+    const T* bias = static_cast<const T*>(a.bias);
+    const T* gate = static_cast<const T*>(a.gate);
+    const T* residual = static_cast<const T*>(a.residual);
+    T* out = static_cast<T*>(a.out);
+    const int M = static_cast<int>(a.M), S = static_cast<int>(a.S);
+    auto finish = [&](int m, float v, float bias_n) {
+        v += bias_n;
+        if (gate)
+            v *= static_cast<float>(gate[m / S * a.gate_bstride + n]);
+        if (residual)
+            v += static_cast<float>(residual[m * a.N + n]);
+        out[m * a.N + n] = static_cast<T>(v);
+    };
+    const float bias_n = warp < 4 && n < a.N && bias ? static_cast<float>(bias[n]) : 0.0f;
+    float* part = reinterpret_cast<float*>(raw + (ring - smem_addr(raw)));  // [m][128]
+    if (warp < 4) {
+        wait(smem_addr(&done), 0);
+        __syncwarp();
+        after_sync();
+        for (int c = 0; c < M; c += 16) {
+            uint32_t v[16];
+            tmem_load16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+            tmem_loads_done();
+#pragma unroll
+            for (int j = 0; j < 16; ++j) {
+                if (f.split > 1)
+                    part[(c + j) * 128 + n_in] = __uint_as_float(v[j]);
+                else if (c + j < M && n < a.N)
+                    finish(c + j, __uint_as_float(v[j]), bias_n);
+            }
+        }
+        before_sync();
+    }
     if (broken)
         drain_pause();
-    __syncthreads();
+    if (f.split > 1) {
+        cluster_barrier();
+        if (warp < 4 && n < a.N) {
+            // this CTA's rows of a, the parts of K in order
+            const uint32_t at = smem_addr(part) + n_in * 4;
+            for (int m = static_cast<int>(rank); m < M; m += f.split) {
+                float p[8];
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                    if (r < f.split)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(p[r])
+                                     : "r"(in_cta(at + m * 512, r)));
+                float v = p[0];
+#pragma unroll
+                for (int r = 1; r < 8; ++r)
+                    if (r < f.split)
+                        v += p[r];
+                finish(m, v, bias_n);
+            }
+        }
+        cluster_barrier();
+    } else {
+        __syncthreads();
+    }
     if (warp == 5) {
-        asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory");
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem),
-                     "r"(kTmemCols));
+        after_sync();
+        tmem_free<false>(tmem);
     }
 }
+
+// ---------------------------------------------------------------------------
+// launches
+// ---------------------------------------------------------------------------
 
 using EncodeTiled = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
@@ -300,43 +711,137 @@ cudaError_t encoder(EncodeTiled& fn)
     return cudaSuccess;
 }
 
-// Rows of K / 2 bytes; boxes of 128 bytes by `box_rows`, zeros outside the matrix.
-cudaError_t rows_map(CUtensorMap& map, const void* p, int64_t rows, int64_t K, int box_rows)
+// `rows` rows of `row_bytes` bytes; boxes of `box_bytes` by `box_rows`, zeros outside the matrix.
+cudaError_t bytes_map(CUtensorMap& map, const void* p, int64_t rows, int64_t row_bytes,
+                      int box_bytes, int box_rows, CUtensorMapSwizzle swizzle)
 {
     EncodeTiled fn = nullptr;
     const cudaError_t e = encoder(fn);
     if (e != cudaSuccess)
         return e;
-    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(K / 2), static_cast<cuuint64_t>(rows)};
-    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(K / 2)};
-    const cuuint32_t box[2] = {kStepBytes, static_cast<cuuint32_t>(box_rows)};
+    const cuuint64_t dims[2] = {static_cast<cuuint64_t>(row_bytes), static_cast<cuuint64_t>(rows)};
+    const cuuint64_t strides[1] = {static_cast<cuuint64_t>(row_bytes)};
+    const cuuint32_t box[2] = {static_cast<cuuint32_t>(box_bytes),
+                               static_cast<cuuint32_t>(box_rows)};
     const cuuint32_t one[2] = {1, 1};
     const CUresult r =
         fn(&map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(p), dims, strides, box, one,
-           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+           CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
+// A 4-bit matrix: its codes in boxes of `box_rows` rows, and its scale tiles as rows of 256 bytes, in
+// boxes of four (the two tiles of a step).
+cudaError_t matrix_maps(CUtensorMap& codes, CUtensorMap& scales, const void* p, const void* sp,
+                        int64_t rows, int64_t K, int box_rows)
+{
+    const cudaError_t e =
+        bytes_map(codes, p, rows, K / 2, kStepBytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
+    if (e != cudaSuccess)
+        return e;
+    const int64_t tiles = (rows + 127) / 128 * ((K + 127) / 128);
+    return bytes_map(scales, sp, tiles * 2, 256, 256, 4, CU_TENSOR_MAP_SWIZZLE_NONE);
+}
+
+template <typename K, typename... Args>
+cudaError_t launch_clusters(K kern, int grid, int cluster, int threads, int smem,
+                            cudaStream_t stream, const Args&... args)
+{
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = static_cast<size_t>(smem);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 2;
+    return cudaLaunchKernelEx(&cfg, kern, args...);
+}
+
+template <typename T, int BN>
+cudaError_t launch_pair(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
+{
+    using P = Pair<BN>;
+    static PerDeviceInt ready;
+    int v = 0;
+    cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
+        n = 1;
+        return cudaFuncSetAttribute(pair_kernel<T, BN>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    P::kSmemBytes);
+    });
+    if (e != cudaSuccess)
+        return e;
+    Maps maps;
+    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, 128)) != cudaSuccess ||
+        (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, BN / 2)) != cudaSuccess)
+        return e;
+    const int64_t tiles_m = (a.M + 255) / 256, tiles = tiles_m * ((a.N + BN - 1) / BN);
+    if (tiles > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const int pairs = static_cast<int>(tiles < dev.sms / 2 ? tiles : dev.sms / 2);
+    return launch_clusters(pair_kernel<T, BN>, 2 * pairs, 2, kPairThreads, P::kSmemBytes, stream, a,
+                           maps, static_cast<int>(tiles_m), static_cast<int>(tiles));
+}
+
 template <typename T>
-cudaError_t launch(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
+cudaError_t launch_few(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
     static PerDeviceInt ready;
     int v = 0;
     cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
         n = 1;
-        return cudaFuncSetAttribute(matmul_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    kSmemBytes);
+        return cudaFuncSetAttribute(few_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    kSmemMax - 1024);
     });
     if (e != cudaSuccess)
         return e;
+    Few f;
+    f.NX = 16;
+    while (f.NX < a.M)
+        f.NX *= 2;
+    f.stage_bytes = kTileBytes + 2 * kScaleBytes + f.NX * kStepBytes;
+    // parts of K until the GPU is full: they depend on N and K alone, so that a row's result does
+    // not depend on the rows beside it
+    const int64_t tiles = (a.N + 127) / 128, steps = (a.K + kStepK - 1) / kStepK;
+    f.split = 1;
+    while (f.split < 8 && 2 * f.split * tiles <= 152 && 2 * f.split <= steps)
+        f.split *= 2;
+    const int most = static_cast<int>((steps + f.split - 1) / f.split);
+    f.stages = (kSmemMax - 4096) / f.stage_bytes;
+    f.stages = f.stages > kFewMaxStages ? kFewMaxStages : f.stages;
+    f.stages = f.stages > most ? most : f.stages;
+    // the parts to be joined take the ring's place
+    int smem = f.stages * f.stage_bytes;
+    if (f.split > 1 && smem < f.NX * 512)
+        smem = f.NX * 512;
+    // more than half of an SM's shared memory: two CTAs that wait for one another's tensor memory
+    // and for the rest of their clusters would never end
+    if (smem < kSmemMax / 2 + 2048)
+        smem = kSmemMax / 2 + 2048;
     Maps maps;
-    if ((e = rows_map(maps.a, a.a, a.M, a.K, kBM)) != cudaSuccess ||
-        (e = rows_map(maps.b, a.b, a.N, a.K, kBN)) != cudaSuccess)
+    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, f.NX)) != cudaSuccess ||
+        (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, 128)) != cudaSuccess)
         return e;
-    const dim3 grid(static_cast<unsigned>((a.M + kBM - 1) / kBM),
-                    static_cast<unsigned>((a.N + kBN - 1) / kBN));
-    return launch_dependent(matmul_kernel<T>, grid, kThreads, kSmemBytes, stream, a, maps);
+    return launch_clusters(few_kernel<T>, static_cast<int>(tiles * f.split), f.split, kFewThreads,
+                           smem + 1024, stream, a, maps, f);
+}
+
+template <typename T>
+cudaError_t launch(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
+{
+    if (a.M <= 128)
+        return launch_few<T>(a, dev, stream);
+    // half as wide tiles where the wide ones leave SMs without work
+    const int64_t wide = (a.M + 255) / 256 * ((a.N + 255) / 256);
+    return wide <= dev.sms / 4 ? launch_pair<T, 128>(a, dev, stream)
+                               : launch_pair<T, 256>(a, dev, stream);
 }
 
 }  // namespace
