@@ -39,10 +39,10 @@ struct Mxfp4MatmulArgs {
     int64_t N;
     int64_t K;
     int f16;
+    bool wide;            // set by the launcher: rows of out and residual start on 32 bytes
 };
 
-cudaError_t launch_mxfp4_matmul(const Mxfp4MatmulArgs& a, const DeviceInfo& dev,
-                                cudaStream_t stream);
+cudaError_t launch_mxfp4_matmul(Mxfp4MatmulArgs a, const DeviceInfo& dev, cudaStream_t stream);
 cudaError_t mxfp4_matmul_error(unsigned* bits, bool clear);
 
 }  // namespace rmsmod

@@ -8,10 +8,12 @@
 // products of 64 values.
 //
 // pair_kernel (more than 128 rows of a): two CTAs of a cluster share a 256 x BN tile
-// (cta_group::2), each with its 128 rows of a and half of b's rows, so that a step takes 32 KB
-// per SM from L2 where a CTA of its own would take 48: at this type's rate the products ask for more
-// than an SM's share of L2 otherwise.  Persistent; eight warps take a finished accumulator into
-// registers, free it for the next tile's products and finish their rows beside them.
+// (cta_group::2), each with its 128 rows of a and half of b's rows, so that a step takes 28 KB
+// per SM from L2 (BN = 192) where a CTA of its own would take 40: at this type's rate the products ask
+// for more than an SM's share of L2 otherwise.  Persistent, with two accumulators: eight warps finish
+// one tile's rows while the next tile's products run.  Two accumulators and the scales fit tensor
+// memory's 512 columns up to BN = 192; one of 256 columns, freed early, measured 140 us where this
+// takes 100 (4216 x 16384 x 4096): its products wait for the rows.
 //
 // few_kernel (up to 128 rows of a, where reading b is what counts): b's rows take the 128-row side of
 // the instruction, a's rows the other.  A cluster of up to eight CTAs splits K, and joins its parts in
@@ -76,21 +78,31 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar)
                  : "memory");
 }
 
-// mbar_wait that also orders what the other CTA did before its arrival.
+__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
+{
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(bar), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// mbar_wait that also orders what the other CTA did before its arrival.  The clock is read once for
+// many tries: its reading would delay every step.
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
 {
+    for (int i = 0; i < 32; ++i)
+        if (mbar_try_wait_cluster(bar, parity))
+            return true;
     const unsigned long long t0 = global_ns();
     for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n\t.reg .pred p;\n\t"
-            "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-            "selp.u32 %0, 1, 0, p;\n\t}"
-            : "=r"(ok)
-            : "r"(bar), "r"(parity)
-            : "memory");
-        if (ok)
-            return true;
+        for (int i = 0; i < 32; ++i)
+            if (mbar_try_wait_cluster(bar, parity))
+                return true;
         if (global_ns() - t0 > kWaitLimitNs)
             return false;
     }
@@ -255,7 +267,7 @@ __host__ __device__ constexpr uint32_t instruction(int M, int N)
 // takes two of a column's four scales.
 template <bool PAIR, int B_TILES>
 __device__ __forceinline__ void step_products(uint32_t acc, uint32_t sfa_col, uint32_t sfb_col,
-                                              uint32_t sa, uint32_t sb, uint32_t sfa, uint32_t sfb,
+                                              uint32_t sfb_at, uint32_t sa, uint32_t sb, uint32_t sfa, uint32_t sfb,
                                               uint32_t idesc, int parts, bool first)
 {
 #pragma unroll
@@ -273,7 +285,7 @@ __device__ __forceinline__ void step_products(uint32_t acc, uint32_t sfa_col, ui
             const uint32_t id = (p & 1) * 2u;
             mma_mxf4<PAIR>(acc, operand_desc(sa + p * 32), operand_desc(sb + p * 32),
                            idesc | (id << 4) | (id << 29), sfa_col + (p >> 1) * 4,
-                           sfb_col + (p >> 1) * (4 * B_TILES), !first || p > 0);
+                           sfb_col + (p >> 1) * (4 * B_TILES) + sfb_at, !first || p > 0);
         }
 }
 
@@ -295,25 +307,54 @@ struct Maps {
 template <int BN>
 struct Pair {
     static constexpr int kBBytes = BN / 2 * kStepBytes;
-    static constexpr int kBTiles = BN / 128;
+    static constexpr int kBTiles = (BN + 127) / 128;  // 128-row scale tiles that a tile of b touches
     static constexpr int kStageBytes = kTileBytes + kBBytes + kScaleBytes * (1 + kBTiles);
     static constexpr int kStages = (kSmemMax - 2048) / kStageBytes;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-    static constexpr int kAccs = BN == 256 ? 1 : 2;  // accumulators that fit beside the scales
-    static constexpr uint32_t kSfaCol = 256;
+    static constexpr int kAccs = 2;
+    static constexpr uint32_t kSfaCol = kAccs * BN;
     static constexpr uint32_t kSfbCol = kSfaCol + 8;
     static constexpr int kCols = BN / 2;  // of an accumulator row in one epilogue thread
+    static_assert(kSfbCol + 8 * kBTiles <= 512, "tensor memory");
     static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
 constexpr int kEpilogueWarps = 8;
 constexpr int kPairThreads = 64 + 32 * kEpilogueWarps;  // producer, issuer, epilogue
 
+// 32 bytes (a whole sector) at once where rows start on 32 bytes, else 16 and 16.
+__device__ __forceinline__ void load_pair(const uint4* p, bool both, bool wide, uint4* v)
+{
+    if (wide) {
+        asm volatile("ld.global.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                     : "=r"(v[0].x), "=r"(v[0].y), "=r"(v[0].z), "=r"(v[0].w), "=r"(v[1].x),
+                       "=r"(v[1].y), "=r"(v[1].z), "=r"(v[1].w)
+                     : "l"(p));
+    } else {
+        v[0] = ld_stream(p);
+        if (both)
+            v[1] = ld_stream(p + 1);
+    }
+}
+
+__device__ __forceinline__ void store_pair(uint4* p, bool both, bool wide, const uint4 (&v)[2])
+{
+    if (wide) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(v[0].x),
+                     "r"(v[0].y), "r"(v[0].z), "r"(v[0].w), "r"(v[1].x), "r"(v[1].y), "r"(v[1].z),
+                     "r"(v[1].w)
+                     : "memory");
+    } else {
+        st_stream(p, v[0]);
+        if (both)
+            st_stream(p + 1, v[1]);
+    }
+}
+
 // Eight columns of one row.
 template <typename T>
-__device__ __forceinline__ uint4 finish8(const uint32_t* acc, const uint4* bias, const uint4* gate,
-                                         const uint4* residual, const uint4& bv, const uint4& gv,
-                                         const uint4& rv)
+__device__ __forceinline__ uint4 finish8(const uint32_t* acc, bool bias, bool gate, bool residual,
+                                         const uint4& bv, const uint4& gv, const uint4& rv)
 {
     uint4 o;
 #pragma unroll
@@ -432,6 +473,8 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 if (!broken)
                     gave_up(mbar_wait_cluster(smem_addr(&acc_empty[acc]), acc_phase));
                 after_sync();
+                // where in its scale tiles the tile of b begins
+                const uint32_t sfb_at = tile / tiles_m * BN % 128 / 32;
                 for (int t = 0; t < steps; ++t) {
                     if (!broken)
                         gave_up(mbar_wait_cluster(smem_addr(&full[s]), phase));
@@ -439,7 +482,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const uint32_t sa = ring + s * P::kStageBytes, sb = sa + kTileBytes;
                     const uint32_t sfa = sb + P::kBBytes, sfb = sfa + kScaleBytes;
                     step_products<true, P::kBTiles>(tmem + acc * BN, tmem + P::kSfaCol,
-                                                    tmem + P::kSfbCol, sa, sb, sfa, sfb, kIdesc,
+                                                    tmem + P::kSfbCol, sfb_at, sa, sb, sfa, sfb, kIdesc,
                                                     parts_of(a.K, t), t == 0);
                     commit<true>(smem_addr(&empty[s]));
                     if (++s == P::kStages) {
@@ -466,41 +509,58 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int tile = pair; tile < tiles; tile += pairs) {
             if (!broken)
                 gave_up(mbar_wait_cluster(smem_addr(&acc_full[acc]), phase));
-            __syncwarp();
-            after_sync();
-            uint32_t v[P::kCols];
+            const int64_t m = static_cast<int64_t>(tile % tiles_m) * 256 + rank * 128 +
+                              quarter * 32 + lane;
+            const int64_t n0 = (static_cast<int64_t>(tile / tiles_m) * BN + half * P::kCols) / 8;
+            const int64_t gate_at = (gate && m < a.M ? m / a.S * a.gate_bstride : 0) / 8;
+            const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN +
+                                  half * P::kCols;
+            // 32 columns at a time
+#pragma unroll 1
+            for (int c = 0; c < P::kCols / 32; ++c) {
+                uint32_t v[32];
+                __syncwarp();
+                after_sync();
+                tmem_load32(from + 32 * c, v);
+                // what they take beside the accumulators, on its way meanwhile
+                const int64_t n = n0 + 4 * c;
+                uint4 bv[4], gv[4], rv[4];
+                if (m < a.M) {
 #pragma unroll
-            for (int c = 0; c < P::kCols; c += 32)
-                tmem_load32(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN +
-                                half * P::kCols + c,
-                            v + c);
-            tmem_loads_done();
-            before_sync();
-            __syncwarp();
-            // the accumulator may take the next tile
-            if (lane == 0)
-                arrive_remote(in_cta(smem_addr(&acc_empty[acc]), 0));
+                    for (int k = 0; k < 4; k += 2)
+                        if (residual && n + k < Nv)
+                            load_pair(residual + m * Nv + n + k, n + k + 1 < Nv, a.wide, rv + k);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        if (bias && n + k < Nv)
+                            bv[k] = ld_cached(bias + n + k);
+                        if (gate && n + k < Nv)
+                            gv[k] = ld_cached(gate + gate_at + n + k);
+                    }
+                }
+                tmem_loads_done();
+                if (c + 1 == P::kCols / 32) {  // the accumulator may take the tile after the next
+                    before_sync();
+                    __syncwarp();
+                    if (lane == 0)
+                        arrive_remote(in_cta(smem_addr(&acc_empty[acc]), 0));
+                }
+                if (m < a.M)
+#pragma unroll
+                    for (int k = 0; k < 4; k += 2) {
+                        uint4 o[2];
+#pragma unroll
+                        for (int i = 0; i < 2; ++i)
+                            o[i] = finish8<T>(v + 8 * (k + i), bias, gate, residual, bv[k + i],
+                                              gv[k + i], rv[k + i]);
+                        if (n + k < Nv)
+                            store_pair(static_cast<uint4*>(a.out) + m * Nv + n + k, n + k + 1 < Nv,
+                                       a.wide, o);
+                    }
+            }
             if (++acc == P::kAccs) {
                 acc = 0;
                 phase ^= 1u;
-            }
-            const int64_t m = static_cast<int64_t>(tile % tiles_m) * 256 + rank * 128 +
-                              quarter * 32 + lane;
-            const int64_t n0 = static_cast<int64_t>(tile / tiles_m) * BN + half * P::kCols;
-            if (m >= a.M)
-                continue;
-            const int64_t gate_at = (gate ? m / a.S * a.gate_bstride : 0) / 8;
-#pragma unroll
-            for (int c = 0; c < P::kCols / 8; ++c) {
-                const int64_t n = n0 / 8 + c;
-                if (n < Nv) {
-                    const uint4 zero = make_uint4(0u, 0u, 0u, 0u);
-                    const uint4 bv = bias ? ld_cached(bias + n) : zero;
-                    const uint4 gv = gate ? ld_cached(gate + gate_at + n) : zero;
-                    const uint4 rv = residual ? ld_stream(residual + m * Nv + n) : zero;
-                    st_stream(static_cast<uint4*>(a.out) + m * Nv + n,
-                              finish8<T>(v + 8 * c, bias, gate, residual, bv, gv, rv));
-                }
             }
         }
     }
@@ -600,7 +660,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 wait(smem_addr(&full[s]), phase);
                 after_sync();
                 const uint32_t sw = ring + s * f.stage_bytes, sfw = sw + kTileBytes;
-                step_products<false, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, sw,
+                step_products<false, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, 0u, sw,
                                         sfw + 2 * kScaleBytes, sfw, sfw + kScaleBytes, idesc,
                                         parts_of(a.K, t), t == begin);
                 commit<false>(smem_addr(&empty[s]));
@@ -838,17 +898,18 @@ cudaError_t launch(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t
 {
     if (a.M <= 128)
         return launch_few<T>(a, dev, stream);
-    // half as wide tiles where the wide ones leave SMs without work
-    const int64_t wide = (a.M + 255) / 256 * ((a.N + 255) / 256);
-    return wide <= dev.sms / 4 ? launch_pair<T, 128>(a, dev, stream)
-                               : launch_pair<T, 256>(a, dev, stream);
+    // narrower tiles where the wide ones leave SMs without work
+    const int64_t wide = (a.M + 255) / 256 * ((a.N + 191) / 192);
+    return wide <= dev.sms / 3 ? launch_pair<T, 128>(a, dev, stream)
+                               : launch_pair<T, 192>(a, dev, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_mxfp4_matmul(const Mxfp4MatmulArgs& a, const DeviceInfo& dev,
-                                cudaStream_t stream)
+cudaError_t launch_mxfp4_matmul(Mxfp4MatmulArgs a, const DeviceInfo& dev, cudaStream_t stream)
 {
+    const auto on32 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; };
+    a.wide = a.N % 16 == 0 && on32(a.out) && on32(a.residual);
     return a.f16 ? launch<__half>(a, dev, stream) : launch<__nv_bfloat16>(a, dev, stream);
 }
 
