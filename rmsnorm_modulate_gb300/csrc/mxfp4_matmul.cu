@@ -3,7 +3,7 @@
 //   acc[m, n] = sum_k a[m, k] * b[n, k]          (fp32 accumulators in tensor memory)
 //   out       = R(residual + gate_b * (acc + bias)),  one rounding
 //
-// A step is 256 values (128 bytes) of every row of a tile, brought by TMA (128-byte swizzle), and two
+// Operand tiles are 256 values (128 bytes) of every row, brought by TMA (128-byte swizzle), with two
 // scale tiles for each 128 rows; one thread copies the scales to tensor memory and starts four
 // products of 64 values.
 //
@@ -78,30 +78,18 @@ __device__ __forceinline__ void arrive_remote(uint32_t bar)
                  : "memory");
 }
 
-__device__ __forceinline__ bool mbar_try_wait_cluster(uint32_t bar, uint32_t parity)
-{
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(bar), "r"(parity)
-        : "memory");
-    return ok != 0;
-}
-
-// mbar_wait that also orders what the other CTA did before its arrival.  The clock is read once for
-// many tries: its reading would delay every step.
-__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
+// mbar_wait for a loop of short steps: the clock is read once for many tries.  (Copies, products and
+// tensor-memory reads order themselves: the barriers need no acquire beyond the CTA's, whose cluster
+// form costs each step some hundred cycles.)
+__device__ __forceinline__ bool step_wait(uint32_t bar, uint32_t parity)
 {
     for (int i = 0; i < 32; ++i)
-        if (mbar_try_wait_cluster(bar, parity))
+        if (mbar_try_wait(bar, parity))
             return true;
     const unsigned long long t0 = global_ns();
     for (;;) {
         for (int i = 0; i < 32; ++i)
-            if (mbar_try_wait_cluster(bar, parity))
+            if (mbar_try_wait(bar, parity))
                 return true;
         if (global_ns() - t0 > kWaitLimitNs)
             return false;
@@ -263,37 +251,41 @@ __host__ __device__ constexpr uint32_t instruction(int M, int N)
            (static_cast<uint32_t>(M / 16) << 24);
 }
 
-// The products of one step.  Scales: two tiles (of four blocks each) for each 128 rows; a product
-// takes two of a column's four scales.
-template <bool PAIR, int B_TILES>
+// The products of one step of SUBS * 256 values: `parts` of 64 values each, four to an operand tile.
+// Scales: two tiles (of four blocks each) for each 128 rows and 256 values; a product takes two of a
+// column's four scales.  b_tile: bytes between b's operand tiles, b_scales: between its row tiles' scales.
+template <bool PAIR, int B_TILES, int SUBS>
 __device__ __forceinline__ void step_products(uint32_t acc, uint32_t sfa_col, uint32_t sfb_col,
-                                              uint32_t sfb_at, uint32_t sa, uint32_t sb, uint32_t sfa, uint32_t sfb,
+                                              uint32_t sfb_at, uint32_t sa, uint32_t sb,
+                                              uint32_t b_tile, uint32_t sfa, uint32_t sfb,
                                               uint32_t idesc, int parts, bool first)
 {
 #pragma unroll
-    for (int h = 0; h < 2; ++h)
+    for (int h = 0; h < 2 * SUBS; ++h)
         if (2 * h < parts) {
             copy_scales<PAIR>(sfa_col + h * 4, scale_desc(sfa + h * 512));
 #pragma unroll
             for (int i = 0; i < B_TILES; ++i)
                 copy_scales<PAIR>(sfb_col + h * (4 * B_TILES) + i * 4,
-                                  scale_desc(sfb + i * kScaleBytes + h * 512));
+                                  scale_desc(sfb + i * (SUBS * kScaleBytes) + h * 512));
         }
 #pragma unroll
-    for (int p = 0; p < 4; ++p)
+    for (int p = 0; p < 4 * SUBS; ++p)
         if (p < parts) {
             const uint32_t id = (p & 1) * 2u;
-            mma_mxf4<PAIR>(acc, operand_desc(sa + p * 32), operand_desc(sb + p * 32),
+            mma_mxf4<PAIR>(acc, operand_desc(sa + (p >> 2) * kTileBytes + (p & 3) * 32),
+                           operand_desc(sb + (p >> 2) * b_tile + (p & 3) * 32),
                            idesc | (id << 4) | (id << 29), sfa_col + (p >> 1) * 4,
                            sfb_col + (p >> 1) * (4 * B_TILES) + sfb_at, !first || p > 0);
         }
 }
 
-// Products that the last step has: 64 values each.
+// Products (of 64 values) of step t.
+template <int SUBS>
 __device__ __forceinline__ int parts_of(int64_t K, int t)
 {
-    const int64_t left = K - static_cast<int64_t>(t) * kStepK;
-    return left >= kStepK ? 4 : static_cast<int>((left + 63) / 64);
+    const int64_t left = K - static_cast<int64_t>(t) * (SUBS * kStepK);
+    return left >= SUBS * kStepK ? 4 * SUBS : static_cast<int>((left + 63) / 64);
 }
 
 struct Maps {
@@ -304,18 +296,23 @@ struct Maps {
 // more than 128 rows
 // ---------------------------------------------------------------------------
 
+// Two operand tiles to a step: waiting for one and passing it on takes the issuing thread as long as
+// several products, 470 cycles of 660 with one tile to a step.
+constexpr int kPairSubs = 2;
+
 template <int BN>
 struct Pair {
-    static constexpr int kBBytes = BN / 2 * kStepBytes;
+    static constexpr int kBBytes = BN / 2 * kStepBytes;  // of one operand tile
     static constexpr int kBTiles = (BN + 127) / 128;  // 128-row scale tiles that a tile of b touches
-    static constexpr int kStageBytes = kTileBytes + kBBytes + kScaleBytes * (1 + kBTiles);
+    static constexpr int kStageBytes =
+        kPairSubs * (kTileBytes + kBBytes + kScaleBytes * (1 + kBTiles));
     static constexpr int kStages = (kSmemMax - 2048) / kStageBytes;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     static constexpr int kAccs = 2;
     static constexpr uint32_t kSfaCol = kAccs * BN;
-    static constexpr uint32_t kSfbCol = kSfaCol + 8;
+    static constexpr uint32_t kSfbCol = kSfaCol + 8 * kPairSubs;
     static constexpr int kCols = BN / 2;  // of an accumulator row in one epilogue thread
-    static_assert(kSfbCol + 8 * kBTiles <= 512, "tensor memory");
+    static_assert(kSfbCol + 8 * kPairSubs * kBTiles <= 512, "tensor memory");
     static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
@@ -393,7 +390,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const uint32_t rank = cluster_rank();
     const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
-    const int steps = static_cast<int>((a.K + kStepK - 1) / kStepK);
+    const int steps = static_cast<int>((a.K + kPairSubs * kStepK - 1) / (kPairSubs * kStepK));
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
 
     if (threadIdx.x == 0) {
@@ -434,20 +431,26 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 const int n0 = tile / tiles_m * BN;
                 for (int t = 0; t < steps; ++t) {
                     if (!broken)
-                        gave_up(mbar_wait_cluster(smem_addr(&empty[s]), phase));
+                        gave_up(step_wait(smem_addr(&empty[s]), phase));
                     const uint32_t bar = in_cta(smem_addr(&full[s]), 0);
                     const uint32_t dst = ring + s * P::kStageBytes;
                     if (rank == 0)
                         mbar_expect_tx(smem_addr(&full[s]), 2 * P::kStageBytes);
-                    tma_box<true>(dst, &maps.a, t * kStepBytes, m0, bar);
-                    tma_box<true>(dst + kTileBytes, &maps.b, t * kStepBytes,
-                                  n0 + static_cast<int>(rank) * (BN / 2), bar);
-                    const uint32_t sf = dst + kTileBytes + P::kBBytes;
-                    tma_box<true>(sf, &maps.a_scales, 0, 2 * (m0 / 128 * block_tiles + 2 * t), bar);
+                    // (operand tiles past K: zeros, which nothing reads)
+#pragma unroll
+                    for (int h = 0; h < kPairSubs; ++h) {
+                        const int x = (kPairSubs * t + h) * kStepBytes;
+                        tma_box<true>(dst + h * kTileBytes, &maps.a, x, m0, bar);
+                        tma_box<true>(dst + kPairSubs * kTileBytes + h * P::kBBytes, &maps.b, x,
+                                      n0 + static_cast<int>(rank) * (BN / 2), bar);
+                    }
+                    const uint32_t sf = dst + kPairSubs * (kTileBytes + P::kBBytes);
+                    tma_box<true>(sf, &maps.a_scales, 0,
+                                  2 * (m0 / 128 * block_tiles + 2 * kPairSubs * t), bar);
 #pragma unroll
                     for (int i = 0; i < P::kBTiles; ++i)
-                        tma_box<true>(sf + (1 + i) * kScaleBytes, &maps.b_scales, 0,
-                                      2 * ((n0 / 128 + i) * block_tiles + 2 * t), bar);
+                        tma_box<true>(sf + (1 + i) * kPairSubs * kScaleBytes, &maps.b_scales, 0,
+                                      2 * ((n0 / 128 + i) * block_tiles + 2 * kPairSubs * t), bar);
                     if (++s == P::kStages) {
                         s = 0;
                         phase ^= 1u;
@@ -457,7 +460,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             // no arrival is left on its way when this CTA's shared memory goes
             for (int i = 0; i < P::kStages; ++i) {
                 if (!broken)
-                    gave_up(mbar_wait_cluster(smem_addr(&empty[s]), phase));
+                    gave_up(step_wait(smem_addr(&empty[s]), phase));
                 if (++s == P::kStages) {
                     s = 0;
                     phase ^= 1u;
@@ -471,19 +474,21 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             uint32_t phase = 0, acc_phase = 1;
             for (int tile = pair; tile < tiles; tile += pairs) {
                 if (!broken)
-                    gave_up(mbar_wait_cluster(smem_addr(&acc_empty[acc]), acc_phase));
+                    gave_up(step_wait(smem_addr(&acc_empty[acc]), acc_phase));
                 after_sync();
                 // where in its scale tiles the tile of b begins
                 const uint32_t sfb_at = tile / tiles_m * BN % 128 / 32;
                 for (int t = 0; t < steps; ++t) {
                     if (!broken)
-                        gave_up(mbar_wait_cluster(smem_addr(&full[s]), phase));
+                        gave_up(step_wait(smem_addr(&full[s]), phase));
                     after_sync();
-                    const uint32_t sa = ring + s * P::kStageBytes, sb = sa + kTileBytes;
-                    const uint32_t sfa = sb + P::kBBytes, sfb = sfa + kScaleBytes;
-                    step_products<true, P::kBTiles>(tmem + acc * BN, tmem + P::kSfaCol,
-                                                    tmem + P::kSfbCol, sfb_at, sa, sb, sfa, sfb, kIdesc,
-                                                    parts_of(a.K, t), t == 0);
+                    const uint32_t sa = ring + s * P::kStageBytes;
+                    const uint32_t sb = sa + kPairSubs * kTileBytes;
+                    const uint32_t sfa = sb + kPairSubs * P::kBBytes;
+                    step_products<true, P::kBTiles, kPairSubs>(
+                        tmem + acc * BN, tmem + P::kSfaCol, tmem + P::kSfbCol, sfb_at, sa, sb,
+                        P::kBBytes, sfa, sfa + kPairSubs * kScaleBytes, kIdesc,
+                        parts_of<kPairSubs>(a.K, t), t == 0);
                     commit<true>(smem_addr(&empty[s]));
                     if (++s == P::kStages) {
                         s = 0;
@@ -508,7 +513,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         uint32_t phase = 0;
         for (int tile = pair; tile < tiles; tile += pairs) {
             if (!broken)
-                gave_up(mbar_wait_cluster(smem_addr(&acc_full[acc]), phase));
+                gave_up(step_wait(smem_addr(&acc_full[acc]), phase));
             const int64_t m = static_cast<int64_t>(tile % tiles_m) * 256 + rank * 128 +
                               quarter * 32 + lane;
             const int64_t n0 = (static_cast<int64_t>(tile / tiles_m) * BN + half * P::kCols) / 8;
@@ -660,9 +665,9 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 wait(smem_addr(&full[s]), phase);
                 after_sync();
                 const uint32_t sw = ring + s * f.stage_bytes, sfw = sw + kTileBytes;
-                step_products<false, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, 0u, sw,
-                                        sfw + 2 * kScaleBytes, sfw, sfw + kScaleBytes, idesc,
-                                        parts_of(a.K, t), t == begin);
+                step_products<false, 1, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, 0u, sw,
+                                           sfw + 2 * kScaleBytes, 0u, sfw, sfw + kScaleBytes, idesc,
+                                           parts_of<1>(a.K, t), t == begin);
                 commit<false>(smem_addr(&empty[s]));
                 if (++s == f.stages) {
                     s = 0;
@@ -792,16 +797,16 @@ cudaError_t bytes_map(CUtensorMap& map, const void* p, int64_t rows, int64_t row
 }
 
 // A 4-bit matrix: its codes in boxes of `box_rows` rows, and its scale tiles as rows of 256 bytes, in
-// boxes of four (the two tiles of a step).
+// boxes of the tiles of `subs` * 256 values (two for each 256).
 cudaError_t matrix_maps(CUtensorMap& codes, CUtensorMap& scales, const void* p, const void* sp,
-                        int64_t rows, int64_t K, int box_rows)
+                        int64_t rows, int64_t K, int box_rows, int subs)
 {
     const cudaError_t e =
         bytes_map(codes, p, rows, K / 2, kStepBytes, box_rows, CU_TENSOR_MAP_SWIZZLE_128B);
     if (e != cudaSuccess)
         return e;
     const int64_t tiles = (rows + 127) / 128 * ((K + 127) / 128);
-    return bytes_map(scales, sp, tiles * 2, 256, 256, 4, CU_TENSOR_MAP_SWIZZLE_NONE);
+    return bytes_map(scales, sp, tiles * 2, 256, 256, 4 * subs, CU_TENSOR_MAP_SWIZZLE_NONE);
 }
 
 template <typename K, typename... Args>
@@ -839,8 +844,10 @@ cudaError_t launch_pair(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStr
     if (e != cudaSuccess)
         return e;
     Maps maps;
-    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, 128)) != cudaSuccess ||
-        (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, BN / 2)) != cudaSuccess)
+    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, 128, kPairSubs)) !=
+            cudaSuccess ||
+        (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, BN / 2, kPairSubs)) !=
+            cudaSuccess)
         return e;
     const int64_t tiles_m = (a.M + 255) / 256, tiles = tiles_m * ((a.N + BN - 1) / BN);
     if (tiles > INT32_MAX)
@@ -886,8 +893,10 @@ cudaError_t launch_few(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStre
     if (smem < kSmemMax / 2 + 2048)
         smem = kSmemMax / 2 + 2048;
     Maps maps;
-    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, f.NX)) != cudaSuccess ||
-        (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, 128)) != cudaSuccess)
+    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, f.NX, 1)) !=
+            cudaSuccess ||
+        (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, 128, 1)) !=
+            cudaSuccess)
         return e;
     return launch_clusters(few_kernel<T>, static_cast<int>(tiles * f.split), f.split, kFewThreads,
                            smem + 1024, stream, a, maps, f);
