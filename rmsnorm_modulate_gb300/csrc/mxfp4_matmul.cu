@@ -8,12 +8,12 @@
 // products of 64 values.
 //
 // pair_kernel (more than 128 rows of a): two CTAs of a cluster share a 256 x BN tile
-// (cta_group::2), each with its 128 rows of a and half of b's rows, so that a step takes 28 KB
-// per SM from L2 (BN = 192) where a CTA of its own would take 40: at this type's rate the products ask
-// for more than an SM's share of L2 otherwise.  Persistent, with two accumulators: eight warps finish
-// one tile's rows while the next tile's products run.  Two accumulators and the scales fit tensor
-// memory's 512 columns up to BN = 192; one of 256 columns, freed early, measured 140 us where this
-// takes 100 (4216 x 16384 x 4096): its products wait for the rows.
+// (cta_group::2), each with its 128 rows of a and half of b's rows.  What bounds it is shared memory:
+// 256 values of K take 512 cycles of products (BN = 256), in which the copies write 35 KB and the
+// products read 32 KB of an SM's 128 bytes a cycle (BN = 192: 31.7 and 28 KB in 384 cycles, measured
+// 93 us where this takes NEW at 4214 x 4096 x 16384; a CTA alone would write half as much again).
+// Persistent, with two accumulators: eight warps finish one tile's rows while the next tile's products
+// run.
 //
 // few_kernel (up to 128 rows of a, where reading b is what counts): b's rows take the 128-row side of
 // the instruction, a's rows the other.  A cluster of up to eight CTAs splits K, and joins its parts in
@@ -251,32 +251,31 @@ __host__ __device__ constexpr uint32_t instruction(int M, int N)
            (static_cast<uint32_t>(M / 16) << 24);
 }
 
-// The products of one step of SUBS * 256 values: `parts` of 64 values each, four to an operand tile.
-// Scales: two tiles (of four blocks each) for each 128 rows and 256 values; a product takes two of a
-// column's four scales.  b_tile: bytes between b's operand tiles, b_scales: between its row tiles' scales.
+// The products of one step of SUBS * 256 values: `parts` of 64 values each, four to an operand tile
+// (b's are b_tile bytes apart).  Scales: two tiles (of four blocks each) for each 128 rows and 256
+// values, copied before each four products; a product takes two of a column's four scales.
 template <bool PAIR, int B_TILES, int SUBS>
 __device__ __forceinline__ void step_products(uint32_t acc, uint32_t sfa_col, uint32_t sfb_col,
-                                              uint32_t sfb_at, uint32_t sa, uint32_t sb,
+                                              uint32_t sa, uint32_t sb,
                                               uint32_t b_tile, uint32_t sfa, uint32_t sfb,
                                               uint32_t idesc, int parts, bool first)
 {
 #pragma unroll
-    for (int h = 0; h < 2 * SUBS; ++h)
-        if (2 * h < parts) {
-            copy_scales<PAIR>(sfa_col + h * 4, scale_desc(sfa + h * 512));
-#pragma unroll
-            for (int i = 0; i < B_TILES; ++i)
-                copy_scales<PAIR>(sfb_col + h * (4 * B_TILES) + i * 4,
-                                  scale_desc(sfb + i * (SUBS * kScaleBytes) + h * 512));
-        }
-#pragma unroll
     for (int p = 0; p < 4 * SUBS; ++p)
         if (p < parts) {
+            const int h = p >> 1;  // scale tile
+            if (p % 2 == 0) {
+                copy_scales<PAIR>(sfa_col + h % 2 * 4, scale_desc(sfa + h * 512));
+#pragma unroll
+                for (int i = 0; i < B_TILES; ++i)
+                    copy_scales<PAIR>(sfb_col + h % 2 * (4 * B_TILES) + i * 4,
+                                      scale_desc(sfb + i * (SUBS * kScaleBytes) + h * 512));
+            }
             const uint32_t id = (p & 1) * 2u;
             mma_mxf4<PAIR>(acc, operand_desc(sa + (p >> 2) * kTileBytes + (p & 3) * 32),
                            operand_desc(sb + (p >> 2) * b_tile + (p & 3) * 32),
-                           idesc | (id << 4) | (id << 29), sfa_col + (p >> 1) * 4,
-                           sfb_col + (p >> 1) * (4 * B_TILES) + sfb_at, !first || p > 0);
+                           idesc | (id << 4) | (id << 29), sfa_col + h % 2 * 4,
+                           sfb_col + h % 2 * (4 * B_TILES), !first || p > 0);
         }
 }
 
@@ -303,16 +302,20 @@ constexpr int kPairSubs = 2;
 template <int BN>
 struct Pair {
     static constexpr int kBBytes = BN / 2 * kStepBytes;  // of one operand tile
-    static constexpr int kBTiles = (BN + 127) / 128;  // 128-row scale tiles that a tile of b touches
+    static constexpr int kBTiles = BN / 128;
     static constexpr int kStageBytes =
         kPairSubs * (kTileBytes + kBBytes + kScaleBytes * (1 + kBTiles));
     static constexpr int kStages = (kSmemMax - 2048) / kStageBytes;
     static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
     static constexpr int kAccs = 2;
-    static constexpr uint32_t kSfaCol = kAccs * BN;
-    static constexpr uint32_t kSfbCol = kSfaCol + 8 * kPairSubs;
+    // Two accumulators of 256 columns and the scales are more than tensor memory's 512: the second
+    // one begins in the last 32 columns of the first, which the epilogue reads before the others.
+    static constexpr bool kOverlap = BN == 256;
+    static constexpr uint32_t kAccStep = kOverlap ? BN - 32 : BN;
+    static constexpr uint32_t kSfaCol = kAccStep + BN;
+    static constexpr uint32_t kSfbCol = kSfaCol + 8;
     static constexpr int kCols = BN / 2;  // of an accumulator row in one epilogue thread
-    static_assert(kSfbCol + 8 * kPairSubs * kBTiles <= 512, "tensor memory");
+    static_assert(kSfbCol + 8 * kBTiles <= kPairTmemCols, "tensor memory");
     static_assert(kStageBytes % 1024 == 0, "swizzled tiles start on 1024 bytes");
 };
 
@@ -384,7 +387,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     using P = Pair<BN>;
     extern __shared__ uint8_t raw[];
     __shared__ __align__(8) unsigned long long full[P::kStages], empty[P::kStages];
-    __shared__ __align__(8) unsigned long long acc_full[P::kAccs], acc_empty[P::kAccs];
+    __shared__ __align__(8) unsigned long long acc_full[P::kAccs], acc_empty[P::kAccs], shared_read;
     __shared__ uint32_t tmem_base;
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -402,6 +405,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             mbar_init(smem_addr(&acc_full[s]), 1u);
             mbar_init(smem_addr(&acc_empty[s]), 2u * kEpilogueWarps);
         }
+        mbar_init(smem_addr(&shared_read), kEpilogueWarps);  // half of the warps of each CTA
         mbar_init_fence();
     }
     if (warp == 1)
@@ -471,13 +475,16 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         if (rank == 0 && elect_one()) {
             constexpr uint32_t kIdesc = instruction(256, BN);
             int s = 0, acc = 0;
-            uint32_t phase = 0, acc_phase = 1;
+            uint32_t phase = 0, acc_phase = 1, read_phase = 1;
             for (int tile = pair; tile < tiles; tile += pairs) {
                 if (!broken)
                     gave_up(step_wait(smem_addr(&acc_empty[acc]), acc_phase));
+                if (P::kOverlap) {  // the last tile's part of the columns that both have
+                    if (!broken)
+                        gave_up(step_wait(smem_addr(&shared_read), read_phase));
+                    read_phase ^= 1u;
+                }
                 after_sync();
-                // where in its scale tiles the tile of b begins
-                const uint32_t sfb_at = tile / tiles_m * BN % 128 / 32;
                 for (int t = 0; t < steps; ++t) {
                     if (!broken)
                         gave_up(step_wait(smem_addr(&full[s]), phase));
@@ -486,7 +493,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     const uint32_t sb = sa + kPairSubs * kTileBytes;
                     const uint32_t sfa = sb + kPairSubs * P::kBBytes;
                     step_products<true, P::kBTiles, kPairSubs>(
-                        tmem + acc * BN, tmem + P::kSfaCol, tmem + P::kSfbCol, sfb_at, sa, sb,
+                        tmem + acc * P::kAccStep, tmem + P::kSfaCol, tmem + P::kSfbCol, sa, sb,
                         P::kBBytes, sfa, sfa + kPairSubs * kScaleBytes, kIdesc,
                         parts_of<kPairSubs>(a.K, t), t == 0);
                     commit<true>(smem_addr(&empty[s]));
@@ -518,11 +525,13 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                               quarter * 32 + lane;
             const int64_t n0 = (static_cast<int64_t>(tile / tiles_m) * BN + half * P::kCols) / 8;
             const int64_t gate_at = (gate && m < a.M ? m / a.S * a.gate_bstride : 0) / 8;
-            const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) + acc * BN +
-                                  half * P::kCols;
-            // 32 columns at a time
+            const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
+                                  acc * P::kAccStep + half * P::kCols;
+            // 32 columns at a time, from the side that the other accumulator has too
+            const bool shares = P::kOverlap && half != acc;
 #pragma unroll 1
-            for (int c = 0; c < P::kCols / 32; ++c) {
+            for (int k0 = 0; k0 < P::kCols / 32; ++k0) {
+                const int c = P::kOverlap && acc == 0 ? P::kCols / 32 - 1 - k0 : k0;
                 uint32_t v[32];
                 __syncwarp();
                 after_sync();
@@ -544,11 +553,15 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     }
                 }
                 tmem_loads_done();
-                if (c + 1 == P::kCols / 32) {  // the accumulator may take the tile after the next
+                if (k0 + 1 == P::kCols / 32 || (shares && k0 == 0)) {
                     before_sync();
                     __syncwarp();
-                    if (lane == 0)
-                        arrive_remote(in_cta(smem_addr(&acc_empty[acc]), 0));
+                    if (lane == 0) {
+                        if (shares && k0 == 0)
+                            arrive_remote(in_cta(smem_addr(&shared_read), 0));
+                        if (k0 + 1 == P::kCols / 32)
+                            arrive_remote(in_cta(smem_addr(&acc_empty[acc]), 0));
+                    }
                 }
                 if (m < a.M)
 #pragma unroll
@@ -665,7 +678,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 wait(smem_addr(&full[s]), phase);
                 after_sync();
                 const uint32_t sw = ring + s * f.stage_bytes, sfw = sw + kTileBytes;
-                step_products<false, 1, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, 0u, sw,
+                step_products<false, 1, 1>(tmem, tmem + kFewSfwCol, tmem + kFewSfxCol, sw,
                                            sfw + 2 * kScaleBytes, 0u, sfw, sfw + kScaleBytes, idesc,
                                            parts_of<1>(a.K, t), t == begin);
                 commit<false>(smem_addr(&empty[s]));
@@ -908,9 +921,9 @@ cudaError_t launch(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t
     if (a.M <= 128)
         return launch_few<T>(a, dev, stream);
     // narrower tiles where the wide ones leave SMs without work
-    const int64_t wide = (a.M + 255) / 256 * ((a.N + 191) / 192);
-    return wide <= dev.sms / 3 ? launch_pair<T, 128>(a, dev, stream)
-                               : launch_pair<T, 192>(a, dev, stream);
+    const int64_t wide = (a.M + 255) / 256 * ((a.N + 255) / 256);
+    return wide <= dev.sms / 4 ? launch_pair<T, 128>(a, dev, stream)
+                               : launch_pair<T, 256>(a, dev, stream);
 }
 
 }  // namespace
