@@ -63,51 +63,112 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t rank, float v)
                  : "memory");
 }
 
-// The threads of a CTA that share rows.
+// The threads of a CTA (or of the two CTAs of a cluster) that share rows.
 struct Group {
-    int warps;       // of a group
+    int warps;       // of a group in this CTA
     int index;       // of this group in its CTA
     int warp;        // of this thread in its group
     int lane;
     uint32_t rank;   // of the CTA in its cluster
+    uint32_t bars;   // the group's barriers with the other CTA's warps (kJoint)
 
     __device__ __forceinline__ bool leader() const { return warp == 0 && lane == 0; }
     __device__ __forceinline__ int at(int j) const { return (j * warps + warp) * 32 + lane; }
 };
 
-template <bool CL>
-__device__ __forceinline__ void group_barrier(const Group& g)
+// Who shares a row: a group of one CTA, the one group of each of two CTAs, or one of the groups of
+// each of two CTAs.
+enum Sharing : int { kAlone = 0, kBoth = 1, kJoint = 2 };
+
+constexpr int kGroupBars = 4;
+constexpr uint32_t kGaveUp = 1u << 31;  // among the phases: a wait ran out, no more are made
+
+__device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
 {
-    if (CL)
-        cluster_barrier();
-    else if (g.warps == 1)
-        __syncwarp();
-    else
-        asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.warps * 32) : "memory");
+    const unsigned long long t0 = global_ns();
+    for (;;) {
+        for (int i = 0; i < 32; ++i) {
+            uint32_t ok;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2;\n\t"
+                "selp.u32 %0, 1, 0, p;\n\t}"
+                : "=r"(ok)
+                : "r"(bar), "r"(parity)
+                : "memory");
+            if (ok)
+                return true;
+        }
+        if (global_ns() - t0 > kWaitLimitNs)
+            return false;
+    }
 }
 
-// Where the warps of a row leave their partial values: per value 32 places, a group's warps from a
-// multiple of four on (in a cluster the two CTAs' warps from 0 and 16 on); zeros where there is no
-// warp.
+// Of the threads that share a row.  Two CTAs of one group each: the cluster's own barrier.  Of several
+// (which that barrier would tie together): the warps of both CTAs arrive on barrier `which` of each;
+// `phases` has a bit for each barrier's next phase.  (At 16384 values the forward pass, of two groups,
+// takes 285 us for 8512 rows with these and 352 us with one group and the cluster's barrier; the
+// backward pass, whose sixteen warps are one group, 394 and 367.)
+template <int CL>
+__device__ __forceinline__ void group_barrier(const Group& g, int which, uint32_t& phases)
+{
+    if (CL == kBoth) {
+        cluster_barrier();
+    } else if (CL == kJoint) {
+        const uint32_t bar = g.bars + 8u * which;
+        __syncwarp();
+        if (g.lane == 0) {
+            mbar_arrive(bar);
+            asm volatile(
+                "{\n\t.reg .b32 p;\n\tmapa.shared::cluster.u32 p, %0, %1;\n\t"
+                "mbarrier.arrive.release.cluster.shared::cluster.b64 _, [p];\n\t}" ::"r"(bar),
+                "r"(g.rank ^ 1u)
+                : "memory");
+        }
+        if (!(phases & kGaveUp) && !mbar_wait_cluster(bar, (phases >> which) & 1u)) {
+            phases |= kGaveUp;
+            atomicOr(&g_error, kErrCopyTimeout);
+        }
+        phases ^= 1u << which;
+    } else if (g.warps == 1) {
+        __syncwarp();
+    } else {
+        asm volatile("bar.sync %0, %1;" ::"r"(g.index + 1), "r"(g.warps * 32) : "memory");
+    }
+}
+
+// Where the warps of a row leave their partial values: per value kPlaces, a group's warps from a
+// multiple of four on (in a cluster a group's warps of both CTAs, one CTA's after the other's); zeros
+// where there is no warp.  32 places, but for three groups of eight in each of two CTAs (kJoint).
 template <int N>
 struct __align__(16) Exchange {
-    float v[N][32];
+    static constexpr int kPlaces = N == 1 ? 48 : 32;
+    float v[N][kPlaces];
 };
 
 template <int N>
 __device__ __forceinline__ void clear(Exchange<N>& ex)
 {
-    for (int i = threadIdx.x; i < N * 32; i += blockDim.x)
-        ex.v[0][i] = 0.0f;
+    for (int i = threadIdx.x; i < N * Exchange<N>::kPlaces; i += blockDim.x)
+        ex.v[i / Exchange<N>::kPlaces][i % Exchange<N>::kPlaces] = 0.0f;
 }
 
 // N sums (or maxima of magnitudes) over all threads of the row, in an order that the row's length
 // fixes; every thread gets them.  One barrier: the same exchange may be used again after one more.
-template <int N, bool CL, bool MAX = false>
-__device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const Group& g)
+template <int N, int CL, bool MAX = false>
+__device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const Group& g,
+                                           int which, uint32_t& phases)
 {
     auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : __fadd_rn(a, b); };
-    const int first = CL ? 0 : g.index * ((g.warps + 3) & ~3);
+    // a group's warps in one CTA have (g.warps + 3) & ~3 places; the other CTA's follow them (kJoint)
+    // or start at 16 (kBoth).  (Worked out where they are used: held over the exchanges, the place
+    // costs the backward pass 5%.)
+    const int first = CL == kBoth ? 0 : g.index * ((g.warps + 3) & ~3) * (CL == kJoint ? 2 : 1);
+    auto mine = [&]() {
+        if (CL == kBoth)
+            return static_cast<int>(g.rank) * 16 + g.warp;
+        return first + g.warp + (CL == kJoint ? static_cast<int>(g.rank) * ((g.warps + 3) & ~3) : 0);
+    };
     if constexpr (N == 3) {
         // three sums in six exchanges: each step halves the values that a lane still carries, so
         // lanes 0-7, 8-15 and 16-23 end with one sum each
@@ -125,7 +186,7 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
             return;
         }
         if ((g.lane & 7) == 0 && g.lane < 24) {
-            float* to = &ex.v[g.lane >> 3][(CL ? static_cast<int>(g.rank) * 16 : first) + g.warp];
+            float* to = &ex.v[g.lane >> 3][mine()];
             *to = a;
             if (CL)
                 st_peer(smem_addr(to), g.rank ^ 1u, a);
@@ -141,16 +202,16 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
         if (g.lane == 0) {
 #pragma unroll
             for (int i = 0; i < N; ++i) {
-                float* to = &ex.v[i][(CL ? static_cast<int>(g.rank) * 16 : first) + g.warp];
+                float* to = &ex.v[i][mine()];
                 *to = x[i];
                 if (CL)
                     st_peer(smem_addr(to), g.rank ^ 1u, x[i]);
             }
         }
     }
-    group_barrier<CL>(g);
+    group_barrier<CL>(g, which, phases);
     // four warps' values a load
-    const int quads = CL ? 8 : (g.warps + 3) / 4;
+    const int quads = CL == kBoth ? 8 : (g.warps + 3) / 4 * (CL == kJoint ? 2 : 1);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float4* q = reinterpret_cast<const float4*>(&ex.v[i][first]);
@@ -180,9 +241,15 @@ __device__ __forceinline__ float sum_squares(const u64 (&x)[V][4])
 // 1 / sqrt of a row whose fp32 sum of squares left fp32's comfortable range although its values are
 // finite: squares of the values over the power of two of the largest, joined in fp64.  The thread's
 // vectors are read again from `from`, so that the callers' registers need not outlive the sum.
-template <typename T, bool CL>
-__device__ __noinline__ float rstd_scaled(const uint4* from, int nv, int vectors, float sum, float n,
-                                          float eps, Exchange<1>* slow, const Group g)
+struct Slow {
+    float rstd;
+    uint32_t phases;
+};
+
+template <typename T, int CL>
+__device__ __noinline__ Slow rstd_scaled(const uint4* from, int nv, int vectors, float sum, float n,
+                                         float eps, Exchange<1>* slow, const Group g,
+                                         uint32_t phases)
 {
     float top[1] = {0.0f};
     for (int j = 0; j < vectors; ++j)
@@ -193,10 +260,10 @@ __device__ __noinline__ float rstd_scaled(const uint4* from, int nv, int vectors
                 top[0] = fmaxf(top[0], fmaxf(fabsf(p.x), fabsf(p.y)));
             }
         }
-    row_reduce<1, CL, true>(top, slow[0], g);
+    row_reduce<1, CL, true>(top, slow[0], g, 2, phases);
     // Inf, or nothing but zeros: the sum says it all.  (A NaN never gets here.)
     if (!(top[0] <= 3.4028235e38f) || top[0] == 0.0f)
-        return __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps)));
+        return {__fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), eps))), phases};
     const int e = ilogbf(top[0]);
     float s[1] = {0.0f};
     for (int j = 0; j < vectors; ++j)
@@ -208,18 +275,22 @@ __device__ __noinline__ float rstd_scaled(const uint4* from, int nv, int vectors
                 s[0] = __fadd_rn(s[0], __fadd_rn(__fmul_rn(a, a), __fmul_rn(b, b)));
             }
         }
-    row_reduce<1, CL>(s, slow[1], g);
+    row_reduce<1, CL>(s, slow[1], g, 3, phases);
     const double ms = scalbn(static_cast<double>(s[0]) / static_cast<double>(n), 2 * e);
-    return static_cast<float>(1.0 / sqrt(ms + static_cast<double>(eps)));
+    return {static_cast<float>(1.0 / sqrt(ms + static_cast<double>(eps))), phases};
 }
 
-template <typename T, bool CL>
+template <typename T, int CL>
 __device__ __forceinline__ float rstd_of(const uint4* from, int nv, int vectors, float sum, float n,
-                                         float inv_n, float eps, Exchange<1>* slow, const Group& g)
+                                         float inv_n, float eps, Exchange<1>* slow, const Group& g,
+                                         uint32_t& phases)
 {
     // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
-    if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f))
-        return rstd_scaled<T, CL>(from, nv, vectors, sum, n, eps, slow, g);
+    if (sum > 1.3e36f || (sum < 8e-25f && eps < 1e-18f)) {
+        const Slow s = rstd_scaled<T, CL>(from, nv, vectors, sum, n, eps, slow, g, phases);
+        phases = s.phases;
+        return s.rstd;
+    }
     // the approximate root and one Newton step: within 2 * 2^-24 of the root, in a tenth of the
     // instructions of a division and a square root, which every warp of a row repeats
     const float ms = __fmaf_rn(sum, inv_n, eps);
@@ -352,13 +423,14 @@ __device__ __forceinline__ void multiplier(u64 (&t)[4], const void* weight, cons
 
 constexpr int kFwdVectorBytes = 80;  // v and m in fp32, shift as stored
 
-template <typename T, int V, bool CL>
+template <typename T, int V, int CL>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     sandwich_kernel(const SandwichArgs a, const Plan plan)
 {
     extern __shared__ __align__(128) uint4 smem[];
     __shared__ __align__(8) unsigned long long full[kMaxWarps][kMaxStages];
     __shared__ Exchange<1> ex[2], slow[2];
+    __shared__ __align__(8) unsigned long long joint[CL == kJoint ? kMaxWarps : 1][kGroupBars];
 
     Group g;
     g.warps = plan.warps;
@@ -366,6 +438,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     g.warp = (threadIdx.x >> 5) - g.index * plan.warps;
     g.lane = threadIdx.x & 31;
     g.rank = CL ? cluster_rank() : 0u;
+    g.bars = smem_addr(&joint[CL == kJoint ? g.index : 0][0]);
     const uint32_t worker = CL ? blockIdx.x / 2 : blockIdx.x;
     const uint32_t workers = CL ? gridDim.x / 2 : gridDim.x;
     const uint32_t first = first_item(plan, worker, workers);
@@ -383,6 +456,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     if (g.leader()) {
         for (int s = 0; s < plan.stages; ++s)
             mbar_init(smem_addr(&full[g.index][s]), 1u);
+        if (CL == kJoint)
+            for (int i = 0; i < kGroupBars; ++i)
+                mbar_init(g.bars + 8u * i, 2u * g.warps);
         mbar_init_fence();
     }
     clear(ex[0]);
@@ -422,7 +498,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             issue();
     }
 
-    uint32_t batch = 0xFFFFFFFFu, phase = 0;
+    uint32_t batch = 0xFFFFFFFFu, phase = 0, phases = 0;
     int get = 0;
     for (uint32_t item = first; item < last; ++item) {
         const Span span(plan, item);
@@ -468,9 +544,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                     f[j][i] = widen<T>(word(u, i));
             }
             float s[1] = {sum_squares<V>(f)};
-            row_reduce<1, CL>(s, ex[0], g);
+            row_reduce<1, CL>(s, ex[0], g, 0, phases);
             const float rp =
-                rstd_of<T, CL>(slot, nv, V, s[0], a.n, inv_n, a.post_eps, slow, g);
+                rstd_of<T, CL>(slot, nv, V, s[0], a.n, inv_n, a.post_eps, slow, g, phases);
             // a barrier has passed (or a warp's exchange, for a group of one): the slot is read
             if (!CL && g.warps == 1)
                 __syncwarp();
@@ -498,9 +574,10 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 a.post_rstd_out[row] = rp;
             if (a.out) {
                 s[0] = sum_squares<V>(f);
-                row_reduce<1, CL>(s, ex[1], g);
+                row_reduce<1, CL>(s, ex[1], g, 1, phases);
                 const float r =
-                    rstd_of<T, CL>(res_out + base, nv, V, s[0], a.n, inv_n, a.eps, slow, g);
+                    rstd_of<T, CL>(res_out + base, nv, V, s[0], a.n, inv_n, a.eps, slow, g,
+                                   phases);
                 const u64 r2 = f2_splat(r);
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
@@ -520,7 +597,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 if (g.leader() && g.rank == 0 && a.rstd_out)
                     a.rstd_out[row] = r;
             } else {
-                group_barrier<CL>(g);  // between two uses of ex[0]
+                group_barrier<CL>(g, 1, phases);  // between two uses of ex[0]
             }
         }
     }
@@ -537,13 +614,14 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 constexpr int kBwdVectorBytes = 64;  // v and m in fp32
 
 // POST: the block's post norm takes part (update), OUT: the norm after the add does (grad_out).
-template <typename T, int V, bool CL, bool POST, bool OUT>
+template <typename T, int V, int CL, bool POST, bool OUT>
 __global__ void __launch_bounds__(kMaxThreads, 1)
     sandwich_bwd_kernel(const SandwichBwdArgs a, const Plan plan)
 {
     extern __shared__ __align__(128) uint4 smem[];
     __shared__ __align__(8) unsigned long long full[kMaxWarps][kMaxStages];
     __shared__ Exchange<3> ex[2];
+    __shared__ __align__(8) unsigned long long joint[CL == kJoint ? kMaxWarps : 1][kGroupBars];
 
     Group g;
     g.warps = plan.warps;
@@ -551,6 +629,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     g.warp = (threadIdx.x >> 5) - g.index * plan.warps;
     g.lane = threadIdx.x & 31;
     g.rank = CL ? cluster_rank() : 0u;
+    g.bars = smem_addr(&joint[CL == kJoint ? g.index : 0][0]);
     const uint32_t worker = CL ? blockIdx.x / 2 : blockIdx.x;
     const uint32_t workers = CL ? gridDim.x / 2 : gridDim.x;
     const uint32_t first = first_item(plan, worker, workers);
@@ -573,6 +652,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
     if (g.leader()) {
         for (int s = 0; s < plan.stages; ++s)
             mbar_init(smem_addr(&full[g.index][s]), 1u);
+        if (CL == kJoint)
+            for (int i = 0; i < kGroupBars; ++i)
+                mbar_init(g.bars + 8u * i, 2u * g.warps);
         mbar_init_fence();
     }
     clear(ex[0]);
@@ -616,7 +698,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
     constexpr int kParts = (OUT ? 2 : 0) + (POST ? 1 : 0);
     u64 sums[V][kParts][4];  // go, go * hh (OUT), dh * uh (POST)
-    uint32_t batch = 0xFFFFFFFFu, phase = 0;
+    uint32_t batch = 0xFFFFFFFFu, phase = 0, phases = 0;
     int get = 0, par = 0;
     for (uint32_t item = first; item < last; ++item) {
         const Span span(plan, item);
@@ -717,7 +799,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             s[1] = __fadd_rn(s[1], hi);
             f2_unpack(t2, s[2], hi);
             s[2] = __fadd_rn(s[2], hi);
-            row_reduce<3, CL>(s, ex[par], g);
+            row_reduce<3, CL>(s, ex[par], g, par, phases);
             par ^= 1;
             // the row is in registers everywhere: its slot takes the next copies
             if (!CL && g.warps == 1)
@@ -956,7 +1038,7 @@ Shape shape_of(int Dv, int V)
     s.cluster = Dv > kMaxDvPerCta;
     s.nv = s.cluster ? (Dv + 1) / 2 : Dv;
     s.warps = (s.nv + 32 * V - 1) / (32 * V);
-    s.groups = s.cluster ? 1 : kMaxWarps / s.warps;
+    s.groups = kMaxWarps / s.warps;  // (one for the backward pass in a cluster: V = 2)
     return s;
 }
 
@@ -1015,7 +1097,7 @@ cudaError_t launch_rows(K kern, const A& a, Plan p, const Shape& s, int fixed, i
     return cudaLaunchKernelEx(&cfg, kern, a, p);
 }
 
-template <typename T, int V, bool CL>
+template <typename T, int V, int CL>
 cudaError_t launch_fwd(const SandwichArgs& a, const Shape& s, const DeviceInfo& dev,
                        cudaStream_t stream)
 {
@@ -1037,14 +1119,14 @@ cudaError_t launch_fwd_t(const SandwichArgs& a, const DeviceInfo& dev, cudaStrea
 {
     const Shape s = shape_of(a.Dv, forward_vectors(a.Dv));
     if (s.cluster)
-        return launch_fwd<T, 4, true>(a, s, dev, stream);
+        return launch_fwd<T, 4, kJoint>(a, s, dev, stream);
     switch (forward_vectors(a.Dv)) {
     case 1:
-        return launch_fwd<T, 1, false>(a, s, dev, stream);
+        return launch_fwd<T, 1, kAlone>(a, s, dev, stream);
     case 2:
-        return launch_fwd<T, 2, false>(a, s, dev, stream);
+        return launch_fwd<T, 2, kAlone>(a, s, dev, stream);
     default:
-        return launch_fwd<T, 4, false>(a, s, dev, stream);
+        return launch_fwd<T, 4, kAlone>(a, s, dev, stream);
     }
 }
 
@@ -1063,7 +1145,7 @@ Plan backward_plan(int64_t B, int64_t S, int Dv)
     return plan_of(B, S, chunk < S ? chunk : S, s);
 }
 
-template <typename T, int V, bool CL, bool POST, bool OUT>
+template <typename T, int V, int CL, bool POST, bool OUT>
 cudaError_t launch_bwd(const SandwichBwdArgs& a, const Shape& s, const Plan& p,
                        const DeviceInfo& dev, cudaStream_t stream)
 {
@@ -1084,10 +1166,10 @@ cudaError_t launch_bwd_t(const SandwichBwdArgs& a, const Plan& p, const DeviceIn
 {
     const Shape s = shape_of(a.Dv, backward_vectors(a.Dv));
     if (s.cluster)
-        return launch_bwd<T, 2, true, POST, OUT>(a, s, p, dev, stream);
+        return launch_bwd<T, 2, kBoth, POST, OUT>(a, s, p, dev, stream);
     if (backward_vectors(a.Dv) == 1)
-        return launch_bwd<T, 1, false, POST, OUT>(a, s, p, dev, stream);
-    return launch_bwd<T, 2, false, POST, OUT>(a, s, p, dev, stream);
+        return launch_bwd<T, 1, kAlone, POST, OUT>(a, s, p, dev, stream);
+    return launch_bwd<T, 2, kAlone, POST, OUT>(a, s, p, dev, stream);
 }
 
 template <typename T>
