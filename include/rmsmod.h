@@ -454,7 +454,9 @@ enum {
     RMSMOD_OP_GATED_RMSNORM_MODULATE = 3,
     RMSMOD_OP_QK_LAYERNORM = 4,
     RMSMOD_OP_RMSNORM_SILU_CL = 5,
-    RMSMOD_OP_LN_MODULATE_FOLDED = 6
+    RMSMOD_OP_LN_MODULATE_FOLDED = 6,
+    RMSMOD_OP_SANDWICH_RMSNORM_MODULATE = 7, /* and its backward, rmsnorm_modulate_backward */
+    RMSMOD_OP_MXFP4 = 8                      /* D_or_C: the row length K */
 };
 
 /* 1 if `op` supports row length / channel count `D_or_C` and every non-NULL
@@ -465,7 +467,8 @@ int rmsmod_supported(int op, int64_t D_or_C, const void* const* ptrs, int nptrs)
 
 /* Device error word of the kernels launched so far on the current device:
  * bit 0 (RMSMOD_DEVICE_ERR_COPY_TIMEOUT) = an asynchronous bulk copy into
- * shared memory did not complete within the kernel's wait limit (1 s); the
+ * shared memory (or, in the 4-bit product and in rows shared by two CTAs,
+ * what a barrier waits for) did not complete within the wait limit (1 s); the
  * kernel then finished without that data instead of hanging, so its output
  * is invalid.  Synchronous (it reads device memory); `clear` != 0 resets the
  * word.  Returns RMSMOD_OK or RMSMOD_ERR_CUDA / RMSMOD_ERR_NULL. */

@@ -8,7 +8,8 @@ no CPU fallback: if the library is not built, or the tensors are not on a
 CUDA device, the call raises.
 
 Tensors are ``torch.bfloat16`` on a CUDA device with a contiguous innermost
-dimension.  Modulation rows (``scale``, ``shift``, ``gate``) may be given
+dimension (the sandwich norms and the 4-bit calls take ``torch.float16`` too,
+and run on their tensors' device whichever is current).  Modulation rows (``scale``, ``shift``, ``gate``) may be given
 as ``[D]``, ``[1, D]``, ``[B, D]``, ``[1, 1, D]`` or ``[B, 1, D]``; per-batch
 rows may be strided views (adaLN chunk views of one projection output).
 """
@@ -34,6 +35,7 @@ __all__ = [
     "selftest_wait_timeout",
     "OP_LN_MODULATE", "OP_RMSNORM_MODULATE", "OP_GATED_RMSNORM_MODULATE",
     "OP_QK_LAYERNORM", "OP_RMSNORM_SILU_CL", "OP_LN_MODULATE_FOLDED",
+    "OP_SANDWICH_RMSNORM_MODULATE", "OP_MXFP4",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -45,6 +47,8 @@ OP_GATED_RMSNORM_MODULATE = 3
 OP_QK_LAYERNORM = 4
 OP_RMSNORM_SILU_CL = 5
 OP_LN_MODULATE_FOLDED = 6
+OP_SANDWICH_RMSNORM_MODULATE = 7
+OP_MXFP4 = 8
 
 _lock = threading.Lock()
 _lib = None
@@ -149,7 +153,7 @@ def _entry(name):
     return fn
 
 
-def _call_on(device, name, *args, stream=None) -> None:
+def _call_on(device, stream, name, *args) -> None:
     """Call `name` on the tensors' own device, with `stream` (default: that device's current one)
     as the last argument.  Pointers are passed as integers (_at): half of a small call's time would
     otherwise go into ctypes objects."""
@@ -160,7 +164,7 @@ def _call_on(device, name, *args, stream=None) -> None:
     else:
         with torch.cuda.device(device):
             st = _entry(name)(*args, raw)
-    if st != 0:
+    if st:
         raise RmsmodError(st, name)
 
 
@@ -604,7 +608,10 @@ def _modulation(scale, shift, dtype, device, B, D):
     if shift is not None:
         if scale is None:
             return _rows(shift, "shift", dtype, device, B, D)
-        if _rows(shift, "shift", dtype, device, B, D) != bs:
+        if (not isinstance(shift, torch.Tensor) or shift.dtype is not dtype or
+                shift.device != device or shift.shape != scale.shape or
+                shift.stride() != scale.stride()) and \
+                _rows(shift, "shift", dtype, device, B, D) != bs:
             raise ValueError("scale and shift must share one batch stride")
     return bs
 
@@ -650,10 +657,10 @@ def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, wei
         out = torch.empty_like(residual)
     _stats(post_rstd_out, "post_rstd_out", device, B * S)
     _stats(rstd_out, "rstd_out", device, B * S)
-    _call_on(device, "sandwich_rmsnorm_modulate", _at(residual), _at(update), _at(post_weight),
+    _call_on(device, stream, "sandwich_rmsnorm_modulate", _at(residual), _at(update), _at(post_weight),
              _at(gate), gs, _at(weight), _at(scale), _at(shift), bs, _at(res_out), _at(out), B, S, D,
              residual_scale, update_scale, eps if post_eps is None else post_eps, eps,
-             _at(post_rstd_out), _at(rstd_out), _DTYPES[dt], stream=stream)
+             _at(post_rstd_out), _at(rstd_out), _DTYPES[dt])
     return res_out, out
 
 
@@ -747,11 +754,11 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
         _row_grads(need_mod and scale is not None, bs, B, D, device))
     workspace, wbytes = _backward_workspace("sandwich_rmsnorm_modulate_backward", workspace,
                                             need_mod, B, S, D, device, stream)
-    _call_on(device, "sandwich_rmsnorm_modulate_backward", _at(update), _at(res),
+    _call_on(device, stream, "sandwich_rmsnorm_modulate_backward", _at(update), _at(res),
              _at(post_weight), _at(gate), gs, _at(weight), _at(scale), bs, _at(grad_res),
              _at(grad_out), _at(post_rstd), _at(rstd), B, S, D, residual_scale, update_scale,
              _at(g.residual), _at(g.update), _at(g.post_weight), _at(g.gate), _at(g.weight),
-             _at(g.scale), _at(g.shift), _at(workspace), wbytes, _DTYPES[dt], stream=stream)
+             _at(g.scale), _at(g.shift), _at(workspace), wbytes, _DTYPES[dt])
     return g
 
 
@@ -777,10 +784,9 @@ def rmsnorm_modulate_backward(x, weight, scale, grad_out, rstd, grad_res=None, n
     grad_shift = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
     workspace, wbytes = _backward_workspace("rmsnorm_modulate_backward", workspace, need_mod, B,
                                             S, D, x.device, stream)
-    _call_on(x.device, "rmsnorm_modulate_backward", _at(x), _at(weight), _at(scale), bs,
+    _call_on(x.device, stream, "rmsnorm_modulate_backward", _at(x), _at(weight), _at(scale), bs,
              _at(grad_out), _at(grad_res), _at(rstd), B, S, D, _at(grad_x),
-             _at(grad_weight), _at(grad_scale), _at(grad_shift), _at(workspace), wbytes,
-             stream=stream)
+             _at(grad_weight), _at(grad_scale), _at(grad_shift), _at(workspace), wbytes)
     return grad_x, grad_weight, grad_scale, grad_shift
 
 
@@ -831,8 +837,8 @@ def mxfp4_quantize(x, out=None, stream=None) -> Mxfp4:
                     torch.empty(mxfp4_scale_bytes(rows, K), dtype=torch.uint8, device=x.device))
     elif _codes(out, "out", x.device) != (rows, K):
         raise ValueError("out must match x")
-    _call_on(x.device, "mxfp4_quantize", _at(x), _at(out.packed), _at(out.scales), rows, K,
-             _DTYPES[x.dtype], stream=stream)
+    _call_on(x.device, stream, "mxfp4_quantize", _at(x), _at(out.packed), _at(out.scales), rows, K,
+             _DTYPES[x.dtype])
     return out
 
 
@@ -847,8 +853,8 @@ def mxfp4_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
         _dense(out, "out", dtype)
         if out.shape != (*q.packed.shape[:-1], K) or out.device != q.packed.device:
             raise ValueError("out must match q")
-    _call_on(out.device, "mxfp4_dequantize", _at(q.packed), _at(q.scales), _at(out), rows, K,
-             _DTYPES[dtype], stream=stream)
+    _call_on(out.device, stream, "mxfp4_dequantize", _at(q.packed), _at(q.scales), _at(out), rows, K,
+             _DTYPES[dtype])
     return out
 
 
@@ -899,9 +905,9 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
         q = _scratch(stream, codes + mxfp4_scale_bytes(M, K), device)
         packed = _at(q)
         scales = packed + codes
-        _call_on(device, "mxfp4_quantize", _at(x), packed, scales, M, K, code, stream=stream)
-    _call_on(device, "mxfp4_matmul", packed, scales, _at(w.packed), _at(w.scales), _at(bias),
-             _at(gate), gs, _at(residual), _at(out), B, S, N, K, code, stream=stream)
+        _call_on(device, stream, "mxfp4_quantize", _at(x), packed, scales, M, K, code)
+    _call_on(device, stream, "mxfp4_matmul", packed, scales, _at(w.packed), _at(w.scales), _at(bias),
+             _at(gate), gs, _at(residual), _at(out), B, S, N, K, code)
     return out
 
 

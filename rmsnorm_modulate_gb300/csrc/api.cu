@@ -170,6 +170,7 @@ RMSMOD_EXPORT int rmsmod_supported(int op, int64_t D_or_C, const void* const* pt
     case RMSMOD_OP_LN_MODULATE_FOLDED:
     case RMSMOD_OP_RMSNORM_MODULATE:
     case RMSMOD_OP_GATED_RMSNORM_MODULATE:
+    case RMSMOD_OP_SANDWICH_RMSNORM_MODULATE:
         if (D_or_C > RMSMOD_MAX_D)
             return 0;
         break;
@@ -179,6 +180,10 @@ RMSMOD_EXPORT int rmsmod_supported(int op, int64_t D_or_C, const void* const* pt
         break;
     case RMSMOD_OP_RMSNORM_SILU_CL:
         if (D_or_C > RMSMOD_MAX_C || D_or_C < 8)
+            return 0;
+        break;
+    case RMSMOD_OP_MXFP4:
+        if (D_or_C > RMSMOD_MXFP4_MAX_K || D_or_C % 32 != 0)
             return 0;
         break;
     default:

@@ -188,6 +188,16 @@ def test_product_quantises_its_rows(rm):
     assert torch.equal(a[5:9], b)
 
 
+def test_rows_do_not_depend_on_how_many_there_are(rm):
+    # past 128 rows: narrow and wide tiles give a row the same bits
+    rng = np.random.default_rng(10)
+    x = rows_of(rng, 6000, 736, torch.bfloat16).cuda()
+    w, _ = make(rm, rng, 2056, 736)
+    whole = rm.mxfp4_linear(x, w)
+    for a, b in ((0, 129), (1000, 1300), (4000, 6000)):
+        assert torch.equal(rm.mxfp4_linear(x[a:b].contiguous(), w), whole[a:b])
+
+
 def test_product_nan_scale_stays_in_its_row(rm):
     rng = np.random.default_rng(4)
     x = rows_of(rng, 70, 256, torch.bfloat16)
