@@ -8,12 +8,13 @@
 // products of 64 values.
 //
 // pair_kernel (more than 128 rows of a): two CTAs of a cluster share a 256 x BN tile
-// (cta_group::2), each with its 128 rows of a and half of b's rows.  What bounds it is shared memory:
-// 256 values of K take 512 cycles of products (BN = 256), in which the copies write 35 KB and the
-// products read 32 KB of an SM's 128 bytes a cycle (BN = 192: 31.7 and 28 KB in 384 cycles, measured
-// 93 us where this takes NEW at 4214 x 4096 x 16384; a CTA alone would write half as much again).
-// Persistent, with two accumulators: eight warps finish one tile's rows while the next tile's products
-// run.
+// (cta_group::2), each with its 128 rows of a and half of b's rows.  256 values of K take 512 cycles of
+// products (BN = 256), in which 35 KB arrive in each SM, 68 bytes a cycle: about what an SM takes from
+// L2, and the next bound beside the products.  (BN = 192 brings 31.7 KB for 384 cycles: 93 us where
+// this takes 85, 4214 x 4096 x 16384; a CTA alone would bring half as much again.)  Persistent, with two
+// accumulators: eight warps finish one tile's rows while the next tile's products run.  Without the
+// copies the products take 73 us, without the epilogue 81; at 4216 x 16384 x 4096, where a tile has a
+// quarter of the steps, 104 us in all, 77 and 94.
 //
 // few_kernel (up to 128 rows of a, where reading b is what counts): b's rows take the 128-row side of
 // the instruction, a's rows the other.  A cluster of up to eight CTAs splits K, and joins its parts in
@@ -296,7 +297,7 @@ struct Maps {
 // ---------------------------------------------------------------------------
 
 // Two operand tiles to a step: waiting for one and passing it on takes the issuing thread as long as
-// several products, 470 cycles of 660 with one tile to a step.
+// several products (one tile to a step: 121 us where two take 100, 4216 x 16384 x 4096).
 constexpr int kPairSubs = 2;
 
 template <int BN>
