@@ -86,11 +86,11 @@ enum RowOp : int { kOpLN = 0, kOpRMS = 1, kOpGated = 2, kOpLNFold = 3 };
 // has completed and its writes are visible, so ordering is unchanged and only
 // the launch gap is hidden.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int block, int smem,
-                             cudaStream_t stream, const Args&... args)
+cudaError_t launch_dependent(void (*kern)(KArgs...), int grid, int block, int smem,
+                             cudaStream_t stream, Args... args)
 {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
+    cfg.gridDim = dim3(static_cast<unsigned>(grid));
     cfg.blockDim = dim3(static_cast<unsigned>(block));
     cfg.dynamicSmemBytes = static_cast<size_t>(smem);
     cfg.stream = stream;
@@ -100,13 +100,6 @@ cudaError_t launch_dependent(void (*kern)(KArgs...), dim3 grid, int block, int s
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kern, args...);
-}
-
-template <typename... KArgs, typename... Args>
-cudaError_t launch_dependent(void (*kern)(KArgs...), int grid, int block, int smem,
-                             cudaStream_t stream, const Args&... args)
-{
-    return launch_dependent(kern, dim3(static_cast<unsigned>(grid)), block, smem, stream, args...);
 }
 
 struct RowArgs {
