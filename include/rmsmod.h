@@ -18,10 +18,11 @@
  *     aligned too (per-channel fp32 bias) or 4-byte aligned (per-row outputs).
  *   - Row statistics are fp32: the exact mean / biased variance / mean square
  *     of the row, rounded once to fp32; rstd = 1 / sqrt(stat + eps) as
- *     three correctly rounded fp32 operations.
+ *     three correctly rounded fp32 operations (the sandwich norms: fp32 sums,
+ *     see there).
  *   - The caller owns every buffer.  The library allocates nothing, needs no
- *     workspace and keeps no global state other than cached device
- *     attributes.  Calls are asynchronous on `stream` (NULL = the legacy
+ *     workspace (but where an entry point says so) and keeps no global state
+ *     other than cached device attributes.  Calls are asynchronous on `stream` (NULL = the legacy
  *     default stream); nothing synchronises the host.
  *   - Output buffers may alias their row input exactly (out == x,
  *     res_out == residual); any other overlap is rejected when detected and

@@ -732,22 +732,29 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     if (f.split > 1) {
         cluster_barrier();
         if (warp < 4 && n < a.N) {
-            // this CTA's rows of a, the parts of K in order
+            // this CTA's rows of a, four at a time (all their loads on the way at once), the parts of
+            // K in order
             const uint32_t at = smem_addr(part) + n_in * 4;
-            for (int m = static_cast<int>(rank); m < M; m += f.split) {
-                float p[8];
+            for (int m = static_cast<int>(rank); m < M; m += 4 * f.split) {
+                float p[4][8];
 #pragma unroll
-                for (int r = 0; r < 8; ++r)
-                    if (r < f.split)
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(p[r])
-                                     : "r"(in_cta(at + m * 512, r)));
-                float v = p[0];
+                for (int i = 0; i < 4; ++i)
 #pragma unroll
-                for (int r = 1; r < 8; ++r)
-                    if (r < f.split)
-                        v += p[r];
-                finish(m, v, bias_n);
+                    for (int r = 0; r < 8; ++r)
+                        if (r < f.split && m + i * f.split < M)
+                            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                         : "=f"(p[i][r])
+                                         : "r"(in_cta(at + (m + i * f.split) * 512, r)));
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (m + i * f.split < M) {
+                        float v = p[i][0];
+#pragma unroll
+                        for (int r = 1; r < 8; ++r)
+                            if (r < f.split)
+                                v += p[i][r];
+                        finish(m + i * f.split, v, bias_n);
+                    }
             }
         }
         cluster_barrier();
@@ -919,9 +926,12 @@ cudaError_t launch_few(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStre
 template <typename T>
 cudaError_t launch(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
+    // 16 rows (N = K = 4096): 5.2 us against the pairs' 8.4, 64 rows 7.0 and 8.2; 128 rows 9.5 and
+    // 8.5, with N = 16384 13.0 and 13.2
     if (a.M <= 128)
         return launch_few<T>(a, dev, stream);
-    // narrower tiles where the wide ones leave SMs without work
+    // narrower tiles where the wide ones leave half of the SMs without work: 256 and 512 rows
+    // (N = K = 4096) 8.7 and 9.3 us against 10.8 and 11.4; 1024 rows 13.1 and 12.2
     const int64_t wide = (a.M + 255) / 256 * ((a.N + 255) / 256);
     return wide <= dev.sms / 4 ? launch_pair<T, 128>(a, dev, stream)
                                : launch_pair<T, 256>(a, dev, stream);
