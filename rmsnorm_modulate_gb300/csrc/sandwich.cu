@@ -15,9 +15,10 @@
 // All in fp32 with one rounding per stored value.  Sums run in an order that D (and, over tokens,
 // S) alone fixes, so a result does not depend on the batch it stands in.
 //
-// Both are bound by HBM: 8 and 12 bytes per value.  One CTA of up to 16 warps per SM; its warps form
-// groups that take a row each, four (forward) or two (backward) 16-byte vectors a thread, and every
-// group has a ring of bulk copies (TMA) that stays ahead of the arithmetic.  The products of a
+// Both are bound by HBM: 8 and 12 bytes per value.  One CTA per SM, of up to 16 warps (forward) or 8
+// (backward, whose column sums take twice the registers); its warps form groups that take a row each,
+// up to four 16-byte vectors a thread, and every group has a ring of bulk copies (TMA) that stays
+// ahead of the arithmetic.  The products of a
 // batch's row vectors lie in shared memory for all groups.  A row's values are in registers when its
 // slot is refilled, before its sums are known.  Rows of more than 8192 values are shared by a
 // cluster of two CTAs, which exchange their partial sums through distributed shared memory.
@@ -33,6 +34,10 @@ namespace {
 __device__ unsigned int g_error;
 
 constexpr int kMaxWarps = 16;      // of a CTA
+// Of a CTA of the backward pass: eight, with 255 registers, for three or four vectors a thread (sixteen
+// of two: 46.4 us where these take 43.8 at 4216 x 4096, 200 and 166 at 4256 x 16384); sixteen for rows
+// of up to 512 values, which have one or two (eight: 62.2 us for 60000 x 256, these 48.2).
+constexpr int backward_warps(int V) { return V <= 2 ? kMaxWarps : kMaxWarps / 2; }
 constexpr int kMaxThreads = 32 * kMaxWarps;
 constexpr int kMaxDvPerCta = 1024; // vectors of a row that one CTA takes
 constexpr int kMaxStages = 4;      // of a group's ring
@@ -615,7 +620,7 @@ constexpr int kBwdVectorBytes = 64;  // v and m in fp32
 
 // POST: the block's post norm takes part (update), OUT: the norm after the add does (grad_out).
 template <typename T, int V, int CL, bool POST, bool OUT>
-__global__ void __launch_bounds__(kMaxThreads, 1)
+__global__ void __launch_bounds__(32 * backward_warps(V), 1)
     sandwich_bwd_kernel(const SandwichBwdArgs a, const Plan plan)
 {
     extern __shared__ __align__(128) uint4 smem[];
@@ -1028,25 +1033,38 @@ __global__ void __launch_bounds__(8 * kColSlices)
 struct Shape {
     bool cluster;
     int nv;      // vectors of a CTA's part of a row
+    int V;
     int warps;   // of a group
     int groups;
 };
 
-Shape shape_of(int Dv, int V)
+Shape shape_of(int Dv, bool backward)
 {
     Shape s;
     s.cluster = Dv > kMaxDvPerCta;
     s.nv = s.cluster ? (Dv + 1) / 2 : Dv;
-    s.warps = (s.nv + 32 * V - 1) / (32 * V);
-    s.groups = kMaxWarps / s.warps;  // (one for the backward pass in a cluster: V = 2)
+    auto with = [&](int V) {
+        s.V = V;
+        const int most = backward ? backward_warps(V) : kMaxWarps;
+        s.warps = (s.nv + 32 * V - 1) / (32 * V);
+        s.groups = most / s.warps;
+        // rows' vectors in the CTA at a time: more is better used lanes
+        return s.groups * s.nv * 12 / V;
+    };
+    // Rows of one 16-byte vector a lane or two take no more than that: 60000 rows of 256 values in
+    // 29.1 us (forward) and 48.2 (backward) with one, 31.5 and 51.5 with two, 38.5 (forward) with
+    // four; 30000 rows of 512 in 21.9 with two and 25.7 with four.
+    if (s.nv <= 64) {
+        with(s.nv <= 32 ? 1 : 2);
+        return s;
+    }
+    // three or four, whichever leaves fewer lanes idle
+    const int four = with(4);
+    if (with(3) > four)  // (no group at all counts none)
+        return s;
+    with(4);
     return s;
 }
-
-// Rows of one 16-byte vector a lane or two take no more than that: 60000 rows of 256 values in 29.1 us
-// (forward) and 48.2 (backward) with one, 31.5 and 51.5 with two, 38.5 with four; 30000 rows of 512 in
-// 21.9 with two and 25.7 with four.
-int forward_vectors(int Dv) { return Dv <= 32 ? 1 : (Dv <= 64 ? 2 : 4); }
-int backward_vectors(int Dv) { return Dv <= 32 ? 1 : 2; }
 
 Plan plan_of(int64_t B, int64_t S, int64_t chunk, const Shape& s)
 {
@@ -1119,14 +1137,17 @@ cudaError_t launch_fwd(const SandwichArgs& a, const Shape& s, const DeviceInfo& 
 template <typename T>
 cudaError_t launch_fwd_t(const SandwichArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
-    const Shape s = shape_of(a.Dv, forward_vectors(a.Dv));
+    const Shape s = shape_of(a.Dv, false);
     if (s.cluster)
-        return launch_fwd<T, 4, kJoint>(a, s, dev, stream);
-    switch (forward_vectors(a.Dv)) {
+        return s.V == 3 ? launch_fwd<T, 3, kJoint>(a, s, dev, stream)
+                        : launch_fwd<T, 4, kJoint>(a, s, dev, stream);
+    switch (s.V) {
     case 1:
         return launch_fwd<T, 1, kAlone>(a, s, dev, stream);
     case 2:
         return launch_fwd<T, 2, kAlone>(a, s, dev, stream);
+    case 3:
+        return launch_fwd<T, 3, kAlone>(a, s, dev, stream);
     default:
         return launch_fwd<T, 4, kAlone>(a, s, dev, stream);
     }
@@ -1136,7 +1157,7 @@ cudaError_t launch_fwd_t(const SandwichArgs& a, const DeviceInfo& dev, cudaStrea
 // depend on the batch.  152 SMs.
 Plan backward_plan(int64_t B, int64_t S, int Dv)
 {
-    const Shape s = shape_of(Dv, backward_vectors(Dv));
+    const Shape s = shape_of(Dv, true);
     // whole rounds of items, of at most 256 rows (whose sums stay within a few 2^-24); of at least
     // eight, and two for each group, so that the partial sums stay under an eighth of the rows' bytes
     const int64_t over = s.cluster ? 76 : 152;
@@ -1166,12 +1187,20 @@ template <typename T, bool POST, bool OUT>
 cudaError_t launch_bwd_t(const SandwichBwdArgs& a, const Plan& p, const DeviceInfo& dev,
                          cudaStream_t stream)
 {
-    const Shape s = shape_of(a.Dv, backward_vectors(a.Dv));
+    const Shape s = shape_of(a.Dv, true);
     if (s.cluster)
-        return launch_bwd<T, 2, kBoth, POST, OUT>(a, s, p, dev, stream);
-    if (backward_vectors(a.Dv) == 1)
+        return s.V == 3 ? launch_bwd<T, 3, kBoth, POST, OUT>(a, s, p, dev, stream)
+                        : launch_bwd<T, 4, kBoth, POST, OUT>(a, s, p, dev, stream);
+    switch (s.V) {
+    case 1:
         return launch_bwd<T, 1, kAlone, POST, OUT>(a, s, p, dev, stream);
-    return launch_bwd<T, 2, kAlone, POST, OUT>(a, s, p, dev, stream);
+    case 2:
+        return launch_bwd<T, 2, kAlone, POST, OUT>(a, s, p, dev, stream);
+    case 3:
+        return launch_bwd<T, 3, kAlone, POST, OUT>(a, s, p, dev, stream);
+    default:
+        return launch_bwd<T, 4, kAlone, POST, OUT>(a, s, p, dev, stream);
+    }
 }
 
 template <typename T>
