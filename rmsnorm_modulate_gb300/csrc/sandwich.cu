@@ -85,7 +85,7 @@ struct Group {
 // each of two CTAs.
 enum Sharing : int { kAlone = 0, kBoth = 1, kJoint = 2 };
 
-constexpr int kGroupBars = 4;
+constexpr int kGroupBars = 6;
 constexpr uint32_t kGaveUp = 1u << 31;  // among the phases: a wait ran out, no more are made
 
 __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
@@ -109,11 +109,18 @@ __device__ __forceinline__ bool mbar_wait_cluster(uint32_t bar, uint32_t parity)
     }
 }
 
+__device__ __forceinline__ void joint_wait(const Group& g, int which, uint32_t& phases)
+{
+    if (!(phases & kGaveUp) && !mbar_wait_cluster(g.bars + 8u * which, (phases >> which) & 1u)) {
+        phases |= kGaveUp;
+        atomicOr(&g_error, kErrCopyTimeout);
+    }
+    phases ^= 1u << which;
+}
+
 // Of the threads that share a row.  Two CTAs of one group each: the cluster's own barrier.  Of several
 // (which that barrier would tie together): the warps of both CTAs arrive on barrier `which` of each;
-// `phases` has a bit for each barrier's next phase.  (At 16384 values the forward pass, of two groups,
-// takes 285 us for 8512 rows with these and 352 us with one group and the cluster's barrier; the
-// backward pass, whose sixteen warps are one group, 394 and 367.)
+// `phases` has a bit for each barrier's next phase.
 template <int CL>
 __device__ __forceinline__ void group_barrier(const Group& g, int which, uint32_t& phases)
 {
@@ -130,11 +137,7 @@ __device__ __forceinline__ void group_barrier(const Group& g, int which, uint32_
                 "r"(g.rank ^ 1u)
                 : "memory");
         }
-        if (!(phases & kGaveUp) && !mbar_wait_cluster(bar, (phases >> which) & 1u)) {
-            phases |= kGaveUp;
-            atomicOr(&g_error, kErrCopyTimeout);
-        }
-        phases ^= 1u << which;
+        joint_wait(g, which, phases);
     } else if (g.warps == 1) {
         __syncwarp();
     } else {
@@ -227,6 +230,48 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
         }
         x[i] = join(join(t.x, t.y), join(t.z, t.w));
     }
+}
+
+// One sum over a row's threads in two CTAs (kJoint), in two halves for work between them.  A warp
+// arrives on its own CTA's barrier alone; its value in the other CTA completes a part of that one's
+// transaction count.  (An arrival there with release semantics would first wait for the warp's
+// stores of the row.)  A barrier is used for every other row: nothing for its next phase is sent
+// before both CTAs have seen this one complete.
+__device__ __forceinline__ void joint_give(float x, Exchange<1>& ex, const Group& g, int which)
+{
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        x = __fadd_rn(x, __shfl_xor_sync(kFullMask, x, off));
+    __syncwarp();
+    if (g.lane == 0) {
+        const int part = (g.warps + 3) & ~3;
+        float* to = &ex.v[0][(2 * g.index + static_cast<int>(g.rank)) * part + g.warp];
+        const uint32_t bar = g.bars + 8u * which;
+        *to = x;
+        mbar_expect_tx(bar, 4u);
+        asm volatile(
+            "{\n\t.reg .b32 p, q;\n\tmapa.shared::cluster.u32 p, %0, %2;\n\t"
+            "mapa.shared::cluster.u32 q, %1, %2;\n\t"
+            "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [p], %3, [q];\n\t}" ::"r"(
+                smem_addr(to)),
+            "r"(bar), "r"(g.rank ^ 1u), "r"(__float_as_uint(x))
+            : "memory");
+    }
+}
+
+__device__ __forceinline__ float joint_take(const Exchange<1>& ex, const Group& g, int which,
+                                            uint32_t& phases)
+{
+    joint_wait(g, which, phases);
+    const int quads = (g.warps + 3) / 4 * 2;
+    const float4* q = reinterpret_cast<const float4*>(ex.v[0]) + g.index * quads;
+    float4 t = q[0];
+    for (int k = 1; k < quads; ++k) {
+        const float4 o = q[k];
+        t = make_float4(__fadd_rn(t.x, o.x), __fadd_rn(t.y, o.y), __fadd_rn(t.z, o.z),
+                        __fadd_rn(t.w, o.w));
+    }
+    return __fadd_rn(__fadd_rn(t.x, t.y), __fadd_rn(t.z, t.w));
 }
 
 template <int V>
@@ -434,7 +479,9 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 {
     extern __shared__ __align__(128) uint4 smem[];
     __shared__ __align__(8) unsigned long long full[kMaxWarps][kMaxStages];
-    __shared__ Exchange<1> ex[2], slow[2];
+    // of the update's sum and of the new residual's; kJoint: two of each, for rows in turn
+    constexpr int kSets = CL == kJoint ? 2 : 1;
+    __shared__ Exchange<1> ex[2 * kSets], slow[2 * kSets];
     __shared__ __align__(8) unsigned long long joint[CL == kJoint ? kMaxWarps : 1][kGroupBars];
 
     Group g;
@@ -463,13 +510,13 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             mbar_init(smem_addr(&full[g.index][s]), 1u);
         if (CL == kJoint)
             for (int i = 0; i < kGroupBars; ++i)
-                mbar_init(g.bars + 8u * i, 2u * g.warps);
+                mbar_init(g.bars + 8u * i, i == 2 || i == 3 ? 2u * g.warps : 1u * g.warps);
         mbar_init_fence();
     }
-    clear(ex[0]);
-    clear(ex[1]);
-    clear(slow[0]);
-    clear(slow[1]);
+    for (int i = 0; i < 2 * kSets; ++i) {
+        clear(ex[i]);
+        clear(slow[i]);
+    }
     if (CL)
         cluster_barrier();
     else
@@ -505,6 +552,97 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
     uint32_t batch = 0xFFFFFFFFu, phase = 0, phases = 0;
     int get = 0;
+    auto next_slot = [&]() {
+        if (!broken && !mbar_wait(smem_addr(&full[g.index][get]), phase, kWaitLimitNs)) {
+            broken = true;
+            atomicOr(&g_error, kErrCopyTimeout);
+        }
+        const uint4* slot = ring + static_cast<size_t>(get) * 2 * half;
+        if (++get == plan.stages) {
+            get = 0;
+            phase ^= 1u;
+        }
+        return slot;
+    };
+    u64 f[V][4];  // update, then res, in fp32: widened once each
+    uint4 x[V];
+    auto load_update = [&](const uint4* slot, u64 (&to)[V][4]) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = g.at(j);
+            const uint4 u = c < nv ? slot[c] : make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                to[j][i] = widen<T>(word(u, i));
+        }
+    };
+    auto load_residual = [&](const uint4* slot) {
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = g.at(j);
+            x[j] = c < nv ? slot[half + c] : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    auto store_res = [&](int64_t base, float rp) {
+        const u64 rp2 = f2_splat(rp);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = g.at(j);
+            if (c < nv) {
+                u64 t[4];
+                get_pairs(v_lo + c, v_hi + c, t);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const uint32_t w = narrow<T>(f2_fma(widen<T>(word(x[j], i)), rs2,
+                                                        f2_mul(f2_mul(f[j][i], rp2), t[i])));
+                    word(x[j], i) = w;
+                    f[j][i] = widen<T>(w);
+                }
+                st_stream(res_out + base + c, x[j]);
+            }
+        }
+    };
+    auto store_out = [&](int64_t base, float r) {
+        const u64 r2 = f2_splat(r);
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            const int c = g.at(j);
+            if (c < nv) {
+                u64 t[4];
+                get_pairs(m_lo + c, m_hi + c, t);
+                const uint4 sf = sh[c];
+                uint4 o;
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    word(o, i) =
+                        narrow<T>(f2_fma(f2_mul(f[j][i], r2), t[i], widen<T>(word(sf, i))));
+                st_stream(out + base + c, o);
+            }
+        }
+    };
+    const bool teller = g.leader() && g.rank == 0;
+    // kJoint: the next row's first sum is given before this row's second is taken, so that neither
+    // exchange is waited for in full (8512 rows of 16384 values: 177 us; 262 with both waited for
+    // where they are needed, and arrivals at the other CTA that release the row's stores; 235 with
+    // those arrivals alone).  Needs a ring of two slots, or no second row.
+    uint32_t left = 0, set = 0;
+    const uint4* slot = nullptr;
+    auto begin_row = [&]() {
+        slot = next_slot();
+        u64 u[V][4];
+        load_update(slot, u);
+        joint_give(sum_squares<V>(u), ex[2 * set], g, set ? 4 : 0);
+        --left;
+    };
+    if (CL == kJoint) {
+        for (uint32_t item = first; item < last; ++item) {
+            const Span span(plan, item);
+            const uint32_t rows = span.end - span.begin + plan.groups - 1 - g.index;
+            left += rows / plan.groups;
+        }
+        if (left)
+            begin_row();
+    }
     for (uint32_t item = first; item < last; ++item) {
         const Span span(plan, item);
         if (span.batch != batch) {  // the row vectors of this batch
@@ -524,85 +662,71 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             __syncthreads();
         }
         for (uint32_t row = span.begin + g.index; row < span.end; row += plan.groups) {
-            if (!broken && !mbar_wait(smem_addr(&full[g.index][get]), phase, kWaitLimitNs)) {
-                broken = true;
-                atomicOr(&g_error, kErrCopyTimeout);
-            }
-            const uint4* slot = ring + static_cast<size_t>(get) * 2 * half;
-            if (++get == plan.stages) {
-                get = 0;
-                phase ^= 1u;
-            }
-            u64 f[V][4];  // update, then res, in fp32: widened once each
-            uint4 x[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = g.at(j);
-                uint4 u = make_uint4(0u, 0u, 0u, 0u);
-                x[j] = u;
-                if (c < nv) {
-                    u = slot[c];
-                    x[j] = slot[half + c];
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    f[j][i] = widen<T>(word(u, i));
-            }
-            float s[1] = {sum_squares<V>(f)};
-            row_reduce<1, CL>(s, ex[0], g, 0, phases);
-            const float rp =
-                rstd_of<T, CL>(slot, nv, V, s[0], a.n, inv_n, a.post_eps, slow, g, phases);
-            // a barrier has passed (or a warp's exchange, for a group of one): the slot is read
-            if (!CL && g.warps == 1)
-                __syncwarp();
-            if (g.leader())
-                issue();
-            const u64 rp2 = f2_splat(rp);
             const int64_t base = static_cast<int64_t>(row) * a.Dv;
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = g.at(j);
-                if (c < nv) {
-                    u64 t[4];
-                    get_pairs(v_lo + c, v_hi + c, t);
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        const uint32_t w = narrow<T>(f2_fma(widen<T>(word(x[j], i)), rs2,
-                                                            f2_mul(f2_mul(f[j][i], rp2), t[i])));
-                        word(x[j], i) = w;
-                        f[j][i] = widen<T>(w);
-                    }
-                    st_stream(res_out + base + c, x[j]);
+            if constexpr (CL == kJoint) {
+                Exchange<1>* mine = ex + 2 * set;
+                const int b0 = set ? 4 : 0, b1 = b0 + 1;
+                float sum = joint_take(mine[0], g, b0, phases);
+                const float rp = rstd_of<T, CL>(slot, nv, V, sum, a.n, inv_n, a.post_eps, slow, g,
+                                                phases);
+                load_update(slot, f);
+                load_residual(slot);
+                store_res(base, rp);
+                if (teller && a.post_rstd_out)
+                    a.post_rstd_out[row] = rp;
+                joint_give(sum_squares<V>(f), mine[1], g, b1);
+                set ^= 1u;
+                if (left)
+                    begin_row();
+                sum = joint_take(mine[1], g, b1, phases);
+                // all have read this row's slot
+                if (g.leader())
+                    issue();
+                if (a.out) {
+                    const float r = rstd_of<T, CL>(res_out + base, nv, V, sum, a.n, inv_n, a.eps,
+                                                   slow + 2, g, phases);
+                    store_out(base, r);
+                    if (teller && a.rstd_out)
+                        a.rstd_out[row] = r;
                 }
-            }
-            if (g.leader() && g.rank == 0 && a.post_rstd_out)
-                a.post_rstd_out[row] = rp;
-            if (a.out) {
-                s[0] = sum_squares<V>(f);
-                row_reduce<1, CL>(s, ex[1], g, 1, phases);
-                const float r =
-                    rstd_of<T, CL>(res_out + base, nv, V, s[0], a.n, inv_n, a.eps, slow, g,
-                                   phases);
-                const u64 r2 = f2_splat(r);
+            } else {
+                const uint4* slot = next_slot();
 #pragma unroll
                 for (int j = 0; j < V; ++j) {
                     const int c = g.at(j);
+                    uint4 u = make_uint4(0u, 0u, 0u, 0u);
+                    x[j] = u;
                     if (c < nv) {
-                        u64 t[4];
-                        get_pairs(m_lo + c, m_hi + c, t);
-                        const uint4 sf = sh[c];
-                        uint4 o;
-#pragma unroll
-                        for (int i = 0; i < 4; ++i)
-                            word(o, i) = narrow<T>(f2_fma(f2_mul(f[j][i], r2), t[i],
-                                                          widen<T>(word(sf, i))));
-                        st_stream(out + base + c, o);
+                        u = slot[c];
+                        x[j] = slot[half + c];
                     }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i)
+                        f[j][i] = widen<T>(word(u, i));
                 }
-                if (g.leader() && g.rank == 0 && a.rstd_out)
-                    a.rstd_out[row] = r;
-            } else {
-                group_barrier<CL>(g, 1, phases);  // between two uses of ex[0]
+                float s[1] = {sum_squares<V>(f)};
+                row_reduce<1, CL>(s, ex[0], g, 0, phases);
+                const float rp =
+                    rstd_of<T, CL>(slot, nv, V, s[0], a.n, inv_n, a.post_eps, slow, g, phases);
+                // a barrier has passed (or a warp's exchange, for a group of one): the slot is read
+                if (!CL && g.warps == 1)
+                    __syncwarp();
+                if (g.leader())
+                    issue();
+                store_res(base, rp);
+                if (teller && a.post_rstd_out)
+                    a.post_rstd_out[row] = rp;
+                if (a.out) {
+                    s[0] = sum_squares<V>(f);
+                    row_reduce<1, CL>(s, ex[1], g, 1, phases);
+                    const float r = rstd_of<T, CL>(res_out + base, nv, V, s[0], a.n, inv_n, a.eps,
+                                                   slow, g, phases);
+                    store_out(base, r);
+                    if (teller && a.rstd_out)
+                        a.rstd_out[row] = r;
+                } else {
+                    group_barrier<CL>(g, 1, phases);  // between two uses of ex[0]
+                }
             }
         }
     }
@@ -1092,13 +1216,13 @@ cudaError_t launch_rows(K kern, const A& a, Plan p, const Shape& s, int fixed, i
     });
     if (e != cudaSuccess)
         return e;
-    // rings no longer than the rows of a group in an item need
+    // rings no longer than the rows of a group in its only item need
+    const int64_t cap = s.cluster ? dev.sms / 2 : dev.sms;
     const int rows = static_cast<int>((p.chunk + p.groups - 1) / p.groups);
     p.stages = (kSmemBytes - fixed) / (slot * p.groups);
     p.stages = p.stages > kMaxStages ? kMaxStages : p.stages;
-    if (p.count <= static_cast<uint32_t>(dev.sms) && rows < p.stages)
+    if (p.count <= cap && rows < p.stages)
         p.stages = rows;
-    const int64_t cap = s.cluster ? dev.sms / 2 : dev.sms;
     const int64_t clusters = static_cast<int64_t>(p.count) < cap ? p.count : cap;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(static_cast<unsigned>(clusters * (s.cluster ? 2 : 1)));
