@@ -550,6 +550,30 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
             issue();
     }
 
+    // Seven rows into a long run its rings are left a slot or two shorter: reads that are too far
+    // ahead get in the way of the stores.  What stays on its way is 56 KB an SM or more.  (With all
+    // slots and with fewer: 17920 rows of 4096 values 105.5 and 94.4 us, 8960 of 8192 108 and 97, 24576
+    // of 1024 38.0 and 36.8; 9830 of 2560 36.7 and 38.0, 3554 of 6144 33.4 and 33.9.  From the first
+    // row on, 4216 of 4096 take 27.2 where these take 26.5.  The exchange of kJoint rows holds them
+    // back by itself; rows of 256 values are issue-bound, and this costs them 3%.)
+    constexpr bool kRest = CL == kAlone && V > 1;
+    __shared__ uint32_t rest[kRest ? kMaxWarps : 1];  // a bit for each refill to come: not made
+    if (kRest && g.leader()) {
+        uint32_t bits = 0;
+        for (int k = 1; (plan.stages - k) * 32 * half * plan.groups >= 56 * 1024; ++k)
+            bits = bits * 2u + 64u;
+        rest[g.index] = bits;
+    }
+    auto issue_or_rest = [&]() {
+        if (kRest) {
+            const uint32_t bits = rest[g.index];
+            rest[g.index] = bits >> 1;
+            if (bits & 1u)
+                return;
+        }
+        issue();
+    };
+
     uint32_t batch = 0xFFFFFFFFu, phase = 0, phases = 0;
     int get = 0;
     auto next_slot = [&]() {
@@ -712,7 +736,7 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
                 if (!CL && g.warps == 1)
                     __syncwarp();
                 if (g.leader())
-                    issue();
+                    issue_or_rest();
                 store_res(base, rp);
                 if (teller && a.post_rstd_out)
                     a.post_rstd_out[row] = rp;
