@@ -68,6 +68,17 @@ __device__ __forceinline__ void st_peer(uint32_t addr, uint32_t rank, float v)
                  : "memory");
 }
 
+// Stores v at the other CTA's `addr`, where it completes four bytes of the phase of `bar`.
+__device__ __forceinline__ void send(uint32_t addr, uint32_t bar, uint32_t rank, float v)
+{
+    asm volatile(
+        "{\n\t.reg .b32 p, q;\n\tmapa.shared::cluster.u32 p, %0, %2;\n\t"
+        "mapa.shared::cluster.u32 q, %1, %2;\n\t"
+        "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [p], %3, [q];\n\t}" ::"r"(addr),
+        "r"(bar), "r"(rank), "r"(__float_as_uint(v))
+        : "memory");
+}
+
 // The threads of a CTA (or of the two CTAs of a cluster) that share rows.
 struct Group {
     int warps;       // of a group in this CTA
@@ -81,9 +92,8 @@ struct Group {
     __device__ __forceinline__ int at(int j) const { return (j * warps + warp) * 32 + lane; }
 };
 
-// Who shares a row: a group of one CTA, the one group of each of two CTAs, or one of the groups of
-// each of two CTAs.
-enum Sharing : int { kAlone = 0, kBoth = 1, kJoint = 2 };
+// Who shares a row: a group of one CTA, or one group of each of two.
+enum Sharing : int { kAlone = 0, kJoint = 1 };
 
 constexpr int kGroupBars = 6;
 constexpr uint32_t kGaveUp = 1u << 31;  // among the phases: a wait ran out, no more are made
@@ -118,15 +128,12 @@ __device__ __forceinline__ void joint_wait(const Group& g, int which, uint32_t& 
     phases ^= 1u << which;
 }
 
-// Of the threads that share a row.  Two CTAs of one group each: the cluster's own barrier.  Of several
-// (which that barrier would tie together): the warps of both CTAs arrive on barrier `which` of each;
-// `phases` has a bit for each barrier's next phase.
+// Of the threads that share a row; kJoint: the warps of both CTAs arrive on barrier `which` of each,
+// and `phases` has a bit for each barrier's next phase.
 template <int CL>
 __device__ __forceinline__ void group_barrier(const Group& g, int which, uint32_t& phases)
 {
-    if (CL == kBoth) {
-        cluster_barrier();
-    } else if (CL == kJoint) {
+    if (CL == kJoint) {
         const uint32_t bar = g.bars + 8u * which;
         __syncwarp();
         if (g.lane == 0) {
@@ -168,14 +175,11 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
                                            int which, uint32_t& phases)
 {
     auto join = [](float a, float b) { return MAX ? fmaxf(a, b) : __fadd_rn(a, b); };
-    // a group's warps in one CTA have (g.warps + 3) & ~3 places; the other CTA's follow them (kJoint)
-    // or start at 16 (kBoth).  (Worked out where they are used: held over the exchanges, the place
-    // costs the backward pass 5%.)
-    const int first = CL == kBoth ? 0 : g.index * ((g.warps + 3) & ~3) * (CL == kJoint ? 2 : 1);
+    // a group's warps in one CTA have (g.warps + 3) & ~3 places, the other CTA's follow them.  (Worked
+    // out where they are used: held over the exchanges, the place costs the backward pass 5%.)
+    const int first = g.index * ((g.warps + 3) & ~3) * (CL ? 2 : 1);
     auto mine = [&]() {
-        if (CL == kBoth)
-            return static_cast<int>(g.rank) * 16 + g.warp;
-        return first + g.warp + (CL == kJoint ? static_cast<int>(g.rank) * ((g.warps + 3) & ~3) : 0);
+        return first + g.warp + (CL ? static_cast<int>(g.rank) * ((g.warps + 3) & ~3) : 0);
     };
     if constexpr (N == 3) {
         // three sums in six exchanges: each step halves the values that a lane still carries, so
@@ -197,7 +201,12 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
             float* to = &ex.v[g.lane >> 3][mine()];
             *to = a;
             if (CL)
-                st_peer(smem_addr(to), g.rank ^ 1u, a);
+                send(smem_addr(to), g.bars + 8u * which, g.rank ^ 1u, a);
+        }
+        if (CL) {
+            __syncwarp();
+            if (g.lane == 0)
+                mbar_expect_tx(g.bars + 8u * which, 12u);
         }
     } else {
 #pragma unroll
@@ -217,9 +226,12 @@ __device__ __forceinline__ void row_reduce(float (&x)[N], Exchange<N>& ex, const
             }
         }
     }
-    group_barrier<CL>(g, which, phases);
+    if (CL && N == 3)
+        joint_wait(g, which, phases);
+    else
+        group_barrier<CL>(g, which, phases);
     // four warps' values a load
-    const int quads = CL == kBoth ? 8 : (g.warps + 3) / 4 * (CL == kJoint ? 2 : 1);
+    const int quads = (g.warps + 3) / 4 * (CL ? 2 : 1);
 #pragma unroll
     for (int i = 0; i < N; ++i) {
         const float4* q = reinterpret_cast<const float4*>(&ex.v[i][first]);
@@ -249,13 +261,7 @@ __device__ __forceinline__ void joint_give(float x, Exchange<1>& ex, const Group
         const uint32_t bar = g.bars + 8u * which;
         *to = x;
         mbar_expect_tx(bar, 4u);
-        asm volatile(
-            "{\n\t.reg .b32 p, q;\n\tmapa.shared::cluster.u32 p, %0, %2;\n\t"
-            "mapa.shared::cluster.u32 q, %1, %2;\n\t"
-            "st.async.shared::cluster.mbarrier::complete_tx::bytes.b32 [p], %3, [q];\n\t}" ::"r"(
-                smem_addr(to)),
-            "r"(bar), "r"(g.rank ^ 1u), "r"(__float_as_uint(x))
-            : "memory");
+        send(smem_addr(to), bar, g.rank ^ 1u, x);
     }
 }
 
@@ -807,7 +813,7 @@ __global__ void __launch_bounds__(32 * backward_warps(V), 1)
             mbar_init(smem_addr(&full[g.index][s]), 1u);
         if (CL == kJoint)
             for (int i = 0; i < kGroupBars; ++i)
-                mbar_init(g.bars + 8u * i, 2u * g.warps);
+                mbar_init(g.bars + 8u * i, 1u * g.warps);
         mbar_init_fence();
     }
     clear(ex[0]);
@@ -1337,8 +1343,8 @@ cudaError_t launch_bwd_t(const SandwichBwdArgs& a, const Plan& p, const DeviceIn
 {
     const Shape s = shape_of(a.Dv, true);
     if (s.cluster)
-        return s.V == 3 ? launch_bwd<T, 3, kBoth, POST, OUT>(a, s, p, dev, stream)
-                        : launch_bwd<T, 4, kBoth, POST, OUT>(a, s, p, dev, stream);
+        return s.V == 3 ? launch_bwd<T, 3, kJoint, POST, OUT>(a, s, p, dev, stream)
+                        : launch_bwd<T, 4, kJoint, POST, OUT>(a, s, p, dev, stream);
     switch (s.V) {
     case 1:
         return launch_bwd<T, 1, kAlone, POST, OUT>(a, s, p, dev, stream);
