@@ -1129,7 +1129,7 @@ RMSMOD_EXPORT int mxfp4_matmul(const void* a, const void* a_scales, const void* 
     if (!dtype_ok(dtype))
         return RMSMOD_ERR_UNSUPPORTED;
     int st;
-    if ((st = check_bstride(gate_bstride)) != RMSMOD_OK)
+    if ((st = check_bstride_span(B, gate_bstride)) != RMSMOD_OK)
         return st;
     if (M == 0 || N == 0)
         return RMSMOD_OK;

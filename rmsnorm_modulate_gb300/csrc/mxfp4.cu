@@ -71,7 +71,7 @@ constexpr int kUnitsPerCta = kThreads / 16;
 // A unit is the 128 values of one block tile in the four rows r, r + 32, r + 64, r + 96 of a row tile,
 // whose sixteen scale bytes are neighbours; 16 lanes take a unit, eight values of each row, so four
 // lanes share a block and a unit's scales are one store.  Neighbouring units are neighbours in the
-// rows.  Bound by HBM: 4216 x 16384 bf16 quantised in 29.8 us and back in 27.0, 0.86 and 0.95 of the
+// rows.  Bound by HBM: 4216 x 16384 bf16 quantised in 28.0 us and back in 27.0, 0.92 and 0.95 of the
 // measured copy peak (both together 49 us; with a unit for each row, whose scales are stores of four
 // bytes, 62).
 struct Unit {

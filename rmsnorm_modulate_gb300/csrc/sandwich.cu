@@ -35,7 +35,7 @@ __device__ unsigned int g_error;
 
 constexpr int kMaxWarps = 16;      // of a CTA
 // Of a CTA of the backward pass: eight, with 255 registers, for three or four vectors a thread (sixteen
-// of two: 46.4 us where these take 43.8 at 4216 x 4096, 200 and 166 at 4256 x 16384); sixteen for rows
+// of two: 46.4 us where these take 43.8 at 4216 x 4096, 186 and 147 at 4256 x 16384); sixteen for rows
 // of up to 512 values, which have one or two (eight: 62.2 us for 60000 x 256, these 48.2).
 constexpr int backward_warps(int V) { return V <= 2 ? kMaxWarps : kMaxWarps / 2; }
 constexpr int kMaxThreads = 32 * kMaxWarps;

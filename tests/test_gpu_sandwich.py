@@ -173,6 +173,40 @@ def test_extreme_rows(rm, D):
         check_forward(rm, t, eps=eps, post_eps=1e-6)
 
 
+@pytest.mark.parametrize("B,S,D", [(1, 20000, 1024), (1, 9000, 4096), (2, 3100, 6144), (3, 700, 16384)])
+def test_forward_long(rm, B, S, D):
+    # many rows to a group of warps, whose rings are shorter by then
+    check_forward(rm, Inputs(B, S, D, torch.bfloat16))
+
+
+@pytest.mark.parametrize("D", [72, 4096, 12288])
+def test_extreme_rows_in_turn(rm, D):
+    # ordinary rows and those that take another way through the sums, next to one another in a group
+    # of warps: every row's result is its own, whatever stands before and after it
+    S = 4000
+    gen = torch.Generator(device="cuda").manual_seed(D)
+    size = torch.tensor([1.0, 0.0, 1e30, 1.0, 1e-30, float("inf"), 1e36, 0.0, 1.0, 1e-36, 1e20],
+                        device="cuda")
+    kind = size[torch.randint(0, len(size), (2, S, 1), device="cuda", generator=gen)]
+    n = torch.randn(2, S, D, device="cuda", generator=gen)
+    u, x = (n * kind).bfloat16()[:, None].unbind(0)
+    flat = lambda t: t.view(torch.int32 if t.dtype is torch.float32 else torch.int16)  # noqa: E731
+
+    def run(x, u):
+        rp, r = (torch.empty(S, dtype=torch.float32, device="cuda") for _ in range(2))
+        res, out = rm.sandwich_rmsnorm_modulate(x, u, eps=1e-30, post_eps=1e-38, post_rstd_out=rp,
+                                                rstd_out=r)
+        return res[0], out[0], rp, r
+
+    there = run(x, u)
+    order = torch.randperm(S, device="cuda", generator=gen)
+    back = run(x[:, order].contiguous(), u[:, order].contiguous())
+    for a, b in zip(there, back):
+        a, b = a[order], b
+        same = (flat(a) == flat(b)) | (a.isnan() & b.isnan())
+        assert same.all()
+
+
 def test_non_finite_rows_stay_alone(rm):
     t = Inputs(1, 6, 512, torch.bfloat16)
     res, out, _, _ = forward(rm, t)
