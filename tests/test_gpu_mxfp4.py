@@ -188,6 +188,22 @@ def test_product_quantises_its_rows(rm):
     assert torch.equal(a[5:9], b)
 
 
+def test_shapes_of_the_product(rm):
+    # leading dimensions are rows; a gate of [N] or [1, N] is every row's, one of [B, N] a batch's
+    rng = np.random.default_rng(11)
+    x = rows_of(rng, 24, 96, torch.float16).cuda()
+    w, _ = make(rm, rng, 40, 96)
+    g = torch.from_numpy(rng.standard_normal((2, 40))).half().cuda()
+    flat = rm.mxfp4_linear(x, w, gate=g[0])
+    for lead in ((24,), (2, 12), (2, 3, 4), (1, 24), (24, 1)):
+        for gate in (g[0], g[:1], g[:1, None].expand(lead[0] if len(lead) > 1 else 1, 1, 40)):
+            out = rm.mxfp4_linear(x.view(*lead, 96), w, gate=gate)
+            assert out.shape == (*lead, 40) and torch.equal(out.view(24, 40), flat)
+    out = rm.mxfp4_linear(x.view(2, 3, 4, 96), w, gate=g)
+    assert torch.equal(out[0].view(12, 40), flat[:12])
+    assert torch.equal(out[1].view(12, 40), rm.mxfp4_linear(x[12:].contiguous(), w, gate=g[1]))
+
+
 def test_rows_do_not_depend_on_how_many_there_are(rm):
     # past 128 rows: narrow and wide tiles give a row the same bits
     rng = np.random.default_rng(10)

@@ -345,6 +345,34 @@ def test_expanded_row_gets_one_gradient(rm):
     assert torch.equal(a.gate, b.gate) and torch.equal(a.scale, b.scale)
 
 
+def test_shapes_of_rows(rm):
+    # [S, D] tensors, and row vectors as [D], [1, D] and [B, D]: the same bits as [B, S, D] with
+    # [B, 1, D]
+    def both(t, two=lambda x: x, rows=lambda x: x):
+        r, rp = (torch.empty(t.B * t.S, dtype=torch.float32, device="cuda") for _ in range(2))
+        g, sc, sh = rows(t.gate), rows(t.scale), rows(t.shift)
+        u = two(t.update)
+        res, out = rm.sandwich_rmsnorm_modulate(two(t.residual), u, t.post_weight, g, t.weight, sc,
+                                                sh, post_rstd_out=rp, rstd_out=r)
+        grads = rm.sandwich_rmsnorm_modulate_backward(u, res, t.post_weight, g, t.weight, sc,
+                                                      two(t.grad_res), two(t.grad_out), rp, r)
+        return [res, out, *grads]
+
+    one, three = Inputs(1, 37, 520, torch.bfloat16), Inputs(3, 37, 520, torch.bfloat16)
+    for t, two, rows in ((one, lambda x: x[0], lambda x: x[0]), (one, lambda x: x[0], lambda x: x[0, 0]),
+                         (one, lambda x: x, lambda x: x[0, 0]), (three, lambda x: x, lambda x: x[:, 0])):
+        for a, b in zip(both(t), both(t, two, rows)):
+            assert torch.equal(a.reshape(-1), b.reshape(-1))
+
+
+def test_statistics_are_any_shape(rm):
+    t = Inputs(2, 5, 128, torch.float16)
+    a, b = (torch.empty(2, 5, 1, dtype=torch.float32, device="cuda") for _ in range(2))
+    rm.sandwich_rmsnorm_modulate(t.residual, t.update, post_rstd_out=a, rstd_out=b)
+    want = ref.rstd(t.update, 1e-6)
+    close(a, want, want, 64, "post_rstd")
+
+
 def check_rms(rm, t, gr=True):
     rstd = torch.empty(t.B * t.S, dtype=torch.float32, device="cuda")
     rm.rmsnorm_modulate(t.residual, t.weight, t.scale if t.scale is not None else
