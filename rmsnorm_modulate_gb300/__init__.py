@@ -667,7 +667,8 @@ def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, wei
 class SandwichGrads(NamedTuple):
     """Gradients of sandwich_rmsnorm_modulate by its inputs: residual and update of their type,
     the row vectors in fp32 ([D]; gate, scale and shift [B, D], or [1, D] where one row is shared
-    by the batches); None for an input that took no part."""
+    by the batches); None for an input that took no part (a gradient of shift comes with that of
+    scale, whether or not the call was given shift)."""
 
     residual: torch.Tensor
     update: torch.Tensor
@@ -716,13 +717,15 @@ def _backward_workspace(name, workspace, wanted, B, S, D, device, stream):
 def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, scale, grad_res,
                                        grad_out, post_rstd, rstd, residual_scale: float = 1.0,
                                        update_scale: float = 1.0, need_x=True, need_mod=True,
-                                       workspace=None, stream=None) -> SandwichGrads:
+                                       workspace=None, stream=None, shift=None) -> SandwichGrads:
     """Gradients of sandwich_rmsnorm_modulate.  update, post_weight, gate, weight, scale and the
     two factors as in the forward, res and the statistics as it left them; grad_res, grad_out: the
     gradients of res and out (grad_res may be None; without grad_out, which drops the second norm,
-    grad_res is needed and res, weight, scale and rstd are not).  need_x: residual and update;
-    need_mod: the row vectors, whose token sums (in an order that S and D fix) take a workspace,
-    allocated here unless one is passed.  A gradient of shift comes with that of scale."""
+    grad_res is needed and res, weight, scale, shift and rstd are not).  need_x: residual and
+    update; need_mod: the row vectors, whose token sums (in an order that S and D fix) take a
+    workspace, allocated here unless one is passed.  A gradient of shift comes with that of scale;
+    where the forward had shift and no scale, it is given here too (its rows' shape and stride are
+    read, its values are not)."""
     _half(update, "update")
     dt, device, shape = update.dtype, update.device, update.shape
     B, S, D = shape if len(shape) == 3 else _bsd(update, "update", dt)
@@ -740,10 +743,10 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
             raise ValueError("res is required with grad_out")
         _input(res, "res", dt, device, shape)
         _vector(weight, "weight", dt, device, D)
-        bs = _rows(scale, "scale", dt, device, B, D)
+        bs = _modulation(scale, shift, dt, device, B, D)
         _need_stats(rstd, "rstd", device, B * S)
     else:
-        res = weight = scale = rstd = None
+        res = weight = scale = shift = rstd = None
     g = SandwichGrads(
         torch.empty_like(update) if need_x else None,
         torch.empty_like(update) if need_x else None,
@@ -751,7 +754,7 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
         _row_grads(need_mod and gate is not None, gs, B, D, device),
         _vector_grad(need_mod and weight is not None, D, device),
         _row_grads(need_mod and scale is not None, bs, B, D, device),
-        _row_grads(need_mod and scale is not None, bs, B, D, device))
+        _row_grads(need_mod and (scale is not None or shift is not None), bs, B, D, device))
     workspace, wbytes = _backward_workspace("sandwich_rmsnorm_modulate_backward", workspace,
                                             need_mod, B, S, D, device, stream)
     _call_on(device, stream, "sandwich_rmsnorm_modulate_backward", _at(update), _at(res),
