@@ -12,6 +12,11 @@ dimension (the sandwich norms and the 4-bit calls take ``torch.float16`` too,
 and run on their tensors' device whichever is current).  Modulation rows (``scale``, ``shift``, ``gate``) may be given
 as ``[D]``, ``[1, D]``, ``[B, D]``, ``[1, 1, D]`` or ``[B, 1, D]``; per-batch
 rows may be strided views (adaLN chunk views of one projection output).
+
+Every call takes a ``stream`` (default: the current one), which the caller orders after its inputs.
+What the sandwich norms, rmsnorm_modulate_backward and the 4-bit calls allocate is that stream's, and
+the current stream is noted as using their results; the other calls allocate on the current stream,
+so with another one pass them their outputs.
 """
 from __future__ import annotations
 
@@ -154,8 +159,8 @@ def _entry(name):
 
 
 def _call_on(device, stream, name, *args) -> None:
-    """Call `name` on the tensors' own device, with `stream` (default: that device's current one)
-    as the last argument.  Pointers are passed as integers (_at): half of a small call's time would
+    """Call `name` on the tensors' own device, with `stream` (None: that device's current one) as the
+    last argument.  Pointers are passed as integers (_at): half of a small call's time would
     otherwise go into ctypes objects."""
     index = device.index
     raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
@@ -172,13 +177,23 @@ def _at(t):
     return None if t is None else t.data_ptr()
 
 
-def _scratch(stream, n, device):
-    """`n` bytes that only work on `stream` uses: they come from that stream's own pool, so that
-    nothing on another stream can be given them before that work is done."""
-    if stream is None:
-        return torch.empty(n, dtype=torch.uint8, device=device)
+def _aside(stream, device, call, *args):
+    """call(*args, None), a call whose last argument is its stream, with `stream` as the current one.
+    For calls that allocate: the memory comes from that stream's own pool, so that nothing on another
+    stream can be given it while the call's work still writes it, and the results are noted as used by
+    the caller's current stream, so that it is not taken again before what that one does is done.
+    (On the host that takes some 20 us, which a call that is given its results does without.)"""
+    if stream.device != device:
+        raise ValueError(f"stream must be on {device}")
+    current = torch.cuda.current_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return call(*args, None)
     with torch.cuda.stream(stream):
-        return torch.empty(n, dtype=torch.uint8, device=device)
+        made = call(*args, None)
+    for t in made if isinstance(made, tuple) else (made,):
+        if t is not None:
+            t.record_stream(current)
+    return made
 
 
 def _bf16(t, name, dtype=torch.bfloat16):
@@ -639,6 +654,10 @@ def sandwich_rmsnorm_modulate(residual, update, post_weight=None, gate=None, wei
     defaults to eps.  post_rstd_out / rstd_out: fp32 [B * S] for the backward pass."""
     _half(residual, "residual")
     dt, device, shape = residual.dtype, residual.device, residual.shape
+    if stream is not None and (res_out is None or (need_out and out is None)):
+        return _aside(stream, device, sandwich_rmsnorm_modulate, residual, update, post_weight, gate,
+                      weight, scale, shift, eps, post_eps, residual_scale, update_scale, need_out,
+                      res_out, out, post_rstd_out, rstd_out)
     B, S, D = shape if len(shape) == 3 else _bsd(residual, "residual", dt)
     _input(update, "update", dt, device, shape)
     _vector(post_weight, "post_weight", dt, device, D)
@@ -700,12 +719,12 @@ def _workspace_bytes(name, B, S, D):
     return int(getattr(library(), name + "_workspace_bytes")(B, S, D))
 
 
-def _backward_workspace(name, workspace, wanted, B, S, D, device, stream):
+def _backward_workspace(name, workspace, wanted, B, S, D, device):
     if not wanted:
         return None, 0
     need = _workspace_bytes(name, B, S, D)
     if workspace is None:
-        workspace = _scratch(stream, max(need, 1), device)
+        workspace = torch.empty(max(need, 1), dtype=torch.uint8, device=device)
     elif workspace.device != device or not workspace.is_contiguous():
         raise ValueError(f"workspace must be contiguous and on {device}")
     wbytes = workspace.numel() * workspace.element_size()
@@ -728,6 +747,11 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
     read, its values are not)."""
     _half(update, "update")
     dt, device, shape = update.dtype, update.device, update.shape
+    if stream is not None:
+        return _aside(stream, device, functools.partial(sandwich_rmsnorm_modulate_backward,
+                                                        shift=shift),
+                      update, res, post_weight, gate, weight, scale, grad_res, grad_out, post_rstd,
+                      rstd, residual_scale, update_scale, need_x, need_mod, workspace)
     B, S, D = shape if len(shape) == 3 else _bsd(update, "update", dt)
     if grad_res is not None:
         _input(grad_res, "grad_res", dt, device, shape)
@@ -756,7 +780,7 @@ def sandwich_rmsnorm_modulate_backward(update, res, post_weight, gate, weight, s
         _row_grads(need_mod and scale is not None, bs, B, D, device),
         _row_grads(need_mod and (scale is not None or shift is not None), bs, B, D, device))
     workspace, wbytes = _backward_workspace("sandwich_rmsnorm_modulate_backward", workspace,
-                                            need_mod, B, S, D, device, stream)
+                                            need_mod, B, S, D, device)
     _call_on(device, stream, "sandwich_rmsnorm_modulate_backward", _at(update), _at(res),
              _at(post_weight), _at(gate), gs, _at(weight), _at(scale), bs, _at(grad_res),
              _at(grad_out), _at(post_rstd), _at(rstd), B, S, D, residual_scale, update_scale,
@@ -774,6 +798,9 @@ def rmsnorm_modulate_backward(x, weight, scale, grad_out, rstd, grad_res=None, n
     modulation: no such gradients).  Workspace as in sandwich_rmsnorm_modulate_backward."""
     _dense(x, "x", torch.bfloat16)
     dt, device, shape = x.dtype, x.device, x.shape
+    if stream is not None:
+        return _aside(stream, device, rmsnorm_modulate_backward, x, weight, scale, grad_out, rstd,
+                      grad_res, need_x, need_mod, workspace)
     B, S, D = shape if len(shape) == 3 else _bsd(x)
     _input(grad_out, "grad_out", dt, device, shape)
     if grad_res is not None:
@@ -786,7 +813,7 @@ def rmsnorm_modulate_backward(x, weight, scale, grad_out, rstd, grad_res=None, n
     grad_scale = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
     grad_shift = _row_grads(need_mod and scale is not None, bs, B, D, x.device)
     workspace, wbytes = _backward_workspace("rmsnorm_modulate_backward", workspace, need_mod, B,
-                                            S, D, x.device, stream)
+                                            S, D, x.device)
     _call_on(x.device, stream, "rmsnorm_modulate_backward", _at(x), _at(weight), _at(scale), bs,
              _at(grad_out), _at(grad_res), _at(rstd), B, S, D, _at(grad_x),
              _at(grad_weight), _at(grad_scale), _at(grad_shift), _at(workspace), wbytes)
@@ -831,6 +858,8 @@ def mxfp4_quantize(x, out=None, stream=None) -> Mxfp4:
     """Rows of x [..., K] (bfloat16 or float16, K a multiple of 32) in blocks of 32 e2m1 codes
     under the least power-of-two scale that holds the block without saturation."""
     _half(x, "x")
+    if stream is not None and out is None:
+        return _aside(stream, x.device, mxfp4_quantize, x, out)
     K = x.shape[-1] if x.dim() else 0
     if K == 0 or K % 32:
         raise ValueError("x must hold rows of a multiple of 32 values")
@@ -848,6 +877,8 @@ def mxfp4_quantize(x, out=None, stream=None) -> Mxfp4:
 def mxfp4_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
     """The values that q stands for, as bfloat16 or float16 [..., K]."""
     rows, K = _codes(q, "q")
+    if stream is not None and out is None:
+        return _aside(stream, q.packed.device, mxfp4_dequantize, q, dtype, out)
     if dtype not in _DTYPES:
         raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
     if out is None:
@@ -869,6 +900,11 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
     bfloat16, is the result's type); w: an Mxfp4 [N, K], laid out once.  bias [N]; gate rows [N]
     or [B, 1, N] (for x [B, S, K]); residual [..., N], all of the result's type.  out may be
     residual."""
+    if stream is not None and (out is None or not isinstance(x, Mxfp4)):
+        at = x.packed if isinstance(x, Mxfp4) else x
+        if not isinstance(at, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor or an Mxfp4")
+        return _aside(stream, at.device, mxfp4_linear, x, w, bias, gate, residual, out, dtype)
     if isinstance(x, Mxfp4):
         dtype = torch.bfloat16 if dtype is None else dtype
         if dtype not in _DTYPES:
@@ -905,7 +941,7 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
         packed, scales = _at(x.packed), _at(x.scales)
     else:
         codes = M * (K // 2)  # a multiple of 16
-        q = _scratch(stream, codes + mxfp4_scale_bytes(M, K), device)
+        q = torch.empty(codes + mxfp4_scale_bytes(M, K), dtype=torch.uint8, device=device)
         packed = _at(q)
         scales = packed + codes
         _call_on(device, stream, "mxfp4_quantize", _at(x), packed, scales, M, K, code)
