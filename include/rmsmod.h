@@ -439,7 +439,10 @@ int mxfp4_dequantize(const void* packed, const void* scales, void* out, int64_t 
  *   in fp32 with one rounding; bias, gate and residual are nullable (no add,
  *   no product).  a [B*S, K], b [N, K] packed with their scales; N a multiple
  *   of 8; gate rows at gate + b * gate_bstride (elements, a multiple of 8);
- *   residual, out [B*S, N], out may equal residual.  One launch. */
+ *   residual, out [B*S, N], out may equal residual.  One launch.
+ *   A row's sum over K is taken in an order that N, K and whether B*S is above
+ *   128 fix: a row has the same bits among the calls of up to 128 rows, and among
+ *   those of more, but not always the same in both. */
 int mxfp4_matmul(const void* a, const void* a_scales, const void* b, const void* b_scales,
                  const void* bias, const void* gate, int64_t gate_bstride, const void* residual,
                  void* out, int64_t B, int64_t S, int64_t N, int64_t K, int dtype,

@@ -896,7 +896,10 @@ cudaError_t launch_few(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStre
         f.NX *= 2;
     f.stage_bytes = kTileBytes + 2 * kScaleBytes + f.NX * kStepBytes;
     // parts of K until the GPU is full: they depend on N and K alone, so that a row's result does
-    // not depend on the rows beside it
+    // not depend on the rows beside it (of up to 128: the pairs sum K without parts, so that the
+    // same row among more may differ in its last bits).  A power of two leaves up to half of the SMs
+    // without a part; what 8 rows take with K = 4096 shows little of it: N = 9728 (152 CTAs) 7.9 us,
+    // 9856 (77) 8.2, 11008 (86) 8.3.
     const int64_t tiles = (a.N + 127) / 128, steps = (a.K + kStepK - 1) / kStepK;
     f.split = 1;
     while (f.split < 8 && 2 * f.split * tiles <= 152 && 2 * f.split <= steps)
@@ -926,8 +929,10 @@ cudaError_t launch_few(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStre
 template <typename T>
 cudaError_t launch(const Mxfp4MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
-    // 16 rows (N = K = 4096): 5.2 us against the pairs' 8.4, 64 rows 7.0 and 8.2; 128 rows 9.5 and
-    // 8.5, with N = 16384 13.0 and 13.2
+    // What the instruction's other side holds.  With K = 4096, N = 4096 and 16 rows 5.6 us against the
+    // pairs' 8.2, 64 rows 7.4 and 8.2, 96 rows 8.6 and 8.4, 128 rows 9.8 and 8.4; with N = 16384
+    // 64 rows 11.0 and 12.8, 128 rows 13.0 and 13.3.  One border for all N and K, so that a row's bits
+    // change at one number of rows.
     if (a.M <= 128)
         return launch_few<T>(a, dev, stream);
     // narrower tiles where the wide ones leave half of the SMs without work: 256 and 512 rows
