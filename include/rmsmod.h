@@ -364,15 +364,17 @@ int sandwich_rmsnorm_modulate(const void* residual, const void* update, const vo
  *   grad_residual, grad_update  nullable [B*S*D] of `dtype`
  *   grad_post_weight, grad_weight  nullable fp32 [D]
  *   grad_gate, grad_scale, grad_shift  nullable fp32 [B, D], or [1, D] where
- *     the row's bstride is 0 (the sum over the batches)
+ *     the row's bstride is 0 (the sum over the batches); mod_bstride is that of
+ *     scale and shift, of shift alone where the forward had no scale
  *   Without grad_out: res, rstd unused; grad_weight, grad_scale, grad_shift
  *   must be NULL.  The token sums are fp32 in an order that S and D fix.
  *   Without rows the sums are zeros.  No output may overlap an input or
  *   another output.
  *   workspace  256-byte aligned device memory of at least
  *     sandwich_rmsnorm_modulate_backward_workspace_bytes(B, S, D) bytes,
- *     needed where a row vector's gradient is wanted; in use until the call's
- *     work on `stream` is done.  Two launches (one without row vectors).
+ *     needed where a row vector's gradient is wanted (at most
+ *     12 * B * D * ceil(S / 8) bytes); in use until the call's work on `stream`
+ *     is done.  Two launches (one without row vectors).
  * ---------------------------------------------------------------------- */
 size_t sandwich_rmsnorm_modulate_backward_workspace_bytes(int64_t B, int64_t S, int64_t D);
 

@@ -558,10 +558,11 @@ __global__ void __launch_bounds__(kMaxThreads, 1)
 
     // Seven rows into a long run its rings are left a slot or two shorter: reads that are too far
     // ahead get in the way of the stores.  What stays on its way is 56 KB an SM or more.  (With all
-    // slots and with fewer: 17920 rows of 4096 values 105.5 and 94.4 us, 8960 of 8192 108 and 97, 24576
-    // of 1024 38.0 and 36.8; 9830 of 2560 36.7 and 38.0, 3554 of 6144 33.4 and 33.9.  From the first
-    // row on, 4216 of 4096 take 27.2 where these take 26.5.  The exchange of kJoint rows holds them
-    // back by itself; rows of 256 values are issue-bound, and this costs them 3%.)
+    // slots and with fewer: 17920 rows of 4096 values 105.7 and 94.8 us, 8960 of 8192 108 and 97.5, 24576
+    // of 1024 37.6 and 36.6, 2 x 1777 of 6144 in fp16 without adaLN rows 31.5 and 31.3; 9830 of 2560
+    // 37.2 and 38.2, 30000 of 512 22.9 and 23.4, 3554 of 6144 33.5 and 33.6.  From the first row on,
+    // 4216 of 4096 take 27.2 where these take 26.4.  The exchange of kJoint rows holds them back by
+    // itself; rows of 256 values are issue-bound.)
     constexpr bool kRest = CL == kAlone && V > 1;
     __shared__ uint32_t rest[kRest ? kMaxWarps : 1];  // a bit for each refill to come: not made
     if (kRest && g.leader()) {
@@ -1276,7 +1277,12 @@ cudaError_t launch_fwd(const SandwichArgs& a, const Shape& s, const DeviceInfo& 
                        cudaStream_t stream)
 {
     static PerDeviceInt ready;
-    // items that spread over the GPU
+    // Items that spread over the GPU.  They are rows of one batch and as many for every batch, so a
+    // number of batches just past half of the CTAs, or past all of them, leaves up to half without
+    // work: 17024 rows of 4096 values take 89 us as 1, 4 or 152 batches, 95 as 39, 129 as 77 and 149 as
+    // 153.  With fewer rows a batch than a CTA has groups the groups past them have none, and the row
+    // vectors are staged for every batch, shared or not: 4096 rows take 25.8 us as one batch, 31 as 512
+    // (36 with rows of their own) and 72 (106) as 4096.
     const int64_t B = a.rows / a.S;
     int64_t per = (CL ? dev.sms / 2 : dev.sms) / B;
     per = per < 1 ? 1 : (per > a.S ? a.S : per);
@@ -1313,7 +1319,11 @@ Plan backward_plan(int64_t B, int64_t S, int Dv)
 {
     const Shape s = shape_of(Dv, true);
     // whole rounds of items, of at most 256 rows (whose sums stay within a few 2^-24); of at least
-    // eight, and two for each group, so that the partial sums stay under an eighth of the rows' bytes
+    // eight, and two for each group, so that the partial sums are some eighth of the rows' bytes.
+    // A batch of fewer rows is an item of those: at S = 1 the partial sums (12 bytes a value, which is
+    // the workspace too) are as many bytes as the rows, and the second launch adds 16 batches at a time.
+    // 4096 rows of 4096 values take 42 us as one batch, 104 (127 with rows of their own) as 512, 163
+    // (208) as 1024 and 535 (781, with a workspace of 201 MB) as 4096.
     const int64_t over = s.cluster ? 76 : 152;
     const int64_t rounds = (S + 256 * over - 1) / (256 * over);
     int64_t chunk = (S + rounds * over - 1) / (rounds * over);
