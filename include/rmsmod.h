@@ -451,6 +451,138 @@ int mxfp4_matmul(const void* a, const void* a_scales, const void* b, const void*
                  rmsmod_stream_t stream);
 
 /* ------------------------------------------------------------------------
+ * Microscaled 8-bit rows (MXFP8): a block's projections trained and served in
+ * 8 bits -- the norm that feeds them, their product, and the checkpoints that
+ * the backward pass takes its activations from.
+ *
+ *   A row of K values (K a multiple of 32, up to RMSMOD_MXFP8_MAX_K) is cut
+ *   into blocks of 32.  Block: 32 e4m3 codes (largest 448, smallest 2^-9)
+ *   under one e8m0 scale 2^(byte - 127), byte 255 = NaN.
+ *     codes   [rows, K] bytes
+ *     scales  mxfp8_scale_bytes(rows, K) bytes, tiled like MXFP4's (above).
+ *             Bytes of blocks past K have to be zero; every call that writes
+ *             scales writes all bytes of the tiles, zeros for what the matrix
+ *             lacks.
+ *   Q(v) below: the scale is 2^e, the least power of two with max|v| <=
+ *   448 * 2^e and e >= -127 (no value saturates), a code v * 2^-e to nearest,
+ *   ties to even, taken from v in fp32 without another rounding before it.  A
+ *   block that holds Inf or NaN gets the NaN scale, a block of zeros byte 0.
+ *   dtype: RMSMOD_BF16 or RMSMOD_F16 (mxfp8_matmul: RMSMOD_F32 too), the type
+ *   of all that is not 8-bit or said to be fp32.  All pointers 16-byte aligned
+ *   (rstd: 4, workspace: 256).  Sums are fp32 in an order that the sizes fix.
+ *   No output may overlap an input or another output, but where said.
+ * ---------------------------------------------------------------------- */
+#define RMSMOD_MXFP8_MAX_K 1048576
+
+enum { RMSMOD_F32 = 2 };
+
+/* act(z): z; z / (1 + e^-z); z Phi(z); 0.5 z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) */
+enum {
+    RMSMOD_ACT_NONE = 0,
+    RMSMOD_ACT_SILU = 1,
+    RMSMOD_ACT_GELU = 2,
+    RMSMOD_ACT_GELU_TANH = 3
+};
+
+/* Bytes of the tiled scales of a [rows, K] matrix; 0 if unsupported. */
+size_t mxfp8_scale_bytes(int64_t rows, int64_t K);
+
+/* mxfp8_quantize: codes, scales = Q(x), x [rows, K]. */
+int mxfp8_quantize(const void* x, void* codes, void* scales, int64_t rows, int64_t K, int dtype,
+                   rmsmod_stream_t stream);
+
+/* mxfp8_dequantize: the values that the codes stand for, rounded to dtype
+ * (exact but for bf16 subnormals, and fp16's range). */
+int mxfp8_dequantize(const void* codes, const void* scales, void* out, int64_t rows, int64_t K,
+                     int dtype, rmsmod_stream_t stream);
+
+/* mxfp8_transpose: the matrix [rows, K] as [K, R] in blocks along its rows,
+ * R = rows up to a multiple of 32 (zeros behind the last row): Q of the values
+ * that the codes stand for.  A value keeps its bits but where it is under 2^-6
+ * of the new block's scale; blocks along the tokens are what a weight's
+ * gradient sums over, blocks along the outputs what an input's does.
+ * out_codes [K, R], out_scales mxfp8_scale_bytes(K, R); rows up to
+ * RMSMOD_MXFP8_MAX_K. */
+int mxfp8_transpose(const void* codes, const void* scales, void* out_codes, void* out_scales,
+                    int64_t rows, int64_t K, rmsmod_stream_t stream);
+
+/* mxfp8_matmul: for every row m = b * S + s of a and row n of b
+ *     z[m, n] = sum_k a[m, k] * b[n, k] + f(bias[n])                 (fp32)
+ *     y[m, n] = f(residual[m, n]) + f(gate_b[n]) * act(z[m, n])      (fp32)
+ *   out = R(y), or with out_scales out, out_scales = Q(y) along n; keep,
+ *   keep_scales (nullable) = Q(z).  bias, gate, residual nullable (no add, no
+ *   product).  a [B*S, K], b [N, K] codes with their scales; N a multiple of 8
+ *   (of 32 where something is written in 8 bits); gate rows at gate + b *
+ *   gate_bstride (elements, a multiple of 8); residual, out, keep [B*S, N];
+ *   out may equal residual (not in 8 bits).  One launch.
+ *   A row's sum over K is taken in an order that N, K and whether B*S is above
+ *   128 fix: a row has the same bits among the calls of up to 128 rows, and
+ *   among those of more, but not always the same in both. */
+int mxfp8_matmul(const void* a, const void* a_scales, const void* b, const void* b_scales,
+                 const void* bias, int activation, const void* gate, int64_t gate_bstride,
+                 const void* residual, void* out, void* out_scales, void* keep,
+                 void* keep_scales, int64_t B, int64_t S, int64_t N, int64_t K, int dtype,
+                 rmsmod_stream_t stream);
+
+/* add_rmsnorm_mxfp8 -- the residual add and the norm before a projection:
+ *     res  = R(f(x) + f(update))                     (x itself without update)
+ *     r    = 1 / sqrt(mean(f(res)^2) + eps)          (over res as stored)
+ *     out  = Q((f(res) * r) * (f(weight) * (1 + f(scale_b))) + f(shift_b))
+ *     keep = Q(f(res))
+ *   x, update (nullable), res_out (with update alone; may equal x or update)
+ *   [B*S*D], D a multiple of 32; weight nullable [D], scale, shift nullable
+ *   rows at base + b * mod_bstride (0 = one row for every batch): a missing
+ *   factor is 1, a missing shift 0.  keep, keep_scales nullable; rstd_out
+ *   nullable fp32 [B*S] (Inf where r is past fp32's range: rows under 2^-128
+ *   without eps; their out does not go through it).  Statistics as in
+ *   sandwich_rmsnorm_modulate.  B * S < 2^31. */
+int add_rmsnorm_mxfp8(const void* x, const void* update, const void* weight, const void* scale,
+                      const void* shift, int64_t mod_bstride, void* res_out, void* out,
+                      void* out_scales, void* keep, void* keep_scales, int64_t B, int64_t S,
+                      int64_t D, float eps, float* rstd_out, int dtype, rmsmod_stream_t stream);
+
+/* rmsnorm_mxfp8_backward -- gradients of that norm by res and its row vectors,
+ * from keep in res's place; rstd: the forward's; roundings passed straight
+ * through; h = what kept stands for, go, gr: the gradients of out and, on the
+ * residual stream, of res (nullable).
+ *     hh = h * r;  m = f(weight) * (1 + f(scale_b))
+ *     grad_x      = R(r * (go * m - hh * mean(go * m * hh)) + gr)
+ *     grad_shift  = sum go;  grad_scale = f(weight) * sum go * hh  over a batch
+ *     grad_weight = sum go * hh * (1 + f(scale_b))                over all
+ *   grad_x nullable [B*S*D]; grad_weight nullable fp32 [D]; grad_scale,
+ *   grad_shift nullable fp32 [B, D], or [1, D] where mod_bstride is 0.
+ *   (grad_x is the gradient by x and by update alike.)
+ *   workspace  at least rmsnorm_mxfp8_backward_workspace_bytes(B, S, D) bytes,
+ *     needed where a row vector's gradient is wanted; in use until the call's
+ *     work on `stream` is done.  Two launches (one without row vectors). */
+size_t rmsnorm_mxfp8_backward_workspace_bytes(int64_t B, int64_t S, int64_t D);
+
+int rmsnorm_mxfp8_backward(const void* kept, const void* kept_scales, const void* weight,
+                           const void* scale, int64_t mod_bstride, const void* grad_out,
+                           const void* grad_res, const float* rstd, int64_t B, int64_t S,
+                           int64_t D, void* grad_x, float* grad_weight, float* grad_scale,
+                           float* grad_shift, void* workspace, size_t workspace_bytes, int dtype,
+                           rmsmod_stream_t stream);
+
+/* mxfp8_activation_backward -- gradients of y = residual + gate_b * act(z)
+ * from the checkpoint of z (mxfp8_matmul's keep) and g, the gradient of y:
+ *     dz = f(g) * act'(z) * f(gate_b);  grad_z, grad_z_scales = Q(dz)
+ *     grad_bias = sum dz over all rows;  grad_gate = sum g * act(z) over a batch
+ *   z, grad_z [B*S, N] codes with their scales; grad_out [B*S, N]; gate
+ *   nullable, rows at gate + b * gate_bstride; grad_bias nullable fp32 [N];
+ *   grad_gate nullable (and without gate NULL) fp32 [B, N], or [1, N] where
+ *   gate_bstride is 0.  workspace as above
+ *   (mxfp8_activation_backward_workspace_bytes(B, S, N)), needed where a sum is
+ *   wanted. */
+size_t mxfp8_activation_backward_workspace_bytes(int64_t B, int64_t S, int64_t N);
+
+int mxfp8_activation_backward(const void* z, const void* z_scales, const void* grad_out,
+                              int activation, const void* gate, int64_t gate_bstride,
+                              void* grad_z, void* grad_z_scales, float* grad_bias,
+                              float* grad_gate, int64_t B, int64_t S, int64_t N, void* workspace,
+                              size_t workspace_bytes, int dtype, rmsmod_stream_t stream);
+
+/* ------------------------------------------------------------------------
  * Predicates and diagnostics
  * ---------------------------------------------------------------------- */
 
@@ -462,7 +594,9 @@ enum {
     RMSMOD_OP_RMSNORM_SILU_CL = 5,
     RMSMOD_OP_LN_MODULATE_FOLDED = 6,
     RMSMOD_OP_SANDWICH_RMSNORM_MODULATE = 7, /* and its backward, rmsnorm_modulate_backward */
-    RMSMOD_OP_MXFP4 = 8                      /* D_or_C: the row length K */
+    RMSMOD_OP_MXFP4 = 8,                     /* D_or_C: the row length K */
+    RMSMOD_OP_MXFP8 = 9,                     /* D_or_C: the row length K (or N) */
+    RMSMOD_OP_ADD_RMSNORM_MXFP8 = 10         /* and rmsnorm_mxfp8_backward */
 };
 
 /* 1 if `op` supports row length / channel count `D_or_C` and every non-NULL
@@ -473,7 +607,7 @@ int rmsmod_supported(int op, int64_t D_or_C, const void* const* ptrs, int nptrs)
 
 /* Device error word of the kernels launched so far on the current device:
  * bit 0 (RMSMOD_DEVICE_ERR_COPY_TIMEOUT) = an asynchronous bulk copy into
- * shared memory (or, in the 4-bit product and in rows shared by two CTAs,
+ * shared memory (or, in the 4-bit and 8-bit products and in rows shared by two CTAs,
  * what a barrier waits for) did not complete within the wait limit (1 s); the
  * kernel then finished without that data instead of hanging, so its output
  * is invalid.  Synchronous (it reads device memory); `clear` != 0 resets the

@@ -8,13 +8,13 @@ no CPU fallback: if the library is not built, or the tensors are not on a
 CUDA device, the call raises.
 
 Tensors are ``torch.bfloat16`` on a CUDA device with a contiguous innermost
-dimension (the sandwich norms and the 4-bit calls take ``torch.float16`` too,
+dimension (the sandwich norms, the 4-bit and the 8-bit calls take ``torch.float16`` too,
 and run on their tensors' device whichever is current).  Modulation rows (``scale``, ``shift``, ``gate``) may be given
 as ``[D]``, ``[1, D]``, ``[B, D]``, ``[1, 1, D]`` or ``[B, 1, D]``; per-batch
 rows may be strided views (adaLN chunk views of one projection output).
 
 Every call takes a ``stream`` (default: the current one), which the caller orders after its inputs.
-What the sandwich norms, rmsnorm_modulate_backward and the 4-bit calls allocate is that stream's, and
+What the sandwich norms, rmsnorm_modulate_backward, the 4-bit and the 8-bit calls allocate is that stream's, and
 the current stream is noted as using their results; the other calls allocate on the current stream,
 so with another one pass them their outputs.
 """
@@ -36,11 +36,13 @@ __all__ = [
     "gated_rmsnorm_modulate", "qk_layernorm", "rmsnorm_silu_cl", "modulate_scale_shift",
     "residual_gate_add", "conv_bias_epilogue", "sandwich_rmsnorm_modulate",
     "sandwich_rmsnorm_modulate_backward", "SandwichGrads", "rmsnorm_modulate_backward", "Mxfp4", "mxfp4_quantize", "mxfp4_dequantize",
-    "mxfp4_scale_bytes", "mxfp4_linear", "supported", "status_string", "device_status",
+    "mxfp4_scale_bytes", "mxfp4_linear", "Mxfp8", "mxfp8_scale_bytes", "mxfp8_quantize",
+    "mxfp8_dequantize", "mxfp8_transpose", "mxfp8_linear", "mxfp8_activation_backward",
+    "add_rmsnorm_mxfp8", "rmsnorm_mxfp8_backward", "supported", "status_string", "device_status",
     "selftest_wait_timeout",
     "OP_LN_MODULATE", "OP_RMSNORM_MODULATE", "OP_GATED_RMSNORM_MODULATE",
     "OP_QK_LAYERNORM", "OP_RMSNORM_SILU_CL", "OP_LN_MODULATE_FOLDED",
-    "OP_SANDWICH_RMSNORM_MODULATE", "OP_MXFP4",
+    "OP_SANDWICH_RMSNORM_MODULATE", "OP_MXFP4", "OP_MXFP8", "OP_ADD_RMSNORM_MXFP8",
 ]
 
 _PKG = os.path.dirname(os.path.abspath(__file__))
@@ -54,6 +56,8 @@ OP_RMSNORM_SILU_CL = 5
 OP_LN_MODULATE_FOLDED = 6
 OP_SANDWICH_RMSNORM_MODULATE = 7
 OP_MXFP4 = 8
+OP_MXFP8 = 9
+OP_ADD_RMSNORM_MXFP8 = 10
 
 _lock = threading.Lock()
 _lib = None
@@ -107,6 +111,15 @@ def library() -> ctypes.CDLL:
             "mxfp4_quantize": [P, P, P, I, I, C, P],
             "mxfp4_dequantize": [P, P, P, I, I, C, P],
             "mxfp4_matmul": [P, P, P, P, P, P, I, P, P, I, I, I, I, C, P],
+            "mxfp8_quantize": [P, P, P, I, I, C, P],
+            "mxfp8_dequantize": [P, P, P, I, I, C, P],
+            "mxfp8_transpose": [P, P, P, P, I, I, P],
+            "mxfp8_matmul": [P, P, P, P, P, C, P, I, P, P, P, P, P, I, I, I, I, C, P],
+            "mxfp8_activation_backward": [P, P, P, C, P, I, P, P, P, P, I, I, I, P,
+                                          ctypes.c_size_t, C, P],
+            "add_rmsnorm_mxfp8": [P, P, P, P, P, I, P, P, P, P, P, I, I, I, F, P, C, P],
+            "rmsnorm_mxfp8_backward": [P, P, P, P, I, P, P, P, I, I, I, P, P, P, P, P,
+                                       ctypes.c_size_t, C, P],
             "rmsmod_supported": [C, I, ctypes.POINTER(P), C],
             "rmsmod_status_string": [C],
             "rmsmod_version": [],
@@ -119,11 +132,14 @@ def library() -> ctypes.CDLL:
             fn.restype = ctypes.c_int
         lib.rmsmod_status_string.restype = ctypes.c_char_p
         for name in ("sandwich_rmsnorm_modulate_backward_workspace_bytes",
-                     "rmsnorm_modulate_backward_workspace_bytes"):
+                     "rmsnorm_modulate_backward_workspace_bytes",
+                     "rmsnorm_mxfp8_backward_workspace_bytes",
+                     "mxfp8_activation_backward_workspace_bytes"):
             getattr(lib, name).argtypes = [I, I, I]
             getattr(lib, name).restype = ctypes.c_size_t
-        lib.mxfp4_scale_bytes.argtypes = [I, I]
-        lib.mxfp4_scale_bytes.restype = ctypes.c_size_t
+        for name in ("mxfp4_scale_bytes", "mxfp8_scale_bytes"):
+            getattr(lib, name).argtypes = [I, I]
+            getattr(lib, name).restype = ctypes.c_size_t
         _lib = lib
         return lib
 
@@ -190,10 +206,17 @@ def _aside(stream, device, call, *args):
         return call(*args, None)
     with torch.cuda.stream(stream):
         made = call(*args, None)
-    for t in made if isinstance(made, tuple) else (made,):
-        if t is not None:
-            t.record_stream(current)
+    _shared_with(made, current)
     return made
+
+
+def _shared_with(made, stream):
+    """Note `stream` on a call's results, however they are grouped."""
+    if isinstance(made, tuple):
+        for t in made:
+            _shared_with(t, stream)
+    elif made is not None:
+        made.record_stream(stream)
 
 
 def _bf16(t, name, dtype=torch.bfloat16):
@@ -948,6 +971,335 @@ def mxfp4_linear(x, w, bias=None, gate=None, residual=None, out=None, dtype=None
     _call_on(device, stream, "mxfp4_matmul", packed, scales, _at(w.packed), _at(w.scales), _at(bias),
              _at(gate), gs, _at(residual), _at(out), B, S, N, K, code)
     return out
+
+
+class Mxfp8(NamedTuple):
+    """A microscaled 8-bit matrix: `codes` torch.float8_e4m3fn [..., K] and `scales` uint8, the tiled
+    e8m0 scale bytes of its rows (mxfp8_scale_bytes(rows, K) of them; layout in include/rmsmod.h)."""
+
+    codes: torch.Tensor
+    scales: torch.Tensor
+
+
+_E4M3 = torch.float8_e4m3fn
+_ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+@functools.lru_cache(maxsize=256)
+def mxfp8_scale_bytes(rows: int, K: int) -> int:
+    """Bytes of the tiled scales of a [rows, K] 8-bit matrix (0 if the size is unsupported)."""
+    return int(library().mxfp8_scale_bytes(rows, K))
+
+
+def _codes8(q, name, device=None):
+    """-> (rows, K) of a checked Mxfp8."""
+    if not isinstance(q, Mxfp8):
+        raise TypeError(f"{name} must be an Mxfp8")
+    codes, scales = q
+    _dense(codes, f"{name}.codes", _E4M3)
+    _dense(scales, f"{name}.scales", torch.uint8)
+    if codes.device != scales.device or (device is not None and codes.device != device):
+        raise ValueError(f"{name} must be on {codes.device if device is None else device}")
+    shape = codes.shape
+    K = shape[-1] if shape else 0
+    if K == 0 or K % 32:
+        raise ValueError(f"{name}.codes must hold rows of a multiple of 32 values")
+    rows = codes.numel() // K
+    need = mxfp8_scale_bytes(rows, K)
+    if scales.numel() != need:
+        raise ValueError(f"{name}.scales must hold {need} bytes")
+    return rows, K
+
+
+def _new8(shape, rows, device):
+    """An Mxfp8 to be written."""
+    return Mxfp8(torch.empty(shape, dtype=_E4M3, device=device),
+                 torch.empty(mxfp8_scale_bytes(rows, shape[-1]), dtype=torch.uint8, device=device))
+
+
+def _out8(q, name, shape, device):
+    """A checked Mxfp8 of that shape to write to."""
+    _codes8(q, name, device)
+    if q.codes.shape != shape:
+        raise ValueError(f"{name}.codes shape {tuple(q.codes.shape)} != {tuple(shape)}")
+    return q
+
+
+def _activation(name):
+    code = _ACTIVATIONS.get(name) if name is None or isinstance(name, str) else None
+    if code is None:
+        raise ValueError(f"activation must be None, 'silu', 'gelu' or 'gelu_tanh', got {name!r}")
+    return code
+
+
+def mxfp8_quantize(x, out=None, stream=None) -> Mxfp8:
+    """Rows of x [..., K] (bfloat16 or float16, K a multiple of 32) in blocks of 32 e4m3 codes
+    under the least power-of-two scale that holds the block without saturation."""
+    _half(x, "x")
+    if stream is not None and out is None:
+        return _aside(stream, x.device, mxfp8_quantize, x, out)
+    K = x.shape[-1] if x.dim() else 0
+    if K == 0 or K % 32:
+        raise ValueError("x must hold rows of a multiple of 32 values")
+    rows = x.numel() // K
+    if out is None:
+        out = _new8(x.shape, rows, x.device)
+    else:
+        _out8(out, "out", x.shape, x.device)
+    _call_on(x.device, stream, "mxfp8_quantize", _at(x), _at(out.codes), _at(out.scales), rows, K,
+             _DTYPES[x.dtype])
+    return out
+
+
+def mxfp8_dequantize(q, dtype=torch.bfloat16, out=None, stream=None):
+    """The values that q stands for, as bfloat16 or float16 [..., K]."""
+    rows, K = _codes8(q, "q")
+    if stream is not None and out is None:
+        return _aside(stream, q.codes.device, mxfp8_dequantize, q, dtype, out)
+    if dtype not in _DTYPES:
+        raise TypeError(f"dtype must be torch.bfloat16 or torch.float16, got {dtype}")
+    if out is None:
+        out = torch.empty(q.codes.shape, dtype=dtype, device=q.codes.device)
+    else:
+        _input(out, "out", dtype, q.codes.device, q.codes.shape)
+    _call_on(out.device, stream, "mxfp8_dequantize", _at(q.codes), _at(q.scales), _at(out), rows, K,
+             _DTYPES[dtype])
+    return out
+
+
+def mxfp8_transpose(q, out=None, stream=None) -> Mxfp8:
+    """The matrix q [..., K] of R rows as [K, R up to a multiple of 32], in blocks along its rows
+    (zeros behind the last one): what a weight's gradient takes of an activation and of its
+    gradient, and an input's gradient of a weight.  A value keeps its bits but where it is under 2^-6
+    of its new block's scale."""
+    rows, K = _codes8(q, "q")
+    device = q.codes.device
+    if stream is not None and out is None:
+        return _aside(stream, device, mxfp8_transpose, q, out)
+    shape = (K, -(-rows // 32) * 32)
+    if out is None:
+        if not rows:
+            raise ValueError("q must have rows")
+        out = _new8(shape, K, device)
+    else:
+        _out8(out, "out", shape, device)
+    _call_on(device, stream, "mxfp8_transpose", _at(q.codes), _at(q.scales), _at(out.codes),
+             _at(out.scales), rows, K)
+    return out
+
+
+def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out=None, dtype=None,
+                 quantize=False, keep=False, stream=None):
+    """A projection in 8 bits with its epilogue:
+
+        z = x w^T + bias,  y = residual + gate * act(z)
+
+    -> y, rounded once, or with `quantize` as an Mxfp8 in blocks along N; with `keep` (y, z), z an
+    Mxfp8 for mxfp8_activation_backward.
+
+    x [..., K]: bfloat16 or float16 (quantised here) or an Mxfp8 (then `dtype`, default bfloat16, is
+    the type of the result, bias, gate and residual; torch.float32 too, for a weight's gradient); w:
+    an Mxfp8 [N, K].  activation: None, "silu", "gelu" or "gelu_tanh".  bias [N]; gate rows [N] or
+    [B, 1, N] (for x [B, S, K]); residual [..., N].  N a multiple of 8, of 32 with `quantize` or
+    `keep`.  out (of y) may be residual; keep may be the Mxfp8 to write z to."""
+    if stream is not None and (out is None or keep is True or not isinstance(x, Mxfp8)):
+        at = x.codes if isinstance(x, Mxfp8) else x
+        if not isinstance(at, torch.Tensor):
+            raise TypeError("x must be a torch.Tensor or an Mxfp8")
+        return _aside(stream, at.device, mxfp8_linear, x, w, bias, activation, gate, residual, out,
+                      dtype, quantize, keep)
+    if isinstance(x, Mxfp8):
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in _DTYPES and dtype != torch.float32:
+            raise TypeError("dtype must be torch.bfloat16, torch.float16 or torch.float32, "
+                            f"got {dtype}")
+        width = _codes8(x, "x")[1]
+        lead, device = x.codes.shape[:-1], x.codes.device
+    else:
+        _half(x, "x")
+        if dtype is not None and dtype != x.dtype:
+            raise TypeError(f"dtype must be x's, {x.dtype}")
+        dtype, lead, device = x.dtype, x.shape[:-1], x.device
+        width = x.shape[-1] if x.dim() else 0
+    act = _activation(activation)
+    N, K = _codes8(w, "w", device)
+    eight = quantize or bool(keep)
+    if w.codes.dim() != 2 or N % (32 if eight else 8):
+        raise ValueError(f"w must be [N, K], N a multiple of {32 if eight else 8}")
+    if len(lead) == 0 or width != K:
+        raise ValueError(f"x must hold rows of K={K} values")
+    B = lead[0] if len(lead) > 1 else 1
+    M = 1
+    for n in lead:
+        M *= n
+    S = M // B if B else 0
+    _vector(bias, "bias", dtype, device, N)
+    gs = _rows(gate, "gate", dtype, device, B, N)
+    shape = (*lead, N)
+    if residual is not None:
+        _input(residual, "residual", dtype, device, shape)
+    if quantize:
+        out = _new8(shape, M, device) if out is None else _out8(out, "out", shape, device)
+        y, y_scales = _at(out.codes), _at(out.scales)
+    else:
+        if out is None:
+            out = torch.empty(shape, dtype=dtype, device=device)
+        else:
+            _input(out, "out", dtype, device, shape)
+        y, y_scales = _at(out), None
+    kept = None
+    if keep is True:
+        kept = _new8(shape, M, device)
+    elif keep:
+        kept = _out8(keep, "keep", shape, device)
+    code = 2 if dtype == torch.float32 else _DTYPES[dtype]
+    if isinstance(x, Mxfp8):
+        codes, scales = _at(x.codes), _at(x.scales)
+    else:
+        n = M * K  # a multiple of 32
+        q = torch.empty(n + mxfp8_scale_bytes(M, K), dtype=torch.uint8, device=device)
+        codes = _at(q)
+        scales = codes + n
+        _call_on(device, stream, "mxfp8_quantize", _at(x), codes, scales, M, K, code)
+    _call_on(device, stream, "mxfp8_matmul", codes, scales, _at(w.codes), _at(w.scales), _at(bias),
+             act, _at(gate), gs, _at(residual), y, y_scales,
+             None if kept is None else _at(kept.codes),
+             None if kept is None else _at(kept.scales), B, S, N, K, code)
+    return out if kept is None else (out, kept)
+
+
+def mxfp8_activation_backward(z, grad_out, activation=None, gate=None, need_sums=True, out=None,
+                              workspace=None, stream=None):
+    """Gradients of y = residual + gate * act(z), z = x w^T + bias, from the checkpoint z [..., N] of
+    mxfp8_linear and grad_out, the gradient of y (bfloat16 or float16): -> (grad_z, grad_bias,
+    grad_gate), grad_z = Q(grad_out * gate * act'(z)) an Mxfp8, grad_bias fp32 [N] (the sum of
+    grad_z's values before Q), grad_gate fp32 [B, N] ([1, N] where one row is shared), None without
+    gate.  The sums (in an order that the sizes fix) take a workspace, allocated here unless one is
+    passed; both are None without need_sums.
+
+    Then the gradients of x and w are products of 8-bit rows again:
+    mxfp8_linear(grad_z, mxfp8_transpose(w)) and
+    mxfp8_linear(mxfp8_transpose(grad_z), mxfp8_transpose(x), dtype=torch.float32)."""
+    if stream is not None:
+        if not isinstance(z, Mxfp8):
+            raise TypeError("z must be an Mxfp8")
+        return _aside(stream, z.codes.device, mxfp8_activation_backward, z, grad_out, activation,
+                      gate, need_sums, out, workspace)
+    rows, N = _codes8(z, "z")
+    device, shape = z.codes.device, z.codes.shape
+    _half(grad_out, "grad_out")
+    dt = grad_out.dtype
+    _input(grad_out, "grad_out", dt, device, shape)
+    act = _activation(activation)
+    B = shape[0] if len(shape) > 2 else 1
+    S = rows // B if B else 0
+    gs = _rows(gate, "gate", dt, device, B, N)
+    out = _new8(shape, rows, device) if out is None else _out8(out, "out", shape, device)
+    grad_bias = _vector_grad(need_sums, N, device)
+    grad_gate = _row_grads(need_sums and gate is not None, gs, B, N, device)
+    workspace, wbytes = _backward_workspace("mxfp8_activation_backward", workspace, need_sums, B, S,
+                                            N, device)
+    _call_on(device, stream, "mxfp8_activation_backward", _at(z.codes), _at(z.scales),
+             _at(grad_out), act, _at(gate), gs, _at(out.codes), _at(out.scales), _at(grad_bias),
+             _at(grad_gate), B, S, N, _at(workspace), wbytes, _DTYPES[dt])
+    return out, grad_bias, grad_gate
+
+
+def add_rmsnorm_mxfp8(x, update=None, weight=None, scale=None, shift=None, eps: float = 1e-6,
+                      keep=False, res_out=None, out=None, rstd_out=None, stream=None):
+    """The residual add and the norm before a projection in 8 bits:
+
+        res = R(x + update),  out = Q(RMSNorm(res) * weight * (1 + scale) + shift)
+
+    -> (res, out, kept): out an Mxfp8 for mxfp8_linear, rounded from fp32 once; kept = Q(res) with
+    `keep` (True, or the Mxfp8 to write to), the checkpoint that rmsnorm_mxfp8_backward takes, else
+    None.  bfloat16 or float16, rows of a multiple of 32 values.  Without update res is x itself.  A
+    missing weight or scale is a factor of 1, a missing shift 0.  res_out may be x or update.
+    rstd_out: fp32 [B * S] for the backward pass."""
+    _half(x, "x")
+    dt, device, shape = x.dtype, x.device, x.shape
+    if stream is not None and (out is None or keep is True or
+                               (update is not None and res_out is None)):
+        made = _aside(stream, device, _add_rmsnorm_mxfp8_made, x, update, weight, scale, shift, eps,
+                      keep, res_out, out, rstd_out)
+        return (x, *made[1:]) if update is None else made
+    B, S, D = shape if len(shape) == 3 else _bsd(x, "x", dt)
+    if D % 32:
+        raise ValueError("x must hold rows of a multiple of 32 values")
+    if update is not None:
+        _input(update, "update", dt, device, shape)
+    elif res_out is not None:
+        raise ValueError("res_out needs update")
+    _vector(weight, "weight", dt, device, D)
+    bs = _modulation(scale, shift, dt, device, B, D)
+    res = x
+    if update is not None:
+        if res_out is None:
+            res_out = torch.empty_like(x)
+        else:
+            _input(res_out, "res_out", dt, device, shape)
+        res = res_out
+    rows = B * S
+    out = _new8(shape, rows, device) if out is None else _out8(out, "out", shape, device)
+    kept = None
+    if keep is True:
+        kept = _new8(shape, rows, device)
+    elif keep:
+        kept = _out8(keep, "keep", shape, device)
+    _stats(rstd_out, "rstd_out", device, rows)
+    _call_on(device, stream, "add_rmsnorm_mxfp8", _at(x), _at(update), _at(weight), _at(scale),
+             _at(shift), bs, _at(res_out), _at(out.codes), _at(out.scales),
+             None if kept is None else _at(kept.codes),
+             None if kept is None else _at(kept.scales), B, S, D, eps, _at(rstd_out), _DTYPES[dt])
+    return res, out, kept
+
+
+def _add_rmsnorm_mxfp8_made(x, update, *args):
+    """add_rmsnorm_mxfp8's results without x among them: what another stream has made."""
+    res, out, kept = add_rmsnorm_mxfp8(x, update, *args)
+    return None if update is None else res, out, kept
+
+
+def rmsnorm_mxfp8_backward(kept, weight, scale, grad_out, rstd, grad_res=None, need_x=True,
+                           need_mod=True, workspace=None, stream=None, shift=None):
+    """Gradients of add_rmsnorm_mxfp8 (weight, scale as in the forward; kept and rstd as it left
+    them) -> (grad_x, grad_weight, grad_scale, grad_shift), grad_x by x and by update alike.
+    grad_out: the gradient of out; grad_res: one that reaches res on the residual stream, added to
+    grad_x before its rounding.  grad_weight fp32 [D]; grad_scale, grad_shift fp32 [B, D] ([1, D]
+    where one row is shared), None without scale; where the forward had shift and no scale, it is
+    given here too (its rows' shape and stride are read, its values are not).  Workspace as in
+    sandwich_rmsnorm_modulate_backward."""
+    if stream is not None:
+        if not isinstance(kept, Mxfp8):
+            raise TypeError("kept must be an Mxfp8")
+        return _aside(stream, kept.codes.device,
+                      functools.partial(rmsnorm_mxfp8_backward, shift=shift), kept, weight, scale,
+                      grad_out, rstd, grad_res, need_x, need_mod, workspace)
+    rows, D = _codes8(kept, "kept")
+    device, shape = kept.codes.device, kept.codes.shape
+    _half(grad_out, "grad_out")
+    dt = grad_out.dtype
+    _input(grad_out, "grad_out", dt, device, shape)
+    if len(shape) != 3 and len(shape) != 2:
+        raise ValueError("kept must be [B, S, D] or [S, D]")
+    B = shape[0] if len(shape) == 3 else 1
+    S = shape[-2]
+    if grad_res is not None:
+        _input(grad_res, "grad_res", dt, device, shape)
+    _vector(weight, "weight", dt, device, D)
+    bs = _modulation(scale, shift, dt, device, B, D)
+    _need_stats(rstd, "rstd", device, rows)
+    grad_x = torch.empty_like(grad_out) if need_x else None
+    grad_weight = _vector_grad(need_mod and weight is not None, D, device)
+    grad_scale = _row_grads(need_mod and scale is not None, bs, B, D, device)
+    grad_shift = _row_grads(need_mod and (scale is not None or shift is not None), bs, B, D, device)
+    workspace, wbytes = _backward_workspace("rmsnorm_mxfp8_backward", workspace, need_mod, B, S, D,
+                                            device)
+    _call_on(device, stream, "rmsnorm_mxfp8_backward", _at(kept.codes), _at(kept.scales),
+             _at(weight), _at(scale), bs, _at(grad_out), _at(grad_res), _at(rstd), B, S, D,
+             _at(grad_x), _at(grad_weight), _at(grad_scale), _at(grad_shift), _at(workspace), wbytes,
+             _DTYPES[dt])
+    return grad_x, grad_weight, grad_scale, grad_shift
 
 
 def device_status(clear: bool = False) -> int:

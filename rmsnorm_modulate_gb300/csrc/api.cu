@@ -11,6 +11,7 @@
 #include "../../include/rmsmod.h"
 #include "launch.h"
 #include "mxfp4.h"
+#include "mxfp8.h"
 #include "sandwich.h"
 #include "selftest.h"
 
@@ -137,18 +138,20 @@ RMSMOD_EXPORT int rmsmod_device_status(unsigned int* bits, int clear)
 {
     if (!bits)
         return RMSMOD_ERR_NULL;
-    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0;
+    unsigned a = 0, b = 0, c = 0, d = 0, e = 0, f = 0, g = 0, h = 0, i = 0;
     if (rmsmod::row_kernels_error(&a, clear != 0) != cudaSuccess ||
         rmsmod::qk_kernel_error(&b, clear != 0) != cudaSuccess ||
         rmsmod::wan_kernel_error(&c, clear != 0) != cudaSuccess ||
         rmsmod::backward_error(&d, clear != 0) != cudaSuccess ||
         rmsmod::selftest_error(&e, clear != 0) != cudaSuccess ||
         rmsmod::mxfp4_matmul_error(&f, clear != 0) != cudaSuccess ||
-        rmsmod::sandwich_error(&g, clear != 0) != cudaSuccess) {
+        rmsmod::sandwich_error(&g, clear != 0) != cudaSuccess ||
+        rmsmod::mxfp8_matmul_error(&h, clear != 0) != cudaSuccess ||
+        rmsmod::mxfp8_norm_error(&i, clear != 0) != cudaSuccess) {
         cudaGetLastError();
         return RMSMOD_ERR_CUDA;
     }
-    *bits = a | b | c | d | e | f | g;
+    *bits = a | b | c | d | e | f | g | h | i;
     return RMSMOD_OK;
 }
 
@@ -184,6 +187,14 @@ RMSMOD_EXPORT int rmsmod_supported(int op, int64_t D_or_C, const void* const* pt
         break;
     case RMSMOD_OP_MXFP4:
         if (D_or_C > RMSMOD_MXFP4_MAX_K || D_or_C % 32 != 0)
+            return 0;
+        break;
+    case RMSMOD_OP_MXFP8:
+        if (D_or_C > RMSMOD_MXFP8_MAX_K || D_or_C % 32 != 0)
+            return 0;
+        break;
+    case RMSMOD_OP_ADD_RMSNORM_MXFP8:
+        if (D_or_C > RMSMOD_MAX_D || D_or_C % 32 != 0)
             return 0;
         break;
     default:
@@ -1163,4 +1174,419 @@ RMSMOD_EXPORT int mxfp4_matmul(const void* a, const void* a_scales, const void* 
     g.K = K;
     g.f16 = dtype == RMSMOD_F16;
     return launch_status(rmsmod::launch_mxfp4_matmul(g, dev, stream));
+}
+
+// ---- microscaled 8-bit rows, the norm before them, their product, and their backward pass ----------
+
+namespace {
+
+// Bytes of the codes and the tiled scales of an 8-bit matrix; false if unsupported.
+struct Mxfp8Size {
+    int64_t codes, scales, block_tiles, row_tiles;
+};
+
+bool mxfp8_size(int64_t rows, int64_t K, Mxfp8Size& z)
+{
+    Mxfp4Size t;  // the same blocks and tiles
+    if (!mxfp4_size(rows, K, t))
+        return false;
+    z = Mxfp8Size{rows * K, t.scale_bytes, t.block_tiles, t.row_tiles};
+    return true;
+}
+
+bool activation_ok(int activation)
+{
+    return activation >= RMSMOD_ACT_NONE && activation <= RMSMOD_ACT_GELU_TANH;
+}
+
+int mxfp8_rows(bool quantize, const void* values, const void* codes, const void* scales,
+               int64_t rows, int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    Mxfp8Size z;
+    if (!mxfp8_size(rows, K, z))
+        return RMSMOD_ERR_SHAPE;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    if (rows == 0)
+        return RMSMOD_OK;
+    if (!values || !codes || !scales)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(values, 16) || !aligned(codes, 16) || !aligned(scales, 16))
+        return RMSMOD_ERR_ALIGN;
+    const Span all[] = {{values, rows * K * 2}, {codes, z.codes}, {scales, z.scales}};
+    const Span none[] = {{nullptr, 0}};
+    if (!apart(none, all))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    const int st = device_info(dev);
+    if (st != RMSMOD_OK)
+        return st;
+    rmsmod::Mxfp8RowsArgs a{};
+    a.values = const_cast<void*>(values);
+    a.codes = const_cast<void*>(codes);
+    a.scales = const_cast<void*>(scales);
+    a.rows = static_cast<uint32_t>(rows);
+    a.rows_padded = static_cast<uint32_t>(z.row_tiles * 128);
+    a.Kv = static_cast<uint32_t>(K / 8);
+    a.by_tiles = rmsmod::FastDiv::make(static_cast<uint32_t>(z.block_tiles));
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_mxfp8_rows(quantize, a, stream));
+}
+
+// check_rows31, and rows of whole blocks.
+int check_blocks31(int64_t B, int64_t S, int64_t D)
+{
+    const int st = check_rows31(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    Mxfp8Size z;
+    return D % 32 != 0 || !mxfp8_size(B * S, D, z) ? RMSMOD_ERR_SHAPE : RMSMOD_OK;
+}
+
+int zeroed(void* p, int64_t bytes, rmsmod_stream_t stream)
+{
+    if (!p || bytes <= 0 ||
+        cudaMemsetAsync(p, 0, static_cast<size_t>(bytes), stream) == cudaSuccess)
+        return RMSMOD_OK;
+    cudaGetLastError();
+    return RMSMOD_ERR_CUDA;
+}
+
+}  // namespace
+
+RMSMOD_EXPORT size_t mxfp8_scale_bytes(int64_t rows, int64_t K)
+{
+    Mxfp8Size z;
+    return mxfp8_size(rows, K, z) ? static_cast<size_t>(z.scales) : 0;
+}
+
+RMSMOD_EXPORT int mxfp8_quantize(const void* x, void* codes, void* scales, int64_t rows,
+                                 int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    return mxfp8_rows(true, x, codes, scales, rows, K, dtype, stream);
+}
+
+RMSMOD_EXPORT int mxfp8_dequantize(const void* codes, const void* scales, void* out, int64_t rows,
+                                   int64_t K, int dtype, rmsmod_stream_t stream)
+{
+    return mxfp8_rows(false, out, codes, scales, rows, K, dtype, stream);
+}
+
+RMSMOD_EXPORT int mxfp8_transpose(const void* codes, const void* scales, void* out_codes,
+                                  void* out_scales, int64_t rows, int64_t K,
+                                  rmsmod_stream_t stream)
+{
+    Mxfp8Size z, t;
+    if (rows < 0 || rows > RMSMOD_MXFP8_MAX_K || !mxfp8_size(rows, K, z))
+        return RMSMOD_ERR_SHAPE;
+    if (rows == 0)
+        return RMSMOD_OK;
+    if (!mxfp8_size(K, (rows + 31) / 32 * 32, t))
+        return RMSMOD_ERR_SHAPE;
+    if (!codes || !scales || !out_codes || !out_scales)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(codes, 16) || !aligned(scales, 16) || !aligned(out_codes, 16) ||
+        !aligned(out_scales, 16))
+        return RMSMOD_ERR_ALIGN;
+    const Span in[] = {{codes, z.codes}, {scales, z.scales}};
+    const Span outs[] = {{out_codes, t.codes}, {out_scales, t.scales}};
+    if (!apart(in, outs))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    const int st = device_info(dev);
+    if (st != RMSMOD_OK)
+        return st;
+    rmsmod::Mxfp8TransposeArgs a{codes, scales, out_codes, out_scales, rows, K};
+    return launch_status(rmsmod::launch_mxfp8_transpose(a, stream));
+}
+
+RMSMOD_EXPORT int mxfp8_matmul(const void* a, const void* a_scales, const void* b,
+                               const void* b_scales, const void* bias, int activation,
+                               const void* gate, int64_t gate_bstride, const void* residual,
+                               void* out, void* out_scales, void* keep, void* keep_scales,
+                               int64_t B, int64_t S, int64_t N, int64_t K, int dtype,
+                               rmsmod_stream_t stream)
+{
+    if (B < 0 || S < 0 || (B != 0 && S > INT64_MAX / B) || N < 0 || N % 8 != 0)
+        return RMSMOD_ERR_SHAPE;
+    const int64_t M = B * S;
+    Mxfp8Size za, zb, zo{0, 0, 0, 0};
+    if (!mxfp8_size(M, K, za) || !mxfp8_size(N, K, zb) || N > (int64_t{1} << 23))
+        return RMSMOD_ERR_SHAPE;
+    if ((out_scales || keep || keep_scales) && N != 0 && !mxfp8_size(M, N, zo))
+        return RMSMOD_ERR_SHAPE;
+    if (!(dtype_ok(dtype) || dtype == RMSMOD_F32) || !activation_ok(activation))
+        return RMSMOD_ERR_UNSUPPORTED;
+    int st;
+    if ((st = check_bstride_span(B, gate_bstride)) != RMSMOD_OK)
+        return st;
+    if (M == 0 || N == 0)
+        return RMSMOD_OK;
+    if (!a || !a_scales || !b || !b_scales || !out || (keep == nullptr) != (keep_scales == nullptr))
+        return RMSMOD_ERR_NULL;
+    if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(b, 16) || !aligned(b_scales, 16) ||
+        !aligned(bias, 16) || !aligned(gate, 16) || !aligned(residual, 16) || !aligned(out, 16) ||
+        !aligned(out_scales, 16) || !aligned(keep, 16) || !aligned(keep_scales, 16))
+        return RMSMOD_ERR_ALIGN;
+    const int64_t each = dtype == RMSMOD_F32 ? 4 : 2;
+    const int64_t out_bytes = M * N * (out_scales ? 1 : each);
+    const Span in[] = {{a, za.codes},    {a_scales, za.scales},
+                       {b, zb.codes},    {b_scales, zb.scales},
+                       {bias, each * N}, {gate, ((B - 1) * gate_bstride + N) * each}};
+    const Span outs[] = {{out, out_bytes},
+                         {out_scales, zo.scales},
+                         {keep, zo.codes},
+                         {keep_scales, zo.scales}};
+    const Span res[] = {{residual, M * N * each}};
+    const Span beside[] = {outs[1], outs[2], outs[3]};
+    const bool in_place = out == residual && !out_scales;
+    if (!apart(in, outs) || !apart(res, beside) ||
+        (!in_place && overlap(out, out_bytes, residual, M * N * each)))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    rmsmod::Mxfp8MatmulArgs g{};
+    g.a = a;
+    g.a_scales = a_scales;
+    g.b = b;
+    g.b_scales = b_scales;
+    g.bias = bias;
+    g.gate = gate;
+    g.gate_bstride = gate_bstride;
+    g.residual = residual;
+    g.out = out;
+    g.out_scales = out_scales;
+    g.keep = keep;
+    g.keep_scales = keep_scales;
+    g.M = M;
+    g.S = S;
+    g.N = N;
+    g.K = K;
+    g.type = dtype;
+    g.activation = activation;
+    return launch_status(rmsmod::launch_mxfp8_matmul(g, dev, stream));
+}
+
+RMSMOD_EXPORT int add_rmsnorm_mxfp8(const void* x, const void* update, const void* weight,
+                                    const void* scale, const void* shift, int64_t mod_bstride,
+                                    void* res_out, void* out, void* out_scales, void* keep,
+                                    void* keep_scales, int64_t B, int64_t S, int64_t D, float eps,
+                                    float* rstd_out, int dtype, rmsmod_stream_t stream)
+{
+    int st = check_blocks31(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    if ((st = check_bstride_span(B, mod_bstride)) != RMSMOD_OK)
+        return st;
+    const int64_t rows = B * S;
+    if (rows == 0)
+        return RMSMOD_OK;
+    if (!x || !out || !out_scales || (update && !res_out) ||
+        (keep == nullptr) != (keep_scales == nullptr))
+        return RMSMOD_ERR_NULL;
+    if (!update && res_out)
+        return RMSMOD_ERR_UNSUPPORTED;
+    if (!aligned(x, 16) || !aligned(update, 16) || !aligned(weight, 16) || !aligned(scale, 16) ||
+        !aligned(shift, 16) || !aligned(res_out, 16) || !aligned(out, 16) ||
+        !aligned(out_scales, 16) || !aligned(keep, 16) || !aligned(keep_scales, 16) ||
+        !aligned(rstd_out, 4))
+        return RMSMOD_ERR_ALIGN;
+    Mxfp8Size z;
+    mxfp8_size(rows, D, z);
+    const int64_t bytes = tensor_bytes(rows, D), mod_bytes = rows_span(B, mod_bstride, D);
+    const Span in[] = {{weight, 2 * D}, {scale, mod_bytes}, {shift, mod_bytes}};
+    const Span outs[] = {{res_out, bytes},  {out, z.codes},          {out_scales, z.scales},
+                         {keep, z.codes},   {keep_scales, z.scales}, {rstd_out, 4 * rows}};
+    const Span rows_in[] = {{x, bytes}, {update, bytes}};
+    const Span beside[] = {outs[1], outs[2], outs[3], outs[4], outs[5]};
+    if (!apart(in, outs) || !apart(rows_in, beside) || bad_alias(res_out, x, bytes, true) ||
+        bad_alias(res_out, update, bytes, true))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    rmsmod::Mxfp8NormArgs a{};
+    a.x = x;
+    a.update = update;
+    a.weight = weight;
+    a.scale = scale;
+    a.shift = shift;
+    a.mod_bstride = mod_bstride;
+    a.res_out = res_out;
+    a.out = out;
+    a.out_scales = out_scales;
+    a.keep = keep;
+    a.keep_scales = keep_scales;
+    a.rstd_out = rstd_out;
+    a.rows = static_cast<uint32_t>(rows);
+    a.S = static_cast<uint32_t>(S);
+    a.D = static_cast<int>(D);
+    a.eps = eps;
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_mxfp8_norm(a, dev, stream));
+}
+
+RMSMOD_EXPORT size_t rmsnorm_mxfp8_backward_workspace_bytes(int64_t B, int64_t S, int64_t D)
+{
+    if (check_blocks31(B, S, D) != RMSMOD_OK || B == 0 || S == 0)
+        return 0;
+    return rmsmod::mxfp8_norm_backward_workspace_bytes(B, S, D);
+}
+
+RMSMOD_EXPORT int rmsnorm_mxfp8_backward(const void* kept, const void* kept_scales,
+                                         const void* weight, const void* scale,
+                                         int64_t mod_bstride, const void* grad_out,
+                                         const void* grad_res, const float* rstd, int64_t B,
+                                         int64_t S, int64_t D, void* grad_x, float* grad_weight,
+                                         float* grad_scale, float* grad_shift, void* workspace,
+                                         size_t workspace_bytes, int dtype,
+                                         rmsmod_stream_t stream)
+{
+    int st = check_blocks31(B, S, D);
+    if (st != RMSMOD_OK)
+        return st;
+    if (!dtype_ok(dtype))
+        return RMSMOD_ERR_UNSUPPORTED;
+    if ((st = check_bstride_span(B, mod_bstride)) != RMSMOD_OK)
+        return st;
+    const int64_t rows = B * S;
+    if (rows != 0 && (!kept || !kept_scales || !grad_out || !rstd))
+        return RMSMOD_ERR_NULL;
+    const bool sums = grad_weight || grad_scale || grad_shift;
+    if (!grad_x && !sums)
+        return RMSMOD_OK;
+    const size_t need =
+        rows && sums ? rmsmod::mxfp8_norm_backward_workspace_bytes(B, S, D) : 0;
+    if (need && !workspace)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(kept, 16) || !aligned(kept_scales, 16) || !aligned(weight, 16) ||
+        !aligned(scale, 16) || !aligned(grad_out, 16) || !aligned(grad_res, 16) ||
+        !aligned(rstd, 4) || !aligned(grad_x, 16) || !aligned(grad_weight, 16) ||
+        !aligned(grad_scale, 16) || !aligned(grad_shift, 16) || !aligned(workspace, 256))
+        return RMSMOD_ERR_ALIGN;
+    if (need && workspace_bytes < need)
+        return RMSMOD_ERR_SHAPE;
+    Mxfp8Size z;
+    mxfp8_size(rows, D, z);
+    const int64_t bytes = tensor_bytes(rows, D), mod_rows = mod_bstride ? B : 1;
+    const Span in[] = {{kept, z.codes},     {kept_scales, z.scales},
+                       {weight, 2 * D},     {scale, rows_span(B, mod_bstride, D)},
+                       {grad_out, bytes},   {grad_res, bytes},
+                       {rstd, 4 * rows}};
+    const Span outs[] = {{grad_x, bytes},
+                         {grad_weight, 4 * D},
+                         {grad_scale, 4 * D * mod_rows},
+                         {grad_shift, 4 * D * mod_rows},
+                         {need ? workspace : nullptr, static_cast<int64_t>(need)}};
+    if (!apart(in, outs))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    if (rows == 0) {  // sums over no tokens
+        for (int i = 1; i < 4 && st == RMSMOD_OK; ++i)
+            st = zeroed(const_cast<void*>(outs[i].p), outs[i].n, stream);
+        return st;
+    }
+    rmsmod::Mxfp8NormBwdArgs a{};
+    a.kept = kept;
+    a.kept_scales = kept_scales;
+    a.weight = weight;
+    a.scale = scale;
+    a.mod_bstride = mod_bstride;
+    a.grad_out = grad_out;
+    a.grad_res = grad_res;
+    a.rstd = rstd;
+    a.grad_x = grad_x;
+    a.grad_weight = grad_weight;
+    a.grad_scale = grad_scale;
+    a.grad_shift = grad_shift;
+    a.sums = sums;
+    a.partials = static_cast<float*>(workspace);
+    a.B = B;
+    a.S = S;
+    a.D = static_cast<int>(D);
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_mxfp8_norm_backward(a, dev, stream));
+}
+
+RMSMOD_EXPORT size_t mxfp8_activation_backward_workspace_bytes(int64_t B, int64_t S, int64_t N)
+{
+    Mxfp8Size z;
+    if (B <= 0 || S <= 0 || S > INT64_MAX / B || !mxfp8_size(B * S, N, z))
+        return 0;
+    return rmsmod::mxfp8_activation_backward_workspace_bytes(B, S, N, true, 2);
+}
+
+RMSMOD_EXPORT int mxfp8_activation_backward(const void* z, const void* z_scales,
+                                            const void* grad_out, int activation,
+                                            const void* gate, int64_t gate_bstride, void* grad_z,
+                                            void* grad_z_scales, float* grad_bias,
+                                            float* grad_gate, int64_t B, int64_t S, int64_t N,
+                                            void* workspace, size_t workspace_bytes, int dtype,
+                                            rmsmod_stream_t stream)
+{
+    Mxfp8Size size;
+    if (B < 0 || S < 0 || (B != 0 && S > INT64_MAX / B) || !mxfp8_size(B * S, N, size))
+        return RMSMOD_ERR_SHAPE;
+    if (!dtype_ok(dtype) || !activation_ok(activation))
+        return RMSMOD_ERR_UNSUPPORTED;
+    int st;
+    if ((st = check_bstride_span(B, gate_bstride)) != RMSMOD_OK)
+        return st;
+    const int64_t rows = B * S;
+    if (grad_gate && !gate)
+        return RMSMOD_ERR_UNSUPPORTED;
+    if (rows != 0 && (!z || !z_scales || !grad_out || !grad_z || !grad_z_scales))
+        return RMSMOD_ERR_NULL;
+    const bool sums = grad_bias || grad_gate;
+    const size_t need =
+        rows && sums ? rmsmod::mxfp8_activation_backward_workspace_bytes(B, S, N, true, 2) : 0;
+    if (need && !workspace)
+        return RMSMOD_ERR_NULL;
+    if (!aligned(z, 16) || !aligned(z_scales, 16) || !aligned(grad_out, 16) || !aligned(gate, 16) ||
+        !aligned(grad_z, 16) || !aligned(grad_z_scales, 16) || !aligned(grad_bias, 16) ||
+        !aligned(grad_gate, 16) || !aligned(workspace, 256))
+        return RMSMOD_ERR_ALIGN;
+    if (need && workspace_bytes < need)
+        return RMSMOD_ERR_SHAPE;
+    const Span in[] = {{z, size.codes},
+                       {z_scales, size.scales},
+                       {grad_out, rows * N * 2},
+                       {gate, rows_span(B, gate_bstride, N)}};
+    const Span outs[] = {{grad_z, size.codes},
+                         {grad_z_scales, size.scales},
+                         {grad_bias, 4 * N},
+                         {grad_gate, 4 * N * (gate_bstride ? B : 1)},
+                         {need ? workspace : nullptr, static_cast<int64_t>(need)}};
+    if (!apart(in, outs))
+        return RMSMOD_ERR_UNSUPPORTED;
+    DeviceInfo dev;
+    if ((st = device_info(dev)) != RMSMOD_OK)
+        return st;
+    if (rows == 0) {  // sums over no tokens
+        for (int i = 2; i < 4 && st == RMSMOD_OK; ++i)
+            st = zeroed(const_cast<void*>(outs[i].p), outs[i].n, stream);
+        return st;
+    }
+    rmsmod::Mxfp8ActBwdArgs a{};
+    a.z = z;
+    a.z_scales = z_scales;
+    a.grad_out = grad_out;
+    a.gate = gate;
+    a.gate_bstride = gate_bstride;
+    a.grad_z = grad_z;
+    a.grad_z_scales = grad_z_scales;
+    a.grad_bias = grad_bias;
+    a.grad_gate = grad_gate;
+    a.partials = static_cast<float*>(workspace);
+    a.B = B;
+    a.S = S;
+    a.N = N;
+    a.activation = activation;
+    a.f16 = dtype == RMSMOD_F16;
+    return launch_status(rmsmod::launch_mxfp8_activation_backward(a, stream));
 }

@@ -1,0 +1,518 @@
+// Microscaled 8-bit rows: quantisation and its inverse, their blocks laid out anew along the other
+// axis, and the gradient of an activation whose input they keep.
+//
+// Layout (what the block-scaled tensor core instructions read):
+//   codes    [rows, K] bytes, e4m3
+//   scales   tiles of 128 rows by 4 blocks, 512 bytes each, [row tile][block tile]; in a tile row r
+//            and block k stand at byte (r % 32) * 16 + (r / 32) * 4 + k.  Bytes of rows and blocks
+//            that the matrix does not have are zero.
+#include "device_common.cuh"
+#include "half_types.cuh"
+#include "launch.h"
+#include "mxfp8.cuh"
+#include "mxfp8.h"
+
+namespace rmsmod {
+
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kUnitsPerCta = kThreads / 16;
+
+// ---------------------------------------------------------------------------
+// rows to blocks and back
+// ---------------------------------------------------------------------------
+
+// A unit is the 128 values of one block tile in the four rows r, r + 32, r + 64, r + 96 of a row tile,
+// whose sixteen scale bytes are neighbours; 16 lanes take a unit, eight values of each row, so four
+// lanes share a block and a unit's scales are one store.  Neighbouring units are neighbours in the
+// rows.
+struct Unit {
+    uint32_t tile, row;
+    int64_t scale_word;  // of 16 bytes
+};
+
+__device__ __forceinline__ Unit unit_of(const Mxfp8RowsArgs& a, uint32_t u)
+{
+    Unit t;
+    const uint32_t line = a.by_tiles.div(u);  // (row tile, r)
+    t.tile = u - line * a.by_tiles.d;
+    t.row = (line >> 5) * 128 + (line & 31);
+    t.scale_word = (static_cast<int64_t>(line >> 5) * a.by_tiles.d + t.tile) * 32 + (line & 31);
+    return t;
+}
+
+// Eight values of one of the four lanes that share a block, to codes; the block's scale byte.
+__device__ __forceinline__ uint32_t quantize8(float (&f)[8], uint2& codes)
+{
+    uint32_t bits = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        bits = max(bits, magnitude_bits(f[j]));
+    bits = max(bits, __shfl_xor_sync(kFullMask, bits, 1));
+    bits = max(bits, __shfl_xor_sync(kFullMask, bits, 2));
+    const uint32_t byte = mx8_scale_byte(bits);
+    const float inv = mx8_inverse(byte);
+#pragma unroll
+    for (int j = 0; j < 8; ++j)
+        f[j] = __fmul_rn(f[j], inv);
+    codes = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
+    return byte;
+}
+
+// The four scale bytes of a row's block tile, from lanes 0, 4, 8 and 12 of its sixteen.
+__device__ __forceinline__ uint32_t join_bytes(uint32_t byte, int base)
+{
+    uint32_t w = __shfl_sync(kFullMask, byte, base);
+    w |= __shfl_sync(kFullMask, byte, base + 4) << 8;
+    w |= __shfl_sync(kFullMask, byte, base + 8) << 16;
+    w |= __shfl_sync(kFullMask, byte, base + 12) << 24;
+    return w;
+}
+
+__device__ __forceinline__ void values8(uint2 codes, float scale, float (&f)[8])
+{
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        const float2 p = e4m3x2_values(((j < 2 ? codes.x : codes.y) >> (16 * (j & 1))) & 0xFFFFu);
+        f[2 * j] = __fmul_rn(p.x, scale);
+        f[2 * j + 1] = __fmul_rn(p.y, scale);
+    }
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) quantize8_kernel(const Mxfp8RowsArgs a)
+{
+    grid_dependency_sync();
+    const int lane = threadIdx.x & 31;
+    const uint32_t sub = threadIdx.x & 15;  // which eight of the tile's 128 values
+    const Unit t = unit_of(a, blockIdx.x * kUnitsPerCta + (threadIdx.x >> 4));
+    const uint32_t col = t.tile * 16 + sub;
+    const uint4* __restrict__ x = static_cast<const uint4*>(a.values);
+    uint2* __restrict__ codes = static_cast<uint2*>(a.codes);
+    uint4 v[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = t.row + 32 * i;
+        v[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (row < a.rows && col < a.Kv)
+            v[i] = ld_stream(x + static_cast<int64_t>(row) * a.Kv + col);
+    }
+    uint4 four;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float f[8];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 p = widen2<T>(word(v[i], j));
+            f[2 * j] = p.x;
+            f[2 * j + 1] = p.y;
+        }
+        uint2 c;
+        word(four, i) = join_bytes(quantize8(f, c), lane & 16);
+        const uint32_t row = t.row + 32 * i;
+        if (row < a.rows && col < a.Kv)
+            codes[static_cast<int64_t>(row) * a.Kv + col] = c;
+    }
+    if (sub == 0 && t.row < a.rows_padded)
+        static_cast<uint4*>(a.scales)[t.scale_word] = four;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) dequantize8_kernel(const Mxfp8RowsArgs a)
+{
+    grid_dependency_sync();
+    const uint32_t sub = threadIdx.x & 15;
+    const Unit t = unit_of(a, blockIdx.x * kUnitsPerCta + (threadIdx.x >> 4));
+    const uint32_t col = t.tile * 16 + sub;
+    if (t.row >= a.rows || col >= a.Kv)
+        return;
+    const uint2* __restrict__ codes = static_cast<const uint2*>(a.codes);
+    uint4* __restrict__ out = static_cast<uint4*>(a.values);
+    const uint4 four = ld_cached(static_cast<const uint4*>(a.scales) + t.scale_word);
+    uint2 c[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = t.row + 32 * i;
+        c[i] = make_uint2(0u, 0u);
+        if (row < a.rows)
+            c[i] = ld_stream2(codes + static_cast<int64_t>(row) * a.Kv + col);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t row = t.row + 32 * i;
+        float f[8];
+        values8(c[i], mx8_scale((word(four, i) >> (8 * (sub >> 2))) & 0xFFu), f);
+        uint4 o;
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            word(o, j) = narrow2<T>(f[2 * j], f[2 * j + 1]);
+        if (row < a.rows)
+            st_stream(out + static_cast<int64_t>(row) * a.Kv + col, o);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// blocks along the other axis
+// ---------------------------------------------------------------------------
+
+// 128 x 128 codes by 128 threads: a thread takes four columns (one word of each row) of 32 rows, which
+// are four of the result's blocks, whole.
+//
+// A value is (1 + m / 8) * 2^(E + e), from a code's fp16 form (every e4m3 value is a normal fp16
+// number) and its scale's exponent: 8 E + m + 8 e, a whole number, orders the magnitudes, so the
+// block's scale is found without rounding whatever the exponents' spread.  Moving a value to the new
+// scale 2^n multiplies it by 2^(e - n), exact in fp32 where the result is not zero; the code keeps its
+// bits but for values under 2^-6 of the new scale's unit, which lose what lies below 2^-9 of it.
+constexpr int kTurn = 128;
+
+__device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
+
+// Order of the two codes' magnitudes (halves of the result), with e8 = 8 * scale byte; zero codes come
+// last.  `nan`: bits 8 and 24 where the code is NaN.
+__device__ __forceinline__ uint32_t order2(uint32_t half2, uint32_t e8, uint32_t& nan)
+{
+    const uint32_t k = (half2 >> 7) & 0x00FF00FFu;
+    nan = (k + 0x00010001u) & 0x01000100u;  // NaN: all of the eight bits
+    return k + (((k + 0x00FF00FFu) >> 8) & 0x00010001u) * e8;
+}
+
+__global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeArgs a)
+{
+    __shared__ __align__(16) uint32_t tile[kTurn * kTurn / 4];
+    __shared__ __align__(16) uint32_t scale_in[128], scale_out[128];
+    grid_dependency_sync();
+    const int64_t tiles_k = (a.K + 127) / 128, tiles_r = (a.rows + 127) / 128;
+    const int64_t tk = blockIdx.x % tiles_k, tr = blockIdx.x / tiles_k;
+    const int64_t r0 = tr * 128, k0 = tk * 128;
+    const int64_t padded = (a.rows + 31) / 32 * 32;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+    const uint8_t* __restrict__ codes = static_cast<const uint8_t*>(a.codes);
+    uint4 in[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int64_t r = r0 + i * 16 + (t >> 3), k = k0 + (t & 7) * 16;
+        in[i] = make_uint4(0u, 0u, 0u, 0u);
+        if (r < a.rows && k < a.K)
+            in[i] = ld_stream(reinterpret_cast<const uint4*>(codes + r * a.K + k));
+    }
+    {  // word t: row t / 4 + 32 * (t % 4)
+        const int64_t r = r0 + (t >> 2) + 32 * (t & 3);
+        scale_in[t] = r < a.rows ? __ldg(static_cast<const uint32_t*>(a.scales) +
+                                         (tr * tiles_k + tk) * 128 + t)
+                                 : 0u;
+        scale_out[t] = 0u;
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+        reinterpret_cast<uint4*>(tile)[i * kTurn + t] = in[i];
+    __syncthreads();
+    // rows r0 + 32 * warp ..., columns k0 + 4 * lane ...
+    const int block = lane >> 3;
+    uint32_t top[2] = {0u, 0u}, nan = 0u;
+#pragma unroll
+    for (int r = 0; r < 32; ++r) {
+        const uint32_t w = tile[(warp * 32 + r) * 32 + lane];
+        const uint32_t e = byte_of(scale_in[r * 4 + warp], block);
+        uint32_t n01, n23;
+        top[0] = __vmaxu2(top[0], order2(e4m3x2_half2(w & 0xFFFFu), e * 8u, n01));
+        top[1] = __vmaxu2(top[1], order2(e4m3x2_half2(w >> 16), e * 8u, n23));
+        nan |= n01 | (n23 << 1);
+        if (e == 255u)
+            nan = 0x03000300u;
+    }
+    uint32_t bytes[4];
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t k = (top[c >> 1] >> (16 * (c & 1))) & 0xFFFFu;
+        const int e = static_cast<int>(k >> 3) - 23 + ((k & 7u) == 7u ? 1 : 0);
+        bytes[c] = e > 0 ? static_cast<uint32_t>(e) : 0u;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+        if (nan & (0x100u << (16 * (c & 1)) << (c >> 1)))
+            bytes[c] = 255u;
+    uint32_t out[4][8];
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        uint32_t w4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * q + i;
+            const uint32_t w = tile[(warp * 32 + r) * 32 + lane];
+            const int e = static_cast<int>(byte_of(scale_in[r * 4 + warp], block));
+            const float2 lo = e4m3x2_values(w & 0xFFFFu), hi = e4m3x2_values(w >> 16);
+            const float v[4] = {lo.x, lo.y, hi.x, hi.y};
+            float s[4];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // 2^(e - n): at most 2^17 where the code is not zero
+                const int d = min(max(e - static_cast<int>(bytes[c]), -126), 17);
+                s[c] = __fmul_rn(v[c], __uint_as_float(static_cast<uint32_t>(d + 127) << 23));
+            }
+            w4[i] = e4m3x4(s[0], s[1], s[2], s[3]);
+        }
+        // four rows of four columns to four columns of four rows
+        const uint32_t a01 = __byte_perm(w4[0], w4[1], 0x5140), b01 = __byte_perm(w4[0], w4[1], 0x7362);
+        const uint32_t a23 = __byte_perm(w4[2], w4[3], 0x5140), b23 = __byte_perm(w4[2], w4[3], 0x7362);
+        out[0][q] = __byte_perm(a01, a23, 0x5410);
+        out[1][q] = __byte_perm(a01, a23, 0x7632);
+        out[2][q] = __byte_perm(b01, b23, 0x5410);
+        out[3][q] = __byte_perm(b01, b23, 0x7632);
+    }
+    const int64_t r = r0 + warp * 32;
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const int kk = 4 * lane + c;
+        const int64_t k = k0 + kk;
+        if (k < a.K && r < padded) {
+            uint4* to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out_codes) + k * padded + r);
+            to[0] = make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
+            to[1] = make_uint4(out[c][4], out[c][5], out[c][6], out[c][7]);
+            reinterpret_cast<uint8_t*>(scale_out)[(kk & 31) * 16 + (kk >> 5) * 4 + warp] =
+                static_cast<uint8_t>(bytes[c]);
+        }
+    }
+    __syncthreads();
+    static_cast<uint32_t*>(a.out_scales)[(tk * tiles_r + tr) * 128 + t] = scale_out[t];
+}
+
+// ---------------------------------------------------------------------------
+// the gradient of an activation
+// ---------------------------------------------------------------------------
+
+// A CTA takes 128 rows of one batch by 128 columns; sixteen lanes a row, eight columns each, so that a
+// thread's columns stay the same and their sums are in registers.  The rows of a batch are counted
+// from its first, so a batch's sums do not depend on what stands before it.
+template <typename T, int ACT>
+__global__ void __launch_bounds__(kThreads)
+    activation_backward_kernel(const Mxfp8ActBwdArgs a, int64_t chunks, int parts)
+{
+    __shared__ float sums[2][kThreads / 32][128];
+    grid_dependency_sync();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int sub = threadIdx.x & 15, hw = threadIdx.x >> 4;
+    const int64_t tiles = (a.N + 127) / 128;
+    const int64_t tile = blockIdx.x % tiles, unit = blockIdx.x / tiles;
+    const int64_t batch = unit / chunks, chunk = unit - batch * chunks;
+    const int64_t n = tile * 128 + sub * 8;
+    const int64_t M = a.B * a.S;
+    const int64_t begin = batch * a.S + chunk * 128;
+    const int64_t end = min(begin + 128, (batch + 1) * a.S);
+    // all rows of a row tile are this CTA's: its scales are stored four rows at a time
+    const bool whole = begin % 128 == 0 && (end == begin + 128 || end == M);
+    const bool has = n < a.N;
+    const uint8_t* __restrict__ z = static_cast<const uint8_t*>(a.z);
+    const T* __restrict__ grad = static_cast<const T*>(a.grad_out);
+    const uint32_t* __restrict__ z_scales = static_cast<const uint32_t*>(a.z_scales);
+    uint32_t* grad_scales = static_cast<uint32_t*>(a.grad_z_scales);
+    float gate[8], sb[8], sg[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        gate[j] = 1.0f;
+        sb[j] = sg[j] = 0.0f;
+    }
+    if (a.gate && has) {
+        const uint4 g = ld_cached(reinterpret_cast<const uint4*>(
+            static_cast<const T*>(a.gate) + batch * a.gate_bstride + n));
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float2 p = widen2<T>(word(g, j));
+            gate[2 * j] = p.x;
+            gate[2 * j + 1] = p.y;
+        }
+    }
+#pragma unroll 1
+    for (int i0 = 0; i0 < 2; ++i0) {
+        const int r = hw + 16 * i0;
+        uint2 c[4];
+        uint4 g[4];
+        uint32_t e[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = begin + r + 32 * i;
+            c[i] = make_uint2(0u, 0u);
+            g[i] = make_uint4(0u, 0u, 0u, 0u);
+            e[i] = 0u;
+            if (m < end && has) {
+                c[i] = ld_stream2(reinterpret_cast<const uint2*>(z + m * a.N + n));
+                g[i] = ld_stream(reinterpret_cast<const uint4*>(grad + m * a.N + n));
+                e[i] = __ldg(z_scales + mx8_scale_at(m, tile * 4, tiles) / 4);
+            }
+        }
+        uint4 four;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int64_t m = begin + r + 32 * i;
+            float f[8], d[8];
+            values8(c[i], mx8_scale((e[i] >> (8 * (sub >> 2))) & 0xFFu), f);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float2 p = widen2<T>(word(g[i], j));
+                d[2 * j] = p.x;
+                d[2 * j + 1] = p.y;
+            }
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                float slope;
+                const float h = activate<ACT>(f[j], slope);
+                sg[j] = __fmaf_rn(d[j], h, sg[j]);
+                d[j] = __fmul_rn(__fmul_rn(d[j], slope), gate[j]);
+                sb[j] = __fadd_rn(sb[j], d[j]);
+            }
+            uint2 out;
+            const uint32_t w = join_bytes(quantize8(d, out), lane & 16);
+            word(four, i) = w;
+            if (m < end && has)
+                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.grad_z) + m * a.N + n) = out;
+            if (!whole && sub == 0 && m < end)
+                grad_scales[mx8_scale_at(m, tile * 4, tiles) / 4] = w;
+        }
+        if (whole && sub == 0)
+            reinterpret_cast<uint4*>(grad_scales)[(begin / 128 * tiles + tile) * 32 + r] = four;
+    }
+    if (!whole && end == M)  // rows behind the last one
+        for (int64_t m = M + threadIdx.x; m < (M + 127) / 128 * 128; m += kThreads)
+            grad_scales[mx8_scale_at(m, tile * 4, tiles) / 4] = 0u;
+    if (!parts)
+        return;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        sb[j] = __fadd_rn(sb[j], __shfl_xor_sync(kFullMask, sb[j], 16));
+        sg[j] = __fadd_rn(sg[j], __shfl_xor_sync(kFullMask, sg[j], 16));
+        if (lane < 16) {
+            sums[0][warp][sub * 8 + j] = sb[j];
+            sums[1][warp][sub * 8 + j] = sg[j];
+        }
+    }
+    __syncthreads();
+    const int part = threadIdx.x >> 7, col = threadIdx.x & 127;
+    // parts: bit 0 the bias's sums, bit 1 the gate's
+    if ((parts >> part & 1) && tile * 128 + col < a.N) {
+        float s = sums[part][0][col];
+#pragma unroll
+        for (int k = 1; k < kThreads / 32; ++k)
+            s = __fadd_rn(s, sums[part][k][col]);
+        const int each = parts == 3 ? 2 : 1;
+        a.partials[(unit * each + (parts == 3 ? part : 0)) * a.N + tile * 128 + col] = s;
+    }
+}
+
+// Sums of the chunks' parts: those of all batches for the bias, of one for a row of the gate's
+// gradient; eight warps take every eighth, 128 columns a CTA.
+__global__ void __launch_bounds__(kThreads)
+    activation_columns_kernel(const Mxfp8ActBwdArgs a, int64_t chunks, int64_t batches, int parts)
+{
+    __shared__ float4 join[kThreads / 32][32];
+    grid_dependency_sync();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int64_t tiles = (a.N + 127) / 128;
+    const int64_t which = blockIdx.x / tiles;
+    const bool bias = which == 0 && a.grad_bias;
+    const int64_t slice = which - (a.grad_bias ? 1 : 0);  // of the gate's gradient
+    const int each = parts == 3 ? 2 : 1, part = parts == 3 && !bias ? 1 : 0;
+    const int64_t first = bias ? 0 : slice * chunks;
+    const int64_t count = bias ? batches * chunks : chunks;
+    const int64_t n = (blockIdx.x - which * tiles) * 128 + lane * 4;
+    float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    if (n < a.N)
+        for (int64_t i = warp; i < count; i += kThreads / 32) {
+            const float4 p = *reinterpret_cast<const float4*>(
+                a.partials + ((first + i) * each + part) * a.N + n);
+            s = make_float4(__fadd_rn(s.x, p.x), __fadd_rn(s.y, p.y), __fadd_rn(s.z, p.z),
+                            __fadd_rn(s.w, p.w));
+        }
+    join[warp][lane] = s;
+    __syncthreads();
+    if (warp || n >= a.N)
+        return;
+#pragma unroll
+    for (int k = 1; k < kThreads / 32; ++k) {
+        const float4 p = join[k][lane];
+        s = make_float4(__fadd_rn(s.x, p.x), __fadd_rn(s.y, p.y), __fadd_rn(s.z, p.z),
+                        __fadd_rn(s.w, p.w));
+    }
+    *reinterpret_cast<float4*>((bias ? a.grad_bias : a.grad_gate + slice * a.N) + n) = s;
+}
+
+// Batches as the sums see them: one where no gate tells them apart.
+int64_t sum_batches(int64_t B, bool per_batch) { return per_batch ? B : 1; }
+
+int64_t sum_chunks(int64_t B, int64_t S, bool per_batch)
+{
+    return ((per_batch ? S : B * S) + 127) / 128;
+}
+
+template <typename T>
+cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int grid, int64_t chunks, int parts,
+                              cudaStream_t stream)
+{
+    switch (a.activation) {
+    case kActSilu:
+        return launch_dependent(activation_backward_kernel<T, kActSilu>, grid, kThreads, 0, stream, a,
+                                chunks, parts);
+    case kActGelu:
+        return launch_dependent(activation_backward_kernel<T, kActGelu>, grid, kThreads, 0, stream, a,
+                                chunks, parts);
+    case kActGeluTanh:
+        return launch_dependent(activation_backward_kernel<T, kActGeluTanh>, grid, kThreads, 0,
+                                stream, a, chunks, parts);
+    default:
+        return launch_dependent(activation_backward_kernel<T, kActNone>, grid, kThreads, 0, stream, a,
+                                chunks, parts);
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_mxfp8_rows(bool quantize, const Mxfp8RowsArgs& a, cudaStream_t stream)
+{
+    const uint32_t units = a.rows_padded / 4 * a.by_tiles.d;
+    const int grid = static_cast<int>((units + kUnitsPerCta - 1) / kUnitsPerCta);
+    if (quantize)
+        return launch_dependent(a.f16 ? quantize8_kernel<__half> : quantize8_kernel<__nv_bfloat16>,
+                                grid, kThreads, 0, stream, a);
+    return launch_dependent(a.f16 ? dequantize8_kernel<__half> : dequantize8_kernel<__nv_bfloat16>,
+                            grid, kThreads, 0, stream, a);
+}
+
+cudaError_t launch_mxfp8_transpose(const Mxfp8TransposeArgs& a, cudaStream_t stream)
+{
+    const int64_t tiles = (a.K + 127) / 128 * ((a.rows + 127) / 128);
+    if (tiles > INT32_MAX)
+        return cudaErrorInvalidValue;
+    return launch_dependent(transpose8_kernel, static_cast<int>(tiles), kTurn, 0, stream, a);
+}
+
+size_t mxfp8_activation_backward_workspace_bytes(int64_t B, int64_t S, int64_t N, bool per_batch,
+                                                 int parts)
+{
+    return static_cast<size_t>(sum_batches(B, per_batch) * sum_chunks(B, S, per_batch) * parts * N) *
+           4;
+}
+
+cudaError_t launch_mxfp8_activation_backward(const Mxfp8ActBwdArgs& args, cudaStream_t stream)
+{
+    Mxfp8ActBwdArgs a = args;
+    const bool per_batch = a.gate && a.gate_bstride != 0;
+    if (!per_batch) {
+        a.S *= a.B;
+        a.B = 1;
+    }
+    const int64_t chunks = (a.S + 127) / 128, tiles = (a.N + 127) / 128;
+    const int parts = (a.grad_bias ? 1 : 0) + (a.grad_gate ? 2 : 0);
+    if (a.B * chunks * tiles > INT32_MAX)
+        return cudaErrorInvalidValue;
+    const int grid = static_cast<int>(a.B * chunks * tiles);
+    const cudaError_t e = a.f16 ? launch_activation<__half>(a, grid, chunks, parts, stream)
+                                : launch_activation<__nv_bfloat16>(a, grid, chunks, parts, stream);
+    if (e != cudaSuccess || !parts)
+        return e;
+    const int64_t slices = (a.grad_bias ? 1 : 0) + (a.grad_gate ? a.B : 0);
+    if (slices * tiles > INT32_MAX)
+        return cudaErrorInvalidValue;
+    return launch_dependent(activation_columns_kernel, static_cast<int>(slices * tiles), kThreads, 0,
+                            stream, a, chunks, a.B, parts);
+}
+
+}  // namespace rmsmod
