@@ -279,14 +279,16 @@ __global__ void __launch_bounds__(kRows * kMaxRowWarps * 32)
 // backward
 // ---------------------------------------------------------------------------
 
-// One CTA per SM, of sixteen warps in groups that take a row each (up to V vectors of eight values a
-// thread); a group walks over runs of rows of one batch, with a ring of bulk copies ahead of it, and
-// keeps its columns' sums in registers, to be left at the run's end as a part for the last launch.
+// One CTA per SM, whose sixteen warps form groups that take a row each, up to V vectors of eight values
+// a thread.  A CTA takes runs of rows of one batch, dealt to its groups in turn; a group has a ring of
+// bulk copies ahead of it and keeps its columns' sums in registers; at a run's end the groups' sums are
+// joined and left as a part for the last launch.  Up to two vectors a thread a row is in registers when
+// its sum over the group's warps is joined, so its slot is filled again from there on.
 constexpr int kBwdWarps = 16;
-constexpr int kBwdThreads = kBwdWarps * 32;
+constexpr int kBwdThreads = 32 * kBwdWarps;
 constexpr int kBwdMaxStages = 8;
+constexpr int kBwdJoin = kBwdThreads * 16;  // bytes a vector
 constexpr int kBwdSmem = 224 * 1024;  // (and 3 KB of barriers and sums)
-constexpr int kBwdRing = 160 * 1024;  // what the rings take of it, where two slots a group allow
 
 struct BwdPlan {
     FastDiv per_batch;  // runs of a batch
@@ -294,83 +296,105 @@ struct BwdPlan {
     uint32_t count;     // runs
     int warps;          // of a group
     int groups;
-    int stages;
+    int stages;         // of a group's ring
     int row_bytes;      // of a slot
 };
 
-// Vectors of a thread: as few as leave a row to one CTA.
-int bwd_vectors(int64_t D) { return D <= 4096 ? 1 : D <= 8192 ? 2 : 4; }
-int bwd_warps(int64_t D) { return static_cast<int>((D / 8 + 32 * bwd_vectors(D) - 1) / (32 * bwd_vectors(D))); }
+int bwd_vectors(int64_t D) { return D <= 256 ? 1 : D <= 8192 ? 2 : 4; }
 
-// Rows of a run: that 152 CTAs' groups have one each, but eight at least, whose parts are then a
-// quarter of the rows' bytes.
+int bwd_warps(int64_t D)
+{
+    const int V = bwd_vectors(D);
+    return static_cast<int>((D / 8 + 32 * V - 1) / (32 * V));
+}
+
+int bwd_groups(int64_t D) { return kBwdWarps / bwd_warps(D); }
+
+// Rows of a run: that 152 CTAs have one each, but a few rows for each group at least.
 int64_t bwd_chunk(int64_t S, int64_t D)
 {
-    const int64_t slots = 152 * (kBwdWarps / bwd_warps(D));
-    const int64_t c = (S + slots - 1) / slots;
-    return c < 8 ? 8 : c;
+    const int64_t c = (S + 151) / 152, least = 4 * bwd_groups(D);
+    return c < least ? least : c;
+}
+
+__device__ __forceinline__ float4 floats(u64 a, u64 b)
+{
+    float4 f;
+    f2_unpack(a, f.x, f.y);
+    f2_unpack(b, f.z, f.w);
+    return f;
 }
 
 template <typename T, int V>
 __global__ void __launch_bounds__(kBwdThreads, 1)
     norm_backward_kernel(const Mxfp8NormBwdArgs a, const BwdPlan plan)
 {
+    // four vectors a thread: the multipliers stand in shared memory, and the row is read again after
+    // its sum
+    constexpr bool kWide = V > 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long full[kBwdWarps][kBwdMaxStages];
-    __shared__ float part[kBwdWarps][2][kBwdWarps];
-    constexpr bool kShared = V == 4;  // the multipliers in shared memory
+    __shared__ float part[2][kBwdWarps];
 
     const int lane = threadIdx.x & 31;
     const int group = (threadIdx.x >> 5) / plan.warps;
     const int warp = (threadIdx.x >> 5) - group * plan.warps;
-    if (group >= plan.groups)
-        return;  // (no barrier of the whole CTA follows)
     const int Dv = a.D / 8;
     const bool leader = warp == 0 && lane == 0;
+    if (group >= plan.groups)
+        return;  // (barriers count the groups' threads)
+    const int threads = plan.groups * plan.warps * 32;
     auto group_sync = [&]() {
         if (plan.warps == 1)
             __syncwarp();
         else
             asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(plan.warps * 32) : "memory");
     };
+    auto cta_sync = [&]() { asm volatile("bar.sync 0, %0;" ::"r"(threads) : "memory"); };
     if (leader) {
         for (int s = 0; s < plan.stages; ++s)
             mbar_init(smem_addr(&full[group][s]), 1u);
         mbar_init_fence();
     }
-    group_sync();
+    cta_sync();
     grid_dependency_sync();
 
-    float4* m_lo = reinterpret_cast<float4*>(smem);  // kShared: [Dv] and [Dv]
-    uint8_t* ring = smem + (kShared ? a.D * 4 : 0) +
+    // the multipliers (kWide), or the groups' sums on their way to one another; then the rings
+    float4* m_lo = reinterpret_cast<float4*>(smem);
+    float4* join = reinterpret_cast<float4*>(smem);
+    uint8_t* ring = smem + (kWide ? a.D * 4 : plan.groups > 1 ? kBwdJoin * V : 0) +
                     static_cast<size_t>(group) * plan.stages * plan.row_bytes;
     const uint8_t* kept = static_cast<const uint8_t*>(a.kept);
     const uint8_t* scales = static_cast<const uint8_t*>(a.kept_scales);
-    const int64_t tiles = (a.D + 127) / 128;
+    const uint32_t tiles = (a.D + 127) / 128;
 
     // a walk over this group's rows
     struct Walk {
-        uint32_t item, row, end;
+        uint32_t item, row, left;
     };
-    const uint32_t stride = gridDim.x * plan.groups;
-    auto open = [&](Walk& w) {
-        if (w.item >= plan.count)
-            return;
-        const uint32_t batch = plan.per_batch.div(w.item);
-        const uint32_t S = static_cast<uint32_t>(a.S);
-        w.row = batch * S + (w.item - batch * plan.per_batch.d) * plan.chunk;
-        const uint32_t last = (batch + 1) * S;
-        w.end = last - w.row < plan.chunk ? last : w.row + plan.chunk;
+    auto open = [&](Walk& w) {  // the first run from w.item on that has a row for the group
+        for (; w.item < plan.count; w.item += gridDim.x) {
+            const uint32_t batch = plan.per_batch.div(w.item);
+            const uint32_t S = static_cast<uint32_t>(a.S), last = (batch + 1) * S;
+            const uint32_t begin = batch * S + (w.item - batch * plan.per_batch.d) * plan.chunk;
+            const uint32_t rows = last - begin < plan.chunk ? last - begin : plan.chunk;
+            if (rows > static_cast<uint32_t>(group)) {
+                w.row = begin + group;
+                w.left = (rows - group + plan.groups - 1) / plan.groups;
+                return;
+            }
+        }
     };
-    auto next = [&](Walk& w) {
-        if (++w.row < w.end)
-            return;
-        w.item += stride;
-        open(w);
+    auto advance = [&](Walk& w) {
+        w.row += plan.groups;
+        if (--w.left == 0) {
+            w.item += gridDim.x;
+            open(w);
+        }
     };
-    Walk now{blockIdx.x * plan.groups + group, 0u, 0u};
+    Walk now{blockIdx.x, 0u, 0u};
     open(now);
-    Walk ahead = now;
+    Walk ahead = now, soon = now;  // `soon`: whose scales and rstd are loaded next
     int put = 0;
     auto issue = [&]() {  // the leader
         if (ahead.item >= plan.count)
@@ -385,88 +409,100 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
         if (a.grad_res)
             bulk_g2s(dst + 3 * a.D, static_cast<const uint8_t*>(a.grad_res) + 2 * at, 2 * a.D, bar);
         put = put + 1 == plan.stages ? 0 : put + 1;
-        next(ahead);
+        advance(ahead);
     };
     if (leader)
         for (int s = 0; s < plan.stages; ++s)
             issue();
 
-    // what a row needs beside the ring, one row ahead
-    uint32_t byte[V];
-    float rstd = 0.0f;
-    auto fetch = [&](const Walk& w) {
-        if (w.item >= plan.count)
-            return;
-        rstd = __ldg(a.rstd + w.row);
+    // a thread's vectors, and their scale bytes, which stand apart from a row's first one by as much in
+    // every row
+    int at[V];
+    bool has[V];
+    uint32_t scale_off[V];
 #pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = (j * plan.warps + warp) * 32 + lane;
-            byte[j] = c < Dv ? __ldg(scales + mx8_scale_at(w.row, c / 4, tiles)) : 0u;
-        }
+    for (int j = 0; j < V; ++j) {
+        at[j] = (j * plan.warps + warp) * 32 + lane;
+        has[j] = at[j] < Dv;
+        const uint32_t block = static_cast<uint32_t>(at[j]) / 4;
+        scale_off[j] = (block >> 2) * 512 + (block & 3);
+    }
+    // what the next two rows need beside the ring
+    struct Beside {
+        uint32_t byte[V];
+        float rstd;
     };
+    auto fetch = [&](Beside& e) {
+        if (soon.item >= plan.count)
+            return;
+        e.rstd = __ldg(a.rstd + soon.row);
+        const uint8_t* from = scales + mx8_scale_at(soon.row, 0, tiles);
 #pragma unroll
-    for (int j = 0; j < V; ++j)
-        byte[j] = 0u;
-    fetch(now);
+        for (int j = 0; j < V; ++j)
+            e.byte[j] = has[j] ? __ldg(from + scale_off[j]) : 0u;
+        advance(soon);
+    };
+    Beside first{}, second{};
+    fetch(first);
+    fetch(second);
 
-    float m[kShared ? 1 : V][8];
-    float hats[V][8], gos[V][8];  // column sums of go * hat and of go
+    u64 m[kWide ? 1 : V][4];
+    u64 hats[V][4], gos[V][4];  // column sums of go * hat and of go
     const float inv_n = __fdiv_rn(1.0f, static_cast<float>(a.D));
     uint32_t batch = 0xFFFFFFFFu, phase = 0;
     int get = 0, odd = 0;
-    bool broken = false;
-    while (now.item < plan.count) {
-        const uint32_t item = now.item;
+    bool broken = false, waiting = false;
+    for (uint32_t item = blockIdx.x; item < plan.count; item += gridDim.x) {
         const uint32_t b = plan.per_batch.div(item);
         if (b != batch) {
-            batch = b;
-            if (kShared)
-                group_sync();
+            batch = b;  // (a thread reads the multipliers that it has written)
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int c = (j * plan.warps + warp) * 32 + lane;
-                float t[8];
+                u64 t[4];
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    t[k] = c < Dv ? 1.0f : 0.0f;
-                if (c < Dv && a.weight) {
-                    const uint4 w = ld_cached(static_cast<const uint4*>(a.weight) + c);
+                for (int k = 0; k < 4; ++k)
+                    t[k] = f2_splat(1.0f);
+                if (has[j] && a.weight) {
+                    const uint4 w = ld_cached(static_cast<const uint4*>(a.weight) + at[j]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 p = widen2<T>(word(w, k));
-                        t[2 * k] = p.x;
-                        t[2 * k + 1] = p.y;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        t[k] = widen<T>(word(w, k));
                 }
-                if (c < Dv && a.scale) {
+                if (has[j] && a.scale) {
                     const uint4 w = ld_cached(reinterpret_cast<const uint4*>(
                                                   static_cast<const T*>(a.scale) +
-                                                  b * a.mod_bstride) + c);
+                                                  b * a.mod_bstride) + at[j]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 p = widen2<T>(word(w, k));
-                        t[2 * k] = __fmul_rn(t[2 * k], __fadd_rn(1.0f, p.x));
-                        t[2 * k + 1] = __fmul_rn(t[2 * k + 1], __fadd_rn(1.0f, p.y));
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        t[k] = f2_mul(t[k], f2_add(f2_splat(1.0f), widen<T>(word(w, k))));
                 }
-                if (kShared) {
-                    if (c < Dv) {
-                        m_lo[c] = make_float4(t[0], t[1], t[2], t[3]);
-                        m_lo[Dv + c] = make_float4(t[4], t[5], t[6], t[7]);
+                if (kWide) {
+                    if (has[j]) {
+                        m_lo[at[j]] = floats(t[0], t[1]);
+                        m_lo[Dv + at[j]] = floats(t[2], t[3]);
                     }
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        m[kShared ? 0 : j][k] = t[k];
+                    for (int k = 0; k < 4; ++k)
+                        m[kWide ? 0 : j][k] = t[k];
                 }
             }
         }
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                hats[j][k] = gos[j][k] = 0.0f;
+            for (int k = 0; k < 4; ++k)
+                hats[j][k] = gos[j][k] = 0ull;
         while (now.item == item) {
+            const uint32_t row = now.row;
+            advance(now);
+            const float r = first.rstd;
+            float factor[V];  // of a code's value, to hat: a vector's eight are of one block
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                factor[j] = __fmul_rn(mx8_scale(first.byte[j]), r);
+            first = second;
+            fetch(second);
             if (!broken && !mbar_wait(smem_addr(&full[group][get]), phase, kWaitLimitNs)) {
                 broken = true;
                 atomicOr(&g_error, kErrCopyTimeout);
@@ -476,201 +512,249 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
                 get = 0;
                 phase ^= 1u;
             }
-            const int64_t at = static_cast<int64_t>(now.row) * Dv;
-            const float r = rstd;
-            float scale[V];
-#pragma unroll
-            for (int j = 0; j < V; ++j)
-                scale[j] = mx8_scale(byte[j]);
-            next(now);
-            fetch(now);
-            // ---- hat and go * m: their product's sum over the row
             uint2 x[V];
-            uint4 g[V];
-            float dot[2] = {0.0f, 0.0f};
-            auto values = [&](int j, float (&hat)[8], float (&go)[8], float (&mm)[8]) {
-                const int c = (j * plan.warps + warp) * 32 + lane;
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    const float2 p = e4m3x2_values(((k < 2 ? x[j].x : x[j].y) >> (16 * (k & 1))) &
-                                                   0xFFFFu);
-                    hat[2 * k] = __fmul_rn(__fmul_rn(p.x, scale[j]), r);
-                    hat[2 * k + 1] = __fmul_rn(__fmul_rn(p.y, scale[j]), r);
-                    const float2 q = widen2<T>(word(g[j], k));
-                    go[2 * k] = q.x;
-                    go[2 * k + 1] = q.y;
-                }
-                if (kShared) {
-                    const float4 lo = c < Dv ? m_lo[c] : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-                    const float4 hi = c < Dv ? m_lo[Dv + c] : lo;
-                    mm[0] = lo.x;
-                    mm[1] = lo.y;
-                    mm[2] = lo.z;
-                    mm[3] = lo.w;
-                    mm[4] = hi.x;
-                    mm[5] = hi.y;
-                    mm[6] = hi.z;
-                    mm[7] = hi.w;
+            uint4 g[V], gr[V];
+            auto read = [&](int j) {
+                x[j] = reinterpret_cast<const uint2*>(slot)[at[j]];
+                g[j] = reinterpret_cast<const uint4*>(slot + a.D)[at[j]];
+            };
+            auto read_stream = [&](int j) {
+                gr[j] = make_uint4(0u, 0u, 0u, 0u);
+                if (a.grad_res)
+                    gr[j] = reinterpret_cast<const uint4*>(slot + 3 * a.D)[at[j]];
+            };
+            auto value = [&](int j, int k) {
+                return widen<__half>(
+                    e4m3x2_half2(((k < 2 ? x[j].x : x[j].y) >> (16 * (k & 1))) & 0xFFFFu));
+            };
+            auto multipliers = [&](int j, u64 (&mm)[4]) {
+                if (kWide) {
+                    const float4 lo = m_lo[at[j]], hi = m_lo[Dv + at[j]];
+                    mm[0] = f2_pack(lo.x, lo.y);
+                    mm[1] = f2_pack(lo.z, lo.w);
+                    mm[2] = f2_pack(hi.x, hi.y);
+                    mm[3] = f2_pack(hi.z, hi.w);
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        mm[k] = m[kShared ? 0 : j][k];
+                    for (int k = 0; k < 4; ++k)
+                        mm[k] = m[kWide ? 0 : j][k];
                 }
             };
+            // ---- the sum over the row of go * m * hat, and the columns'
+            float sum = 0.0f;
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const int c = (j * plan.warps + warp) * 32 + lane;
-                x[j] = make_uint2(0u, 0u);
-                g[j] = make_uint4(0u, 0u, 0u, 0u);
-                if (c < Dv) {
-                    x[j] = reinterpret_cast<const uint2*>(slot)[c];
-                    g[j] = reinterpret_cast<const uint4*>(slot + a.D)[c];
-                }
-                float hat[8], go[8], mm[8];
-                values(j, hat, go, mm);
+            for (int j = 0; j < V; ++j)
+                if (has[j]) {
+                    read(j);
+                    if (!kWide)
+                        read_stream(j);
+                    u64 mm[4], d = 0ull;
+                    const u64 f = f2_splat(factor[j]);
+                    multipliers(j, mm);
 #pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    dot[k & 1] = __fmaf_rn(__fmul_rn(go[k], mm[k]), hat[k], dot[k & 1]);
-                    hats[j][k] = __fmaf_rn(go[k], hat[k], hats[j][k]);
-                    gos[j][k] = __fadd_rn(gos[j][k], go[k]);
+                    for (int k = 0; k < 4; ++k) {
+                        const u64 go = widen<T>(word(g[j], k));
+                        const u64 p = f2_mul(go, value(j, k));
+                        d = f2_fma(p, mm[k], d);
+                        hats[j][k] = f2_fma(p, f, hats[j][k]);
+                        gos[j][k] = f2_add(gos[j][k], go);
+                    }
+                    float lo, hi;
+                    f2_unpack(d, lo, hi);
+                    sum = __fmaf_rn(__fadd_rn(lo, hi), factor[j], sum);
                 }
-            }
-            float sum = warp_sum(__fadd_rn(dot[0], dot[1]));
+            sum = warp_sum(sum);
             if (plan.warps > 1) {
                 if (lane == 0)
-                    part[group][odd][warp] = sum;
+                    part[odd][group * plan.warps + warp] = sum;
                 group_sync();
-                sum = 0.0f;
-                for (int k = 0; k < plan.warps; ++k)
-                    sum = __fadd_rn(sum, part[group][odd][k]);
+                // every warp joins them, in the lanes' order
+                sum = (lane & 15) < plan.warps ? part[odd][group * plan.warps + (lane & 15)] : 0.0f;
+#pragma unroll
+                for (int off = 8; off > 0; off >>= 1)
+                    sum = __fadd_rn(sum, __shfl_xor_sync(kFullMask, sum, off));
                 odd ^= 1;
             } else {
                 __syncwarp();
             }
-            const float c1 = __fmul_rn(sum, inv_n);
-            if (a.grad_x) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    const int c = (j * plan.warps + warp) * 32 + lane;
-                    if (c < Dv) {
-                        float hat[8], go[8], mm[8];
-                        values(j, hat, go, mm);
-                        uint4 gr = make_uint4(0u, 0u, 0u, 0u);
-                        if (a.grad_res)
-                            gr = reinterpret_cast<const uint4*>(slot + 3 * a.D)[c];
-                        uint4 o;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float2 q = widen2<T>(word(gr, k));
-                            const float lo = __fmaf_rn(-hat[2 * k], c1, __fmul_rn(go[2 * k], mm[2 * k]));
-                            const float hi = __fmaf_rn(-hat[2 * k + 1], c1,
-                                                       __fmul_rn(go[2 * k + 1], mm[2 * k + 1]));
-                            word(o, k) = narrow2<T>(__fmaf_rn(r, lo, q.x), __fmaf_rn(r, hi, q.y));
-                        }
-                        st_stream(static_cast<uint4*>(a.grad_x) + at + c, o);
-                    }
-                }
-            }
-            // the slot is free when all of the group's warps have read it
-            group_sync();
-            if (leader)
+            // every warp is past this row's slot (kWide: past the one before it)
+            if (leader && (!kWide || waiting))
                 issue();
+            waiting = true;
+            if (!a.grad_x)
+                continue;
+            const float c = __fmul_rn(__fmul_rn(-sum, inv_n), r);
+            const u64 rr = f2_splat(r);
+            uint4* to = static_cast<uint4*>(a.grad_x) + static_cast<int64_t>(row) * Dv;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (has[j]) {
+                    u64 mm[4];
+                    multipliers(j, mm);
+                    if (kWide) {
+                        read(j);
+                        read_stream(j);
+                    }
+                    const u64 f = f2_splat(__fmul_rn(factor[j], c));
+                    uint4 o;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const u64 d = f2_fma(value(j, k), f, widen<T>(word(gr[j], k)));
+                        word(o, k) = narrow<T>(
+                            f2_fma(f2_mul(widen<T>(word(g[j], k)), mm[k]), rr, d));
+                    }
+                    st_stream(to + at[j], o);
+                }
         }
-        if (a.sums) {
+        if (!a.sums)
+            continue;
+        float4* to = reinterpret_cast<float4*>(a.partials + static_cast<int64_t>(item) * 2 * a.D);
+        if (plan.groups == 1) {
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+                if (has[j]) {
+                    float4* t = to + 2 * at[j];
+                    t[0] = floats(hats[j][0], hats[j][1]);
+                    t[1] = floats(hats[j][2], hats[j][3]);
+                    t += 2 * Dv;
+                    t[0] = floats(gos[j][0], gos[j][1]);
+                    t[1] = floats(gos[j][2], gos[j][3]);
+                }
+            continue;
+        }
+        // half of each vector at a time, [vector][thread]: the sums of go * hat and then those of go
+        const int per_group = plan.warps * 32;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                const int c = (j * plan.warps + warp) * 32 + lane;
+                const u64(&mine)[4] = q >= 2 ? gos[j] : hats[j];
+                join[j * kBwdThreads + threadIdx.x] = floats(mine[q % 2 * 2], mine[q % 2 * 2 + 1]);
+            }
+            cta_sync();
+            for (int c = threadIdx.x; c < V * per_group; c += threads) {
+                const int j = c >= per_group ? 1 : 0;  // (V is at most 2 where groups are joined)
                 if (c < Dv) {
-                    float4* to = reinterpret_cast<float4*>(a.partials +
-                                                           static_cast<int64_t>(item) * 2 * a.D) + 2 * c;
-                    to[0] = make_float4(hats[j][0], hats[j][1], hats[j][2], hats[j][3]);
-                    to[1] = make_float4(hats[j][4], hats[j][5], hats[j][6], hats[j][7]);
-                    to += 2 * Dv;
-                    to[0] = make_float4(gos[j][0], gos[j][1], gos[j][2], gos[j][3]);
-                    to[1] = make_float4(gos[j][4], gos[j][5], gos[j][6], gos[j][7]);
+                    const float4* from = join + j * kBwdThreads + c - j * per_group;
+                    float4 t = from[0];
+                    for (int g = 1; g < plan.groups; ++g) {
+                        const float4 p = from[g * per_group];
+                        t = make_float4(__fadd_rn(t.x, p.x), __fadd_rn(t.y, p.y),
+                                        __fadd_rn(t.z, p.z), __fadd_rn(t.w, p.w));
+                    }
+                    to[q / 2 * 2 * Dv + 2 * c + q % 2] = t;
                 }
             }
+            cta_sync();
         }
     }
     if (broken)
         drain_pause();
 }
 
-// The row vectors' gradients from the runs' parts: for grad_weight those of all batches, each under
-// its 1 + scale, for a row of grad_scale and grad_shift those of one; eight warps take every eighth,
-// 128 columns a CTA.
-constexpr int kColumnThreads = 256;
+// The row vectors' gradients from the runs' parts, 64 columns a CTA, half a warp a part.  With one batch
+// a CTA forms all of them from the same sums; else those of grad_weight are over all batches, each
+// under its 1 + scale, and those of a row of grad_scale and grad_shift over one.
+constexpr int kColumnThreads = 1024;
+constexpr int kColumnWarps = kColumnThreads / 32;
 
 template <typename T>
 __global__ void __launch_bounds__(kColumnThreads)
     norm_columns_kernel(const Mxfp8NormBwdArgs a, FastDiv per_batch, uint32_t count)
 {
-    __shared__ float4 join[2][kColumnThreads / 32][32];
+    __shared__ float4 join[2][kColumnWarps][16];
     grid_dependency_sync();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t tiles = (a.D + 127) / 128;
+    const uint32_t tiles = (a.D + 63) / 64;
     const uint32_t which = blockIdx.x / tiles;
-    const bool weight = which == 0 && a.grad_weight;
-    const uint32_t slice = which - (a.grad_weight ? 1u : 0u);
+    const bool one = a.B == 1;
+    const bool weight = !one && which == 0 && a.grad_weight;  // of several batches
+    const uint32_t slice = one ? 0u : which - (a.grad_weight ? 1u : 0u);
     const uint32_t first = weight ? 0u : slice * per_batch.d;
     const uint32_t end = weight ? count : first + per_batch.d;
-    const int n = static_cast<int>(blockIdx.x - which * tiles) * 128 + lane * 4;
+    const int n = static_cast<int>(blockIdx.x - which * tiles) * 64 + (lane & 15) * 4;
+    auto add4 = [](float4 p, float4 q) {
+        return make_float4(__fadd_rn(p.x, q.x), __fadd_rn(p.y, q.y), __fadd_rn(p.z, q.z),
+                           __fadd_rn(p.w, q.w));
+    };
+    auto mul4 = [](float4 p, float4 q) {
+        return make_float4(__fmul_rn(p.x, q.x), __fmul_rn(p.y, q.y), __fmul_rn(p.z, q.z),
+                           __fmul_rn(p.w, q.w));
+    };
     auto row4 = [&](const void* p, int64_t at) {
         const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const T*>(p) + at + n);
         const float2 lo = widen2<T>(w.x), hi = widen2<T>(w.y);
         return make_float4(lo.x, lo.y, hi.x, hi.y);
     };
+    const float4 ones = make_float4(1.0f, 1.0f, 1.0f, 1.0f);
+    auto under_scale = [&](float4 p, uint32_t batch) {
+        return a.scale ? mul4(p, add4(ones, row4(a.scale, batch * a.mod_bstride))) : p;
+    };
     float4 s = make_float4(0.0f, 0.0f, 0.0f, 0.0f), t = s;
-    if (n < a.D)
-        for (uint32_t i = first + warp; i < end; i += kColumnThreads / 32) {
-            const float* from = a.partials + static_cast<int64_t>(i) * 2 * a.D + n;
-            float4 p = *reinterpret_cast<const float4*>(from);
-            if (weight) {
-                if (a.scale) {
-                    const float4 f = row4(a.scale, per_batch.div(i) * a.mod_bstride);
-                    p = make_float4(__fmul_rn(p.x, __fadd_rn(1.0f, f.x)),
-                                    __fmul_rn(p.y, __fadd_rn(1.0f, f.y)),
-                                    __fmul_rn(p.z, __fadd_rn(1.0f, f.z)),
-                                    __fmul_rn(p.w, __fadd_rn(1.0f, f.w)));
-                }
-            } else {
-                const float4 q = *reinterpret_cast<const float4*>(from + a.D);
-                t = make_float4(__fadd_rn(t.x, q.x), __fadd_rn(t.y, q.y), __fadd_rn(t.z, q.z),
-                                __fadd_rn(t.w, q.w));
-            }
-            s = make_float4(__fadd_rn(s.x, p.x), __fadd_rn(s.y, p.y), __fadd_rn(s.z, p.z),
-                            __fadd_rn(s.w, p.w));
-        }
-    join[0][warp][lane] = s;
-    join[1][warp][lane] = t;
-    __syncthreads();
-    if (warp > 1 || n >= a.D || (warp == 1 && weight))
-        return;
-    s = join[warp][0][lane];
+    if (n < a.D) {
+        constexpr uint32_t kStep = 2 * kColumnWarps;
+        const float* from = a.partials + n;
+        for (uint32_t i = first + 2 * warp + (lane >> 4); i < end; i += 4 * kStep) {
+            float4 p[4], q[4];  // on their way at once
 #pragma unroll
-    for (int k = 1; k < kColumnThreads / 32; ++k) {
-        const float4 p = join[warp][k][lane];
-        s = make_float4(__fadd_rn(s.x, p.x), __fadd_rn(s.y, p.y), __fadd_rn(s.z, p.z),
-                        __fadd_rn(s.w, p.w));
-    }
-    float* to = weight ? a.grad_weight : warp ? a.grad_shift : a.grad_scale;
-    if (!to)
-        return;
-    if (!weight) {
-        to += static_cast<int64_t>(slice) * a.D;
-        if (warp == 0 && a.weight) {
-            const float4 f = row4(a.weight, 0);
-            s = make_float4(__fmul_rn(s.x, f.x), __fmul_rn(s.y, f.y), __fmul_rn(s.z, f.z),
-                            __fmul_rn(s.w, f.w));
+            for (int k = 0; k < 4; ++k) {
+                p[k] = q[k] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+                if (i + k * kStep < end) {
+                    const float* at = from + static_cast<int64_t>(i + k * kStep) * 2 * a.D;
+                    p[k] = *reinterpret_cast<const float4*>(at);
+                    if (!weight)
+                        q[k] = *reinterpret_cast<const float4*>(at + a.D);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                if (weight && i + k * kStep < end)
+                    p[k] = under_scale(p[k], per_batch.div(i + k * kStep));
+                s = add4(s, p[k]);
+                t = add4(t, q[k]);
+            }
         }
     }
-    *reinterpret_cast<float4*>(to + n) = s;
+    auto halves = [&](float4 p) {
+        return add4(p, make_float4(__shfl_xor_sync(kFullMask, p.x, 16),
+                                   __shfl_xor_sync(kFullMask, p.y, 16),
+                                   __shfl_xor_sync(kFullMask, p.z, 16),
+                                   __shfl_xor_sync(kFullMask, p.w, 16)));
+    };
+    s = halves(s);
+    t = halves(t);
+    join[lane >> 4][warp][lane & 15] = lane >> 4 ? t : s;
+    __syncthreads();
+    if (warp)
+        return;
+    s = join[lane >> 4][0][lane & 15];  // lanes 16 and on: the sums of go
+#pragma unroll
+    for (int k = 1; k < kColumnWarps; ++k)
+        s = add4(s, join[lane >> 4][k][lane & 15]);
+    if (n >= a.D)
+        return;
+    const int64_t at = static_cast<int64_t>(slice) * a.D + n;
+    if (lane >> 4) {
+        if (!weight && a.grad_shift)
+            *reinterpret_cast<float4*>(a.grad_shift + at) = s;
+        return;
+    }
+    if (weight || (one && a.grad_weight))
+        *reinterpret_cast<float4*>(a.grad_weight + n) = weight ? s : under_scale(s, 0);
+    if (!weight && a.grad_scale)
+        *reinterpret_cast<float4*>(a.grad_scale + at) = a.weight ? mul4(s, row4(a.weight, 0)) : s;
 }
 
 template <typename T, int V>
-cudaError_t launch_backward_rows(const Mxfp8NormBwdArgs& a, const BwdPlan& plan, int grid, int smem,
-                                 const DeviceInfo& dev, cudaStream_t stream)
+cudaError_t launch_backward_rows(const Mxfp8NormBwdArgs& a, BwdPlan p, const DeviceInfo& dev,
+                                 cudaStream_t stream)
 {
+    const int fixed = V > 2 ? a.D * 4 : p.groups > 1 ? V * kBwdJoin : 0;
+    const int slot = p.groups * p.row_bytes;
+    p.stages = (kBwdSmem - fixed) / slot;
+    p.stages = p.stages > kBwdMaxStages ? kBwdMaxStages : p.stages;
+    if (p.stages < 2)  // (four vectors: that of the row before stays taken until this one is summed)
+        return cudaErrorInvalidValue;
     static PerDeviceInt ready;
     int v = 0;
     const cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
@@ -680,7 +764,9 @@ cudaError_t launch_backward_rows(const Mxfp8NormBwdArgs& a, const BwdPlan& plan,
     });
     if (e != cudaSuccess)
         return e;
-    return launch_dependent(norm_backward_kernel<T, V>, grid, kBwdThreads, smem, stream, a, plan);
+    const int grid = static_cast<int>(p.count) < dev.sms ? static_cast<int>(p.count) : dev.sms;
+    return launch_dependent(norm_backward_kernel<T, V>, grid, kBwdThreads,
+                            fixed + p.stages * slot, stream, a, p);
 }
 
 template <typename T>
@@ -690,33 +776,22 @@ cudaError_t launch_backward(const Mxfp8NormBwdArgs& a, const DeviceInfo& dev, cu
     const int64_t per_batch = (a.S + chunk - 1) / chunk, count = a.B * per_batch;
     if (count > INT32_MAX)
         return cudaErrorInvalidValue;
-    const int V = bwd_vectors(a.D);
     BwdPlan p{};
     p.per_batch = FastDiv::make(static_cast<uint32_t>(per_batch));
     p.chunk = static_cast<uint32_t>(chunk);
     p.count = static_cast<uint32_t>(count);
     p.warps = bwd_warps(a.D);
-    p.groups = kBwdWarps / p.warps;
+    p.groups = bwd_groups(a.D);
     p.row_bytes = a.D * (a.grad_res ? 5 : 3);
-    const int fixed = V == 4 ? a.D * 4 : 0;
-    p.stages = (kBwdRing - 0) / (p.groups * p.row_bytes);
-    p.stages = p.stages < 2 ? 2 : p.stages > kBwdMaxStages ? kBwdMaxStages : p.stages;
-    const int smem = fixed + p.groups * p.stages * p.row_bytes;
-    if (smem > kBwdSmem)
-        return cudaErrorInvalidValue;
-    const int64_t ctas = (count + p.groups - 1) / p.groups;
-    const int grid = static_cast<int>(ctas < dev.sms ? ctas : dev.sms);
-    cudaError_t e;
-    if (V == 1)
-        e = launch_backward_rows<T, 1>(a, p, grid, smem, dev, stream);
-    else if (V == 2)
-        e = launch_backward_rows<T, 2>(a, p, grid, smem, dev, stream);
-    else
-        e = launch_backward_rows<T, 4>(a, p, grid, smem, dev, stream);
+    const int V = bwd_vectors(a.D);
+    const cudaError_t e = V == 1   ? launch_backward_rows<T, 1>(a, p, dev, stream)
+                          : V == 2 ? launch_backward_rows<T, 2>(a, p, dev, stream)
+                                   : launch_backward_rows<T, 4>(a, p, dev, stream);
     if (e != cudaSuccess || !a.sums)
         return e;
-    const int64_t tiles = (a.D + 127) / 128;
-    const int64_t slices = (a.grad_weight ? 1 : 0) + (a.grad_scale || a.grad_shift ? a.B : 0);
+    const int64_t tiles = (a.D + 63) / 64;
+    const int64_t slices =
+        a.B == 1 ? 1 : (a.grad_weight ? 1 : 0) + (a.grad_scale || a.grad_shift ? a.B : 0);
     if (slices * tiles > INT32_MAX)
         return cudaErrorInvalidValue;
     return launch_dependent(norm_columns_kernel<T>, static_cast<int>(slices * tiles), kColumnThreads,
