@@ -42,24 +42,6 @@ __device__ __forceinline__ Unit unit_of(const Mxfp8RowsArgs& a, uint32_t u)
     return t;
 }
 
-// Eight values of one of the four lanes that share a block, to codes; the block's scale byte.
-__device__ __forceinline__ uint32_t quantize8(float (&f)[8], uint2& codes)
-{
-    uint32_t bits = 0;
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        bits = max(bits, magnitude_bits(f[j]));
-    bits = max(bits, __shfl_xor_sync(kFullMask, bits, 1));
-    bits = max(bits, __shfl_xor_sync(kFullMask, bits, 2));
-    const uint32_t byte = mx8_scale_byte(bits);
-    const float inv = mx8_inverse(byte);
-#pragma unroll
-    for (int j = 0; j < 8; ++j)
-        f[j] = __fmul_rn(f[j], inv);
-    codes = make_uint2(e4m3x4(f[0], f[1], f[2], f[3]), e4m3x4(f[4], f[5], f[6], f[7]));
-    return byte;
-}
-
 // The four scale bytes of a row's block tile, from lanes 0, 4, 8 and 12 of its sixteen.
 __device__ __forceinline__ uint32_t join_bytes(uint32_t byte, int base)
 {
@@ -70,14 +52,13 @@ __device__ __forceinline__ uint32_t join_bytes(uint32_t byte, int base)
     return w;
 }
 
-__device__ __forceinline__ void values8(uint2 codes, float scale, float (&f)[8])
+__device__ __forceinline__ void values8(uint2 codes, float scale, u64 (&f)[4])
 {
+    e4m3x4_values(codes.x, f[0], f[1]);
+    e4m3x4_values(codes.y, f[2], f[3]);
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const float2 p = e4m3x2_values(((j < 2 ? codes.x : codes.y) >> (16 * (j & 1))) & 0xFFFFu);
-        f[2 * j] = __fmul_rn(p.x, scale);
-        f[2 * j + 1] = __fmul_rn(p.y, scale);
-    }
+    for (int j = 0; j < 4; ++j)
+        f[j] = f2_mul(f[j], f2_splat(scale));
 }
 
 template <typename T>
@@ -101,18 +82,15 @@ __global__ void __launch_bounds__(kThreads) quantize8_kernel(const Mxfp8RowsArgs
     uint4 four;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        float f[8];
+        u64 f[4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 p = widen2<T>(word(v[i], j));
-            f[2 * j] = p.x;
-            f[2 * j + 1] = p.y;
-        }
-        uint2 c;
-        word(four, i) = join_bytes(quantize8(f, c), lane & 16);
+        for (int j = 0; j < 4; ++j)
+            f[j] = widen<T>(word(v[i], j));
+        uint32_t c[2];
+        word(four, i) = join_bytes(quantize_pairs<4, 4>(f, c), lane & 16);
         const uint32_t row = t.row + 32 * i;
         if (row < a.rows && col < a.Kv)
-            codes[static_cast<int64_t>(row) * a.Kv + col] = c;
+            codes[static_cast<int64_t>(row) * a.Kv + col] = make_uint2(c[0], c[1]);
     }
     if (sub == 0 && t.row < a.rows_padded)
         static_cast<uint4*>(a.scales)[t.scale_word] = four;
@@ -141,12 +119,12 @@ __global__ void __launch_bounds__(kThreads) dequantize8_kernel(const Mxfp8RowsAr
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t row = t.row + 32 * i;
-        float f[8];
+        u64 f[4];
         values8(c[i], mx8_scale((word(four, i) >> (8 * (sub >> 2))) & 0xFFu), f);
         uint4 o;
 #pragma unroll
         for (int j = 0; j < 4; ++j)
-            word(o, j) = narrow2<T>(f[2 * j], f[2 * j + 1]);
+            word(o, j) = narrow<T>(f[j]);
         if (row < a.rows)
             st_stream(out + static_cast<int64_t>(row) * a.Kv + col, o);
     }
@@ -241,9 +219,11 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
             const int r = 4 * q + i;
             const uint32_t w = tile[(warp * 32 + r) * 32 + lane];
             const int e = static_cast<int>(byte_of(scale_in[r * 4 + warp], block));
-            const float2 lo = e4m3x2_values(w & 0xFFFFu), hi = e4m3x2_values(w >> 16);
-            const float v[4] = {lo.x, lo.y, hi.x, hi.y};
-            float s[4];
+            u64 lo, hi;
+            e4m3x4_values(w, lo, hi);
+            float v[4], s[4];
+            f2_unpack(lo, v[0], v[1]);
+            f2_unpack(hi, v[2], v[3]);
 #pragma unroll
             for (int c = 0; c < 4; ++c) {
                 // 2^(e - n): at most 2^17 where the code is not zero
@@ -284,7 +264,7 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
 // A CTA takes 128 rows of one batch by 128 columns; sixteen lanes a row, eight columns each, so that a
 // thread's columns stay the same and their sums are in registers.  The rows of a batch are counted
 // from its first, so a batch's sums do not depend on what stands before it.
-template <typename T, int ACT>
+template <typename T, int ACT, bool GATED>
 __global__ void __launch_bounds__(kThreads)
     activation_backward_kernel(const Mxfp8ActBwdArgs a, int64_t chunks, int parts)
 {
@@ -302,25 +282,24 @@ __global__ void __launch_bounds__(kThreads)
     // all rows of a row tile are this CTA's: its scales are stored four rows at a time
     const bool whole = begin % 128 == 0 && (end == begin + 128 || end == M);
     const bool has = n < a.N;
-    const uint8_t* __restrict__ z = static_cast<const uint8_t*>(a.z);
-    const T* __restrict__ grad = static_cast<const T*>(a.grad_out);
+    const uint8_t* __restrict__ z = static_cast<const uint8_t*>(a.z) + begin * a.N + n;
+    const T* __restrict__ grad = static_cast<const T*>(a.grad_out) + begin * a.N + n;
     const uint32_t* __restrict__ z_scales = static_cast<const uint32_t*>(a.z_scales);
+    uint8_t* grad_z = static_cast<uint8_t*>(a.grad_z) + begin * a.N + n;
     uint32_t* grad_scales = static_cast<uint32_t*>(a.grad_z_scales);
-    float gate[8], sb[8], sg[8];
+    const int rows = static_cast<int>(end - begin), N = static_cast<int>(a.N);
+    u64 gate[4], sb[4], sg[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        gate[j] = 1.0f;
-        sb[j] = sg[j] = 0.0f;
+    for (int j = 0; j < 4; ++j) {
+        gate[j] = f2_splat(1.0f);
+        sb[j] = sg[j] = 0ull;
     }
-    if (a.gate && has) {
+    if (GATED && has) {
         const uint4 g = ld_cached(reinterpret_cast<const uint4*>(
             static_cast<const T*>(a.gate) + batch * a.gate_bstride + n));
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float2 p = widen2<T>(word(g, j));
-            gate[2 * j] = p.x;
-            gate[2 * j + 1] = p.y;
-        }
+        for (int j = 0; j < 4; ++j)
+            gate[j] = widen<T>(word(g, j));
     }
 #pragma unroll 1
     for (int i0 = 0; i0 < 2; ++i0) {
@@ -330,46 +309,56 @@ __global__ void __launch_bounds__(kThreads)
         uint32_t e[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t m = begin + r + 32 * i;
+            const int m = r + 32 * i;
             c[i] = make_uint2(0u, 0u);
             g[i] = make_uint4(0u, 0u, 0u, 0u);
             e[i] = 0u;
-            if (m < end && has) {
-                c[i] = ld_stream2(reinterpret_cast<const uint2*>(z + m * a.N + n));
-                g[i] = ld_stream(reinterpret_cast<const uint4*>(grad + m * a.N + n));
-                e[i] = __ldg(z_scales + mx8_scale_at(m, tile * 4, tiles) / 4);
+            if (m < rows && has) {
+                c[i] = ld_stream2(reinterpret_cast<const uint2*>(z + static_cast<int64_t>(m) * N));
+                g[i] = ld_stream(reinterpret_cast<const uint4*>(grad + static_cast<int64_t>(m) * N));
+                if (!whole)
+                    e[i] = __ldg(z_scales + mx8_scale_at(begin + m, tile * 4, tiles) / 4);
             }
+        }
+        const int64_t four_at = (begin / 128 * tiles + tile) * 32 + r;  // `whole`
+        if (whole) {
+            const uint4 w = ld_cached(reinterpret_cast<const uint4*>(z_scales) + four_at);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                e[i] = word(w, i);
         }
         uint4 four;
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const int64_t m = begin + r + 32 * i;
-            float f[8], d[8];
-            values8(c[i], mx8_scale((e[i] >> (8 * (sub >> 2))) & 0xFFu), f);
+            const int m = r + 32 * i;
+            const uint32_t byte = (e[i] >> (8 * (sub >> 2))) & 0xFFu;
+            // past 2^32 the derivative is 1 or 0 all the same
+            const float scale = mx8_scale(byte > 159u && byte != 255u ? 159u : byte);
+            u64 f[4], d[4];
+            values8(c[i], scale, f);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float2 p = widen2<T>(word(g[i], j));
-                d[2 * j] = p.x;
-                d[2 * j + 1] = p.y;
+                const u64 go = widen<T>(word(g[i], j));
+                u64 part;
+                d[j] = f2_mul(go, slope2<ACT>(f[j], part));
+                if (GATED) {
+                    d[j] = f2_mul(d[j], gate[j]);
+                    if (parts & 2)
+                        sg[j] = f2_fma(f2_mul(go, f[j]), part, sg[j]);
+                }
+                sb[j] = f2_add(sb[j], d[j]);
             }
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                float slope;
-                const float h = activate<ACT>(f[j], slope);
-                sg[j] = __fmaf_rn(d[j], h, sg[j]);
-                d[j] = __fmul_rn(__fmul_rn(d[j], slope), gate[j]);
-                sb[j] = __fadd_rn(sb[j], d[j]);
-            }
-            uint2 out;
-            const uint32_t w = join_bytes(quantize8(d, out), lane & 16);
+            uint32_t out[2];
+            const uint32_t w = join_bytes(quantize_pairs<4, 4>(d, out), lane & 16);
             word(four, i) = w;
-            if (m < end && has)
-                *reinterpret_cast<uint2*>(static_cast<uint8_t*>(a.grad_z) + m * a.N + n) = out;
-            if (!whole && sub == 0 && m < end)
-                grad_scales[mx8_scale_at(m, tile * 4, tiles) / 4] = w;
+            if (m < rows && has)
+                *reinterpret_cast<uint2*>(grad_z + static_cast<int64_t>(m) * N) =
+                    make_uint2(out[0], out[1]);
+            if (!whole && sub == 0 && m < rows)
+                grad_scales[mx8_scale_at(begin + m, tile * 4, tiles) / 4] = w;
         }
         if (whole && sub == 0)
-            reinterpret_cast<uint4*>(grad_scales)[(begin / 128 * tiles + tile) * 32 + r] = four;
+            reinterpret_cast<uint4*>(grad_scales)[four_at] = four;
     }
     if (!whole && end == M)  // rows behind the last one
         for (int64_t m = M + threadIdx.x; m < (M + 127) / 128 * 128; m += kThreads)
@@ -377,12 +366,20 @@ __global__ void __launch_bounds__(kThreads)
     if (!parts)
         return;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        sb[j] = __fadd_rn(sb[j], __shfl_xor_sync(kFullMask, sb[j], 16));
-        sg[j] = __fadd_rn(sg[j], __shfl_xor_sync(kFullMask, sg[j], 16));
+    for (int j = 0; j < 4; ++j) {
+        float4 v;
+        f2_unpack(sb[j], v.x, v.y);
+        f2_unpack(sg[j], v.z, v.w);
+        v.x = __fadd_rn(v.x, __shfl_xor_sync(kFullMask, v.x, 16));
+        v.y = __fadd_rn(v.y, __shfl_xor_sync(kFullMask, v.y, 16));
+        if (GATED) {
+            v.z = __fadd_rn(v.z, __shfl_xor_sync(kFullMask, v.z, 16));
+            v.w = __fadd_rn(v.w, __shfl_xor_sync(kFullMask, v.w, 16));
+        }
         if (lane < 16) {
-            sums[0][warp][sub * 8 + j] = sb[j];
-            sums[1][warp][sub * 8 + j] = sg[j];
+            *reinterpret_cast<float2*>(&sums[0][warp][sub * 8 + 2 * j]) = make_float2(v.x, v.y);
+            if (GATED)
+                *reinterpret_cast<float2*>(&sums[1][warp][sub * 8 + 2 * j]) = make_float2(v.z, v.w);
         }
     }
     __syncthreads();
@@ -443,23 +440,28 @@ int64_t sum_chunks(int64_t B, int64_t S, bool per_batch)
     return ((per_batch ? S : B * S) + 127) / 128;
 }
 
+template <typename T, int ACT>
+cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int grid, int64_t chunks, int parts,
+                              cudaStream_t stream)
+{
+    return launch_dependent(a.gate ? activation_backward_kernel<T, ACT, true>
+                                   : activation_backward_kernel<T, ACT, false>,
+                            grid, kThreads, 0, stream, a, chunks, parts);
+}
+
 template <typename T>
 cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int grid, int64_t chunks, int parts,
                               cudaStream_t stream)
 {
     switch (a.activation) {
     case kActSilu:
-        return launch_dependent(activation_backward_kernel<T, kActSilu>, grid, kThreads, 0, stream, a,
-                                chunks, parts);
+        return launch_activation<T, kActSilu>(a, grid, chunks, parts, stream);
     case kActGelu:
-        return launch_dependent(activation_backward_kernel<T, kActGelu>, grid, kThreads, 0, stream, a,
-                                chunks, parts);
+        return launch_activation<T, kActGelu>(a, grid, chunks, parts, stream);
     case kActGeluTanh:
-        return launch_dependent(activation_backward_kernel<T, kActGeluTanh>, grid, kThreads, 0,
-                                stream, a, chunks, parts);
+        return launch_activation<T, kActGeluTanh>(a, grid, chunks, parts, stream);
     default:
-        return launch_dependent(activation_backward_kernel<T, kActNone>, grid, kThreads, 0, stream, a,
-                                chunks, parts);
+        return launch_activation<T, kActNone>(a, grid, chunks, parts, stream);
     }
 }
 

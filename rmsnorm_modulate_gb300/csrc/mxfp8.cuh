@@ -40,6 +40,15 @@ __device__ __forceinline__ uint32_t magnitude_bits(float v)
     return __float_as_uint(v) & 0x7FFFFFFFu;
 }
 
+// max(m, |v.lo|, |v.hi|), NaN if one is.
+__device__ __forceinline__ float absmax2(float m, u64 v)
+{
+    float lo, hi, r;
+    f2_unpack(v, lo, hi);
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(m), "f"(lo), "f"(hi));
+    return r;
+}
+
 // Four e4m3 codes, element 0 in the lowest byte.
 __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
 {
@@ -51,6 +60,14 @@ __device__ __forceinline__ uint32_t e4m3x4(float a, float b, float c, float d)
         : "=r"(r)
         : "f"(a), "f"(b), "f"(c), "f"(d));
     return r;
+}
+
+__device__ __forceinline__ uint32_t e4m3x4(u64 ab, u64 cd)
+{
+    float a, b, c, d;
+    f2_unpack(ab, a, b);
+    f2_unpack(cd, c, d);
+    return e4m3x4(a, b, c, d);
 }
 
 __device__ __forceinline__ uint32_t e4m3_code(float v)
@@ -66,10 +83,11 @@ __device__ __forceinline__ uint32_t e4m3x2_half2(uint32_t codes)
     return h;
 }
 
-__device__ __forceinline__ float2 e4m3x2_values(uint32_t codes)
+// Four codes as two pairs of fp32, exact.
+__device__ __forceinline__ void e4m3x4_values(uint32_t codes, u64& lo, u64& hi)
 {
-    const uint32_t h = e4m3x2_half2(codes);
-    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+    lo = widen<__half>(e4m3x2_half2(codes & 0xFFFFu));
+    hi = widen<__half>(e4m3x2_half2(codes >> 16));
 }
 
 // Where the scale byte of row r, block k of a matrix of `tiles` block tiles (128 values) a row stands.
@@ -78,91 +96,153 @@ __device__ __forceinline__ int64_t mx8_scale_at(int64_t r, int64_t k, int64_t ti
     return ((r >> 7) * tiles + (k >> 2)) * 512 + (r & 31) * 16 + ((r >> 5) & 3) * 4 + (k & 3);
 }
 
-// Thirty-two neighbours that one thread holds, to codes and their scale byte.
-__device__ __forceinline__ uint32_t quantize32(const float (&v)[32], uint4 (&codes)[2])
+// 2 * N neighbours of a block that LANES lanes share, each with as many, to codes and the block's scale
+// byte.
+template <int N, int LANES>
+__device__ __forceinline__ uint32_t quantize_pairs(const u64 (&v)[N], uint32_t (&codes)[N / 2])
 {
-    uint32_t m[4] = {0u, 0u, 0u, 0u};
+    float m[2] = {0.0f, 0.0f};
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        m[i & 3] = max(m[i & 3], magnitude_bits(v[i]));
-    const uint32_t byte = mx8_scale_byte(max(max(m[0], m[1]), max(m[2], m[3])));
-    const float inv = mx8_inverse(byte);
+    for (int i = 0; i < N; ++i)
+        m[i & 1] = absmax2(m[i & 1], v[i]);
+    uint32_t bits = max(__float_as_uint(m[0]), __float_as_uint(m[1]));
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        word(codes[i >> 2], i & 3) =
-            e4m3x4(__fmul_rn(v[4 * i], inv), __fmul_rn(v[4 * i + 1], inv),
-                   __fmul_rn(v[4 * i + 2], inv), __fmul_rn(v[4 * i + 3], inv));
+    for (int off = 1; off < LANES; off *= 2)
+        bits = max(bits, __shfl_xor_sync(kFullMask, bits, off));
+    const uint32_t byte = mx8_scale_byte(bits);
+    const u64 inv = f2_splat(mx8_inverse(byte));
+#pragma unroll
+    for (int i = 0; i < N / 2; ++i)
+        codes[i] = e4m3x4(f2_mul(v[2 * i], inv), f2_mul(v[2 * i + 1], inv));
     return byte;
 }
 
 // ---------------------------------------------------------------------------
-// activations
+// activations, two values at a time
 // ---------------------------------------------------------------------------
 
 // SiLU z p(z); GELU z Phi(z); its tanh form z p(2 sqrt(2 / pi) (z + 0.044715 z^3)), since
 // (1 + tanh(a / 2)) / 2 = p(a); p(a) = 1 / (1 + e^-a).
 enum Activation : int { kActNone = 0, kActSilu = 1, kActGelu = 2, kActGeluTanh = 3 };
 
-// p(a), and q = p(a) (1 - p(a)), from t = e^-|a| <= 1: nothing overflows on either side.  The
-// approximate instructions are good to 2^-22 each and the exponent's rounding to |a| 2^-24, so p is
-// good to 2^-18 where it is 2^-40 and better above: far inside a step of what its products are
-// rounded to.
-__device__ __forceinline__ float logistic(float a, float& q)
+__device__ __forceinline__ float ex2(float v)
 {
-    float t, r;
-    asm("ex2.approx.f32 %0, %1;" : "=f"(t) : "f"(__fmul_rn(fabsf(a), -1.4426950408889634f)));
-    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(__fadd_rn(1.0f, t)));
-    const float s = __fmul_rn(t, r);
-    q = __fmul_rn(s, r);
-    return a >= 0.0f || a != a ? r : s;
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ float rcp(float v)
+{
+    float r;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+__device__ __forceinline__ u64 rcp2(u64 v)
+{
+    float lo, hi;
+    f2_unpack(v, lo, hi);
+    return f2_pack(rcp(lo), rcp(hi));
+}
+
+// `a` where z >= 0 (or is NaN), else b.
+__device__ __forceinline__ u64 by_sign(u64 z, u64 a, u64 b)
+{
+    float zl, zh, al, ah, bl, bh;
+    f2_unpack(z, zl, zh);
+    f2_unpack(a, al, ah);
+    f2_unpack(b, bl, bh);
+    return f2_pack(zl < 0.0f ? bl : al, zh < 0.0f ? bh : ah);
+}
+
+constexpr float kLog2e = 1.4426950408889634f;
+
+// p(a) for a = x log2(e), and q = p(a) (1 - p(a)), from t = e^-|x| <= 1: nothing overflows on either
+// side.  The approximate instructions are good to 2^-22 each and the exponent's rounding to |x| 2^-24,
+// so p is good to 2^-18 where it is 2^-40 and better above: far inside a step of what its products are
+// rounded to.
+__device__ __forceinline__ u64 logistic2(u64 x, u64& q)
+{
+    float lo, hi;
+    f2_unpack(x, lo, hi);
+    const u64 t = f2_pack(ex2(-fabsf(lo)), ex2(-fabsf(hi)));
+    const u64 r = rcp2(f2_add(t, f2_splat(1.0f)));
+    const u64 s = f2_mul(t, r);
+    q = f2_mul(s, r);
+    return by_sign(x, r, s);
 }
 
 constexpr float kGeluSlope = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
-__device__ __forceinline__ float gelu_argument(float z)
+// log2(e) times the logistic's argument.
+__device__ __forceinline__ u64 gelu_argument(u64 z, u64 zz)
 {
-    const float zz = __fmul_rn(z, z);
-    return __fmul_rn(kGeluSlope, __fmaf_rn(__fmul_rn(kGeluCubic, zz), z, z));
+    constexpr float c = kGeluSlope * kLog2e;
+    return f2_mul(z, f2_fma(zz, f2_splat(c * kGeluCubic), f2_splat(c)));
+}
+
+// Phi(z), and e^(-z^2 / 2).  With t = 1 / (1 + c |z|) and P a polynomial,
+//     Phi(-|z|) = e^(-z^2 / 2) t P(t):
+// e^(z^2 / 2) Phi(-|z|) is smooth in t, and goes like t for large |z|.  P is the least maximum of the
+// relative error over |z| <= 19.8, 2^-25.2, found by weighted least squares against erfcx in 64 bits; in
+// fp32 the product is good to 2^-21 (and e^(-z^2 / 2) to z^2 2^-25).  Beyond 19.8 it is 0.
+__device__ __forceinline__ u64 normal2(u64 z, u64 zz, u64& e)
+{
+    constexpr float c = 0.26870057f;
+    constexpr float P[9] = {0.10720491409301758f,  0.10697222501039505f,  0.10184260457754135f,
+                            0.06984031200408936f,  0.1136091947555542f,   -0.07841922342777252f,
+                            0.17966914176940918f,  -0.1299300491809845f,  0.02921086549758911f};
+    float lo, hi;
+    f2_unpack(z, lo, hi);
+    const u64 az = f2_pack(fminf(fabsf(lo), 19.75f), fminf(fabsf(hi), 19.75f));
+    const u64 t = rcp2(f2_fma(az, f2_splat(c), f2_splat(1.0f)));
+    u64 p = f2_splat(P[8]);
+#pragma unroll
+    for (int i = 7; i >= 0; --i)
+        p = f2_fma(p, t, f2_splat(P[i]));
+    f2_unpack(f2_mul(zz, f2_splat(-0.5f * kLog2e)), lo, hi);
+    e = f2_pack(ex2(lo), ex2(hi));
+    const u64 tail = f2_mul(f2_mul(p, t), e);
+    return by_sign(z, f2_sub(f2_splat(1.0f), tail), tail);
 }
 
 template <int ACT>
-__device__ __forceinline__ float activate(float z)
+__device__ __forceinline__ u64 activate2(u64 z)
 {
-    float q;
+    u64 unused;
     if (ACT == kActSilu)
-        return __fmul_rn(z, logistic(z, q));
-    if (ACT == kActGeluTanh)
-        return __fmul_rn(z, logistic(gelu_argument(z), q));
+        return f2_mul(z, logistic2(f2_mul(z, f2_splat(kLog2e)), unused));
     if (ACT == kActGelu)
-        return __fmul_rn(__fmul_rn(0.5f, z), erfcf(__fmul_rn(z, -0.70710678118654752f)));
+        return f2_mul(z, normal2(z, f2_mul(z, z), unused));
+    if (ACT == kActGeluTanh)
+        return f2_mul(z, logistic2(gelu_argument(z, f2_mul(z, z)), unused));
     return z;
 }
 
-// The activation and, in `slope`, its derivative.
+// act'(z), and act(z) / z in `part`.  |z| up to 2^60: the derivative's factors stay finite.
 template <int ACT>
-__device__ __forceinline__ float activate(float z, float& slope)
+__device__ __forceinline__ u64 slope2(u64 z, u64& part)
 {
-    if (ACT == kActSilu || ACT == kActGeluTanh) {
-        float q, rise = 1.0f;
-        const float p = logistic(ACT == kActSilu ? z : gelu_argument(z), q);
-        if (ACT == kActGeluTanh)
-            rise = __fmul_rn(kGeluSlope, __fmaf_rn(3.0f * kGeluCubic, __fmul_rn(z, z), 1.0f));
-        // (q is 0 before z^2 leaves fp32's range)
-        slope = q > 0.0f ? __fmaf_rn(__fmul_rn(z, q), rise, p) : p;
-        return __fmul_rn(z, p);
+    if (ACT == kActNone) {
+        part = f2_splat(1.0f);
+        return part;
     }
+    const u64 zz = f2_mul(z, z);
     if (ACT == kActGelu) {
-        const float phi = __fmul_rn(0.5f, erfcf(__fmul_rn(z, -0.70710678118654752f)));
-        float t;  // e^(-z^2 / 2)
-        asm("ex2.approx.f32 %0, %1;"
-            : "=f"(t)
-            : "f"(__fmul_rn(__fmul_rn(z, z), -0.72134752044448170f)));
-        slope = t > 0.0f ? __fmaf_rn(__fmul_rn(z, 0.39894228040143268f), t, phi) : phi;
-        return __fmul_rn(z, phi);
+        u64 e;
+        part = normal2(z, zz, e);
+        return f2_fma(f2_mul(z, f2_splat(0.39894228040143268f)), e, part);
     }
-    slope = 1.0f;
-    return z;
+    u64 q;
+    if (ACT == kActSilu) {
+        part = logistic2(f2_mul(z, f2_splat(kLog2e)), q);
+        return f2_fma(z, q, part);
+    }
+    part = logistic2(gelu_argument(z, zz), q);
+    const u64 rise = f2_fma(zz, f2_splat(3.0f * kGeluCubic * kGeluSlope), f2_splat(kGeluSlope));
+    return f2_fma(f2_mul(z, q), rise, part);
 }
 
 }  // namespace rmsmod

@@ -107,45 +107,47 @@ struct Maps {
 
 // Eight values, exact in fp32.
 template <typename T>
-__device__ __forceinline__ void widen8(const uint4* v, float* f)
+__device__ __forceinline__ void widen8(const uint4* v, u64 (&f)[4])
 {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            f[i] = __uint_as_float(word(v[i >> 2], i & 3));
+        for (int i = 0; i < 4; ++i)
+            f[i] = f2_pack(__uint_as_float(word(v[i >> 1], i % 2 * 2)),
+                           __uint_as_float(word(v[i >> 1], i % 2 * 2 + 1)));
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 p = widen2<T>(word(v[0], i));
-            f[2 * i] = p.x;
-            f[2 * i + 1] = p.y;
-        }
+        for (int i = 0; i < 4; ++i)
+            f[i] = widen<T>(word(v[0], i));
     }
 }
 
 template <typename T>
-__device__ __forceinline__ void narrow8(const float* f, uint4* v)
+__device__ __forceinline__ void narrow8(const u64* f, uint4* v)
 {
     if constexpr (sizeof(T) == 4) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            word(v[i >> 2], i & 3) = __float_as_uint(f[i]);
+        for (int i = 0; i < 4; ++i) {
+            float lo, hi;
+            f2_unpack(f[i], lo, hi);
+            word(v[i >> 1], i % 2 * 2) = __float_as_uint(lo);
+            word(v[i >> 1], i % 2 * 2 + 1) = __float_as_uint(hi);
+        }
     } else {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            word(v[0], i) = narrow2<T>(f[2 * i], f[2 * i + 1]);
+            word(v[0], i) = narrow<T>(f[i]);
     }
 }
 
 template <int ACT>
-__device__ __forceinline__ void activate32(float (&v)[32])
+__device__ __forceinline__ void activate32(u64 (&v)[16])
 {
 #pragma unroll
-    for (int i = 0; i < 32; ++i)
-        v[i] = activate<ACT>(v[i]);
+    for (int i = 0; i < 16; ++i)
+        v[i] = activate2<ACT>(v[i]);
 }
 
-__device__ __forceinline__ void activate32(int act, float (&v)[32])
+__device__ __forceinline__ void activate32(int act, u64 (&v)[16])
 {
     switch (act) {
     case kActSilu:
@@ -159,15 +161,23 @@ __device__ __forceinline__ void activate32(int act, float (&v)[32])
     }
 }
 
+template <int ACT>
+__device__ __forceinline__ float activate1(float v)
+{
+    float lo, hi;
+    f2_unpack(activate2<ACT>(f2_splat(v)), lo, hi);
+    return lo;
+}
+
 __device__ __forceinline__ float activate1(int act, float v)
 {
     switch (act) {
     case kActSilu:
-        return activate<kActSilu>(v);
+        return activate1<kActSilu>(v);
     case kActGelu:
-        return activate<kActGelu>(v);
+        return activate1<kActGelu>(v);
     case kActGeluTanh:
-        return activate<kActGeluTanh>(v);
+        return activate1<kActGeluTanh>(v);
     default:
         return v;
     }
@@ -175,9 +185,10 @@ __device__ __forceinline__ float activate1(int act, float v)
 
 // A block's codes at row m, column n of a matrix of N columns.
 __device__ __forceinline__ void store_codes(void* codes, int64_t m, int64_t N, int64_t n,
-                                            bool wide, const uint4 (&c)[2])
+                                            bool wide, const uint32_t (&c)[8])
 {
-    store_pair(reinterpret_cast<uint4*>(static_cast<uint8_t*>(codes) + m * N + n), true, wide, c);
+    const uint4 two[2] = {make_uint4(c[0], c[1], c[2], c[3]), make_uint4(c[4], c[5], c[6], c[7])};
+    store_pair(reinterpret_cast<uint4*>(static_cast<uint8_t*>(codes) + m * N + n), true, wide, two);
 }
 
 // ---------------------------------------------------------------------------
@@ -378,10 +389,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 #pragma unroll 1
             for (int k0 = 0; k0 < P::kCols / 32; ++k0) {
                 const int c = P::kOverlap && acc == 0 ? P::kCols / 32 - 1 - k0 : k0;
-                float v[32];
+                uint32_t acc_bits[32];
                 __syncwarp();
                 after_sync();
-                tmem_load32(from + 32 * c, reinterpret_cast<uint32_t*>(v));
+                tmem_load32(from + 32 * c, acc_bits);
                 // the residual, on its way meanwhile
                 const int64_t n = n0 + 32 * c;
                 uint4 rv[4 * kVecs];
@@ -405,23 +416,28 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                 }
                 if (m >= a.M || n >= a.N)
                     continue;
+                u64 v[16];
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    v[i] = f2_pack(__uint_as_float(acc_bits[2 * i]),
+                                   __uint_as_float(acc_bits[2 * i + 1]));
                 if (bias)
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
                         if (n + 8 * k < a.N) {
                             uint4 q[kVecs];
-                            float f[8];
+                            u64 f[4];
 #pragma unroll
                             for (int i = 0; i < kVecs; ++i)
                                 q[i] = ld_cached(reinterpret_cast<const uint4*>(bias + n + 8 * k) + i);
                             widen8<T>(q, f);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                v[8 * k + i] = __fadd_rn(v[8 * k + i], f[i]);
+                            for (int i = 0; i < 4; ++i)
+                                v[4 * k + i] = f2_add(v[4 * k + i], f[i]);
                         }
-                uint4 codes[2];
+                uint32_t codes[8];
                 if (a.keep) {
-                    keep_bytes |= quantize32(v, codes) << (8 * c);
+                    keep_bytes |= quantize_pairs<16, 1>(v, codes) << (8 * c);
                     store_codes(a.keep, m, a.N, n, a.wide, codes);
                 }
                 activate32(a.activation, v);
@@ -430,33 +446,33 @@ __global__ void __launch_bounds__(kPairThreads, 1)
                     for (int k = 0; k < 4; ++k)
                         if (n + 8 * k < a.N) {
                             uint4 q[kVecs];
-                            float f[8];
+                            u64 f[4];
 #pragma unroll
                             for (int i = 0; i < kVecs; ++i)
                                 q[i] = ld_cached(reinterpret_cast<const uint4*>(gate_b + n + 8 * k) + i);
                             widen8<T>(q, f);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i)
-                                v[8 * k + i] = __fmul_rn(v[8 * k + i], f[i]);
+                            for (int i = 0; i < 4; ++i)
+                                v[4 * k + i] = f2_mul(v[4 * k + i], f[i]);
                         }
                 if (residual)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        float f[8];
+                        u64 f[4];
                         widen8<T>(rv + k * kVecs, f);
 #pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            v[8 * k + i] = __fadd_rn(v[8 * k + i], f[i]);
+                        for (int i = 0; i < 4; ++i)
+                            v[4 * k + i] = f2_add(v[4 * k + i], f[i]);
                     }
                 if (a.out_scales) {
-                    out_bytes |= quantize32(v, codes) << (8 * c);
+                    out_bytes |= quantize_pairs<16, 1>(v, codes) << (8 * c);
                     store_codes(a.out, m, a.N, n, a.wide, codes);
                     continue;
                 }
                 uint4 o[4 * kVecs];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    narrow8<T>(v + 8 * k, o + k * kVecs);
+                    narrow8<T>(v + 4 * k, o + k * kVecs);
                 uint4* to = reinterpret_cast<uint4*>(static_cast<T*>(a.out) + m * a.N + n);
 #pragma unroll
                 for (int k = 0; k < 4 * kVecs; k += 2)

@@ -93,22 +93,21 @@ __global__ void __launch_bounds__(kRows * kMaxRowWarps * 32)
 #pragma unroll
         for (int j = 0; j < V; ++j)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 p = widen2<T>(word(x[j][k >> 2], k & 3));
-                const float2 q = widen2<T>(word(u[j][k >> 2], k & 3));
-                word(x[j][k >> 2], k & 3) = narrow2<T>(__fadd_rn(p.x, q.x), __fadd_rn(p.y, q.y));
-            }
+            for (int k = 0; k < 8; ++k)
+                word(x[j][k >> 2], k & 3) = narrow<T>(f2_add(
+                    widen<T>(word(x[j][k >> 2], k & 3)), widen<T>(word(u[j][k >> 2], k & 3))));
     }
-    float s[2] = {0.0f, 0.0f};
+    u64 s[2] = {0ull, 0ull};
 #pragma unroll
     for (int j = 0; j < V; ++j)
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
-            const float2 p = widen2<T>(word(x[j][k >> 2], k & 3));
-            s[0] = __fmaf_rn(p.x, p.x, s[0]);
-            s[1] = __fmaf_rn(p.y, p.y, s[1]);
+            const u64 p = widen<T>(word(x[j][k >> 2], k & 3));
+            s[k & 1] = f2_fma(p, p, s[k & 1]);
         }
-    const float mine = warp_sum(__fadd_rn(s[0], s[1]));
+    float lo, hi;
+    f2_unpack(f2_add(s[0], s[1]), lo, hi);
+    const float mine = warp_sum(__fadd_rn(lo, hi));
     if (lane == 0)
         part[i][warp] = mine;
     auto joined = [&](int which) {
@@ -177,37 +176,26 @@ __global__ void __launch_bounds__(kRows * kMaxRowWarps * 32)
     // ---- its blocks
     const int64_t mod = has ? by_S.div(row) * a.mod_bstride : 0;
     // a chunk's codes; the four scale bytes of its block tile go to shared memory
-    auto store_chunk = [&](const float (&f)[16], int c, void* codes, int which) {
-        uint32_t bits = 0;
-#pragma unroll
-        for (int k = 0; k < 16; ++k)
-            bits = max(bits, magnitude_bits(f[k]));
-        bits = max(bits, __shfl_xor_sync(kFullMask, bits, 1));
-        const uint32_t byte = mx8_scale_byte(bits);
-        const float inv = mx8_inverse(byte);
-        uint4 o;
-#pragma unroll
-        for (int k = 0; k < 4; ++k)
-            word(o, k) = e4m3x4(__fmul_rn(f[4 * k], inv), __fmul_rn(f[4 * k + 1], inv),
-                                __fmul_rn(f[4 * k + 2], inv), __fmul_rn(f[4 * k + 3], inv));
+    auto store_chunk = [&](const u64 (&f)[8], int c, void* codes, int which) {
+        uint32_t o[4];
+        const uint32_t byte = quantize_pairs<8, 2>(f, o);
         if (has && c < chunks)
-            st_stream(reinterpret_cast<uint4*>(static_cast<uint8_t*>(codes) + base + c * 16), o);
+            st_stream(reinterpret_cast<uint4*>(static_cast<uint8_t*>(codes) + base + c * 16),
+                      make_uint4(o[0], o[1], o[2], o[3]));
         uint32_t w = has && c < chunks ? byte << (8 * ((lane >> 1) & 3)) : 0u;
         w |= __shfl_xor_sync(kFullMask, w, 2);
         w |= __shfl_xor_sync(kFullMask, w, 4);
         if ((lane & 7) == 0 && c < tiles * 8)
             words[(which * tiles + c / 8) * kRows + i] = w;
     };
+    const u64 r2 = f2_splat(rstd), down2 = f2_splat(down);
 #pragma unroll
     for (int j = 0; j < V; ++j) {
         const int c = j * step + at;
-        float f[16];
+        u64 f[8];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const float2 p = widen2<T>(word(x[j][k >> 2], k & 3));
-            f[2 * k] = p.x;
-            f[2 * k + 1] = p.y;
-        }
+        for (int k = 0; k < 8; ++k)
+            f[k] = widen<T>(word(x[j][k >> 2], k & 3));
         if (has && c < chunks && a.update)
             store_pair(reinterpret_cast<uint4*>(static_cast<T*>(a.res_out) + base + c * 16), true,
                        a.wide, x[j]);
@@ -215,52 +203,44 @@ __global__ void __launch_bounds__(kRows * kMaxRowWarps * 32)
             store_chunk(f, c, a.keep, 1);
         if (look)
 #pragma unroll
-            for (int k = 0; k < 16; ++k)
-                f[k] = __fmul_rn(f[k], down);
+            for (int k = 0; k < 8; ++k)
+                f[k] = f2_mul(f[k], down2);
 #pragma unroll
-        for (int k = 0; k < 16; ++k)
-            f[k] = __fmul_rn(f[k], rstd);
+        for (int k = 0; k < 8; ++k)
+            f[k] = f2_mul(f[k], r2);
         if (has && c < chunks) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                float m[8];
+                u64 m[4];
+                auto row = [&](const void* p, int64_t at) {
+                    return ld_cached(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at +
+                                                                    c * 16 + 8 * h));
+                };
                 if (a.weight) {
-                    const uint4 w = ld_cached(reinterpret_cast<const uint4*>(
-                        static_cast<const T*>(a.weight) + c * 16 + 8 * h));
+                    const uint4 w = row(a.weight, 0);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 p = widen2<T>(word(w, k));
-                        m[2 * k] = p.x;
-                        m[2 * k + 1] = p.y;
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        m[k] = widen<T>(word(w, k));
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        m[k] = 1.0f;
+                    for (int k = 0; k < 4; ++k)
+                        m[k] = f2_splat(1.0f);
                 }
                 if (a.scale) {
-                    const uint4 w = ld_cached(reinterpret_cast<const uint4*>(
-                        static_cast<const T*>(a.scale) + mod + c * 16 + 8 * h));
+                    const uint4 w = row(a.scale, mod);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 p = widen2<T>(word(w, k));
-                        m[2 * k] = __fmul_rn(m[2 * k], __fadd_rn(1.0f, p.x));
-                        m[2 * k + 1] = __fmul_rn(m[2 * k + 1], __fadd_rn(1.0f, p.y));
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        m[k] = f2_mul(m[k], f2_add(f2_splat(1.0f), widen<T>(word(w, k))));
                 }
                 if (a.shift) {
-                    const uint4 w = ld_cached(reinterpret_cast<const uint4*>(
-                        static_cast<const T*>(a.shift) + mod + c * 16 + 8 * h));
+                    const uint4 w = row(a.shift, mod);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 p = widen2<T>(word(w, k));
-                        f[8 * h + 2 * k] = __fmaf_rn(f[8 * h + 2 * k], m[2 * k], p.x);
-                        f[8 * h + 2 * k + 1] = __fmaf_rn(f[8 * h + 2 * k + 1], m[2 * k + 1], p.y);
-                    }
+                    for (int k = 0; k < 4; ++k)
+                        f[4 * h + k] = f2_fma(f[4 * h + k], m[k], widen<T>(word(w, k)));
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 8; ++k)
-                        f[8 * h + k] = __fmul_rn(f[8 * h + k], m[k]);
+                    for (int k = 0; k < 4; ++k)
+                        f[4 * h + k] = f2_mul(f[4 * h + k], m[k]);
                 }
             }
         }
