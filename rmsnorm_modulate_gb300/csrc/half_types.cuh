@@ -37,7 +37,21 @@ __device__ __forceinline__ uint32_t narrow2<__half>(float lo, float hi)
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
-// the same on packed fp32 pairs
+// the sum of two words' values, one rounding each (what fp32's sum rounds to as well)
+template <typename T>
+__device__ __forceinline__ uint32_t add2(uint32_t a, uint32_t b);
+template <>
+__device__ __forceinline__ uint32_t add2<__nv_bfloat16>(uint32_t a, uint32_t b)
+{
+    return bf2_add(a, b);
+}
+template <>
+__device__ __forceinline__ uint32_t add2<__half>(uint32_t a, uint32_t b)
+{
+    return h2_add(a, b);
+}
+
+// widening and rounding of packed fp32 pairs
 template <typename T>
 __device__ __forceinline__ u64 widen(uint32_t w)
 {

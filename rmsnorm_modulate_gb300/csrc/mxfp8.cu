@@ -11,6 +11,7 @@
 #include "launch.h"
 #include "mxfp8.cuh"
 #include "mxfp8.h"
+#include "sectors.cuh"
 
 namespace rmsmod {
 
@@ -137,14 +138,30 @@ __global__ void __launch_bounds__(kThreads) dequantize8_kernel(const Mxfp8RowsAr
 // 128 x 128 codes by 128 threads: a thread takes four columns (one word of each row) of 32 rows, which
 // are four of the result's blocks, whole.
 //
-// A value is (1 + m / 8) * 2^(E + e), from a code's fp16 form (every e4m3 value is a normal fp16
-// number) and its scale's exponent: 8 E + m + 8 e, a whole number, orders the magnitudes, so the
-// block's scale is found without rounding whatever the exponents' spread.  Moving a value to the new
-// scale 2^n multiplies it by 2^(e - n), exact in fp32 where the result is not zero; the code keeps its
-// bits but for values under 2^-6 of the new scale's unit, which lose what lies below 2^-9 of it.
+// With the largest scale 2^E of the 32 rows' blocks, a value times 2^(7 - E) is at most 448 * 2^7: an
+// fp16 number, exact down to 2^-24.  So in packed fp16 a column's largest magnitude costs a product and
+// a maximum for two values, and its codes one more product, by the power of two that brings it under
+// the new scale 2^x.  That is the definition's own result while the largest is 2^-3 or more: x is then
+// -11 or more, so what has a code that is not zero is at least 2^(x - 10) = 2^-21 and keeps its four
+// bits.  Else (a column far below its rows' largest, scales 2^32 apart, NaN, the least scale)
+// turn_slowly() goes by whole numbers and fp32.
 constexpr int kTurn = 128;
 
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
+
+__device__ __forceinline__ uint32_t h2_absmax(uint32_t a, uint32_t b)
+{
+    uint32_t d;
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+__device__ __forceinline__ uint32_t e4m3x2_of_half2(uint32_t h)
+{
+    uint16_t r;
+    asm("cvt.rn.satfinite.e4m3x2.f16x2 %0, %1;" : "=h"(r) : "r"(h));
+    return r;
+}
 
 // Order of the two codes' magnitudes (halves of the result), with e8 = 8 * scale byte; zero codes come
 // last.  `nan`: bits 8 and 24 where the code is NaN.
@@ -155,10 +172,71 @@ __device__ __forceinline__ uint32_t order2(uint32_t half2, uint32_t e8, uint32_t
     return k + (((k + 0x00FF00FFu) >> 8) & 0x00010001u) * e8;
 }
 
+// Four rows of four columns to four columns of four rows, at word q of each column.
+__device__ __forceinline__ void turn4(const uint32_t (&w)[4], uint32_t (&out)[4][8], int q)
+{
+    const uint32_t a01 = __byte_perm(w[0], w[1], 0x5140), b01 = __byte_perm(w[0], w[1], 0x7362);
+    const uint32_t a23 = __byte_perm(w[2], w[3], 0x5140), b23 = __byte_perm(w[2], w[3], 0x7362);
+    out[0][q] = __byte_perm(a01, a23, 0x5410);
+    out[1][q] = __byte_perm(a01, a23, 0x7632);
+    out[2][q] = __byte_perm(b01, b23, 0x5410);
+    out[3][q] = __byte_perm(b01, b23, 0x7632);
+}
+
+// For any codes and scales.  A value is (1 + m / 8) * 2^(E + e), from a code's fp16 form (every e4m3
+// value is a normal fp16 number) and its scale's exponent: 8 E + m + 8 e, a whole number, orders the
+// magnitudes, so the block's scale is found without rounding whatever the exponents' spread.  Moving a
+// value to the new scale 2^n multiplies it by 2^(e - n), exact in fp32 where the result is not zero.
+__device__ __noinline__ void turn_slowly(const uint32_t* words, const uint32_t* scale_words, int block,
+                                         uint32_t (&bytes)[4], uint32_t (&out)[4][8])
+{
+    uint32_t top[2] = {0u, 0u}, nan = 0u;
+    for (int r = 0; r < 32; ++r) {
+        const uint32_t w = words[r * 32], e = byte_of(scale_words[r * 4], block);
+        uint32_t n01, n23;
+        top[0] = __vmaxu2(top[0], order2(e4m3x2_half2(w & 0xFFFFu), e * 8u, n01));
+        top[1] = __vmaxu2(top[1], order2(e4m3x2_half2(w >> 16), e * 8u, n23));
+        nan |= n01 | (n23 << 1);
+        if (e == 255u)
+            nan = 0x03000300u;
+    }
+#pragma unroll
+    for (int c = 0; c < 4; ++c) {
+        const uint32_t k = (top[c >> 1] >> (16 * (c & 1))) & 0xFFFFu;
+        const int e = static_cast<int>(k >> 3) - 23 + ((k & 7u) == 7u ? 1 : 0);
+        bytes[c] = e > 0 ? static_cast<uint32_t>(e) : 0u;
+        if (nan & (0x100u << (16 * (c & 1)) << (c >> 1)))
+            bytes[c] = 255u;
+    }
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+        uint32_t w4[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int r = 4 * q + i;
+            const int e = static_cast<int>(byte_of(scale_words[r * 4], block));
+            u64 lo, hi;
+            e4m3x4_values(words[r * 32], lo, hi);
+            float v[4];
+            f2_unpack(lo, v[0], v[1]);
+            f2_unpack(hi, v[2], v[3]);
+#pragma unroll
+            for (int c = 0; c < 4; ++c) {
+                // 2^(e - n): at most 2^17 where the code is not zero
+                const int d = min(max(e - static_cast<int>(bytes[c]), -126), 17);
+                v[c] = __fmul_rn(v[c], __uint_as_float(static_cast<uint32_t>(d + 127) << 23));
+            }
+            w4[i] = e4m3x4(v[0], v[1], v[2], v[3]);
+        }
+        turn4(w4, out, q);
+    }
+}
+
 __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeArgs a)
 {
     __shared__ __align__(16) uint32_t tile[kTurn * kTurn / 4];
     __shared__ __align__(16) uint32_t scale_in[128], scale_out[128];
+    __shared__ uint32_t factors[4][32][4];  // [rows][row][block], in both halves
     grid_dependency_sync();
     const int64_t tiles_k = (a.K + 127) / 128, tiles_r = (a.rows + 127) / 128;
     const int64_t tk = blockIdx.x % tiles_k, tr = blockIdx.x / tiles_k;
@@ -187,68 +265,86 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
     __syncthreads();
     // rows r0 + 32 * warp ..., columns k0 + 4 * lane ...
     const int block = lane >> 3;
-    uint32_t top[2] = {0u, 0u}, nan = 0u;
+    uint32_t top_byte = 0u;  // of this thread's blocks
+    uint32_t far = 0u;       // a bit for each block tile's: a factor that fp16 lacks would count
+    {
+        const uint32_t w = scale_in[lane * 4 + warp];
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            const uint32_t e = byte_of(w, k), most = __reduce_max_sync(kFullMask, e);
+            // 2^(7 - (most - e)): fp16 ends at 2^-24, what counts (448 * 2^-30 > 2^-22) later
+            const int x = 22 - static_cast<int>(most - e);  // biased exponent
+            const uint32_t f = x > 0 ? static_cast<uint32_t>(x) << 10 : x >= -9 ? 1u << (9 + x) : 0u;
+            far |= (x < -9 && x >= -15 ? 1u : 0u) << k;
+            factors[warp][lane][k] = f * 0x00010001u;
+            if (k == block)
+                top_byte = most;
+        }
+    }
+    far = __reduce_or_sync(kFullMask, far);
+    __syncwarp();
+    const uint32_t* words = tile + warp * 32 * 32 + lane;
+    uint32_t v[32][2], top[2], any = 0u;
 #pragma unroll
     for (int r = 0; r < 32; ++r) {
-        const uint32_t w = tile[(warp * 32 + r) * 32 + lane];
-        const uint32_t e = byte_of(scale_in[r * 4 + warp], block);
-        uint32_t n01, n23;
-        top[0] = __vmaxu2(top[0], order2(e4m3x2_half2(w & 0xFFFFu), e * 8u, n01));
-        top[1] = __vmaxu2(top[1], order2(e4m3x2_half2(w >> 16), e * 8u, n23));
-        nan |= n01 | (n23 << 1);
-        if (e == 255u)
-            nan = 0x03000300u;
+        const uint32_t w = words[r * 32], f = factors[warp][r][block];
+        any |= w;
+        v[r][0] = h2_mul(e4m3x2_half2(w & 0xFFFFu), f);
+        v[r][1] = h2_mul(e4m3x2_half2(w >> 16), f);
+        // (begun with the first row: against a constant zero a negative row's magnitude was lost)
+        top[0] = r ? h2_absmax(top[0], v[r][0]) : v[r][0];
+        top[1] = r ? h2_absmax(top[1], v[r][1]) : v[r][1];
     }
-    uint32_t bytes[4];
+    uint32_t bytes[4], g[2] = {0u, 0u};
+    bool slow = top_byte == 255u || (far >> block & 1u);
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
-        const uint32_t k = (top[c >> 1] >> (16 * (c & 1))) & 0xFFFFu;
-        const int e = static_cast<int>(k >> 3) - 23 + ((k & 7u) == 7u ? 1 : 0);
-        bytes[c] = e > 0 ? static_cast<uint32_t>(e) : 0u;
-    }
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-        if (nan & (0x100u << (16 * (c & 1)) << (c >> 1)))
-            bytes[c] = 255u;
-    uint32_t out[4][8];
-#pragma unroll
-    for (int q = 0; q < 8; ++q) {
-        uint32_t w4[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = 4 * q + i;
-            const uint32_t w = tile[(warp * 32 + r) * 32 + lane];
-            const int e = static_cast<int>(byte_of(scale_in[r * 4 + warp], block));
-            u64 lo, hi;
-            e4m3x4_values(w, lo, hi);
-            float v[4], s[4];
-            f2_unpack(lo, v[0], v[1]);
-            f2_unpack(hi, v[2], v[3]);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) {
-                // 2^(e - n): at most 2^17 where the code is not zero
-                const int d = min(max(e - static_cast<int>(bytes[c]), -126), 17);
-                s[c] = __fmul_rn(v[c], __uint_as_float(static_cast<uint32_t>(d + 127) << 23));
-            }
-            w4[i] = e4m3x4(s[0], s[1], s[2], s[3]);
+        const uint32_t h = (top[c >> 1] >> (16 * (c & 1))) & 0x7FFFu;
+        // least x with the largest <= 448 * 2^x (448 = 1.75 * 2^8), and 2^-x in fp16
+        const int x = static_cast<int>(h >> 10) - 23 + ((h & 0x3FFu) > 0x300u ? 1 : 0);
+        const int byte = static_cast<int>(top_byte) - 7 + x;
+        if (((any >> (8 * c)) & 0x7Fu) == 0u) {  // zeros, with either sign
+            bytes[c] = 0u;
+            g[c >> 1] |= 0x3C00u << (16 * (c & 1));
+        } else {
+            slow = slow || h < 0x3000u || h >= 0x7C00u || byte < 0;
+            bytes[c] = static_cast<uint32_t>(byte);
+            g[c >> 1] |= (static_cast<uint32_t>(15 - x) << 10 & 0x7C00u) << (16 * (c & 1));
         }
-        // four rows of four columns to four columns of four rows
-        const uint32_t a01 = __byte_perm(w4[0], w4[1], 0x5140), b01 = __byte_perm(w4[0], w4[1], 0x7362);
-        const uint32_t a23 = __byte_perm(w4[2], w4[3], 0x5140), b23 = __byte_perm(w4[2], w4[3], 0x7362);
-        out[0][q] = __byte_perm(a01, a23, 0x5410);
-        out[1][q] = __byte_perm(a01, a23, 0x7632);
-        out[2][q] = __byte_perm(b01, b23, 0x5410);
-        out[3][q] = __byte_perm(b01, b23, 0x7632);
+    }
+    uint32_t out[4][8];
+    if (slow) {
+        uint32_t slow_bytes[4], slow_out[4][8];
+        turn_slowly(words, scale_in + warp, block, slow_bytes, slow_out);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) {
+            bytes[c] = slow_bytes[c];
+#pragma unroll
+            for (int q = 0; q < 8; ++q)
+                out[c][q] = slow_out[c][q];
+        }
+    } else {
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+            uint32_t w4[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                w4[i] = e4m3x2_of_half2(h2_mul(v[4 * q + i][0], g[0])) |
+                        e4m3x2_of_half2(h2_mul(v[4 * q + i][1], g[1])) << 16;
+            turn4(w4, out, q);
+        }
     }
     const int64_t r = r0 + warp * 32;
+    const bool wide = reinterpret_cast<uintptr_t>(a.out_codes) % 32 == 0;
 #pragma unroll
     for (int c = 0; c < 4; ++c) {
         const int kk = 4 * lane + c;
         const int64_t k = k0 + kk;
         if (k < a.K && r < padded) {
-            uint4* to = reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out_codes) + k * padded + r);
-            to[0] = make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]);
-            to[1] = make_uint4(out[c][4], out[c][5], out[c][6], out[c][7]);
+            const uint4 two[2] = {make_uint4(out[c][0], out[c][1], out[c][2], out[c][3]),
+                                  make_uint4(out[c][4], out[c][5], out[c][6], out[c][7])};
+            store_pair(reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.out_codes) + k * padded + r),
+                       true, wide, two);
             reinterpret_cast<uint8_t*>(scale_out)[(kk & 31) * 16 + (kk >> 5) * 4 + warp] =
                 static_cast<uint8_t>(bytes[c]);
         }

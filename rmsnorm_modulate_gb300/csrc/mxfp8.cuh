@@ -12,20 +12,13 @@
 namespace rmsmod {
 
 // Scale byte of a block whose largest magnitude has the fp32 pattern `bits`: the exponent of the
-// least power of two with max <= 448 * 2^e (448 = 1.75 * 2^8), biased by 127; 255 (NaN) for a block
-// that holds Inf or NaN.
-__device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t bits)
+// least power of two with max <= 448 * 2^e (448 = 1.75 * 2^8: past its mantissa the sum carries into the
+// exponent), biased by 127; 255 (NaN) for a block that holds Inf or NaN.  `inverse`: 2^-e.
+__device__ __forceinline__ uint32_t mx8_scale_byte(uint32_t bits, float& inverse)
 {
-    if (bits >= 0x7F800000u)
-        return 255u;
-    const int e = static_cast<int>(bits >> 23) - 8 + ((bits & 0x7FFFFFu) > 0x600000u ? 1 : 0);
-    return e > 0 ? static_cast<uint32_t>(e) : 0u;
-}
-
-// 2^-e of a scale byte that mx8_scale_byte gave (at most 247, or 255: then 0).
-__device__ __forceinline__ float mx8_inverse(uint32_t byte)
-{
-    return __uint_as_float((254u - (byte == 255u ? 254u : byte)) << 23);
+    const int e = max(static_cast<int>((bits + 0x1FFFFFu) >> 23) - 8, 0);
+    inverse = __uint_as_float(0x7F000000u - (static_cast<uint32_t>(e) << 23));
+    return bits >= 0x7F800000u ? 255u : static_cast<uint32_t>(e);
 }
 
 // What a scale byte stands for.
@@ -109,8 +102,9 @@ __device__ __forceinline__ uint32_t quantize_pairs(const u64 (&v)[N], uint32_t (
 #pragma unroll
     for (int off = 1; off < LANES; off *= 2)
         bits = max(bits, __shfl_xor_sync(kFullMask, bits, off));
-    const uint32_t byte = mx8_scale_byte(bits);
-    const u64 inv = f2_splat(mx8_inverse(byte));
+    float inverse;
+    const uint32_t byte = mx8_scale_byte(bits, inverse);
+    const u64 inv = f2_splat(inverse);
 #pragma unroll
     for (int i = 0; i < N / 2; ++i)
         codes[i] = e4m3x4(f2_mul(v[2 * i], inv), f2_mul(v[2 * i + 1], inv));

@@ -83,10 +83,9 @@ struct Mxfp8NormArgs {
     int D;
     float eps;
     int f16;
-    bool wide;            // set by the launcher: x, update and res_out start on 32 bytes
 };
 
-cudaError_t launch_mxfp8_norm(Mxfp8NormArgs a, const DeviceInfo& dev, cudaStream_t stream);
+cudaError_t launch_mxfp8_norm(const Mxfp8NormArgs& a, const DeviceInfo& dev, cudaStream_t stream);
 
 // Gradients of that norm by res and by its row vectors.
 struct Mxfp8NormBwdArgs {

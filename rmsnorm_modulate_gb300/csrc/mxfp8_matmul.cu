@@ -611,8 +611,10 @@ __global__ void __launch_bounds__(kFewThreads, 1)
     const int64_t scale_tile = static_cast<int64_t>(n0 / 128) * 512 + warp;
     // a warp's 32 values of row m as a block
     auto block = [&](void* codes, void* scales, int m, float v) {
-        const uint32_t byte = mx8_scale_byte(__reduce_max_sync(kFullMask, magnitude_bits(v)));
-        const uint32_t code = e4m3_code(__fmul_rn(v, mx8_inverse(byte)));
+        float inverse;
+        const uint32_t byte =
+            mx8_scale_byte(__reduce_max_sync(kFullMask, magnitude_bits(v)), inverse);
+        const uint32_t code = e4m3_code(__fmul_rn(v, inverse));
         if (has)
             static_cast<uint8_t*>(codes)[m * a.N + n] = static_cast<uint8_t>(code);
         if (lane == 0)

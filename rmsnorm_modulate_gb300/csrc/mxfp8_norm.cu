@@ -16,7 +16,6 @@
 #include "launch.h"
 #include "mxfp8.cuh"
 #include "mxfp8.h"
-#include "sectors.cuh"
 
 namespace rmsmod {
 
@@ -32,6 +31,14 @@ __device__ __forceinline__ float rstd_fast(float sum, float inv_n, float eps)
     return __fmaf_rn(__fmul_rn(0.5f, y), __fmaf_rn(__fmul_rn(-ms, y), y, 1.0f), y);
 }
 
+__device__ __forceinline__ float4 floats(u64 a, u64 b)
+{
+    float4 f;
+    f2_unpack(a, f.x, f.y);
+    f2_unpack(b, f.z, f.w);
+    return f;
+}
+
 __device__ __forceinline__ float warp_sum(float v)
 {
 #pragma unroll
@@ -44,215 +51,369 @@ __device__ __forceinline__ float warp_sum(float v)
 // forward
 // ---------------------------------------------------------------------------
 
-// A CTA takes the four rows r, r + 32, r + 64, r + 96 of a row tile, whose scale bytes are neighbours
-// (they are stored 16 bytes at a time); `warps` warps take a row, each thread V chunks of 16
-// neighbouring values, so that two lanes share a block.
-constexpr int kRows = 4;
-constexpr int kMaxRowWarps = 8;
+// One CTA per SM, whose sixteen warps form groups that take a row each, up to V vectors of eight values
+// a thread.  A unit is the rows r, r + 32, r + 64, r + 96 of a row tile, whose scale bytes are
+// neighbours: a group takes a unit's rows in turn, with a ring of bulk copies ahead of it, and stores
+// their scales 16 bytes at a time.  A CTA has a range of units, dealt to its groups.  A row is in
+// registers when its sum over the group's warps is joined, so its slot is filled again from there on.
+constexpr int kFwdWarps = 16;
+constexpr int kFwdThreads = 32 * kFwdWarps;
+constexpr int kFwdMaxStages = 8;
+constexpr int kFwdSmem = 224 * 1024;  // at four vectors; up to three leave 4 KB more to scale bytes
+
+struct FwdPlan {
+    FastDiv by_S;
+    uint32_t units;
+    int warps;      // of a group
+    int groups;
+    int stages;     // of a group's ring
+    int row_bytes;  // of a slot
+};
 
 template <typename T, int V>
-__global__ void __launch_bounds__(kRows * kMaxRowWarps * 32)
-    norm_kernel(const Mxfp8NormArgs a, int warps, FastDiv by_S)
+__global__ void __launch_bounds__(kFwdThreads, 1)
+    norm_kernel(const Mxfp8NormArgs a, const FwdPlan plan)
 {
-    __shared__ __align__(16) float part[kRows][kMaxRowWarps];
-    extern __shared__ uint32_t words[];  // [out, keep][block tile][row]
-    const int tid = threadIdx.x, lane = tid & 31;
-    const int i = (tid >> 5) / warps;          // which of the four rows
-    const int warp = (tid >> 5) - i * warps;   // of the row
-    const int at = warp * 32 + lane, step = warps * 32;
-    const int chunks = a.D / 16, tiles = (a.D + 127) / 128;
-    const uint32_t tile = blockIdx.x >> 5, r = blockIdx.x & 31;
-    const uint32_t row = tile * 128 + r + 32 * i;
-    const bool has = row < a.rows;
-    if (warp == 0 && lane >= warps && lane < kMaxRowWarps)
-        part[i][lane] = 0.0f;
+    constexpr bool kWide = V > 2;  // the row vectors' products in shared memory, for each group
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ __align__(8) unsigned long long full[kFwdWarps][kFwdMaxStages];
+    // a unit's scale bytes, [warp][half][out, keep][vector][row]; four vectors a thread leave no room
+    // for them: then a row's are stored by themselves, four bytes at a time
+    constexpr bool kStaged = V < 4;
+    __shared__ __align__(16) uint32_t words[kFwdWarps][2][2][kStaged ? V : 1][4];
+    __shared__ float part[2][kFwdWarps], slow[2][kFwdWarps];
+
+    const int lane = threadIdx.x & 31;
+    const int group = (threadIdx.x >> 5) / plan.warps;
+    const int warp = (threadIdx.x >> 5) - group * plan.warps;
+    const int Dv = a.D / 8;
+    const uint32_t tiles = (a.D + 127) / 128;
+    const bool leader = warp == 0 && lane == 0;
+    if (group >= plan.groups)
+        return;  // (no barrier of the whole CTA)
+    auto group_sync = [&]() {
+        if (plan.warps == 1)
+            __syncwarp();
+        else
+            asm volatile("bar.sync %0, %1;" ::"r"(group + 1), "r"(plan.warps * 32) : "memory");
+    };
+    if (leader) {
+        for (int s = 0; s < plan.stages; ++s)
+            mbar_init(smem_addr(&full[group][s]), 1u);
+        mbar_init_fence();
+    }
+    group_sync();
     grid_dependency_sync();
 
-    // ---- the row
-    const int64_t base = static_cast<int64_t>(row) * a.D;
-    uint4 x[V][2];
-#pragma unroll
-    for (int j = 0; j < V; ++j) {
-        const int c = j * step + at;
-        x[j][0] = x[j][1] = make_uint4(0u, 0u, 0u, 0u);
-        if (has && c < chunks)
-            load_pair(reinterpret_cast<const uint4*>(static_cast<const T*>(a.x) + base + c * 16), true,
-                      a.wide, x[j]);
-    }
-    if (a.update) {
-        uint4 u[V][2];
-#pragma unroll
-        for (int j = 0; j < V; ++j) {
-            const int c = j * step + at;
-            u[j][0] = u[j][1] = make_uint4(0u, 0u, 0u, 0u);
-            if (has && c < chunks)
-                load_pair(reinterpret_cast<const uint4*>(static_cast<const T*>(a.update) + base +
-                                                         c * 16),
-                          true, a.wide, u[j]);
-        }
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int k = 0; k < 8; ++k)
-                word(x[j][k >> 2], k & 3) = narrow<T>(f2_add(
-                    widen<T>(word(x[j][k >> 2], k & 3)), widen<T>(word(u[j][k >> 2], k & 3))));
-    }
-    u64 s[2] = {0ull, 0ull};
-#pragma unroll
-    for (int j = 0; j < V; ++j)
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const u64 p = widen<T>(word(x[j][k >> 2], k & 3));
-            s[k & 1] = f2_fma(p, p, s[k & 1]);
-        }
-    float lo, hi;
-    f2_unpack(f2_add(s[0], s[1]), lo, hi);
-    const float mine = warp_sum(__fadd_rn(lo, hi));
-    if (lane == 0)
-        part[i][warp] = mine;
-    auto joined = [&](int which) {
-        const float4 p = *reinterpret_cast<const float4*>(&part[which][0]);
-        const float4 q = *reinterpret_cast<const float4*>(&part[which][4]);
-        return __fadd_rn(__fadd_rn(__fadd_rn(p.x, p.y), __fadd_rn(p.z, p.w)),
-                         __fadd_rn(__fadd_rn(q.x, q.y), __fadd_rn(q.z, q.w)));
-    };
-    // squares that leave fp32's comfortable range: past 2^120 (a warp's part past 2^117), or so small
-    // that a tiny eps leaves them to decide
-    const bool look = __syncthreads_or(mine > 1.6e35f || a.eps < 1e-18f);
-    const float sum = joined(i);
-    const float n = static_cast<float>(a.D);
-    float rstd = rstd_fast(sum, __fdiv_rn(1.0f, n), a.eps);
-    float stored = rstd, down = 1.0f;  // (of scaled rows the values are multiplied by `down` first)
-    if (look) {
-        // again over the power of two of the largest magnitude, joined in fp64
-        uint32_t top = 0u;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 p = widen2<T>(word(x[j][k >> 2], k & 3));
-                top = max(top, max(magnitude_bits(p.x), magnitude_bits(p.y)));
-            }
-        top = __reduce_max_sync(kFullMask, top);
-        __syncthreads();
-        if (lane == 0)
-            part[i][warp] = __uint_as_float(top);
-        __syncthreads();
-        top = 0u;
-#pragma unroll
-        for (int k = 0; k < kMaxRowWarps; ++k)
-            top = max(top, __float_as_uint(part[i][k]));
-        // (Inf, NaN, or nothing but zeros: the sum says it all)
-        const bool scaled = top != 0u && top < 0x7F800000u && (sum > 1.3e36f || sum < 8e-25f);
-        const int e = scaled ? max(ilogbf(__uint_as_float(top)), -126) : 0;
-        float t = 0.0f;
-#pragma unroll
-        for (int j = 0; j < V; ++j)
-#pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float2 p = widen2<T>(word(x[j][k >> 2], k & 3));
-                const float u = scalbnf(p.x, -e), v = scalbnf(p.y, -e);
-                t = __fadd_rn(t, __fadd_rn(__fmul_rn(u, u), __fmul_rn(v, v)));
-            }
-        t = warp_sum(t);
-        __syncthreads();
-        if (lane == 0)
-            part[i][warp] = t;
-        __syncthreads();
-        if (scaled) {
-            const double ms = scalbn(static_cast<double>(joined(i)) / a.D, 2 * e);
-            const double r = 1.0 / sqrt(ms + static_cast<double>(a.eps));
-            // without eps 1 / rms of the smallest rows is past fp32, not so its product with them
-            stored = static_cast<float>(r);
-            rstd = static_cast<float>(scalbn(r, e));
-            down = scalbnf(1.0f, -e);
-        } else if (top == 0u || top >= 0x7F800000u) {  // where Newton's step would multiply 0 by Inf
-            stored = rstd = __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), a.eps)));
-        }
-    }
-    if (has && a.rstd_out && warp == 0 && lane == 0)
-        a.rstd_out[row] = stored;
+    // kWide: the multipliers [Dv], [Dv], and the shifts [Dv]
+    float4* m_lo = reinterpret_cast<float4*>(smem + (kWide ? group * a.D * 6 : 0));
+    uint4* shifts = reinterpret_cast<uint4*>(m_lo + 2 * Dv);
+    uint8_t* ring = smem + (kWide ? plan.groups * a.D * 6 : 0) +
+                    static_cast<size_t>(group) * plan.stages * plan.row_bytes;
 
-    // ---- its blocks
-    const int64_t mod = has ? by_S.div(row) * a.mod_bstride : 0;
-    // a chunk's codes; the four scale bytes of its block tile go to shared memory
-    auto store_chunk = [&](const u64 (&f)[8], int c, void* codes, int which) {
-        uint32_t o[4];
-        const uint32_t byte = quantize_pairs<8, 2>(f, o);
-        if (has && c < chunks)
-            st_stream(reinterpret_cast<uint4*>(static_cast<uint8_t*>(codes) + base + c * 16),
-                      make_uint4(o[0], o[1], o[2], o[3]));
-        uint32_t w = has && c < chunks ? byte << (8 * ((lane >> 1) & 3)) : 0u;
-        w |= __shfl_xor_sync(kFullMask, w, 2);
-        w |= __shfl_xor_sync(kFullMask, w, 4);
-        if ((lane & 7) == 0 && c < tiles * 8)
-            words[(which * tiles + c / 8) * kRows + i] = w;
+    // the CTA's units: ranges whose lengths differ by one at most
+    const uint32_t each = plan.units / gridDim.x, more = plan.units - each * gridDim.x;
+    const uint32_t first = blockIdx.x * each + (blockIdx.x < more ? blockIdx.x : more);
+    const uint32_t last = first + each + (blockIdx.x < more ? 1u : 0u);
+
+    // a walk over this group's rows
+    struct Walk {
+        uint32_t unit, row;
     };
-    const u64 r2 = f2_splat(rstd), down2 = f2_splat(down);
+    auto row_of = [&](uint32_t unit) { return (unit >> 5) * 128 + (unit & 31); };
+    auto open = [&](Walk& w) {  // the first unit from w.unit on that has a row
+        while (w.unit < last && row_of(w.unit) >= a.rows)
+            w.unit += plan.groups;
+        w.row = row_of(w.unit);
+    };
+    auto next = [&](Walk& w) {
+        w.row += 32;
+        if (w.row >= a.rows || (w.row & 127u) < 32u) {
+            w.unit += plan.groups;
+            open(w);
+        }
+    };
+    Walk ahead{first + group, 0u};
+    open(ahead);
+    int put = 0;
+    auto issue = [&]() {  // the leader
+        if (ahead.unit >= last)
+            return;
+        const uint32_t bar = smem_addr(&full[group][put]);
+        const uint32_t dst = smem_addr(ring + static_cast<size_t>(put) * plan.row_bytes);
+        const int64_t from = static_cast<int64_t>(ahead.row) * a.D * 2;
+        fence_proxy_async();
+        mbar_expect_tx(bar, static_cast<uint32_t>(plan.row_bytes));
+        bulk_g2s(dst, static_cast<const uint8_t*>(a.x) + from, a.D * 2, bar);
+        if (a.update)
+            bulk_g2s(dst + a.D * 2, static_cast<const uint8_t*>(a.update) + from, a.D * 2, bar);
+        put = put + 1 == plan.stages ? 0 : put + 1;
+        next(ahead);
+    };
+    if (leader)
+        for (int s = 0; s < plan.stages; ++s)
+            issue();
+
+    int at[V];  // a thread's vectors
+    bool has[V];
 #pragma unroll
     for (int j = 0; j < V; ++j) {
-        const int c = j * step + at;
-        u64 f[8];
+        at[j] = (j * plan.warps + warp) * 32 + lane;
+        has[j] = at[j] < Dv;
+    }
+    // join over the group's warps, in their order; `odd`: two places in turn
+    auto joined = [&](const float (&p)[kFwdWarps]) {
+        float v = (lane & 15) < plan.warps ? p[group * plan.warps + (lane & 15)] : 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f[k] = widen<T>(word(x[j][k >> 2], k & 3));
-        if (has && c < chunks && a.update)
-            store_pair(reinterpret_cast<uint4*>(static_cast<T*>(a.res_out) + base + c * 16), true,
-                       a.wide, x[j]);
-        if (a.keep)
-            store_chunk(f, c, a.keep, 1);
-        if (look)
+        for (int off = 8; off > 0; off >>= 1)
+            v = __fadd_rn(v, __shfl_xor_sync(kFullMask, v, off));
+        return v;
+    };
+    const float n = static_cast<float>(a.D), inv_n = __fdiv_rn(1.0f, n);
+    u64 m[kWide ? 1 : V][4], shift[kWide ? 1 : V][4];
+    uint32_t(*mine)[kStaged ? V : 1][4] = words[group * plan.warps + warp][lane >> 4];  // lanes 0, 16
+    const uint32_t tile_off = static_cast<uint32_t>(at[0]) >> 4;  // of its vector 0 in a row's tiles
+    uint32_t batch = 0xFFFFFFFFu, phase = 0;
+    int get = 0, odd = 0;
+    bool broken = false;
+    for (uint32_t unit = first + group; unit < last; unit += plan.groups) {
+        const uint32_t row0 = row_of(unit);
+        // (not unrolled: four times the code is more than the instruction cache takes)
+#pragma unroll 1
+        for (int i = 0; i < 4; ++i) {
+            const uint32_t row = row0 + 32 * i;
+            // word of vector j in the scales of this row (padding rows have theirs)
+            auto put_word = [&](void* scales, int which, int j, uint32_t w) {
+                if (lane & 15)
+                    return;
+                if (kStaged)
+                    mine[which][kStaged ? j : 0][i] = w;
+                else if (tile_off + 2 * j * plan.warps < tiles)
+                    static_cast<uint32_t*>(scales)[mx8_scale_at(row, 0, tiles) / 4 +
+                                                   (tile_off + 2 * j * plan.warps) * 128] = w;
+            };
+            if (row >= a.rows) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k)
-                f[k] = f2_mul(f[k], down2);
-#pragma unroll
-        for (int k = 0; k < 8; ++k)
-            f[k] = f2_mul(f[k], r2);
-        if (has && c < chunks) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                u64 m[4];
-                auto row = [&](const void* p, int64_t at) {
-                    return ld_cached(reinterpret_cast<const uint4*>(static_cast<const T*>(p) + at +
-                                                                    c * 16 + 8 * h));
+                for (int j = 0; j < V; ++j) {
+                    put_word(a.out_scales, 0, j, 0u);
+                    if (a.keep)
+                        put_word(a.keep_scales, 1, j, 0u);
+                }
+                continue;
+            }
+            const uint32_t b = plan.by_S.div(row);
+            if (b != batch) {
+                batch = b;  // (a thread reads the products that it has written)
+                const int64_t mod = static_cast<int64_t>(b) * a.mod_bstride;
+                auto vec = [&](const void* p, int64_t off, int j) {
+                    return ld_cached(
+                        reinterpret_cast<const uint4*>(static_cast<const T*>(p) + off) + at[j]);
                 };
-                if (a.weight) {
-                    const uint4 w = row(a.weight, 0);
+#pragma unroll
+                for (int j = 0; j < V; ++j) {
+                    u64 t[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k)
-                        m[k] = widen<T>(word(w, k));
+                        t[k] = f2_splat(1.0f);
+                    uint4 sh = make_uint4(0u, 0u, 0u, 0u);
+                    if (has[j] && a.weight) {
+                        const uint4 w = vec(a.weight, 0, j);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            t[k] = widen<T>(word(w, k));
+                    }
+                    if (has[j] && a.scale) {
+                        const uint4 w = vec(a.scale, mod, j);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            t[k] = f2_mul(t[k], f2_add(f2_splat(1.0f), widen<T>(word(w, k))));
+                    }
+                    if (has[j] && a.shift)
+                        sh = vec(a.shift, mod, j);
+                    if (kWide) {
+                        if (has[j]) {
+                            m_lo[at[j]] = floats(t[0], t[1]);
+                            m_lo[Dv + at[j]] = floats(t[2], t[3]);
+                            shifts[at[j]] = sh;
+                        }
+                    } else {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            m[kWide ? 0 : j][k] = t[k];
+                            shift[kWide ? 0 : j][k] = widen<T>(word(sh, k));
+                        }
+                    }
+                }
+            }
+            // ---- the row: R(x + update), and the sum of its squares
+            if (!broken && !mbar_wait(smem_addr(&full[group][get]), phase, kWaitLimitNs)) {
+                broken = true;
+                atomicOr(&g_error, kErrCopyTimeout);
+            }
+            const uint4* slot = reinterpret_cast<const uint4*>(
+                ring + static_cast<size_t>(get) * plan.row_bytes);
+            if (++get == plan.stages) {
+                get = 0;
+                phase ^= 1u;
+            }
+            u64 f[V][4], s[2] = {0ull, 0ull};
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                uint4 x = make_uint4(0u, 0u, 0u, 0u);
+                if (has[j]) {
+                    x = slot[at[j]];
+                    if (a.update) {
+                        const uint4 u = slot[Dv + at[j]];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            word(x, k) = add2<T>(word(x, k), word(u, k));
+                        st_stream(static_cast<uint4*>(a.res_out) +
+                                      static_cast<int64_t>(row) * Dv + at[j], x);
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    f[j][k] = widen<T>(word(x, k));
+                    s[k & 1] = f2_fma(f[j][k], f[j][k], s[k & 1]);
+                }
+            }
+            float lo, hi;
+            f2_unpack(f2_add(s[0], s[1]), lo, hi);
+            float sum = warp_sum(__fadd_rn(lo, hi));
+            if (plan.warps > 1) {
+                if (lane == 0)
+                    part[odd][group * plan.warps + warp] = sum;
+                group_sync();
+                sum = joined(part[odd]);
+                odd ^= 1;
+            } else {
+                __syncwarp();
+            }
+            if (leader)  // every warp is past this row's slot
+                issue();
+            float rstd, stored;
+            u64 down = f2_splat(1.0f);  // of scaled rows, before rstd
+            // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
+            const bool extreme = sum > 1.3e36f || (sum < 8e-25f && a.eps < 1e-18f);
+            if (!extreme) {
+                rstd = stored = rstd_fast(sum, inv_n, a.eps);
+            } else {
+                // again over the power of two of the largest magnitude, joined in fp64
+                float top = 0.0f;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        top = absmax2(top, f[j][k]);
+                uint32_t bits = __reduce_max_sync(kFullMask, __float_as_uint(top));
+                if (lane == 0)
+                    slow[0][group * plan.warps + warp] = __uint_as_float(bits);
+                group_sync();
+                bits = 0u;
+                for (int k = 0; k < plan.warps; ++k)
+                    bits = max(bits, __float_as_uint(slow[0][group * plan.warps + k]));
+                // (Inf, or nothing but zeros: the sum says it all)
+                const bool scaled = bits != 0u && bits < 0x7F800000u;
+                const int e = scaled ? max(ilogbf(__uint_as_float(bits)), -126) : 0;
+                float t = 0.0f;
+#pragma unroll
+                for (int j = 0; j < V; ++j)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        float u, v;
+                        f2_unpack(f[j][k], u, v);
+                        u = scalbnf(u, -e);
+                        v = scalbnf(v, -e);
+                        t = __fadd_rn(t, __fadd_rn(__fmul_rn(u, u), __fmul_rn(v, v)));
+                    }
+                t = warp_sum(t);
+                if (lane == 0)
+                    slow[1][group * plan.warps + warp] = t;
+                group_sync();
+                if (scaled) {
+                    const double ms = scalbn(static_cast<double>(joined(slow[1])) / a.D, 2 * e);
+                    const double r = 1.0 / sqrt(ms + static_cast<double>(a.eps));
+                    // without eps 1 / rms of the smallest rows is past fp32, not so its product with
+                    // them
+                    stored = static_cast<float>(r);
+                    rstd = static_cast<float>(scalbn(r, e));
+                    down = f2_splat(scalbnf(1.0f, -e));
+                } else {
+                    stored = rstd =
+                        __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), a.eps)));
+                }
+            }
+            if (leader && a.rstd_out)
+                a.rstd_out[row] = stored;
+            // ---- its blocks
+            const u64 r2 = f2_splat(rstd);
+            const int64_t base = static_cast<int64_t>(row) * Dv;
+            auto store = [&](const u64 (&v)[4], int j, void* codes, void* scales, int which) {
+                uint32_t o[2];
+                const uint32_t byte = quantize_pairs<4, 4>(v, o);
+                if (has[j])
+                    static_cast<uint2*>(codes)[base + at[j]] = make_uint2(o[0], o[1]);
+                // the four blocks of sixteen lanes' tile
+                uint32_t t = has[j] ? byte << (2 * (lane & 12)) : 0u;
+                t |= __shfl_xor_sync(kFullMask, t, 4);
+                t |= __shfl_xor_sync(kFullMask, t, 8);
+                put_word(scales, which, j, t);
+            };
+#pragma unroll
+            for (int j = 0; j < V; ++j) {
+                if (a.keep)
+                    store(f[j], j, a.keep, a.keep_scales, 1);
+                if (extreme)
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        f[j][k] = f2_mul(f[j][k], down);
+                u64 mm[4], sh[4];
+                if (kWide) {
+                    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
+                    uint4 t = make_uint4(0u, 0u, 0u, 0u);
+                    if (has[j]) {
+                        p = m_lo[at[j]];
+                        q = m_lo[Dv + at[j]];
+                        t = shifts[at[j]];
+                    }
+                    mm[0] = f2_pack(p.x, p.y);
+                    mm[1] = f2_pack(p.z, p.w);
+                    mm[2] = f2_pack(q.x, q.y);
+                    mm[3] = f2_pack(q.z, q.w);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        sh[k] = widen<T>(word(t, k));
                 } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        m[k] = f2_splat(1.0f);
+                    for (int k = 0; k < 4; ++k) {
+                        mm[k] = m[kWide ? 0 : j][k];
+                        sh[k] = shift[kWide ? 0 : j][k];
+                    }
                 }
-                if (a.scale) {
-                    const uint4 w = row(a.scale, mod);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        m[k] = f2_mul(m[k], f2_add(f2_splat(1.0f), widen<T>(word(w, k))));
-                }
-                if (a.shift) {
-                    const uint4 w = row(a.shift, mod);
+                for (int k = 0; k < 4; ++k)
+                    f[j][k] = f2_fma(f2_mul(f[j][k], r2), mm[k], sh[k]);
+                store(f[j], j, a.out, a.out_scales, 0);
+            }
+        }
+        if (kStaged && (lane & 15) == 0) {
+            const uint32_t tile = unit >> 5, r = unit & 31;
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        f[4 * h + k] = f2_fma(f[4 * h + k], m[k], widen<T>(word(w, k)));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        f[4 * h + k] = f2_mul(f[4 * h + k], m[k]);
+            for (int j = 0; j < V; ++j) {
+                const uint32_t t = tile_off + 2 * j * plan.warps;
+                if (t < tiles) {
+                    const int64_t to = (static_cast<int64_t>(tile) * tiles + t) * 32 + r;
+                    static_cast<uint4*>(a.out_scales)[to] =
+                        *reinterpret_cast<const uint4*>(mine[0][kStaged ? j : 0]);
+                    if (a.keep)
+                        static_cast<uint4*>(a.keep_scales)[to] =
+                            *reinterpret_cast<const uint4*>(mine[1][kStaged ? j : 0]);
                 }
             }
         }
-        store_chunk(f, c, a.out, 0);
     }
-    __syncthreads();
-    for (int t = tid; t < tiles * (a.keep ? 2 : 1); t += blockDim.x) {
-        const int which = t >= tiles ? 1 : 0;
-        static_cast<uint4*>(which ? a.keep_scales : a.out_scales)
-            [(static_cast<int64_t>(tile) * tiles + t - which * tiles) * 32 + r] =
-                reinterpret_cast<const uint4*>(words)[t];
-    }
+    if (broken)
+        drain_pause();
 }
 
 // ---------------------------------------------------------------------------
@@ -280,29 +441,21 @@ struct BwdPlan {
     int row_bytes;      // of a slot
 };
 
-int bwd_vectors(int64_t D) { return D <= 256 ? 1 : D <= 8192 ? 2 : 4; }
+int row_vectors(int64_t D) { return D <= 256 ? 1 : D <= 8192 ? 2 : 4; }
 
-int bwd_warps(int64_t D)
+int row_warps(int64_t D)
 {
-    const int V = bwd_vectors(D);
+    const int V = row_vectors(D);
     return static_cast<int>((D / 8 + 32 * V - 1) / (32 * V));
 }
 
-int bwd_groups(int64_t D) { return kBwdWarps / bwd_warps(D); }
+int row_groups(int64_t D) { return kBwdWarps / row_warps(D); }
 
 // Rows of a run: that 152 CTAs have one each, but a few rows for each group at least.
 int64_t bwd_chunk(int64_t S, int64_t D)
 {
-    const int64_t c = (S + 151) / 152, least = 4 * bwd_groups(D);
+    const int64_t c = (S + 151) / 152, least = 4 * row_groups(D);
     return c < least ? least : c;
-}
-
-__device__ __forceinline__ float4 floats(u64 a, u64 b)
-{
-    float4 f;
-    f2_unpack(a, f.x, f.y);
-    f2_unpack(b, f.z, f.w);
-    return f;
 }
 
 template <typename T, int V>
@@ -760,10 +913,10 @@ cudaError_t launch_backward(const Mxfp8NormBwdArgs& a, const DeviceInfo& dev, cu
     p.per_batch = FastDiv::make(static_cast<uint32_t>(per_batch));
     p.chunk = static_cast<uint32_t>(chunk);
     p.count = static_cast<uint32_t>(count);
-    p.warps = bwd_warps(a.D);
-    p.groups = bwd_groups(a.D);
+    p.warps = row_warps(a.D);
+    p.groups = row_groups(a.D);
     p.row_bytes = a.D * (a.grad_res ? 5 : 3);
-    const int V = bwd_vectors(a.D);
+    const int V = row_vectors(a.D);
     const cudaError_t e = V == 1   ? launch_backward_rows<T, 1>(a, p, dev, stream)
                           : V == 2 ? launch_backward_rows<T, 2>(a, p, dev, stream)
                                    : launch_backward_rows<T, 4>(a, p, dev, stream);
@@ -778,31 +931,54 @@ cudaError_t launch_backward(const Mxfp8NormBwdArgs& a, const DeviceInfo& dev, cu
                             0, stream, a, p.per_batch, p.count);
 }
 
-template <typename T>
-cudaError_t launch_forward(const Mxfp8NormArgs& a, cudaStream_t stream)
+template <typename T, int V>
+cudaError_t launch_forward_rows(const Mxfp8NormArgs& a, FwdPlan p, const DeviceInfo& dev,
+                                cudaStream_t stream)
 {
-    // two chunks a thread while eight warps hold the row, one where a warp holds it that way
-    const int chunks = a.D / 16;
-    const int V = chunks <= 32 ? 1 : chunks <= 64 * kMaxRowWarps ? 2 : 4;
-    const int warps = (chunks + 32 * V - 1) / (32 * V);
-    const int grid = static_cast<int>((a.rows + 127u) / 128u * 32u);
-    const int smem = (a.D + 127) / 128 * kRows * 4 * (a.keep ? 2 : 1);
-    const FastDiv by_S = FastDiv::make(a.S);
-    const int threads = kRows * warps * 32;
-    if (V == 1)
-        return launch_dependent(norm_kernel<T, 1>, grid, threads, smem, stream, a, warps, by_S);
-    if (V == 2)
-        return launch_dependent(norm_kernel<T, 2>, grid, threads, smem, stream, a, warps, by_S);
-    return launch_dependent(norm_kernel<T, 4>, grid, threads, smem, stream, a, warps, by_S);
+    const int fixed = V > 2 ? p.groups * a.D * 6 : 0;
+    const int most = kFwdSmem - (V < 4 ? 4096 : 0);
+    p.stages = (most - fixed) / (p.groups * p.row_bytes);
+    p.stages = p.stages > kFwdMaxStages ? kFwdMaxStages : p.stages;
+    if (p.stages < 1)
+        return cudaErrorInvalidValue;
+    static PerDeviceInt ready;
+    int v = 0;
+    const cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
+        n = 1;
+        return cudaFuncSetAttribute(norm_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                    most);
+    });
+    if (e != cudaSuccess)
+        return e;
+    const int grid = static_cast<int>(p.units < static_cast<uint32_t>(dev.sms) ? p.units : dev.sms);
+    return launch_dependent(norm_kernel<T, V>, grid, kFwdThreads,
+                            fixed + p.groups * p.stages * p.row_bytes, stream, a, p);
+}
+
+template <typename T>
+cudaError_t launch_forward(const Mxfp8NormArgs& a, const DeviceInfo& dev, cudaStream_t stream)
+{
+    // as many vectors a thread as leave a row to eight warps: two groups, one of which works while the
+    // other waits for its sum
+    const int Dv = a.D / 8, V = Dv <= 32 ? 1 : Dv <= 512 ? 2 : Dv <= 768 ? 3 : 4;
+    FwdPlan p{};
+    p.by_S = FastDiv::make(a.S);
+    p.units = (a.rows + 127u) / 128u * 32u;
+    p.warps = (Dv + 32 * V - 1) / (32 * V);
+    p.groups = kFwdWarps / p.warps;
+    p.row_bytes = a.D * (a.update ? 4 : 2);
+    return V == 1   ? launch_forward_rows<T, 1>(a, p, dev, stream)
+           : V == 2 ? launch_forward_rows<T, 2>(a, p, dev, stream)
+           : V == 3 ? launch_forward_rows<T, 3>(a, p, dev, stream)
+                    : launch_forward_rows<T, 4>(a, p, dev, stream);
 }
 
 }  // namespace
 
-cudaError_t launch_mxfp8_norm(Mxfp8NormArgs a, const DeviceInfo&, cudaStream_t stream)
+cudaError_t launch_mxfp8_norm(const Mxfp8NormArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
-    const auto on32 = [](const void* p) { return reinterpret_cast<uintptr_t>(p) % 32 == 0; };
-    a.wide = on32(a.x) && on32(a.update) && on32(a.res_out);
-    return a.f16 ? launch_forward<__half>(a, stream) : launch_forward<__nv_bfloat16>(a, stream);
+    return a.f16 ? launch_forward<__half>(a, dev, stream)
+                 : launch_forward<__nv_bfloat16>(a, dev, stream);
 }
 
 size_t mxfp8_norm_backward_workspace_bytes(int64_t B, int64_t S, int64_t D)
