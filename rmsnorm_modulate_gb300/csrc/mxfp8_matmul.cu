@@ -162,24 +162,24 @@ __device__ __forceinline__ void activate32(int act, u64 (&v)[16])
 }
 
 template <int ACT>
-__device__ __forceinline__ float activate1(float v)
+__device__ __forceinline__ void activate4(float (&v)[4])
 {
-    float lo, hi;
-    f2_unpack(activate2<ACT>(f2_splat(v)), lo, hi);
-    return lo;
+    const u64 a = activate2<ACT>(f2_pack(v[0], v[1])), b = activate2<ACT>(f2_pack(v[2], v[3]));
+    f2_unpack(a, v[0], v[1]);
+    f2_unpack(b, v[2], v[3]);
 }
 
-__device__ __forceinline__ float activate1(int act, float v)
+__device__ __forceinline__ void activate4(int act, float (&v)[4])
 {
     switch (act) {
     case kActSilu:
-        return activate1<kActSilu>(v);
+        return activate4<kActSilu>(v);
     case kActGelu:
-        return activate1<kActGelu>(v);
+        return activate4<kActGelu>(v);
     case kActGeluTanh:
-        return activate1<kActGeluTanh>(v);
+        return activate4<kActGeluTanh>(v);
     default:
-        return v;
+        return;
     }
 }
 
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
 // up to 128 rows
 // ---------------------------------------------------------------------------
 
-constexpr int kFewThreads = 192;  // four epilogue warps, producer, issuer
+constexpr int kFewThreads = 320;  // eight epilogue warps, producer, issuer
 constexpr int kFewMaxStages = 10;
 constexpr uint32_t kFewSfwCol = 128;            // accumulators in columns 0..127
 constexpr uint32_t kFewSfxCol = kFewSfwCol + 8;
@@ -541,7 +541,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         mbar_init(smem_addr(&done), 1u);
         mbar_init_fence();
     }
-    if (warp == 5)
+    if (warp == 9)
         tmem_alloc<false, kFewTmemCols>(smem_addr(&tmem_base));
     before_sync();
     __syncthreads();
@@ -557,7 +557,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         }
     };
 
-    if (warp == 4) {
+    if (warp == 8) {
         if (elect_one()) {
             const int block_tiles = static_cast<int>((a.K + 127) / 128);
             int s = 0;
@@ -578,7 +578,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
         }
-    } else if (warp == 5) {
+    } else if (warp == 9) {
         if (elect_one()) {
             const uint32_t idesc = instruction(128, f.NX);
             int s = 0;
@@ -599,104 +599,119 @@ __global__ void __launch_bounds__(kFewThreads, 1)
             commit<false>(smem_addr(&done));
         }
     }
-    // ---- lane n of tensor memory, column m
-    const int n_in = warp * 32 + lane;
+    // ---- lane n of tensor memory, column m: to shared memory, sixteen columns at a time, dealt to the
+    // two warps that see a lane
+    const int quarter = warp & 3, half = warp >> 2;
+    const int n_in = quarter * 32 + lane;
     const int64_t n = n0 + n_in;
-    const bool has = warp < 4 && n < a.N;
+    const bool epilogue = warp < 8, has = epilogue && n < a.N;
     const T* bias = static_cast<const T*>(a.bias);
     const T* gate = static_cast<const T*>(a.gate);
     const T* residual = static_cast<const T*>(a.residual);
     const int M = static_cast<int>(a.M), S = static_cast<int>(a.S);
     const float bias_n = has && bias ? static_cast<float>(bias[n]) : 0.0f;
-    const int64_t scale_tile = static_cast<int64_t>(n0 / 128) * 512 + warp;
-    // a warp's 32 values of row m as a block
-    auto block = [&](void* codes, void* scales, int m, float v) {
-        float inverse;
-        const uint32_t byte =
-            mx8_scale_byte(__reduce_max_sync(kFullMask, magnitude_bits(v)), inverse);
-        const uint32_t code = e4m3_code(__fmul_rn(v, inverse));
-        if (has)
-            static_cast<uint8_t*>(codes)[m * a.N + n] = static_cast<uint8_t>(code);
-        if (lane == 0)
-            static_cast<uint8_t*>(scales)[scale_tile + m % 32 * 16 + m / 32 * 4] =
-                static_cast<uint8_t>(has ? byte : 0u);
-    };
-    // of a whole warp
-    auto finish = [&](int m, float v) {
-        v = __fadd_rn(v, bias_n);
-        if (a.keep)
-            block(a.keep, a.keep_scales, m, v);
-        v = activate1(a.activation, v);
-        if (has && gate)
-            v = __fmul_rn(v, static_cast<float>(gate[m / S * a.gate_bstride + n]));
-        if (has && residual)
-            v = __fadd_rn(v, static_cast<float>(residual[m * a.N + n]));
-        if (a.out_scales)
-            block(a.out, a.out_scales, m, v);
-        else if (has)
-            static_cast<T*>(a.out)[m * a.N + n] = static_cast<T>(v);
-    };
     // scale bytes of rows that the matrix does not have
-    if (warp < 4 && rank == 0) {
+    if (epilogue && half == 0 && rank == 0)
         for (void* scales : {a.keep ? a.keep_scales : nullptr, a.out_scales})
             if (scales && n_in >= M)
                 *reinterpret_cast<uint32_t*>(static_cast<uint8_t*>(scales) + n0 / 128 * 512ll +
                                              n_in % 32 * 16 + n_in / 32 * 4) = 0u;
-    }
     float* part = reinterpret_cast<float*>(raw + (ring - smem_addr(raw)));  // [m][128]
-    if (warp < 4) {
+    if (epilogue) {
         wait(smem_addr(&done), 0);
         __syncwarp();
         after_sync();
-        for (int c = 0; c < M; c += 16) {
+        for (int c = half * 16; c < M; c += 32) {
             uint32_t v[16];
-            tmem_load16(tmem + (static_cast<uint32_t>(warp * 32) << 16) + c, v);
+            tmem_load16(tmem + (static_cast<uint32_t>(quarter * 32) << 16) + c, v);
             tmem_loads_done();
 #pragma unroll
-            for (int j = 0; j < 16; ++j) {
-                if (f.split > 1)
-                    part[(c + j) * 128 + n_in] = __uint_as_float(v[j]);
-                else if (c + j < M)
-                    finish(c + j, __uint_as_float(v[j]));
-            }
+            for (int j = 0; j < 16; ++j)
+                part[(c + j) * 128 + n_in] = __uint_as_float(v[j]);
         }
         before_sync();
     }
     if (broken)
         drain_pause();
-    if (f.split > 1) {
+    if (f.split > 1)
         cluster_barrier();
-        if (warp < 4) {
-            // this CTA's rows of a, four at a time (all their loads on the way at once), the parts of
-            // K in order
-            const uint32_t at = smem_addr(part) + n_in * 4;
-            for (int m = static_cast<int>(rank); m < M; m += 4 * f.split) {
-                float p[4][8];
+    else
+        __syncthreads();
+    if (epilogue) {
+        const int64_t scale_tile = static_cast<int64_t>(n0 / 128) * 512 + quarter;
+        // a warp's 32 values of row m as a block
+        auto block = [&](void* codes, void* scales, int m, float v) {
+            float inverse;
+            const uint32_t byte =
+                mx8_scale_byte(__reduce_max_sync(kFullMask, magnitude_bits(v)), inverse);
+            const uint32_t code = e4m3_code(__fmul_rn(v, inverse));
+            if (has)
+                static_cast<uint8_t*>(codes)[m * a.N + n] = static_cast<uint8_t>(code);
+            if (lane == 0)
+                static_cast<uint8_t*>(scales)[scale_tile + m % 32 * 16 + m / 32 * 4] =
+                    static_cast<uint8_t>(has ? byte : 0u);
+        };
+        // this CTA's rows of a, four at a time (all their loads on the way at once), the parts of K in
+        // order
+        const uint32_t at = smem_addr(part) + n_in * 4;
+        const int step = 2 * f.split;
+#pragma unroll 1
+        for (int m0 = static_cast<int>(rank) * 2 + half; m0 < M; m0 += 4 * step) {
+            float p[4][8], g[4], r[4], v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int m = m0 + i * step;
+                g[i] = 1.0f;
+                r[i] = 0.0f;
+                if (m >= M)
+                    continue;
+                if (has && gate)
+                    g[i] = static_cast<float>(gate[m / S * a.gate_bstride + n]);
+                if (has && residual)
+                    r[i] = static_cast<float>(residual[m * a.N + n]);
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    if (k < f.split)
+                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                                     : "=f"(p[i][k])
+                                     : "r"(in_cta(at + m * 512, k)));
+            }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                v[i] = m0 + i * step < M ? p[i][0] : 0.0f;
+#pragma unroll
+                for (int k = 1; k < 8; ++k)
+                    if (k < f.split && m0 + i * step < M)
+                        v[i] = __fadd_rn(v[i], p[i][k]);
+                v[i] = __fadd_rn(v[i], bias_n);
+            }
+            if (a.keep)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
+                    if (m0 + i * step < M)
+                        block(a.keep, a.keep_scales, m0 + i * step, v[i]);
+            activate4(a.activation, v);
 #pragma unroll
-                    for (int r = 0; r < 8; ++r)
-                        if (r < f.split && m + i * f.split < M)
-                            asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                         : "=f"(p[i][r])
-                                         : "r"(in_cta(at + (m + i * f.split) * 512, r)));
-#pragma unroll
-                for (int i = 0; i < 4; ++i)
-                    if (m + i * f.split < M) {
-                        float v = p[i][0];
-#pragma unroll
-                        for (int r = 1; r < 8; ++r)
-                            if (r < f.split)
-                                v = __fadd_rn(v, p[i][r]);
-                        finish(m + i * f.split, v);
-                    }
+            for (int i = 0; i < 4; ++i) {
+                const int m = m0 + i * step;
+                if (m >= M)
+                    continue;
+                if (gate)
+                    v[i] = __fmul_rn(v[i], g[i]);
+                if (residual)
+                    v[i] = __fadd_rn(v[i], r[i]);
+                if (a.out_scales)
+                    block(a.out, a.out_scales, m, v[i]);
+                else if (has)
+                    static_cast<T*>(a.out)[m * a.N + n] = static_cast<T>(v[i]);
             }
         }
-        cluster_barrier();
-    } else {
-        __syncthreads();
     }
-    if (warp == 5) {
+    if (f.split > 1)
+        cluster_barrier();
+    else
+        __syncthreads();
+    if (warp == 9) {
         after_sync();
         tmem_free<false, kFewTmemCols>(tmem);
     }
@@ -773,9 +788,9 @@ cudaError_t launch_few(const Mxfp8MatmulArgs& a, const DeviceInfo& dev, cudaStre
     f.stages = (kSmemMax - 4096) / f.stage_bytes;
     f.stages = f.stages > kFewMaxStages ? kFewMaxStages : f.stages;
     f.stages = f.stages > most ? most : f.stages;
-    // the parts to be joined take the ring's place
+    // the parts to be joined (or one part on its way to its rows) take the ring's place
     int smem = f.stages * f.stage_bytes;
-    if (f.split > 1 && smem < f.NX * 512)
+    if (smem < f.NX * 512)
         smem = f.NX * 512;
     // more than half of an SM's shared memory: two CTAs that wait for one another's tensor memory
     // and for the rest of their clusters would never end
