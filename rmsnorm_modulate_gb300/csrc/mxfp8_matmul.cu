@@ -517,6 +517,29 @@ struct Few {
     int split;        // CTAs of a cluster, each with a range of the steps
 };
 
+// Sums over the cluster's SPLIT parts, in their order, of four rows (the last one again past M).
+template <int SPLIT>
+__device__ __forceinline__ void join4(float (&v)[4], uint32_t at, int m0, int step, int M)
+{
+    float p[4][SPLIT];
+#pragma unroll
+    for (int k = 0; k < SPLIT; ++k) {
+        const uint32_t from = in_cta(at, k);
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            asm volatile("ld.shared::cluster.f32 %0, [%1];"
+                         : "=f"(p[i][k])
+                         : "r"(from + min(m0 + i * step, M - 1) * 512));
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        v[i] = p[i][0];
+#pragma unroll
+        for (int k = 1; k < SPLIT; ++k)
+            v[i] = __fadd_rn(v[i], p[i][k]);
+    }
+}
+
 template <typename T>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const Mxfp8MatmulArgs a, const __grid_constant__ Maps maps, const Few f)
@@ -657,34 +680,36 @@ __global__ void __launch_bounds__(kFewThreads, 1)
         const int step = 2 * f.split;
 #pragma unroll 1
         for (int m0 = static_cast<int>(rank) * 2 + half; m0 < M; m0 += 4 * step) {
-            float p[4][8], g[4], r[4], v[4];
+            float g[4], r[4], v[4];
+            if (gate)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int m = m0 + i * step;
-                g[i] = 1.0f;
-                r[i] = 0.0f;
-                if (m >= M)
-                    continue;
-                if (has && gate)
-                    g[i] = static_cast<float>(gate[m / S * a.gate_bstride + n]);
-                if (has && residual)
-                    r[i] = static_cast<float>(residual[m * a.N + n]);
+                for (int i = 0; i < 4; ++i) {
+                    const int m = min(m0 + i * step, M - 1);
+                    g[i] = has ? static_cast<float>(gate[m / S * a.gate_bstride + n]) : 0.0f;
+                }
+            if (residual)
 #pragma unroll
-                for (int k = 0; k < 8; ++k)
-                    if (k < f.split)
-                        asm volatile("ld.shared::cluster.f32 %0, [%1];"
-                                     : "=f"(p[i][k])
-                                     : "r"(in_cta(at + m * 512, k)));
+                for (int i = 0; i < 4; ++i) {
+                    const int m = min(m0 + i * step, M - 1);
+                    r[i] = has ? static_cast<float>(residual[m * a.N + n]) : 0.0f;
+                }
+            switch (f.split) {
+            case 1:
+                join4<1>(v, at, m0, step, M);
+                break;
+            case 2:
+                join4<2>(v, at, m0, step, M);
+                break;
+            case 4:
+                join4<4>(v, at, m0, step, M);
+                break;
+            default:
+                join4<8>(v, at, m0, step, M);
             }
+            if (bias)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                v[i] = m0 + i * step < M ? p[i][0] : 0.0f;
-#pragma unroll
-                for (int k = 1; k < 8; ++k)
-                    if (k < f.split && m0 + i * step < M)
-                        v[i] = __fadd_rn(v[i], p[i][k]);
-                v[i] = __fadd_rn(v[i], bias_n);
-            }
+                for (int i = 0; i < 4; ++i)
+                    v[i] = __fadd_rn(v[i], bias_n);
             if (a.keep)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
