@@ -473,6 +473,7 @@ int mxfp4_matmul(const void* a, const void* a_scales, const void* b, const void*
  *   No output may overlap an input or another output, but where said.
  * ---------------------------------------------------------------------- */
 #define RMSMOD_MXFP8_MAX_K 1048576
+#define RMSMOD_MXFP8_DIRECT_ROWS 32
 
 enum { RMSMOD_F32 = 2 };
 
@@ -511,7 +512,9 @@ int mxfp8_transpose(const void* codes, const void* scales, void* out_codes, void
  *     y[m, n] = f(residual[m, n]) + f(gate_b[n]) * act(z[m, n])      (fp32)
  *   out = R(y), or with out_scales out, out_scales = Q(y) along n; keep,
  *   keep_scales (nullable) = Q(z).  bias, gate, residual nullable (no add, no
- *   product).  a [B*S, K], b [N, K] codes with their scales; N a multiple of 8
+ *   product).  a [B*S, K], b [N, K] codes with their scales; without a_scales
+ *   a is up to RMSMOD_MXFP8_DIRECT_ROWS rows of dtype (BF16, F16), which the
+ *   call takes through Q itself.  N a multiple of 8
  *   (of 32 where something is written in 8 bits); gate rows at gate + b *
  *   gate_bstride (elements, a multiple of 8); residual, out, keep [B*S, N];
  *   out may equal residual (not in 8 bits).  One launch.

@@ -982,6 +982,7 @@ class Mxfp8(NamedTuple):
 
 
 _E4M3 = torch.float8_e4m3fn
+_DIRECT_ROWS = 32  # RMSMOD_MXFP8_DIRECT_ROWS
 _ACTIVATIONS = {None: 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 
@@ -1155,6 +1156,8 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
     code = 2 if dtype == torch.float32 else _DTYPES[dtype]
     if isinstance(x, Mxfp8):
         codes, scales = _at(x.codes), _at(x.scales)
+    elif M <= _DIRECT_ROWS:
+        codes, scales = _at(x), None  # quantised by the product itself
     else:
         n = M * K  # a multiple of 32
         q = torch.empty(n + mxfp8_scale_bytes(M, K), dtype=torch.uint8, device=device)

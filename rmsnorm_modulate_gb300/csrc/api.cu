@@ -1178,6 +1178,8 @@ RMSMOD_EXPORT int mxfp4_matmul(const void* a, const void* a_scales, const void* 
 
 // ---- microscaled 8-bit rows, the norm before them, their product, and their backward pass ----------
 
+static_assert(RMSMOD_MXFP8_DIRECT_ROWS == rmsmod::kMxfp8DirectRows, "as the header says");
+
 namespace {
 
 // Bytes of the codes and the tiled scales of an 8-bit matrix; false if unsupported.
@@ -1322,15 +1324,21 @@ RMSMOD_EXPORT int mxfp8_matmul(const void* a, const void* a_scales, const void* 
         return st;
     if (M == 0 || N == 0)
         return RMSMOD_OK;
-    if (!a || !a_scales || !b || !b_scales || !out || (keep == nullptr) != (keep_scales == nullptr))
+    if (!a || !b || !b_scales || !out || (keep == nullptr) != (keep_scales == nullptr))
         return RMSMOD_ERR_NULL;
+    // rows that are quantised on the way
+    if (!a_scales && dtype == RMSMOD_F32)
+        return RMSMOD_ERR_UNSUPPORTED;
+    if (!a_scales && M > RMSMOD_MXFP8_DIRECT_ROWS)
+        return RMSMOD_ERR_SHAPE;
     if (!aligned(a, 16) || !aligned(a_scales, 16) || !aligned(b, 16) || !aligned(b_scales, 16) ||
         !aligned(bias, 16) || !aligned(gate, 16) || !aligned(residual, 16) || !aligned(out, 16) ||
         !aligned(out_scales, 16) || !aligned(keep, 16) || !aligned(keep_scales, 16))
         return RMSMOD_ERR_ALIGN;
     const int64_t each = dtype == RMSMOD_F32 ? 4 : 2;
     const int64_t out_bytes = M * N * (out_scales ? 1 : each);
-    const Span in[] = {{a, za.codes},    {a_scales, za.scales},
+    const Span in[] = {{a, a_scales ? za.codes : 2 * za.codes},
+                       {a_scales, za.scales},
                        {b, zb.codes},    {b_scales, zb.scales},
                        {bias, each * N}, {gate, ((B - 1) * gate_bstride + N) * each}};
     const Span outs[] = {{out, out_bytes},

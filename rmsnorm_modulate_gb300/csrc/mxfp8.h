@@ -38,9 +38,11 @@ cudaError_t launch_mxfp8_transpose(const Mxfp8TransposeArgs& a, cudaStream_t str
 
 // z = a b^T + bias, y = residual + gate * act(z); y to `out` (rounded to the type, or to 8-bit blocks
 // where out_scales are given), z to 8-bit blocks where `keep` is given.
+constexpr int kMxfp8DirectRows = 32;
+
 struct Mxfp8MatmulArgs {
-    const void* a;        // codes [M, K]
-    const void* a_scales;
+    const void* a;        // codes [M, K], or up to kMxfp8DirectRows rows of bf16 or fp16
+    const void* a_scales; // null: of those
     const void* b;        // codes [N, K]
     const void* b_scales;
     const void* bias;     // nullable [N]

@@ -540,7 +540,48 @@ __device__ __forceinline__ void join4(float (&v)[4], uint32_t at, int m0, int st
     }
 }
 
+// Rows of a that come in 16 bits (RAW, up to kMxfp8DirectRows of them): the operand tile and scales of
+// step t, as quantisation and the copies would have laid them.  One warp; sixteen lanes a row.
 template <typename T>
+__device__ __forceinline__ void quantize_step(const Mxfp8MatmulArgs& a, int NX, int t, uint32_t tile,
+                                              uint32_t scales)
+{
+    const int lane = threadIdx.x & 31, sub = lane & 15;
+    const int64_t k = static_cast<int64_t>(t) * kStepK + sub * 8;
+    const T* x = static_cast<const T*>(a.a);
+#pragma unroll 1
+    for (int r0 = 0; r0 < NX; r0 += 16) {
+        uint4 v[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 2 * i + (lane >> 4);
+            v[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (r < a.M && k < a.K)
+                v[i] = ld_stream(reinterpret_cast<const uint4*>(x + r * a.K + k));
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int r = r0 + 2 * i + (lane >> 4);
+            u64 f[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                f[j] = widen<T>(word(v[i], j));
+            uint32_t o[2];
+            uint32_t w = quantize_pairs<4, 4>(f, o) << (2 * (lane & 12));
+            w |= __shfl_xor_sync(kFullMask, w, 4);
+            w |= __shfl_xor_sync(kFullMask, w, 8);
+            // rows of 128 bytes, whose 16-byte chunks are swizzled by the row
+            const uint32_t at = tile + r * kStepK + (((sub >> 1) ^ (r & 7)) << 4) + (sub & 1) * 8;
+            asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(at), "r"(o[0]), "r"(o[1])
+                         : "memory");
+            if (sub == 0)
+                asm volatile("st.shared.b32 [%0], %1;" ::"r"(scales + r * 16), "r"(w) : "memory");
+        }
+    }
+    fence_proxy_async();
+}
+
+template <typename T, bool RAW>
 __global__ void __launch_bounds__(kFewThreads, 1)
     few_kernel(const Mxfp8MatmulArgs a, const __grid_constant__ Maps maps, const Few f)
 {
@@ -558,7 +599,7 @@ __global__ void __launch_bounds__(kFewThreads, 1)
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < f.stages; ++s) {
-            mbar_init(smem_addr(&full[s]), 1u);
+            mbar_init(smem_addr(&full[s]), RAW ? 2u : 1u);
             mbar_init(smem_addr(&empty[s]), 1u);
         }
         mbar_init(smem_addr(&done), 1u);
@@ -589,12 +630,14 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 wait(smem_addr(&empty[s]), phase);
                 const uint32_t bar = smem_addr(&full[s]);
                 const uint32_t dst = ring + s * f.stage_bytes;
-                mbar_expect_tx(bar, f.stage_bytes);
+                mbar_expect_tx(bar, RAW ? kTileBytes + kScaleBytes : f.stage_bytes);
                 tma_box<false>(dst, &maps.b, t * kStepK, n0, bar);
                 tma_box<false>(dst + kTileBytes, &maps.b_scales, 0,
                                2 * (n0 / 128 * block_tiles + t), bar);
-                tma_box<false>(dst + kTileBytes + kScaleBytes, &maps.a_scales, 0, 2 * t, bar);
-                tma_box<false>(dst + kTileBytes + 2 * kScaleBytes, &maps.a, t * kStepK, 0, bar);
+                if (!RAW) {
+                    tma_box<false>(dst + kTileBytes + kScaleBytes, &maps.a_scales, 0, 2 * t, bar);
+                    tma_box<false>(dst + kTileBytes + 2 * kScaleBytes, &maps.a, t * kStepK, 0, bar);
+                }
                 if (++s == f.stages) {
                     s = 0;
                     phase ^= 1u;
@@ -620,6 +663,18 @@ __global__ void __launch_bounds__(kFewThreads, 1)
                 }
             }
             commit<false>(smem_addr(&done));
+        }
+    } else if (RAW) {
+        // the warps that finish the rows later: each takes every eighth step
+        for (int i = warp; i < end - begin; i += 8) {
+            const int s = i % f.stages;
+            wait(smem_addr(&empty[s]), (i / f.stages & 1) ^ 1);
+            const uint32_t sx = ring + s * f.stage_bytes + kTileBytes + kScaleBytes;
+            if constexpr (sizeof(T) == 2)
+                quantize_step<T>(a, f.NX, begin + i, sx + kScaleBytes, sx);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(smem_addr(&full[s]));
         }
     }
     // ---- lane n of tensor memory, column m: to shared memory, sixteen columns at a time, dealt to the
@@ -785,14 +840,14 @@ cudaError_t launch_pair(const Mxfp8MatmulArgs& a, const DeviceInfo& dev, cudaStr
                            maps, static_cast<int>(tiles_m), static_cast<int>(tiles));
 }
 
-template <typename T>
+template <typename T, bool RAW>
 cudaError_t launch_few(const Mxfp8MatmulArgs& a, const DeviceInfo& dev, cudaStream_t stream)
 {
     static PerDeviceInt ready;
     int v = 0;
     cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
         n = 1;
-        return cudaFuncSetAttribute(few_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+        return cudaFuncSetAttribute(few_kernel<T, RAW>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                     kSmemMax - 1024);
     });
     if (e != cudaSuccess)
@@ -821,13 +876,13 @@ cudaError_t launch_few(const Mxfp8MatmulArgs& a, const DeviceInfo& dev, cudaStre
     // and for the rest of their clusters would never end
     if (smem < kSmemMax / 2 + 2048)
         smem = kSmemMax / 2 + 2048;
-    Maps maps;
-    if ((e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, f.NX, 1)) !=
-            cudaSuccess ||
+    Maps maps{};
+    if ((!RAW && (e = matrix_maps(maps.a, maps.a_scales, a.a, a.a_scales, a.M, a.K, f.NX, 1)) !=
+                     cudaSuccess) ||
         (e = matrix_maps(maps.b, maps.b_scales, a.b, a.b_scales, a.N, a.K, 128, 1)) !=
             cudaSuccess)
         return e;
-    return launch_clusters(few_kernel<T>, static_cast<int>(tiles * f.split), f.split, kFewThreads,
+    return launch_clusters(few_kernel<T, RAW>, static_cast<int>(tiles * f.split), f.split, kFewThreads,
                            smem + 1024, stream, a, maps, f);
 }
 
@@ -836,8 +891,13 @@ cudaError_t launch(const Mxfp8MatmulArgs& a, const DeviceInfo& dev, cudaStream_t
 {
     // what the instruction's other side holds; one border for all N and K, so that a row's bits change
     // at one number of rows
+    if (!a.a_scales) {
+        if constexpr (sizeof(T) == 2)
+            return launch_few<T, true>(a, dev, stream);
+        return cudaErrorInvalidValue;
+    }
     if (a.M <= 128)
-        return launch_few<T>(a, dev, stream);
+        return launch_few<T, false>(a, dev, stream);
     // narrower tiles where the wide ones leave half of the SMs without work
     const int64_t wide = (a.M + 255) / 256 * ((a.N + 255) / 256);
     return wide <= dev.sms / 4 ? launch_pair<T, 128>(a, dev, stream)

@@ -303,6 +303,28 @@ def test_product_quantises_its_rows(rm):
     assert torch.equal(a[5:9], rm.mxfp8_linear(x[5:9].contiguous(), w))
 
 
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("M,N,K,kw", [
+    (1, 8, 32, {}), (1, 4096, 4096, {}), (7, 264, 96, {}), (16, 136, 2080, dict(activation="silu")),
+    (17, 96, 352, dict(quantize=True, keep=True)), (32, 4096, 4128, dict(keep=True)),
+    (32, 128, 20480, {}), (33, 128, 160, {}), (5, 16384, 160, dict(quantize=True)),
+])
+def test_product_quantises_few_rows_itself(rm, M, N, K, kw, dtype):
+    # the same bits as with rows that were quantised before
+    rng = np.random.default_rng(M * N + K)
+    x = rows_of(rng, M, K, dtype)
+    x[M // 2, K // 2] = 0.0
+    if M > 2:
+        x[2, :32] = 0.0  # a block of zeros
+    x = x.cuda()
+    w, _ = make(rm, rng, N, K)
+    a = rm.mxfp8_linear(x, w, dtype=dtype, **kw)
+    b = rm.mxfp8_linear(rm.mxfp8_quantize(x), w, dtype=dtype, **kw)
+    flat = lambda v: [t for u in v for t in flat(u)] if isinstance(v, tuple) else [v]  # noqa: E731
+    for p, q in zip(flat(a), flat(b)):
+        assert torch.equal(p.view(torch.uint8), q.view(torch.uint8))
+
+
 def test_rows_do_not_depend_on_how_many_there_are(rm):
     # past 128 rows: narrow and wide tiles give a row the same bits
     rng = np.random.default_rng(10)

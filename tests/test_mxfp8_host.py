@@ -131,8 +131,11 @@ def test_matmul_refusals(rm):
     assert call(dtype=7) == ERR_UNSUPPORTED and call(dtype=-1) == ERR_UNSUPPORTED
     assert call(act=4) == ERR_UNSUPPORTED and call(act=-1) == ERR_UNSUPPORTED
     assert call(gs=4) == ERR_STRIDE and call(gs=-8) == ERR_STRIDE
-    for k in ("a", "sa", "b", "sb", "out", "keep", "sk"):
+    for k in ("a", "b", "sb", "out", "keep", "sk"):
         assert call(**{k: 0}) == ERR_NULL, k
+    # rows that the call quantises: few, and 16 bits wide
+    assert call(sa=0, S=17) == ERR_SHAPE and call(sa=0, S=2, dtype=2) == ERR_UNSUPPORTED
+    assert call(sa=0, S=2, out=at(0) + 4 * 64) == ERR_UNSUPPORTED  # over the second half of a
     for k in ("a", "sa", "b", "sb", "bias", "gate", "res", "out", "so", "keep", "sk"):
         assert call(**{k: at(11) + 8}) == ERR_ALIGN, k
     assert call(S=0, a=0) == OK and call(N=0, a=0) == OK
