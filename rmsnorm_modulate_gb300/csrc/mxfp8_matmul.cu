@@ -101,6 +101,20 @@ struct Maps {
     CUtensorMap a, a_scales, b, b_scales;
 };
 
+// The tiles in the pairs' order: groups of some eight rows of tiles, whose columns come one after the
+// other, so that the pairs that run at a time share few rows of a and of b.
+struct Raster {
+    int tiles_m, tiles_n, group;
+
+    __device__ __forceinline__ void at(int tile, int& m, int& n) const
+    {
+        const int per_group = group * tiles_n, g = tile / per_group, rest = tile - g * per_group;
+        const int first = g * group, rows = tiles_m - first < group ? tiles_m - first : group;
+        n = rest / rows;
+        m = first + rest - n * rows;
+    }
+};
+
 // ---------------------------------------------------------------------------
 // the epilogue
 // ---------------------------------------------------------------------------
@@ -238,7 +252,7 @@ __device__ __forceinline__ void store_scales(void* scales, int64_t m, int64_t M,
 
 template <typename T, int BN>
 __global__ void __launch_bounds__(kPairThreads, 1)
-    pair_kernel(const Mxfp8MatmulArgs a, const __grid_constant__ Maps maps, int tiles_m, int tiles)
+    pair_kernel(const Mxfp8MatmulArgs a, const __grid_constant__ Maps maps, const Raster raster)
 {
     using P = Pair<BN>;
     constexpr int kVecs = sizeof(T) / 2;  // 16-byte vectors of eight columns
@@ -252,6 +266,7 @@ __global__ void __launch_bounds__(kPairThreads, 1)
     const uint32_t ring = (smem_addr(raw) + 1023u) & ~1023u;
     const int steps = static_cast<int>((a.K + kPairSubs * kStepK - 1) / (kPairSubs * kStepK));
     const int pair = blockIdx.x >> 1, pairs = gridDim.x >> 1;
+    const int tiles = raster.tiles_m * raster.tiles_n;
 
     if (threadIdx.x == 0) {
         for (int s = 0; s < P::kStages; ++s) {
@@ -288,8 +303,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
             int s = 0;
             uint32_t phase = 1;
             for (int tile = pair; tile < tiles; tile += pairs) {
-                const int m0 = tile % tiles_m * 256 + static_cast<int>(rank) * 128;
-                const int n0 = tile / tiles_m * BN;
+                int m0, n0;
+                raster.at(tile, m0, n0);
+                m0 = m0 * 256 + static_cast<int>(rank) * 128;
+                n0 *= BN;
                 for (int t = 0; t < steps; ++t) {
                     if (!broken)
                         gave_up(step_wait(smem_addr(&empty[s]), phase));
@@ -377,9 +394,10 @@ __global__ void __launch_bounds__(kPairThreads, 1)
         for (int tile = pair; tile < tiles; tile += pairs) {
             if (!broken)
                 gave_up(step_wait(smem_addr(&acc_full[acc]), phase));
-            const int64_t m = static_cast<int64_t>(tile % tiles_m) * 256 + rank * 128 +
-                              quarter * 32 + lane;
-            const int64_t n0 = static_cast<int64_t>(tile / tiles_m) * BN + half * P::kCols;
+            int tile_m, tile_n;
+            raster.at(tile, tile_m, tile_n);
+            const int64_t m = static_cast<int64_t>(tile_m) * 256 + rank * 128 + quarter * 32 + lane;
+            const int64_t n0 = static_cast<int64_t>(tile_n) * BN + half * P::kCols;
             const T* gate_b = gate && m < a.M ? gate + m / a.S * a.gate_bstride : gate;
             const uint32_t from = tmem + (static_cast<uint32_t>(quarter * 32) << 16) +
                                   acc * P::kAccStep + half * P::kCols;
@@ -836,8 +854,13 @@ cudaError_t launch_pair(const Mxfp8MatmulArgs& a, const DeviceInfo& dev, cudaStr
     if (tiles > INT32_MAX)
         return cudaErrorInvalidValue;
     const int pairs = static_cast<int>(tiles < dev.sms / 2 ? tiles : dev.sms / 2);
+    Raster r;
+    r.tiles_m = static_cast<int>(tiles_m);
+    r.tiles_n = static_cast<int>((a.N + BN - 1) / BN);
+    const int groups = r.tiles_m < 18 ? 1 : (r.tiles_m + 6) / 12;
+    r.group = (r.tiles_m + groups - 1) / groups;
     return launch_clusters(pair_kernel<T, BN>, 2 * pairs, 2, kPairThreads, P::kSmemBytes, stream, a,
-                           maps, static_cast<int>(tiles_m), static_cast<int>(tiles));
+                           maps, r);
 }
 
 template <typename T, bool RAW>
