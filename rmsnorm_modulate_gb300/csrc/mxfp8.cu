@@ -43,13 +43,12 @@ __device__ __forceinline__ Unit unit_of(const Mxfp8RowsArgs& a, uint32_t u)
     return t;
 }
 
-// The four scale bytes of a row's block tile, from lanes 0, 4, 8 and 12 of its sixteen.
-__device__ __forceinline__ uint32_t join_bytes(uint32_t byte, int base)
+// The four scale bytes of a row's block tile, of which each of its sixteen lanes has its block's.
+__device__ __forceinline__ uint32_t join_bytes(uint32_t byte, int lane)
 {
-    uint32_t w = __shfl_sync(kFullMask, byte, base);
-    w |= __shfl_sync(kFullMask, byte, base + 4) << 8;
-    w |= __shfl_sync(kFullMask, byte, base + 8) << 16;
-    w |= __shfl_sync(kFullMask, byte, base + 12) << 24;
+    uint32_t w = byte << (2 * (lane & 12));
+    w |= __shfl_xor_sync(kFullMask, w, 4);
+    w |= __shfl_xor_sync(kFullMask, w, 8);
     return w;
 }
 
@@ -88,7 +87,7 @@ __global__ void __launch_bounds__(kThreads) quantize8_kernel(const Mxfp8RowsArgs
         for (int j = 0; j < 4; ++j)
             f[j] = widen<T>(word(v[i], j));
         uint32_t c[2];
-        word(four, i) = join_bytes(quantize_pairs<4, 4>(f, c), lane & 16);
+        word(four, i) = join_bytes(quantize_pairs<4, 4>(f, c), lane);
         const uint32_t row = t.row + 32 * i;
         if (row < a.rows && col < a.Kv)
             codes[static_cast<int64_t>(row) * a.Kv + col] = make_uint2(c[0], c[1]);
@@ -445,7 +444,7 @@ __global__ void __launch_bounds__(kThreads)
                 sb[j] = f2_add(sb[j], d[j]);
             }
             uint32_t out[2];
-            const uint32_t w = join_bytes(quantize_pairs<4, 4>(d, out), lane & 16);
+            const uint32_t w = join_bytes(quantize_pairs<4, 4>(d, out), lane);
             word(four, i) = w;
             if (m < rows && has)
                 *reinterpret_cast<uint2*>(grad_z + static_cast<int64_t>(m) * N) =

@@ -152,28 +152,29 @@ __device__ __forceinline__ u64 by_sign(u64 z, u64 a, u64 b)
 
 constexpr float kLog2e = 1.4426950408889634f;
 
-// p(a) for a = x log2(e), and q = p(a) (1 - p(a)), from t = e^-|x| <= 1: nothing overflows on either
-// side.  The approximate instructions are good to 2^-22 each and the exponent's rounding to |x| 2^-24,
-// so p is good to 2^-18 where it is 2^-40 and better above: far inside a step of what its products are
-// rounded to.
+// p(a) for a = -x log(2), and q = p(a) (1 - p(a)), from t = 2^x = e^-a, at most 2^127: then t p is 1 - p
+// without a difference, and nothing overflows on either side.  (Past 2^126 p is 0, which the reciprocal
+// flushes to.)
+// The approximate instructions are good to 2^-22 each and the exponent's rounding to |x| 2^-24, so p is
+// good to 2^-18 where it is 2^-40 and better above: far inside a step of what its products are rounded
+// to.  A NaN is left to the factors z.
 __device__ __forceinline__ u64 logistic2(u64 x, u64& q)
 {
     float lo, hi;
     f2_unpack(x, lo, hi);
-    const u64 t = f2_pack(ex2(-fabsf(lo)), ex2(-fabsf(hi)));
-    const u64 r = rcp2(f2_add(t, f2_splat(1.0f)));
-    const u64 s = f2_mul(t, r);
-    q = f2_mul(s, r);
-    return by_sign(x, r, s);
+    const u64 t = f2_pack(ex2(fminf(lo, 127.0f)), ex2(fminf(hi, 127.0f)));
+    const u64 p = rcp2(f2_add(t, f2_splat(1.0f)));
+    q = f2_mul(f2_mul(t, p), p);
+    return p;
 }
 
 constexpr float kGeluSlope = 1.5957691216057308f;  // 2 sqrt(2 / pi)
 constexpr float kGeluCubic = 0.044715f;
 
-// log2(e) times the logistic's argument.
+// -log2(e) times the logistic's argument.
 __device__ __forceinline__ u64 gelu_argument(u64 z, u64 zz)
 {
-    constexpr float c = kGeluSlope * kLog2e;
+    constexpr float c = -kGeluSlope * kLog2e;
     return f2_mul(z, f2_fma(zz, f2_splat(c * kGeluCubic), f2_splat(c)));
 }
 
@@ -207,7 +208,7 @@ __device__ __forceinline__ u64 activate2(u64 z)
 {
     u64 unused;
     if (ACT == kActSilu)
-        return f2_mul(z, logistic2(f2_mul(z, f2_splat(kLog2e)), unused));
+        return f2_mul(z, logistic2(f2_mul(z, f2_splat(-kLog2e)), unused));
     if (ACT == kActGelu)
         return f2_mul(z, normal2(z, f2_mul(z, z), unused));
     if (ACT == kActGeluTanh)
@@ -231,7 +232,7 @@ __device__ __forceinline__ u64 slope2(u64 z, u64& part)
     }
     u64 q;
     if (ACT == kActSilu) {
-        part = logistic2(f2_mul(z, f2_splat(kLog2e)), q);
+        part = logistic2(f2_mul(z, f2_splat(-kLog2e)), q);
         return f2_fma(z, q, part);
     }
     part = logistic2(gelu_argument(z, zz), q);
