@@ -166,6 +166,10 @@ def _stream(stream):
 
 _entries = {}  # the library's functions by name, once looked up
 
+# (torch without CUDA has neither, and no call gets that far)
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", None)
+
 
 def _entry(name):
     fn = _entries.get(name)
@@ -179,12 +183,13 @@ def _call_on(device, stream, name, *args) -> None:
     last argument.  Pointers are passed as integers (_at): half of a small call's time would
     otherwise go into ctypes objects."""
     index = device.index
-    raw = torch._C._cuda_getCurrentRawStream(index) if stream is None else stream.cuda_stream
-    if index == torch._C._cuda_getDevice():
-        st = _entry(name)(*args, raw)
+    raw = _raw_stream(index) if stream is None else stream.cuda_stream
+    fn = _entries.get(name) or _entry(name)
+    if index == _current_device():
+        st = fn(*args, raw)
     else:
         with torch.cuda.device(device):
-            st = _entry(name)(*args, raw)
+            st = fn(*args, raw)
     if st:
         raise RmsmodError(st, name)
 
@@ -588,6 +593,8 @@ _DTYPES = {torch.bfloat16: 0, torch.float16: 1}
 
 
 def _half(t, name):
+    if isinstance(t, torch.Tensor) and t.dtype in _DTYPES and t.is_cuda and t.is_contiguous():
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype not in _DTYPES:
@@ -597,6 +604,9 @@ def _half(t, name):
 
 def _input(t, name, dtype, device, shape):
     """A required contiguous tensor."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and \
+            t.device == device and t.is_contiguous():
+        return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
     if t.dtype is not dtype:
@@ -611,7 +621,8 @@ def _input(t, name, dtype, device, shape):
 
 def _vector(t, name, dtype, device, D):
     """A nullable vector of D elements."""
-    if t is None:
+    if t is None or (isinstance(t, torch.Tensor) and t.dtype is dtype and t.numel() == D and
+                     t.device == device and t.is_contiguous()):
         return
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
@@ -997,10 +1008,14 @@ def _codes8(q, name, device=None):
     if not isinstance(q, Mxfp8):
         raise TypeError(f"{name} must be an Mxfp8")
     codes, scales = q
-    _dense(codes, f"{name}.codes", _E4M3)
-    _dense(scales, f"{name}.scales", torch.uint8)
-    if codes.device != scales.device or (device is not None and codes.device != device):
-        raise ValueError(f"{name} must be on {codes.device if device is None else device}")
+    if not (isinstance(codes, torch.Tensor) and isinstance(scales, torch.Tensor) and
+            codes.dtype is _E4M3 and scales.dtype is torch.uint8 and codes.is_cuda and
+            codes.is_contiguous() and scales.is_contiguous()):
+        _dense(codes, f"{name}.codes", _E4M3)
+        _dense(scales, f"{name}.scales", torch.uint8)
+    at = codes.device
+    if at != scales.device or (device is not None and at != device):
+        raise ValueError(f"{name} must be on {at if device is None else device}")
     shape = codes.shape
     K = shape[-1] if shape else 0
     if K == 0 or K % 32:
