@@ -23,12 +23,18 @@ namespace {
 
 __device__ unsigned int g_error;
 
-// The approximate root and one Newton step: within 2 * 2^-24 of the root.
-__device__ __forceinline__ float rstd_fast(float sum, float inv_n, float eps)
+// 1 / sqrt(sum / n + eps) to half a step and little more, where the sum and the root are normal: every
+// value of a row has its error in common, and what is rounded to e4m3 a step off in it is then on the
+// other side of a border that much more often.  The quotient has its remainder added; one Newton step from
+// the approximate root, whose products' low parts are kept.
+__device__ __forceinline__ float rstd_fast(float sum, float n, float inv_n, float eps)
 {
-    const float ms = __fmaf_rn(sum, inv_n, eps);
+    const float q = __fmul_rn(sum, inv_n);
+    const float ms = __fadd_rn(__fmaf_rn(__fmaf_rn(-q, n, sum), inv_n, q), eps);
     const float y = rsqrtf(ms);
-    return __fmaf_rn(__fmul_rn(0.5f, y), __fmaf_rn(__fmul_rn(-ms, y), y, 1.0f), y);
+    const float h = __fmul_rn(ms, y), l = __fmaf_rn(ms, y, -h);
+    const float e = __fmaf_rn(-l, y, __fmaf_rn(-h, y, 1.0f));  // 1 - ms y^2
+    return __fmaf_rn(__fmul_rn(0.5f, y), e, y);
 }
 
 __device__ __forceinline__ float4 floats(u64 a, u64 b)
@@ -296,7 +302,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
             const bool extreme = sum > 1.3e36f || (sum < 8e-25f && a.eps < 1e-18f);
             if (!extreme) {
-                rstd = stored = rstd_fast(sum, inv_n, a.eps);
+                rstd = stored = rstd_fast(sum, n, inv_n, a.eps);
             } else {
                 // again over the power of two of the largest magnitude, joined in fp64
                 float top = 0.0f;
