@@ -58,18 +58,19 @@ __device__ __forceinline__ float warp_sum(float v)
 // ---------------------------------------------------------------------------
 
 // One CTA per SM, whose sixteen warps form groups that take a row each, up to V vectors of eight values
-// a thread.  A unit is the rows r, r + 32, r + 64, r + 96 of a row tile, whose scale bytes are
-// neighbours: a group takes a unit's rows in turn, with a ring of bulk copies ahead of it, and stores
-// their scales 16 bytes at a time.  A CTA has a range of units, dealt to its groups.  A row is in
-// registers when its sum over the group's warps is joined, so its slot is filled again from there on.
+// a thread.  A CTA has a range of rows, dealt to its groups in turn, and a group a ring of bulk copies
+// ahead of it.  A row is in registers when its sum over the group's warps is joined, so its slot is filled
+// again from there on.  Sixteen lanes' blocks are a block tile, whose scales in the row are one store of
+// four bytes.  (Rows 32 apart in turn, whose scales are neighbours, and one store for four of them: no
+// faster, and a CTA that has two batches' rows changes its row vectors with every row.)
 constexpr int kFwdWarps = 16;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 constexpr int kFwdMaxStages = 8;
-constexpr int kFwdSmem = 224 * 1024;  // at four vectors; up to three leave 4 KB more to scale bytes
+constexpr int kFwdSmem = 224 * 1024;
 
 struct FwdPlan {
     FastDiv by_S;
-    uint32_t units;
+    uint32_t rows;  // those behind the last one, which have scales, among them
     int warps;      // of a group
     int groups;
     int stages;     // of a group's ring
@@ -83,10 +84,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     constexpr bool kWide = V > 2;  // the row vectors' products in shared memory, for each group
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long full[kFwdWarps][kFwdMaxStages];
-    // a unit's scale bytes, [warp][half][out, keep][vector][row]; four vectors a thread leave no room
-    // for them: then a row's are stored by themselves, four bytes at a time
-    constexpr bool kStaged = V < 4;
-    __shared__ __align__(16) uint32_t words[kFwdWarps][2][2][kStaged ? V : 1][4];
     __shared__ float part[2][kFwdWarps], slow[2][kFwdWarps];
 
     const int lane = threadIdx.x & 31;
@@ -117,44 +114,27 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     uint8_t* ring = smem + (kWide ? plan.groups * a.D * 6 : 0) +
                     static_cast<size_t>(group) * plan.stages * plan.row_bytes;
 
-    // the CTA's units: ranges whose lengths differ by one at most
-    const uint32_t each = plan.units / gridDim.x, more = plan.units - each * gridDim.x;
+    // the CTA's rows: ranges whose lengths differ by one at most
+    const uint32_t each = plan.rows / gridDim.x, more = plan.rows - each * gridDim.x;
     const uint32_t first = blockIdx.x * each + (blockIdx.x < more ? blockIdx.x : more);
     const uint32_t last = first + each + (blockIdx.x < more ? 1u : 0u);
+    const uint32_t filled = last < a.rows ? last : a.rows;
 
-    // a walk over this group's rows
-    struct Walk {
-        uint32_t unit, row;
-    };
-    auto row_of = [&](uint32_t unit) { return (unit >> 5) * 128 + (unit & 31); };
-    auto open = [&](Walk& w) {  // the first unit from w.unit on that has a row
-        while (w.unit < last && row_of(w.unit) >= a.rows)
-            w.unit += plan.groups;
-        w.row = row_of(w.unit);
-    };
-    auto next = [&](Walk& w) {
-        w.row += 32;
-        if (w.row >= a.rows || (w.row & 127u) < 32u) {
-            w.unit += plan.groups;
-            open(w);
-        }
-    };
-    Walk ahead{first + group, 0u};
-    open(ahead);
+    uint32_t ahead = first + group;
     int put = 0;
     auto issue = [&]() {  // the leader
-        if (ahead.unit >= last)
+        if (ahead >= filled)
             return;
         const uint32_t bar = smem_addr(&full[group][put]);
         const uint32_t dst = smem_addr(ring + static_cast<size_t>(put) * plan.row_bytes);
-        const int64_t from = static_cast<int64_t>(ahead.row) * a.D * 2;
+        const int64_t from = static_cast<int64_t>(ahead) * a.D * 2;
         fence_proxy_async();
         mbar_expect_tx(bar, static_cast<uint32_t>(plan.row_bytes));
         bulk_g2s(dst, static_cast<const uint8_t*>(a.x) + from, a.D * 2, bar);
         if (a.update)
             bulk_g2s(dst + a.D * 2, static_cast<const uint8_t*>(a.update) + from, a.D * 2, bar);
         put = put + 1 == plan.stages ? 0 : put + 1;
-        next(ahead);
+        ahead += plan.groups;
     };
     if (leader)
         for (int s = 0; s < plan.stages; ++s)
@@ -177,245 +157,220 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     };
     const float n = static_cast<float>(a.D), inv_n = __fdiv_rn(1.0f, n);
     u64 m[kWide ? 1 : V][4], shift[kWide ? 1 : V][4];
-    uint32_t(*mine)[kStaged ? V : 1][4] = words[group * plan.warps + warp][lane >> 4];  // lanes 0, 16
-    const uint32_t tile_off = static_cast<uint32_t>(at[0]) >> 4;  // of its vector 0 in a row's tiles
+    const uint32_t tile0 = static_cast<uint32_t>(at[0]) >> 4;  // of its vector 0 among a row's block tiles
     uint32_t batch = 0xFFFFFFFFu, phase = 0;
     int get = 0, odd = 0;
     bool broken = false;
-    for (uint32_t unit = first + group; unit < last; unit += plan.groups) {
-        const uint32_t row0 = row_of(unit);
-        // (not unrolled: four times the code is more than the instruction cache takes)
-#pragma unroll 1
-        for (int i = 0; i < 4; ++i) {
-            const uint32_t row = row0 + 32 * i;
-            // word of vector j in the scales of this row (padding rows have theirs)
-            auto put_word = [&](void* scales, int which, int j, uint32_t w) {
-                if (lane & 15)
-                    return;
-                if (kStaged)
-                    mine[which][kStaged ? j : 0][i] = w;
-                else if (tile_off + 2 * j * plan.warps < tiles)
-                    static_cast<uint32_t*>(scales)[mx8_scale_at(row, 0, tiles) / 4 +
-                                                   (tile_off + 2 * j * plan.warps) * 128] = w;
-            };
-            if (row >= a.rows) {
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    put_word(a.out_scales, 0, j, 0u);
-                    if (a.keep)
-                        put_word(a.keep_scales, 1, j, 0u);
-                }
-                continue;
-            }
-            const uint32_t b = plan.by_S.div(row);
-            if (b != batch) {
-                batch = b;  // (a thread reads the products that it has written)
-                const int64_t mod = static_cast<int64_t>(b) * a.mod_bstride;
-                auto vec = [&](const void* p, int64_t off, int j) {
-                    return ld_cached(
-                        reinterpret_cast<const uint4*>(static_cast<const T*>(p) + off) + at[j]);
-                };
-#pragma unroll
-                for (int j = 0; j < V; ++j) {
-                    u64 t[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        t[k] = f2_splat(1.0f);
-                    uint4 sh = make_uint4(0u, 0u, 0u, 0u);
-                    if (has[j] && a.weight) {
-                        const uint4 w = vec(a.weight, 0, j);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            t[k] = widen<T>(word(w, k));
-                    }
-                    if (has[j] && a.scale) {
-                        const uint4 w = vec(a.scale, mod, j);
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            t[k] = f2_mul(t[k], f2_add(f2_splat(1.0f), widen<T>(word(w, k))));
-                    }
-                    if (has[j] && a.shift)
-                        sh = vec(a.shift, mod, j);
-                    if (kWide) {
-                        if (has[j]) {
-                            m_lo[at[j]] = floats(t[0], t[1]);
-                            m_lo[Dv + at[j]] = floats(t[2], t[3]);
-                            shifts[at[j]] = sh;
-                        }
-                    } else {
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            m[kWide ? 0 : j][k] = t[k];
-                            shift[kWide ? 0 : j][k] = widen<T>(word(sh, k));
-                        }
-                    }
-                }
-            }
-            // ---- the row: R(x + update), and the sum of its squares
-            if (!broken && !mbar_wait(smem_addr(&full[group][get]), phase, kWaitLimitNs)) {
-                broken = true;
-                atomicOr(&g_error, kErrCopyTimeout);
-            }
-            const uint4* slot = reinterpret_cast<const uint4*>(
-                ring + static_cast<size_t>(get) * plan.row_bytes);
-            if (++get == plan.stages) {
-                get = 0;
-                phase ^= 1u;
-            }
-            u64 f[V][4], s[2] = {0ull, 0ull};
+    for (uint32_t row = first + group; row < last; row += plan.groups) {
+        // the scales of a thread's sixteen lanes' block tile of vector j
+        const int64_t scales_at = mx8_scale_at(row, 0, tiles) / 4;
+        auto put_word = [&](void* scales, int j, uint32_t w) {
+            const uint32_t t = tile0 + 2 * j * plan.warps;
+            if ((lane & 15) == 0 && t < tiles)
+                static_cast<uint32_t*>(scales)[scales_at + t * 128] = w;
+        };
+        if (row >= a.rows) {
 #pragma unroll
             for (int j = 0; j < V; ++j) {
-                uint4 x = make_uint4(0u, 0u, 0u, 0u);
-                if (has[j]) {
-                    x = slot[at[j]];
-                    if (a.update) {
-                        const uint4 u = slot[Dv + at[j]];
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            word(x, k) = add2<T>(word(x, k), word(u, k));
-                        st_stream(static_cast<uint4*>(a.res_out) +
-                                      static_cast<int64_t>(row) * Dv + at[j], x);
-                    }
-                }
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    f[j][k] = widen<T>(word(x, k));
-                    s[k & 1] = f2_fma(f[j][k], f[j][k], s[k & 1]);
-                }
-            }
-            float lo, hi;
-            f2_unpack(f2_add(s[0], s[1]), lo, hi);
-            float sum = warp_sum(__fadd_rn(lo, hi));
-            if (plan.warps > 1) {
-                if (lane == 0)
-                    part[odd][group * plan.warps + warp] = sum;
-                group_sync();
-                sum = joined(part[odd]);
-                odd ^= 1;
-            } else {
-                __syncwarp();
-            }
-            if (leader)  // every warp is past this row's slot
-                issue();
-            float rstd, stored;
-            u64 down = f2_splat(1.0f);  // of scaled rows, before rstd
-            // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
-            const bool extreme = sum > 1.3e36f || (sum < 8e-25f && a.eps < 1e-18f);
-            if (!extreme) {
-                rstd = stored = rstd_fast(sum, n, inv_n, a.eps);
-            } else {
-                // again over the power of two of the largest magnitude, joined in fp64
-                float top = 0.0f;
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        top = absmax2(top, f[j][k]);
-                uint32_t bits = __reduce_max_sync(kFullMask, __float_as_uint(top));
-                if (lane == 0)
-                    slow[0][group * plan.warps + warp] = __uint_as_float(bits);
-                group_sync();
-                bits = 0u;
-                for (int k = 0; k < plan.warps; ++k)
-                    bits = max(bits, __float_as_uint(slow[0][group * plan.warps + k]));
-                // (Inf, or nothing but zeros: the sum says it all)
-                const bool scaled = bits != 0u && bits < 0x7F800000u;
-                const int e = scaled ? max(ilogbf(__uint_as_float(bits)), -126) : 0;
-                float t = 0.0f;
-#pragma unroll
-                for (int j = 0; j < V; ++j)
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        float u, v;
-                        f2_unpack(f[j][k], u, v);
-                        u = scalbnf(u, -e);
-                        v = scalbnf(v, -e);
-                        t = __fadd_rn(t, __fadd_rn(__fmul_rn(u, u), __fmul_rn(v, v)));
-                    }
-                t = warp_sum(t);
-                if (lane == 0)
-                    slow[1][group * plan.warps + warp] = t;
-                group_sync();
-                if (scaled) {
-                    const double ms = scalbn(static_cast<double>(joined(slow[1])) / a.D, 2 * e);
-                    const double r = 1.0 / sqrt(ms + static_cast<double>(a.eps));
-                    // without eps 1 / rms of the smallest rows is past fp32, not so its product with
-                    // them
-                    stored = static_cast<float>(r);
-                    rstd = static_cast<float>(scalbn(r, e));
-                    down = f2_splat(scalbnf(1.0f, -e));
-                } else {
-                    stored = rstd =
-                        __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), a.eps)));
-                }
-            }
-            if (leader && a.rstd_out)
-                a.rstd_out[row] = stored;
-            // ---- its blocks
-            const u64 r2 = f2_splat(rstd);
-            const int64_t base = static_cast<int64_t>(row) * Dv;
-            auto store = [&](const u64 (&v)[4], int j, void* codes, void* scales, int which) {
-                uint32_t o[2];
-                const uint32_t byte = quantize_pairs<4, 4>(v, o);
-                if (has[j])
-                    static_cast<uint2*>(codes)[base + at[j]] = make_uint2(o[0], o[1]);
-                // the four blocks of sixteen lanes' tile
-                uint32_t t = has[j] ? byte << (2 * (lane & 12)) : 0u;
-                t |= __shfl_xor_sync(kFullMask, t, 4);
-                t |= __shfl_xor_sync(kFullMask, t, 8);
-                put_word(scales, which, j, t);
-            };
-#pragma unroll
-            for (int j = 0; j < V; ++j) {
+                put_word(a.out_scales, j, 0u);
                 if (a.keep)
-                    store(f[j], j, a.keep, a.keep_scales, 1);
-                if (extreme)
+                    put_word(a.keep_scales, j, 0u);
+            }
+            continue;
+        }
+        const uint32_t b = plan.by_S.div(row);
+        if (b != batch) {
+            batch = b;  // (a thread reads the products that it has written)
+            const int64_t mod = static_cast<int64_t>(b) * a.mod_bstride;
+            auto vec = [&](const void* p, int64_t off, int j) {
+                return ld_cached(
+                    reinterpret_cast<const uint4*>(static_cast<const T*>(p) + off) + at[j]);
+            };
 #pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        f[j][k] = f2_mul(f[j][k], down);
-                u64 mm[4], sh[4];
-                if (kWide) {
-                    float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
-                    uint4 t = make_uint4(0u, 0u, 0u, 0u);
-                    if (has[j]) {
-                        p = m_lo[at[j]];
-                        q = m_lo[Dv + at[j]];
-                        t = shifts[at[j]];
-                    }
-                    mm[0] = f2_pack(p.x, p.y);
-                    mm[1] = f2_pack(p.z, p.w);
-                    mm[2] = f2_pack(q.x, q.y);
-                    mm[3] = f2_pack(q.z, q.w);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        sh[k] = widen<T>(word(t, k));
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        mm[k] = m[kWide ? 0 : j][k];
-                        sh[k] = shift[kWide ? 0 : j][k];
-                    }
-                }
+            for (int j = 0; j < V; ++j) {
+                u64 t[4];
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    f[j][k] = f2_fma(f2_mul(f[j][k], r2), mm[k], sh[k]);
-                store(f[j], j, a.out, a.out_scales, 0);
-            }
-        }
-        if (kStaged && (lane & 15) == 0) {
-            const uint32_t tile = unit >> 5, r = unit & 31;
+                    t[k] = f2_splat(1.0f);
+                uint4 sh = make_uint4(0u, 0u, 0u, 0u);
+                if (has[j] && a.weight) {
+                    const uint4 w = vec(a.weight, 0, j);
 #pragma unroll
-            for (int j = 0; j < V; ++j) {
-                const uint32_t t = tile_off + 2 * j * plan.warps;
-                if (t < tiles) {
-                    const int64_t to = (static_cast<int64_t>(tile) * tiles + t) * 32 + r;
-                    static_cast<uint4*>(a.out_scales)[to] =
-                        *reinterpret_cast<const uint4*>(mine[0][kStaged ? j : 0]);
-                    if (a.keep)
-                        static_cast<uint4*>(a.keep_scales)[to] =
-                            *reinterpret_cast<const uint4*>(mine[1][kStaged ? j : 0]);
+                    for (int k = 0; k < 4; ++k)
+                        t[k] = widen<T>(word(w, k));
+                }
+                if (has[j] && a.scale) {
+                    const uint4 w = vec(a.scale, mod, j);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        t[k] = f2_mul(t[k], f2_add(f2_splat(1.0f), widen<T>(word(w, k))));
+                }
+                if (has[j] && a.shift)
+                    sh = vec(a.shift, mod, j);
+                if (kWide) {
+                    if (has[j]) {
+                        m_lo[at[j]] = floats(t[0], t[1]);
+                        m_lo[Dv + at[j]] = floats(t[2], t[3]);
+                        shifts[at[j]] = sh;
+                    }
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        m[kWide ? 0 : j][k] = t[k];
+                        shift[kWide ? 0 : j][k] = widen<T>(word(sh, k));
+                    }
                 }
             }
+        }
+        // ---- the row: R(x + update), and the sum of its squares
+        if (!broken && !mbar_wait(smem_addr(&full[group][get]), phase, kWaitLimitNs)) {
+            broken = true;
+            atomicOr(&g_error, kErrCopyTimeout);
+        }
+        const uint4* slot = reinterpret_cast<const uint4*>(
+            ring + static_cast<size_t>(get) * plan.row_bytes);
+        if (++get == plan.stages) {
+            get = 0;
+            phase ^= 1u;
+        }
+        u64 f[V][4], s[2] = {0ull, 0ull};
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            uint4 x = make_uint4(0u, 0u, 0u, 0u);
+            if (has[j]) {
+                x = slot[at[j]];
+                if (a.update) {
+                    const uint4 u = slot[Dv + at[j]];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        word(x, k) = add2<T>(word(x, k), word(u, k));
+                    st_stream(static_cast<uint4*>(a.res_out) +
+                                  static_cast<int64_t>(row) * Dv + at[j], x);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                f[j][k] = widen<T>(word(x, k));
+                s[k & 1] = f2_fma(f[j][k], f[j][k], s[k & 1]);
+            }
+        }
+        float lo, hi;
+        f2_unpack(f2_add(s[0], s[1]), lo, hi);
+        float sum = warp_sum(__fadd_rn(lo, hi));
+        if (plan.warps > 1) {
+            if (lane == 0)
+                part[odd][group * plan.warps + warp] = sum;
+            group_sync();
+            sum = joined(part[odd]);
+            odd ^= 1;
+        } else {
+            __syncwarp();
+        }
+        if (leader)  // every warp is past this row's slot
+            issue();
+        float rstd, stored;
+        u64 down = f2_splat(1.0f);  // of scaled rows, before rstd
+        // past 2^120, or so small that a tiny eps leaves it to decide (uniform over the row)
+        const bool extreme = sum > 1.3e36f || (sum < 8e-25f && a.eps < 1e-18f);
+        if (!extreme) {
+            rstd = stored = rstd_fast(sum, n, inv_n, a.eps);
+        } else {
+            // again over the power of two of the largest magnitude, joined in fp64
+            float top = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    top = absmax2(top, f[j][k]);
+            uint32_t bits = __reduce_max_sync(kFullMask, __float_as_uint(top));
+            if (lane == 0)
+                slow[0][group * plan.warps + warp] = __uint_as_float(bits);
+            group_sync();
+            bits = 0u;
+            for (int k = 0; k < plan.warps; ++k)
+                bits = max(bits, __float_as_uint(slow[0][group * plan.warps + k]));
+            // (Inf, or nothing but zeros: the sum says it all)
+            const bool scaled = bits != 0u && bits < 0x7F800000u;
+            const int e = scaled ? max(ilogbf(__uint_as_float(bits)), -126) : 0;
+            float t = 0.0f;
+#pragma unroll
+            for (int j = 0; j < V; ++j)
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    float u, v;
+                    f2_unpack(f[j][k], u, v);
+                    u = scalbnf(u, -e);
+                    v = scalbnf(v, -e);
+                    t = __fadd_rn(t, __fadd_rn(__fmul_rn(u, u), __fmul_rn(v, v)));
+                }
+            t = warp_sum(t);
+            if (lane == 0)
+                slow[1][group * plan.warps + warp] = t;
+            group_sync();
+            if (scaled) {
+                const double ms = scalbn(static_cast<double>(joined(slow[1])) / a.D, 2 * e);
+                const double r = 1.0 / sqrt(ms + static_cast<double>(a.eps));
+                // without eps 1 / rms of the smallest rows is past fp32, not so its product with
+                // them
+                stored = static_cast<float>(r);
+                rstd = static_cast<float>(scalbn(r, e));
+                down = f2_splat(scalbnf(1.0f, -e));
+            } else {
+                stored = rstd =
+                    __fdiv_rn(1.0f, __fsqrt_rn(__fadd_rn(__fdiv_rn(sum, n), a.eps)));
+            }
+        }
+        if (leader && a.rstd_out)
+            a.rstd_out[row] = stored;
+        // ---- its blocks
+        const u64 r2 = f2_splat(rstd);
+        const int64_t base = static_cast<int64_t>(row) * Dv;
+        auto store = [&](const u64 (&v)[4], int j, void* codes, void* scales) {
+            uint32_t o[2];
+            const uint32_t byte = quantize_pairs<4, 4>(v, o);
+            if (has[j])
+                static_cast<uint2*>(codes)[base + at[j]] = make_uint2(o[0], o[1]);
+            // the four blocks of sixteen lanes' tile
+            uint32_t t = has[j] ? byte << (2 * (lane & 12)) : 0u;
+            t |= __shfl_xor_sync(kFullMask, t, 4);
+            t |= __shfl_xor_sync(kFullMask, t, 8);
+            put_word(scales, j, t);
+        };
+#pragma unroll
+        for (int j = 0; j < V; ++j) {
+            if (a.keep)
+                store(f[j], j, a.keep, a.keep_scales);
+            if (extreme)
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    f[j][k] = f2_mul(f[j][k], down);
+            u64 mm[4], sh[4];
+            if (kWide) {
+                float4 p = make_float4(0.0f, 0.0f, 0.0f, 0.0f), q = p;
+                uint4 t = make_uint4(0u, 0u, 0u, 0u);
+                if (has[j]) {
+                    p = m_lo[at[j]];
+                    q = m_lo[Dv + at[j]];
+                    t = shifts[at[j]];
+                }
+                mm[0] = f2_pack(p.x, p.y);
+                mm[1] = f2_pack(p.z, p.w);
+                mm[2] = f2_pack(q.x, q.y);
+                mm[3] = f2_pack(q.z, q.w);
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    sh[k] = widen<T>(word(t, k));
+            } else {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    mm[k] = m[kWide ? 0 : j][k];
+                    sh[k] = shift[kWide ? 0 : j][k];
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+                f[j][k] = f2_fma(f2_mul(f[j][k], r2), mm[k], sh[k]);
+            store(f[j], j, a.out, a.out_scales);
         }
     }
     if (broken)
@@ -942,8 +897,7 @@ cudaError_t launch_forward_rows(const Mxfp8NormArgs& a, FwdPlan p, const DeviceI
                                 cudaStream_t stream)
 {
     const int fixed = V > 2 ? p.groups * a.D * 6 : 0;
-    const int most = kFwdSmem - (V < 4 ? 4096 : 0);
-    p.stages = (most - fixed) / (p.groups * p.row_bytes);
+    p.stages = (kFwdSmem - fixed) / (p.groups * p.row_bytes);
     p.stages = p.stages > kFwdMaxStages ? kFwdMaxStages : p.stages;
     if (p.stages < 1)
         return cudaErrorInvalidValue;
@@ -952,11 +906,11 @@ cudaError_t launch_forward_rows(const Mxfp8NormArgs& a, FwdPlan p, const DeviceI
     const cudaError_t e = ready.get(dev.device, v, [&](int& n) -> cudaError_t {
         n = 1;
         return cudaFuncSetAttribute(norm_kernel<T, V>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                    most);
+                                    kFwdSmem);
     });
     if (e != cudaSuccess)
         return e;
-    const int grid = static_cast<int>(p.units < static_cast<uint32_t>(dev.sms) ? p.units : dev.sms);
+    const int grid = static_cast<int>(p.rows < static_cast<uint32_t>(dev.sms) ? p.rows : dev.sms);
     return launch_dependent(norm_kernel<T, V>, grid, kFwdThreads,
                             fixed + p.groups * p.stages * p.row_bytes, stream, a, p);
 }
@@ -969,7 +923,7 @@ cudaError_t launch_forward(const Mxfp8NormArgs& a, const DeviceInfo& dev, cudaSt
     const int Dv = a.D / 8, V = Dv <= 32 ? 1 : Dv <= 512 ? 2 : Dv <= 768 ? 3 : 4;
     FwdPlan p{};
     p.by_S = FastDiv::make(a.S);
-    p.units = (a.rows + 127u) / 128u * 32u;
+    p.rows = (a.rows + 127u) / 128u * 128u;
     p.warps = (Dv + 32 * V - 1) / (32 * V);
     p.groups = kFwdWarps / p.warps;
     p.row_bytes = a.D * (a.update ? 4 : 2);
