@@ -1596,5 +1596,5 @@ RMSMOD_EXPORT int mxfp8_activation_backward(const void* z, const void* z_scales,
     a.N = N;
     a.activation = activation;
     a.f16 = dtype == RMSMOD_F16;
-    return launch_status(rmsmod::launch_mxfp8_activation_backward(a, stream));
+    return launch_status(rmsmod::launch_mxfp8_activation_backward(a, dev, stream));
 }

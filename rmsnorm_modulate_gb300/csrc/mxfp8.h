@@ -138,6 +138,7 @@ struct Mxfp8ActBwdArgs {
 
 size_t mxfp8_activation_backward_workspace_bytes(int64_t B, int64_t S, int64_t N, bool per_batch,
                                                  int parts);
-cudaError_t launch_mxfp8_activation_backward(const Mxfp8ActBwdArgs& a, cudaStream_t stream);
+cudaError_t launch_mxfp8_activation_backward(const Mxfp8ActBwdArgs& a, const DeviceInfo& dev,
+                                             cudaStream_t stream);
 
 }  // namespace rmsmod

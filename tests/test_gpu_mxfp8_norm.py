@@ -366,3 +366,22 @@ def test_act_grad_nan_stays_in_its_block(rm):
     t, _, _ = rm.mxfp8_activation_backward(rm.mxfp8_quantize(z), torch.ones_like(z), "gelu_tanh")
     bad = torch.isnan(rm.mxfp8_dequantize(t))
     assert bad[1, 32:64].all() and bad.sum() == 32
+
+
+@pytest.mark.parametrize("act", _mx8.ACTIVATIONS)
+@pytest.mark.parametrize("rows,N,lo,hi", [
+    (130, 96, 108, 134),    # both sides of the scales whose derivatives are looked up
+    (37, 64, 0, 40), (37, 64, 160, 200),
+    (2500, 4128, 111, 131),  # more pieces than run at a time
+])
+def test_act_grad_under_every_scale(rm, rows, N, lo, hi, act):
+    codes, e = _mx8.random_codes(np.random.default_rng(rows + lo), rows, N, lo, hi)
+    z = _mx8.held(rm, codes, e)
+    g = torch.from_numpy(np.random.default_rng(1).standard_normal((rows, N))).bfloat16().cuda()
+    h, slope = _mx8.activation(act, _mx8.decoded(z))
+    dz = g.double() * slope
+    grad_z, grad_bias, _ = rm.mxfp8_activation_backward(z, g, activation=act)
+    slack = 2.0 ** -20 * g.double().abs() * (1 if act else 0) + 2.0 ** -22 * dz.abs()
+    _mx8.check_held(grad_z, dz, slack)
+    bound = (rows + 8) * 2.0 ** -24 * dz.abs().sum(0) + slack.sum(0) + 1e-30
+    assert ((grad_bias.double() - dz.sum(0)).abs() <= bound).all()
