@@ -504,8 +504,11 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
             } else {
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    // past 2^32 the derivative is 1 or 0 all the same
-                    const float scale = mx8_scale(e[i] > 159u && e[i] != 255u ? 159u : e[i]);
+                    // Past 2^32 the derivative is 1 or 0 all the same, and so is act(z) / z: such a z
+                    // is taken down to there, and only act(z) has the rest of its scale.
+                    const bool far = ACT != kActNone && e[i] > 159u && e[i] != 255u;
+                    const float scale = mx8_scale(far ? 159u : e[i]);
+                    const u64 rest = f2_splat(far ? mx8_scale(e[i] - 32u) : 1.0f);
                     u64 f[4], d[4];
                     values8(c[i], scale, f);
 #pragma unroll
@@ -516,7 +519,7 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
                         if (GATED) {
                             d[j] = f2_mul(d[j], gate[j]);
                             if (parts & 2)
-                                sg[j] = f2_fma(f2_mul(go, f[j]), part, sg[j]);
+                                sg[j] = f2_fma(f2_mul(go, f2_mul(f[j], part)), rest, sg[j]);
                         }
                     }
                     finish(i, d);

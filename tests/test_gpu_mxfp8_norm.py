@@ -385,3 +385,15 @@ def test_act_grad_under_every_scale(rm, rows, N, lo, hi, act):
     _mx8.check_held(grad_z, dz, slack)
     bound = (rows + 8) * 2.0 ** -24 * dz.abs().sum(0) + slack.sum(0) + 1e-30
     assert ((grad_bias.double() - dz.sum(0)).abs() <= bound).all()
+
+
+@pytest.mark.parametrize("act", _mx8.ACTIVATIONS)
+def test_gate_grad_of_large_values(rm, act):
+    # powers of two that the activation leaves as they are or takes to zero: the sum is exact
+    z = torch.zeros(1, 3, 64, dtype=torch.bfloat16, device="cuda")
+    z[0, 0], z[0, 1, :32], z[0, 2, :32] = 2.0 ** 44, 2.0 ** 100, -2.0 ** 90
+    g = torch.full_like(z, 0.5)
+    _, _, grad_gate = rm.mxfp8_activation_backward(rm.mxfp8_quantize(z), g, act, g[:, :1])
+    want = torch.full((64,), 2.0 ** 43, dtype=torch.float64, device="cuda")
+    want[:32] += 2.0 ** 99 - (2.0 ** 89 if act is None else 0.0)
+    assert torch.equal(grad_gate[0], want.float())
