@@ -1117,7 +1117,7 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
     the type of the result, bias, gate and residual; torch.float32 too, for a weight's gradient); w:
     an Mxfp8 [N, K].  activation: None, "silu", "gelu" or "gelu_tanh".  bias [N]; gate rows [N] or
     [B, 1, N] (for x [B, S, K]); residual [..., N].  N a multiple of 8, of 32 with `quantize` or
-    `keep`.  out (of y) may be residual; keep may be the Mxfp8 to write z to."""
+    `keep`.  out (of y) may be residual, a 16-bit x too; keep may be the Mxfp8 to write z to."""
     if stream is not None and (out is None or keep is True or not isinstance(x, Mxfp8)):
         at = x.codes if isinstance(x, Mxfp8) else x
         if not isinstance(at, torch.Tensor):
@@ -1171,8 +1171,8 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
     code = 2 if dtype == torch.float32 else _DTYPES[dtype]
     if isinstance(x, Mxfp8):
         codes, scales = _at(x.codes), _at(x.scales)
-    elif M <= _DIRECT_ROWS:
-        codes, scales = _at(x), None  # quantised by the product itself
+    elif M <= _DIRECT_ROWS and y != x.data_ptr():
+        codes, scales = _at(x), None  # quantised by the product itself, which does not write to it
     else:
         n = M * K  # a multiple of 32
         q = torch.empty(n + mxfp8_scale_bytes(M, K), dtype=torch.uint8, device=device)

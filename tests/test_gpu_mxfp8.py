@@ -393,3 +393,16 @@ def test_empty_product(rm):
     assert rm.mxfp8_linear(x, w).shape == (0, 32)
     y, kept = rm.mxfp8_linear(x, w, quantize=True, keep=True)
     assert y.codes.shape == kept.codes.shape == (0, 32)
+
+
+@pytest.mark.parametrize("M", [1, 32, 33, 200])
+def test_product_added_to_its_own_rows(rm, M):
+    x = torch.randn(M, 160, device="cuda").bfloat16()
+    w = rm.mxfp8_quantize(torch.randn(160, 160, device="cuda").bfloat16())
+    want = rm.mxfp8_linear(x, w, activation="silu", residual=x)
+    plain = rm.mxfp8_linear(x, w)
+    y = x.clone()
+    assert rm.mxfp8_linear(y, w, activation="silu", residual=y, out=y) is y and torch.equal(y, want)
+    y = x.clone()
+    rm.mxfp8_linear(y, w, out=y)
+    assert torch.equal(y, plain)
