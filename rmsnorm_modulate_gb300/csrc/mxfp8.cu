@@ -358,19 +358,25 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
 
 // An item is 128 rows of one batch by 128 columns; sixteen lanes a row, eight columns each, so that a
 // thread's columns stay the same and their sums are in registers.  The rows of a batch are counted from
-// its first, so a batch's sums do not depend on what stands before it.  Reads 3 bytes a value and writes
-// one: 41 us of HBM time at 4216 x 16384, where it takes 44 without an activation, 59 with the tanh form
-// of GELU, 60 with the exact one and 81 with SiLU and a gate.
+// its first, so a batch's sums do not depend on what stands before it.
 //
 // With an activation the instructions bound it: a derivative worked out for every value made it 72 us
-// (tanh) and 92 (exact).  But a scale has 256 values only, so persistent CTAs, four to an SM, work out
-// the derivatives of the kRows scales 2^-16 ... 2^3 (blocks whose largest is between 0.004 and 3584)
-// once, by the same function, while the kernel before them ends, and look them up; four rows of a
-// warp with a block under any other scale work out their own.  Faster at all sizes: 5.1 against 6.0 us
-// at 77 x 4096, 19.3 against 20.9 at 4216 x 4096, 57.7 against 67.0 at 4096 x 16384.  With a gate whose
-// gradient is taken as well there would be two values to look up: 134 us, against the 81 of working
-// them out.
+// at 4216 x 16384 with the tanh form of GELU and 92 with the exact one.  But a scale has 256 values only, so
+// persistent CTAs, four to an SM, work out the derivatives of the kRows scales 2^-16 ... 2^3 (blocks
+// whose largest is between 0.004 and 3584) once, by the same function, while the kernel before them
+// ends, and look them up; four rows of a warp with a block under any other scale work out their own.
+// Faster at all sizes: 5.1 against 6.0 us at 77 x 4096, 19.3 against 20.9 at 4216 x 4096, 57.7 against
+// 67.0 at 4096 x 16384.  With a gate whose gradient is taken as well there would be two values to look
+// up: 134 us, against 79 of working them out.
+//
+// Now at 4216 x 16384: 56 us (GELU's tanh form; 54 the exact one; HBM's time 41), without an activation
+// 39 (z is not read: 31), with a gate and its gradient 60 (41), with both 79.  Some 22 instructions a value are
+// issued, a fourth of them for an item's start and its sums.
 constexpr int kRows = 20, kFirstByte = 127 - 16;
+
+struct ActWalk {
+    FastDiv tiles, chunks;  // items: [batch][chunk][tile]
+};
 
 __device__ __forceinline__ float table_value(uint32_t address)
 {
@@ -379,9 +385,17 @@ __device__ __forceinline__ float table_value(uint32_t address)
     return v;
 }
 
+// (a call of its own: the registers of the rows that look theirs up are theirs)
+template <int ACT>
+__device__ __noinline__ u64 slope_apart(u64 z)
+{
+    u64 unused;
+    return slope2<ACT>(z, unused);
+}
+
 template <typename T, int ACT, bool GATED>
-__global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
-    activation_backward_kernel(const Mxfp8ActBwdArgs a, int64_t chunks, int items, int parts)
+__global__ void __launch_bounds__(kThreads, GATED && ACT != kActNone ? 3 : 4)
+    activation_backward_kernel(const Mxfp8ActBwdArgs a, ActWalk walk, int items, int parts)
 {
     constexpr bool TABLE = ACT != kActNone && !GATED;
     extern __shared__ uint8_t dynamic[];
@@ -413,18 +427,18 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
     const uint32_t* __restrict__ z_scales = static_cast<const uint32_t*>(a.z_scales);
     uint8_t* grad_scales = static_cast<uint8_t*>(a.grad_z_scales);
     for (int item = blockIdx.x; item < items; item += gridDim.x) {
-        const int unit = item / tiles, tile = item - unit * tiles;
-        const int64_t batch = unit / chunks, chunk = unit - batch * chunks;
+        const uint32_t unit = walk.tiles.div(item), tile = item - unit * tiles;
+        const uint32_t batch = walk.chunks.div(unit), chunk = unit - batch * walk.chunks.d;
         const int64_t n = static_cast<int64_t>(tile) * 128 + sub * 8;
-        const int64_t begin = batch * a.S + chunk * 128;
-        const int64_t end = min(begin + 128, (batch + 1) * a.S);
+        const int64_t begin = batch * a.S + static_cast<int64_t>(chunk) * 128;
+        const int64_t end = min(begin + 128, (batch + int64_t{1}) * a.S);
         // all rows of a row tile are this CTA's: its scales are stored four rows at a time
         const bool whole = begin % 128 == 0 && (end == begin + 128 || end == M);
         const bool has = n < a.N;
         const uint8_t* __restrict__ z = static_cast<const uint8_t*>(a.z) + begin * N + n;
         const T* __restrict__ grad = static_cast<const T*>(a.grad_out) + begin * N + n;
         uint8_t* grad_z = static_cast<uint8_t*>(a.grad_z) + begin * N + n;
-        const int rows = static_cast<int>(end - begin);
+        const int rows = static_cast<int>(end - begin), live = has ? rows : 0;  // (m * N is under 2^27)
         u64 gate[4], sb[4], sg[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -450,12 +464,9 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
                 c[i] = make_uint2(0u, 0u);
                 g[i] = make_uint4(0u, 0u, 0u, 0u);
                 e[i] = 0x7F7F7F7Fu;
-                if (m < rows && has) {
-                    c[i] = ld_stream2(reinterpret_cast<const uint2*>(z + static_cast<int64_t>(m) * N));
-                    g[i] = ld_stream(
-                        reinterpret_cast<const uint4*>(grad + static_cast<int64_t>(m) * N));
-                    if (!whole)
-                        e[i] = __ldg(z_scales + mx8_scale_at(begin + m, tile * 4, tiles) / 4);
+                if (m < live) {
+                    c[i] = ld_stream2(reinterpret_cast<const uint2*>(z + m * N));
+                    g[i] = ld_stream(reinterpret_cast<const uint4*>(grad + m * N));
                 }
             }
             if (whole) {
@@ -463,8 +474,14 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
                                           (begin / 128 * tiles + tile) * 32 + r);
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
-                    if (r + 32 * i < rows && has)
+                    if (r + 32 * i < live)
                         e[i] = word(w, i);
+            } else {
+#pragma unroll
+                for (int i = 0; i < 4; ++i)
+                    if (r + 32 * i < live)
+                        e[i] = __ldg(z_scales +
+                                     mx8_scale_at(begin + r + 32 * i, tile * 4, tiles) / 4);
             }
             uint32_t mine = 0u;  // the scale byte of row r + 32 * (sub % 4), which this lane stores
             const auto finish = [&](int i, const u64(&d)[4]) {
@@ -475,9 +492,8 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
                 uint32_t out[2];
                 const uint32_t byte = quantize_pairs<4, 4>(d, out);
                 mine = (sub & 3) == i ? byte : mine;
-                if (m < rows && has)
-                    *reinterpret_cast<uint2*>(grad_z + static_cast<int64_t>(m) * N) =
-                        make_uint2(out[0], out[1]);
+                if (m < live)
+                    *reinterpret_cast<uint2*>(grad_z + m * N) = make_uint2(out[0], out[1]);
             };
             bool near = true;
 #pragma unroll
@@ -510,16 +526,21 @@ __global__ void __launch_bounds__(kThreads, GATED ? 3 : 4)
                     const float scale = mx8_scale(far ? 159u : e[i]);
                     const u64 rest = f2_splat(far ? mx8_scale(e[i] - 32u) : 1.0f);
                     u64 f[4], d[4];
-                    values8(c[i], scale, f);
+                    if (ACT != kActNone || GATED)
+                        values8(c[i], scale, f);
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
                         const u64 go = widen<T>(word(g[i], j));
                         u64 part;
-                        d[j] = f2_mul(go, slope2<ACT>(f[j], part));
+                        d[j] = ACT == kActNone ? go
+                               : TABLE         ? f2_mul(go, slope_apart<ACT>(f[j]))
+                                               : f2_mul(go, slope2<ACT>(f[j], part));
                         if (GATED) {
                             d[j] = f2_mul(d[j], gate[j]);
                             if (parts & 2)
-                                sg[j] = f2_fma(f2_mul(go, f2_mul(f[j], part)), rest, sg[j]);
+                                sg[j] = ACT == kActNone
+                                            ? f2_fma(go, f[j], sg[j])
+                                            : f2_fma(f2_mul(go, f2_mul(f[j], part)), rest, sg[j]);
                         }
                     }
                     finish(i, d);
@@ -615,34 +636,34 @@ int64_t sum_chunks(int64_t B, int64_t S, bool per_batch)
 }
 
 template <typename T, int ACT>
-cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int items, int64_t chunks, int parts,
+cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int items, ActWalk walk, int parts,
                               const DeviceInfo& dev, cudaStream_t stream)
 {
     if (a.gate)
         return launch_dependent(activation_backward_kernel<T, ACT, true>, items, kThreads, 0, stream,
-                                a, chunks, items, parts);
+                                a, walk, items, parts);
     const int resident = 4 * dev.sms;
     return ACT == kActNone
                ? launch_dependent(activation_backward_kernel<T, ACT, false>, items, kThreads, 0,
-                                  stream, a, chunks, items, parts)
+                                  stream, a, walk, items, parts)
                : launch_dependent(activation_backward_kernel<T, ACT, false>,
                                   items < resident ? items : resident, kThreads, kRows * 1024 + 1024,
-                                  stream, a, chunks, items, parts);
+                                  stream, a, walk, items, parts);
 }
 
 template <typename T>
-cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int items, int64_t chunks, int parts,
+cudaError_t launch_activation(const Mxfp8ActBwdArgs& a, int items, ActWalk walk, int parts,
                               const DeviceInfo& dev, cudaStream_t stream)
 {
     switch (a.activation) {
     case kActSilu:
-        return launch_activation<T, kActSilu>(a, items, chunks, parts, dev, stream);
+        return launch_activation<T, kActSilu>(a, items, walk, parts, dev, stream);
     case kActGelu:
-        return launch_activation<T, kActGelu>(a, items, chunks, parts, dev, stream);
+        return launch_activation<T, kActGelu>(a, items, walk, parts, dev, stream);
     case kActGeluTanh:
-        return launch_activation<T, kActGeluTanh>(a, items, chunks, parts, dev, stream);
+        return launch_activation<T, kActGeluTanh>(a, items, walk, parts, dev, stream);
     default:
-        return launch_activation<T, kActNone>(a, items, chunks, parts, dev, stream);
+        return launch_activation<T, kActNone>(a, items, walk, parts, dev, stream);
     }
 }
 
@@ -688,9 +709,11 @@ cudaError_t launch_mxfp8_activation_backward(const Mxfp8ActBwdArgs& args, const 
     if (a.B * chunks * tiles > INT32_MAX - 4 * dev.sms)
         return cudaErrorInvalidValue;
     const int items = static_cast<int>(a.B * chunks * tiles);
+    const ActWalk walk{FastDiv::make(static_cast<uint32_t>(tiles)),
+                       FastDiv::make(static_cast<uint32_t>(chunks))};
     const cudaError_t e = a.f16
-                              ? launch_activation<__half>(a, items, chunks, parts, dev, stream)
-                              : launch_activation<__nv_bfloat16>(a, items, chunks, parts, dev, stream);
+                              ? launch_activation<__half>(a, items, walk, parts, dev, stream)
+                              : launch_activation<__nv_bfloat16>(a, items, walk, parts, dev, stream);
     if (e != cudaSuccess || !parts)
         return e;
     const int64_t slices = (a.grad_bias ? 1 : 0) + (a.grad_gate ? a.B : 0);
