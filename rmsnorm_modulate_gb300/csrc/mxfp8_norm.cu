@@ -53,6 +53,28 @@ __device__ __forceinline__ float warp_sum(float v)
     return v;
 }
 
+// The parts of a row's sum that a group's warps leave, zeros behind the last, and their sum in an order
+// that the number of warps fixes: a few wide loads of the same words in every lane, which are sooner done
+// than four exchanges.
+struct __align__(16) Parts {
+    float of[16];
+
+    __device__ __forceinline__ float joined(int warps) const
+    {
+        const float4* p = reinterpret_cast<const float4*>(of);
+        auto four = [&](int i) {
+            const float4 v = p[i];
+            return __fadd_rn(__fadd_rn(v.x, v.y), __fadd_rn(v.z, v.w));
+        };
+        float s = four(0);
+        if (warps > 4)
+            s = __fadd_rn(s, four(1));
+        if (warps > 8)
+            s = __fadd_rn(s, __fadd_rn(four(2), four(3)));
+        return s;
+    }
+};
+
 // ---------------------------------------------------------------------------
 // forward
 // ---------------------------------------------------------------------------
@@ -84,7 +106,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
     constexpr bool kWide = V > 2;  // the row vectors' products in shared memory, for each group
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long full[kFwdWarps][kFwdMaxStages];
-    __shared__ float part[2][kFwdWarps], slow[2][kFwdWarps];
+    __shared__ Parts part[2][kFwdWarps];  // [group]
 
     const int lane = threadIdx.x & 31;
     const int group = (threadIdx.x >> 5) / plan.warps;
@@ -105,6 +127,8 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
             mbar_init(smem_addr(&full[group][s]), 1u);
         mbar_init_fence();
     }
+    if (warp == 0 && lane < 16)
+        part[0][group].of[lane] = part[1][group].of[lane] = 0.0f;
     group_sync();
     grid_dependency_sync();
 
@@ -147,14 +171,6 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         at[j] = (j * plan.warps + warp) * 32 + lane;
         has[j] = at[j] < Dv;
     }
-    // join over the group's warps, in their order; `odd`: two places in turn
-    auto joined = [&](const float (&p)[kFwdWarps]) {
-        float v = (lane & 15) < plan.warps ? p[group * plan.warps + (lane & 15)] : 0.0f;
-#pragma unroll
-        for (int off = 8; off > 0; off >>= 1)
-            v = __fadd_rn(v, __shfl_xor_sync(kFullMask, v, off));
-        return v;
-    };
     const float n = static_cast<float>(a.D), inv_n = __fdiv_rn(1.0f, n);
     u64 m[kWide ? 1 : V][4], shift[kWide ? 1 : V][4];
     const uint32_t tile0 = static_cast<uint32_t>(at[0]) >> 4;  // of its vector 0 among a row's block tiles
@@ -259,9 +275,9 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         float sum = warp_sum(__fadd_rn(lo, hi));
         if (plan.warps > 1) {
             if (lane == 0)
-                part[odd][group * plan.warps + warp] = sum;
+                part[odd][group].of[warp] = sum;  // two places in turn
             group_sync();
-            sum = joined(part[odd]);
+            sum = part[odd][group].joined(plan.warps);
             odd ^= 1;
         } else {
             __syncwarp();
@@ -275,7 +291,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!extreme) {
             rstd = stored = rstd_fast(sum, n, inv_n, a.eps);
         } else {
-            // again over the power of two of the largest magnitude, joined in fp64
+            // again over the power of two of the largest magnitude, joined in fp64; the next row's
+            // place takes the largest, and then this row's, which every warp has read, the sums
+            Parts& tops = part[odd][group];
+            Parts& sums = part[odd ^ 1][group];
             float top = 0.0f;
 #pragma unroll
             for (int j = 0; j < V; ++j)
@@ -284,11 +303,11 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                     top = absmax2(top, f[j][k]);
             uint32_t bits = __reduce_max_sync(kFullMask, __float_as_uint(top));
             if (lane == 0)
-                slow[0][group * plan.warps + warp] = __uint_as_float(bits);
+                tops.of[warp] = __uint_as_float(bits);
             group_sync();
             bits = 0u;
             for (int k = 0; k < plan.warps; ++k)
-                bits = max(bits, __float_as_uint(slow[0][group * plan.warps + k]));
+                bits = max(bits, __float_as_uint(tops.of[k]));
             // (Inf, or nothing but zeros: the sum says it all)
             const bool scaled = bits != 0u && bits < 0x7F800000u;
             const int e = scaled ? max(ilogbf(__uint_as_float(bits)), -126) : 0;
@@ -305,10 +324,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
                 }
             t = warp_sum(t);
             if (lane == 0)
-                slow[1][group * plan.warps + warp] = t;
+                sums.of[warp] = t;
             group_sync();
             if (scaled) {
-                const double ms = scalbn(static_cast<double>(joined(slow[1])) / a.D, 2 * e);
+                const double ms = scalbn(static_cast<double>(sums.joined(plan.warps)) / a.D, 2 * e);
                 const double r = 1.0 / sqrt(ms + static_cast<double>(a.eps));
                 // without eps 1 / rms of the smallest rows is past fp32, not so its product with
                 // them
@@ -428,7 +447,7 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     constexpr bool kWide = V > 2;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) unsigned long long full[kBwdWarps][kBwdMaxStages];
-    __shared__ float part[2][kBwdWarps];
+    __shared__ Parts part[2][kBwdWarps];  // [group]
 
     const int lane = threadIdx.x & 31;
     const int group = (threadIdx.x >> 5) / plan.warps;
@@ -450,6 +469,8 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             mbar_init(smem_addr(&full[group][s]), 1u);
         mbar_init_fence();
     }
+    if (warp == 0 && lane < 16)
+        part[0][group].of[lane] = part[1][group].of[lane] = 0.0f;
     cta_sync();
     grid_dependency_sync();
 
@@ -660,13 +681,9 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
             sum = warp_sum(sum);
             if (plan.warps > 1) {
                 if (lane == 0)
-                    part[odd][group * plan.warps + warp] = sum;
+                    part[odd][group].of[warp] = sum;
                 group_sync();
-                // every warp joins them, in the lanes' order
-                sum = (lane & 15) < plan.warps ? part[odd][group * plan.warps + (lane & 15)] : 0.0f;
-#pragma unroll
-                for (int off = 8; off > 0; off >>= 1)
-                    sum = __fadd_rn(sum, __shfl_xor_sync(kFullMask, sum, off));
+                sum = part[odd][group].joined(plan.warps);
                 odd ^= 1;
             } else {
                 __syncwarp();
