@@ -976,6 +976,8 @@ cudaError_t launch_mxfp8_norm_backward(const Mxfp8NormBwdArgs& args, const Devic
         a.S *= a.B;
         a.B = 1;
     }
+    if (!a.grad_x)
+        a.grad_res = nullptr;  // (nothing to add it to: not read)
     return a.f16 ? launch_backward<__half>(a, dev, stream)
                  : launch_backward<__nv_bfloat16>(a, dev, stream);
 }
