@@ -397,3 +397,11 @@ def test_gate_grad_of_large_values(rm, act):
     want = torch.full((64,), 2.0 ** 43, dtype=torch.float64, device="cuda")
     want[:32] += 2.0 ** 99 - (2.0 ** 89 if act is None else 0.0)
     assert torch.equal(grad_gate[0], want.float())
+
+
+@pytest.mark.parametrize("D", [256, 288, 4096, 4128, 5120, 5152, 6144, 6176, 8192, 8224, 16352])
+def test_norm_either_side_of_its_variants(rm, D):
+    # the widths at which a row goes to more vectors a thread, or to fewer groups
+    c = Case(2, 40, D, torch.bfloat16)
+    check_norm(rm, c)
+    check_norm_grad(rm, c)
