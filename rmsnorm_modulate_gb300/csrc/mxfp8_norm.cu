@@ -10,7 +10,8 @@
 //             of shift, scale and weight
 //
 // fp32 throughout, one rounding per stored value (Q: mxfp8.cuh).  Sums run in an order that D (and,
-// over tokens, S) alone fixes.  Both are bound by HBM: 7 to 8 bytes a value forward, 7 backward.
+// over tokens, S) alone fixes.  7 to 8 bytes a value forward, 7 backward: the forward pass is bound by HBM,
+// the backward pass by its instructions and their latency about as much.
 #include "device_common.cuh"
 #include "half_types.cuh"
 #include "launch.h"
@@ -85,6 +86,9 @@ struct __align__(16) Parts {
 // again from there on.  Sixteen lanes' blocks are a block tile, whose scales in the row are one store of
 // four bytes.  (Rows 32 apart in turn, whose scales are neighbours, and one store for four of them: no
 // faster, and a CTA that has two batches' rows changes its row vectors with every row.)
+//
+// 4 x 1 x 4096 2.9 us; 1 x 4216 x 4096 29.2 with `keep` and 25.7 without (20.5 and 17.9 of HBM time: the
+// rest is the launch, the first rows' latency and the last rows' stores); 17024 x 4096 80 (72).
 constexpr int kFwdWarps = 16;
 constexpr int kFwdThreads = 32 * kFwdWarps;
 constexpr int kFwdMaxStages = 8;
@@ -405,6 +409,10 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 // bulk copies ahead of it and keeps its columns' sums in registers; at a run's end the groups' sums are
 // joined and left as a part for the last launch.  Up to two vectors a thread a row is in registers when
 // its sum over the group's warps is joined, so its slot is filled again from there on.
+//
+// At 1 x 4216 x 4096 30.9 us, 4 of them the last launch; its bytes are 17.9 of HBM time, and twice the rows
+// take 24.3 more.  No one part bounds it: without the loads of the scales 29.5, without the reduction over
+// the row 29.2, without the columns' sums 30.1, without all three 26.2.
 constexpr int kBwdWarps = 16;
 constexpr int kBwdThreads = 32 * kBwdWarps;
 constexpr int kBwdMaxStages = 8;
@@ -421,6 +429,9 @@ struct BwdPlan {
     int row_bytes;      // of a slot
 };
 
+// Vectors a thread, us measured: 16384 x 256 one 12.9, two 14.0; 16384 x 1024 two 30.0, one 35.5; 2108 x
+// 8192 two 31.9, four 34.2; past that two would not hold a row.  (Eight warps with 255 registers, four
+// vectors a thread and every value widened once: 4216 x 4096 32.6, against the 30.9 of sixteen with two.)
 int row_vectors(int64_t D) { return D <= 256 ? 1 : D <= 8192 ? 2 : 4; }
 
 int row_warps(int64_t D)
@@ -431,10 +442,13 @@ int row_warps(int64_t D)
 
 int row_groups(int64_t D) { return kBwdWarps / row_warps(D); }
 
-// Rows of a run: that 152 CTAs have one each, but a few rows for each group at least.
+// Rows of a run: that 152 CTAs have one each, but two for each group at least.  It depends on S and D
+// alone, so a batch's sums do not depend on the batches beside it.  One row a group is sooner done where
+// there is one batch (154 x 1024: 7.6 us, two 8.8, four 11.4) and later where the runs of several are then
+// more than the SMs (4 x 512 x 1024: 13.3, two 9.6, four 11.6).
 int64_t bwd_chunk(int64_t S, int64_t D)
 {
-    const int64_t c = (S + 151) / 152, least = 4 * row_groups(D);
+    const int64_t c = (S + 151) / 152, least = 2 * row_groups(D);
     return c < least ? least : c;
 }
 
