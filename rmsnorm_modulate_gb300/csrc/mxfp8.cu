@@ -27,7 +27,8 @@ constexpr int kUnitsPerCta = kThreads / 16;
 // A unit is the 128 values of one block tile in the four rows r, r + 32, r + 64, r + 96 of a row tile,
 // whose sixteen scale bytes are neighbours; 16 lanes take a unit, eight values of each row, so four
 // lanes share a block and a unit's scales are one store.  Neighbouring units are neighbours in the
-// rows.
+// rows.  Bound by HBM: at 4216 x 16384 33 to 36 us to codes and 32 back, of 31; at 4216 x 4096 (in part
+// from L2) 11 and 9.
 struct Unit {
     uint32_t tile, row;
     int64_t scale_word;  // of 16 bytes
@@ -144,6 +145,8 @@ __global__ void __launch_bounds__(kThreads) dequantize8_kernel(const Mxfp8RowsAr
 // -11 or more, so what has a code that is not zero is at least 2^(x - 10) = 2^-21 and keeps its four
 // bits.  Else (a column far below its rows' largest, scales 2^32 apart, NaN, the least scale)
 // turn_slowly() goes by whole numbers and fp32.
+//
+// Bound by its instructions as much as by HBM: 33 us at 4216 x 16384, whose bytes take 21.
 constexpr int kTurn = 128;
 
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
@@ -238,7 +241,8 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
     __shared__ uint32_t factors[4][32][4];  // [rows][row][block], in both halves
     grid_dependency_sync();
     const int64_t tiles_k = (a.K + 127) / 128, tiles_r = (a.rows + 127) / 128;
-    const int64_t tk = blockIdx.x % tiles_k, tr = blockIdx.x / tiles_k;
+    const uint32_t across = blockIdx.x / static_cast<uint32_t>(tiles_k);
+    const int64_t tr = across, tk = blockIdx.x - across * static_cast<uint32_t>(tiles_k);
     const int64_t r0 = tr * 128, k0 = tk * 128;
     const int64_t padded = (a.rows + 31) / 32 * 32;
     const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -361,8 +365,8 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
 // its first, so a batch's sums do not depend on what stands before it.
 //
 // With an activation the instructions bound it: a derivative worked out for every value made it 72 us
-// at 4216 x 16384 with the tanh form of GELU and 92 with the exact one.  But a scale has 256 values only, so
-// persistent CTAs, four to an SM, work out the derivatives of the kRows scales 2^-16 ... 2^3 (blocks
+// at 4216 x 16384 with the tanh form of GELU and 92 with the exact one.  But a scale has 256 values only,
+// so persistent CTAs, four to an SM, work out the derivatives of the kRows scales 2^-16 ... 2^3 (blocks
 // whose largest is between 0.004 and 3584) once, by the same function, while the kernel before them
 // ends, and look them up; four rows of a warp with a block under any other scale work out their own.
 // Faster at all sizes: 5.1 against 6.0 us at 77 x 4096, 19.3 against 20.9 at 4216 x 4096, 57.7 against
@@ -370,8 +374,9 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
 // up: 134 us, against 79 of working them out.
 //
 // Now at 4216 x 16384: 56 us (GELU's tanh form; 54 the exact one; HBM's time 41), without an activation
-// 39 (z is not read: 31), with a gate and its gradient 60 (41), with both 79.  Some 22 instructions a value are
-// issued, a fourth of them for an item's start and its sums.
+// 39 (z is not read: 31), with a gate and its gradient 60 (41), with both 79.  Some 22 instructions a
+// value are issued, a fourth of them for an item's start and its sums.  Rows copied ahead to shared
+// memory: 76 us (tanh form), by TMA 78.
 constexpr int kRows = 20, kFirstByte = 127 - 16;
 
 struct ActWalk {

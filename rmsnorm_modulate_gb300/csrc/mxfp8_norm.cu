@@ -951,11 +951,11 @@ cudaError_t launch_forward(const Mxfp8NormArgs& a, const DeviceInfo& dev, cudaSt
 {
     // Vectors a thread: few enough that a row is a warp's or that two groups share the CTA at least (one
     // works while the other waits for its sum), and past two those that leave fewer lanes idle.
-    // Measured, us with `keep`: 16384 x 256 one 8.9, two 11.6; 4216 x 1024 two 8.0, one 9.5, four 8.3; 3400 x
-    // 5120 (four by the rule) four 28.6, three 31.3, two 37.3; 2800 x 6144 (three) three 28.6, four 30.8,
-    // two 33.1; 2108 x 8192 four 29.3, two 30.7, three 34.8.  At 4096 four would be faster in the middle (4216
-    // rows: 27.8 against 29.1) and slower at both ends (4 rows: 4.0 against 2.8; 17024 rows, not kept:
-    // 90.6 against 79.5).
+    // Measured, us with `keep`: 16384 x 256 one 8.9, two 11.6; 4216 x 1024 two 8.0, one 9.5, four 8.3;
+    // 3400 x 5120 (four by the rule) four 28.6, three 31.3, two 37.3; 2800 x 6144 (three) three 28.6,
+    // four 30.8, two 33.1; 2108 x 8192 four 29.3, two 30.7, three 34.8.  At 4096 four would be faster in
+    // the middle (4216 rows: 27.8 against 29.1) and slower at both ends (4 rows: 4.0 against 2.8; 17024
+    // rows, not kept: 90.6 against 79.5).
     const int Dv = a.D / 8;
     const auto busy = [Dv](int V) { return 12 / V * (kFwdWarps / ((Dv + 32 * V - 1) / (32 * V))); };
     const int V = Dv <= 32 ? 1 : Dv <= 512 ? 2 : Dv <= 768 && busy(3) > busy(4) ? 3 : 4;
