@@ -146,7 +146,8 @@ __global__ void __launch_bounds__(kThreads) dequantize8_kernel(const Mxfp8RowsAr
 // bits.  Else (a column far below its rows' largest, scales 2^32 apart, NaN, the least scale)
 // turn_slowly() goes by whole numbers and fp32.
 //
-// Bound by its instructions as much as by HBM: 33 us at 4216 x 16384, whose bytes take 21.
+// Bound by its instructions as much as by HBM: 30 us at 4216 x 16384, whose bytes take 21 (six CTAs an SM;
+// five 33, seven 36, eight 39).
 constexpr int kTurn = 128;
 
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
@@ -234,7 +235,7 @@ __device__ __noinline__ void turn_slowly(const uint32_t* words, const uint32_t* 
     }
 }
 
-__global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeArgs a)
+__global__ void __launch_bounds__(kTurn, 6) transpose8_kernel(const Mxfp8TransposeArgs a)
 {
     __shared__ __align__(16) uint32_t tile[kTurn * kTurn / 4];
     __shared__ __align__(16) uint32_t scale_in[128], scale_out[128];
@@ -374,7 +375,7 @@ __global__ void __launch_bounds__(kTurn) transpose8_kernel(const Mxfp8TransposeA
 // up: 134 us, against 79 of working them out.
 //
 // Now at 4216 x 16384: 56 us (GELU's tanh form; 54 the exact one; HBM's time 41), without an activation
-// 39 (z is not read: 31), with a gate and its gradient 60 (41), with both 79.  Some 22 instructions a
+// 39 (z is not read: 31), with a gate and its gradient 60 (41), with both 79.  Some 18 instructions a
 // value are issued, a fourth of them for an item's start and its sums.  Rows copied ahead to shared
 // memory: 76 us (tanh form), by TMA 78.
 constexpr int kRows = 20, kFirstByte = 127 - 16;
