@@ -28,13 +28,18 @@ constexpr unsigned kFullMask = 0xFFFFFFFFu;
 // loads / stores
 // ---------------------------------------------------------------------------
 
-// Streaming 16-byte load of data touched once (no L1 allocation).  The
-// coherent path, not the read-only one: an output may alias its input.
-// 8-byte read-only streaming load (input never written by the same kernel).
+// Every kernel lets its successor start while it still runs (grid_dependency_sync below), so what a
+// kernel reads may be written by another within its own lifetime: before its wait, but after its
+// launch.  The read-only path (.nc) does not allow for that, and a load that is not volatile is not held
+// behind the wait.  So all loads of tensors here are coherent and volatile.
+
+// Streaming loads of data touched once (no L1 allocation).  (An output may alias such an input.)
 __device__ __forceinline__ uint2 ld_stream2(const uint2* p)
 {
     uint2 v;
-    asm("ld.global.nc.L1::no_allocate.v2.u32 {%0,%1}, [%2];" : "=r"(v.x), "=r"(v.y) : "l"(p));
+    asm volatile("ld.global.L1::no_allocate.v2.u32 {%0,%1}, [%2];"
+                 : "=r"(v.x), "=r"(v.y)
+                 : "l"(p));
     return v;
 }
 
@@ -47,23 +52,43 @@ __device__ __forceinline__ uint4 ld_stream(const uint4* p)
     return v;
 }
 
-// 16-byte load of small tensors re-read by every row (scale, shift, weight):
-// read-only path, cached.
+// Loads of small tensors re-read by every row (scale, shift, weight): cached.
 __device__ __forceinline__ uint4 ld_cached(const uint4* p)
 {
     uint4 v;
-    asm("ld.global.nc.v4.u32 {%0,%1,%2,%3}, [%4];"
-        : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-        : "l"(p));
+    asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
     return v;
 }
 
 __device__ __forceinline__ float4 ld_cached_f4(const float4* p)
 {
     float4 v;
-    asm("ld.global.nc.v4.f32 {%0,%1,%2,%3}, [%4];"
-        : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-        : "l"(p));
+    asm volatile("ld.global.v4.f32 {%0,%1,%2,%3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_cached(const uint32_t* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.u32 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ uint32_t ld_cached(const uint8_t* p)
+{
+    uint32_t v;
+    asm volatile("ld.global.u8 %0, [%1];" : "=r"(v) : "l"(p));
+    return v;
+}
+
+__device__ __forceinline__ float ld_cached(const float* p)
+{
+    float v;
+    asm volatile("ld.global.f32 %0, [%1];" : "=f"(v) : "l"(p));
     return v;
 }
 

@@ -159,7 +159,7 @@ __global__ void __launch_bounds__(kThreads) dequantize_kernel(const Mxfp4RowsArg
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const uint32_t row = t.row + 32 * i;
-        codes[i] = row < a.rows ? __ldg(packed + static_cast<int64_t>(row) * a.Kv + col) : 0u;
+        codes[i] = row < a.rows ? ld_cached(packed + static_cast<int64_t>(row) * a.Kv + col) : 0u;
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {

@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kTurn, 6) transpose8_kernel(const Mxfp8Transpo
     }
     {  // word t: row t / 4 + 32 * (t % 4)
         const int64_t r = r0 + (t >> 2) + 32 * (t & 3);
-        scale_in[t] = r < a.rows ? __ldg(static_cast<const uint32_t*>(a.scales) +
+        scale_in[t] = r < a.rows ? ld_cached(static_cast<const uint32_t*>(a.scales) +
                                          (tr * tiles_k + tk) * 128 + t)
                                  : 0u;
         scale_out[t] = 0u;
@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kThreads, GATED && ACT != kActNone ? 3 : 4)
 #pragma unroll
                 for (int i = 0; i < 4; ++i)
                     if (r + 32 * i < live)
-                        e[i] = __ldg(z_scales +
+                        e[i] = ld_cached(z_scales +
                                      mx8_scale_at(begin + r + 32 * i, tile * 4, tiles) / 4);
             }
             uint32_t mine = 0u;  // the scale byte of row r + 32 * (sub % 4), which this lane stores

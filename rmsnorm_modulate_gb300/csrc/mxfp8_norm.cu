@@ -564,11 +564,11 @@ __global__ void __launch_bounds__(kBwdThreads, 1)
     auto fetch = [&](Beside& e) {
         if (soon.item >= plan.count)
             return;
-        e.rstd = __ldg(a.rstd + soon.row);
+        e.rstd = ld_cached(a.rstd + soon.row);
         const uint8_t* from = scales + mx8_scale_at(soon.row, 0, tiles);
 #pragma unroll
         for (int j = 0; j < V; ++j)
-            e.byte[j] = has[j] ? __ldg(from + scale_off[j]) : 0u;
+            e.byte[j] = has[j] ? ld_cached(from + scale_off[j]) : 0u;
         advance(soon);
     };
     Beside first{}, second{};

@@ -151,6 +151,7 @@ __global__ void __launch_bounds__(kThreads, kBlocksPerSm) wan_kernel(const WanAr
     __syncthreads();
     {
         uint32_t gm = 0;
+#pragma unroll 1
         for (int c = threadIdx.x; c < Cv; c += kThreads) {
             const uint4 g = ld_cached(static_cast<const uint4*>(a.gamma) + c);
             uint4 bb = make_uint4(0u, 0u, 0u, 0u);
