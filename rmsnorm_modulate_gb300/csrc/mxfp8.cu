@@ -445,6 +445,7 @@ __global__ void __launch_bounds__(kThreads, GATED && ACT != kActNone ? 3 : 4)
         const T* __restrict__ grad = static_cast<const T*>(a.grad_out) + begin * N + n;
         uint8_t* grad_z = static_cast<uint8_t*>(a.grad_z) + begin * N + n;
         const int rows = static_cast<int>(end - begin), live = has ? rows : 0;  // (m * N is under 2^27)
+        const bool partial = rows < 128;
         u64 gate[4], sb[4], sg[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
@@ -490,8 +491,11 @@ __global__ void __launch_bounds__(kThreads, GATED && ACT != kActNone ? 3 : 4)
                                      mx8_scale_at(begin + r + 32 * i, tile * 4, tiles) / 4);
             }
             uint32_t mine = 0u;  // the scale byte of row r + 32 * (sub % 4), which this lane stores
-            const auto finish = [&](int i, const u64(&d)[4]) {
+            const auto finish = [&](int i, u64(&d)[4]) {
                 const int m = r + 32 * i;
+                // rows that there are not: 0 * gate is NaN under a gate that is not finite
+                if (GATED && partial && m >= live)
+                    d[0] = d[1] = d[2] = d[3] = 0ull;
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
                     sb[j] = f2_add(sb[j], d[j]);
