@@ -1041,6 +1041,21 @@ def _out8(q, name, shape, device):
     return q
 
 
+def _written_over(x, *outs):
+    """Whether one of the given outputs (tensors, Mxfp8 or None) has bytes of the contiguous x."""
+    begin = x.data_ptr()
+    end = begin + x.numel() * x.element_size()
+    for t in outs:
+        if isinstance(t, Mxfp8):
+            if _written_over(x, *t):
+                return True
+        elif t is not None:
+            at = t.data_ptr()
+            if at < end and begin < at + t.numel() * t.element_size():
+                return True
+    return False
+
+
 def _activation(name):
     code = _ACTIVATIONS.get(name) if name is None or isinstance(name, str) else None
     if code is None:
@@ -1117,7 +1132,8 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
     the type of the result, bias, gate and residual; torch.float32 too, for a weight's gradient); w:
     an Mxfp8 [N, K].  activation: None, "silu", "gelu" or "gelu_tanh".  bias [N]; gate rows [N] or
     [B, 1, N] (for x [B, S, K]); residual [..., N].  N a multiple of 8, of 32 with `quantize` or
-    `keep`.  out (of y) may be residual, a 16-bit x too; keep may be the Mxfp8 to write z to."""
+    `keep`.  out (of y) may be residual; keep may be the Mxfp8 to write z to; either may lie in a 16-bit
+    x, which is quantised before."""
     if stream is not None and (out is None or keep is True or not isinstance(x, Mxfp8)):
         at = x.codes if isinstance(x, Mxfp8) else x
         if not isinstance(at, torch.Tensor):
@@ -1154,6 +1170,7 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
     shape = (*lead, N)
     if residual is not None:
         _input(residual, "residual", dtype, device, shape)
+    fresh = out is None and not isinstance(keep, Mxfp8)
     if quantize:
         out = _new8(shape, M, device) if out is None else _out8(out, "out", shape, device)
         y, y_scales = _at(out.codes), _at(out.scales)
@@ -1171,7 +1188,7 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
     code = 2 if dtype == torch.float32 else _DTYPES[dtype]
     if isinstance(x, Mxfp8):
         codes, scales = _at(x.codes), _at(x.scales)
-    elif M <= _DIRECT_ROWS and y != x.data_ptr():
+    elif M <= _DIRECT_ROWS and (fresh or not _written_over(x, out, kept)):
         codes, scales = _at(x), None  # quantised by the product itself, which does not write to it
     else:
         n = M * K  # a multiple of 32
