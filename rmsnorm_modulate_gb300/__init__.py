@@ -1130,7 +1130,8 @@ def mxfp8_linear(x, w, bias=None, activation=None, gate=None, residual=None, out
 
     x [..., K]: bfloat16 or float16 (quantised here) or an Mxfp8 (then `dtype`, default bfloat16, is
     the type of the result, bias, gate and residual; torch.float32 too, for a weight's gradient); w:
-    an Mxfp8 [N, K].  activation: None, "silu", "gelu" or "gelu_tanh".  bias [N]; gate rows [N] or
+    an Mxfp8 [N, K].  activation: None, "silu", "gelu" or "gelu_tanh", good to (16 + 4 |ln p|) 2^-24
+    of itself with p = act(z) / z (2^-19 for z >= 0) whatever the dtype.  bias [N]; gate rows [N] or
     [B, 1, N] (for x [B, S, K]); residual [..., N].  N a multiple of 8, of 32 with `quantize` or
     `keep`.  out (of y) may be residual; keep may be the Mxfp8 to write z to; either may lie in a 16-bit
     x, which is quantised before."""

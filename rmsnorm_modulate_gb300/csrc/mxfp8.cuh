@@ -155,9 +155,10 @@ constexpr float kLog2e = 1.4426950408889634f;
 // p(a) for a = -x log(2), and q = p(a) (1 - p(a)), from t = 2^x = e^-a, at most 2^127: then t p is 1 - p
 // without a difference, and nothing overflows on either side.  (Past 2^126 p is 0, which the reciprocal
 // flushes to.)
-// The approximate instructions are good to 2^-22 each and the exponent's rounding to |x| 2^-24, so p is
-// good to 2^-18 where it is 2^-40 and better above: far inside a step of what its products are rounded
-// to.  A NaN is left to the factors z.
+// The approximate instructions are good to 2^-22 each and x to its own rounding, |x| 2^-24, and those of
+// its factors (four or so for the cubic argument): z p is good to (16 + 4 |ln p|) 2^-24, which is 2^-19
+// where p >= 1/2 and 2^-17 where it is 2^-40, far inside a step of 8- and 16-bit results.  fp32 results
+// have no more than that either.  A NaN is left to the factors z.
 __device__ __forceinline__ u64 logistic2(u64 x, u64& q)
 {
     float lo, hi;
@@ -182,7 +183,7 @@ __device__ __forceinline__ u64 gelu_argument(u64 z, u64 zz)
 //     Phi(-|z|) = e^(-z^2 / 2) t P(t):
 // e^(z^2 / 2) Phi(-|z|) is smooth in t, and goes like t for large |z|.  P is the least maximum of the
 // relative error over |z| <= 19.8, 2^-25.2, found by weighted least squares against erfcx in 64 bits; in
-// fp32 the product is good to 2^-21 (and e^(-z^2 / 2) to z^2 2^-25).  Beyond 19.8 it is 0.
+// fp32 the product is good to 2^-21 (and e^(-z^2 / 2) to z^2 2^-24).  Beyond 19.8 it is 0.
 __device__ __forceinline__ u64 normal2(u64 z, u64 zz, u64& e)
 {
     constexpr float c = 0.26870057f;
