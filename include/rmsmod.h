@@ -560,7 +560,8 @@ int add_rmsnorm_mxfp8(const void* x, const void* update, const void* weight, con
  *   grad_x nullable [B*S*D]; grad_weight nullable fp32 [D]; grad_scale,
  *   grad_shift nullable fp32 [B, D], or [1, D] where mod_bstride is 0.
  *   (grad_x is the gradient by x and by update alike.)
- *   workspace  at least rmsnorm_mxfp8_backward_workspace_bytes(B, S, D) bytes,
+ *   workspace  at least rmsnorm_mxfp8_backward_workspace_bytes(B, S, D) bytes
+ *     ((1, B * S, D) where mod_bstride is 0),
  *     needed where a row vector's gradient is wanted; in use until the call's
  *     work on `stream` is done.  Two launches (one without row vectors). */
 size_t rmsnorm_mxfp8_backward_workspace_bytes(int64_t B, int64_t S, int64_t D);
@@ -580,8 +581,8 @@ int rmsnorm_mxfp8_backward(const void* kept, const void* kept_scales, const void
  *   nullable, rows at gate + b * gate_bstride; grad_bias nullable fp32 [N];
  *   grad_gate nullable (and without gate NULL) fp32 [B, N], or [1, N] where
  *   gate_bstride is 0.  workspace as above
- *   (mxfp8_activation_backward_workspace_bytes(B, S, N)), needed where a sum is
- *   wanted. */
+ *   (mxfp8_activation_backward_workspace_bytes(B, S, N), (1, B * S, N) without
+ *   gate or where gate_bstride is 0), needed where a sum is wanted. */
 size_t mxfp8_activation_backward_workspace_bytes(int64_t B, int64_t S, int64_t N);
 
 int mxfp8_activation_backward(const void* z, const void* z_scales, const void* grad_out,

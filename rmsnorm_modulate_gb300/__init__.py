@@ -1233,8 +1233,8 @@ def mxfp8_activation_backward(z, grad_out, activation=None, gate=None, need_sums
     out = _new8(shape, rows, device) if out is None else _out8(out, "out", shape, device)
     grad_bias = _vector_grad(need_sums, N, device)
     grad_gate = _row_grads(need_sums and gate is not None, gs, B, N, device)
-    workspace, wbytes = _backward_workspace("mxfp8_activation_backward", workspace, need_sums, B, S,
-                                            N, device)
+    workspace, wbytes = _backward_workspace("mxfp8_activation_backward", workspace, need_sums,
+                                            *((B, S) if gs else (1, rows)), N, device)
     _call_on(device, stream, "mxfp8_activation_backward", _at(z.codes), _at(z.scales),
              _at(grad_out), act, _at(gate), gs, _at(out.codes), _at(out.scales), _at(grad_bias),
              _at(grad_gate), B, S, N, _at(workspace), wbytes, _DTYPES[dt])
@@ -1329,8 +1329,8 @@ def rmsnorm_mxfp8_backward(kept, weight, scale, grad_out, rstd, grad_res=None, n
     grad_weight = _vector_grad(need_mod and weight is not None, D, device)
     grad_scale = _row_grads(need_mod and scale is not None, bs, B, D, device)
     grad_shift = _row_grads(need_mod and (scale is not None or shift is not None), bs, B, D, device)
-    workspace, wbytes = _backward_workspace("rmsnorm_mxfp8_backward", workspace, need_mod, B, S, D,
-                                            device)
+    workspace, wbytes = _backward_workspace("rmsnorm_mxfp8_backward", workspace, need_mod,
+                                            *((B, S) if bs else (1, rows)), D, device)
     _call_on(device, stream, "rmsnorm_mxfp8_backward", _at(kept.codes), _at(kept.scales),
              _at(weight), _at(scale), bs, _at(grad_out), _at(grad_res), _at(rstd), B, S, D,
              _at(grad_x), _at(grad_weight), _at(grad_scale), _at(grad_shift), _at(workspace), wbytes,

@@ -1466,8 +1466,10 @@ RMSMOD_EXPORT int rmsnorm_mxfp8_backward(const void* kept, const void* kept_scal
     const bool sums = grad_weight || grad_scale || grad_shift;
     if (!grad_x && !sums)
         return RMSMOD_OK;
-    const size_t need =
-        rows && sums ? rmsmod::mxfp8_norm_backward_workspace_bytes(B, S, D) : 0;
+    // (one row for all batches: their rows are one batch's)
+    const size_t need = !rows || !sums ? 0
+                        : mod_bstride  ? rmsmod::mxfp8_norm_backward_workspace_bytes(B, S, D)
+                                       : rmsmod::mxfp8_norm_backward_workspace_bytes(1, rows, D);
     if (need && !workspace)
         return RMSMOD_ERR_NULL;
     if (!aligned(kept, 16) || !aligned(kept_scales, 16) || !aligned(weight, 16) ||
@@ -1526,7 +1528,7 @@ RMSMOD_EXPORT size_t mxfp8_activation_backward_workspace_bytes(int64_t B, int64_
     Mxfp8Size z;
     if (B <= 0 || S <= 0 || S > INT64_MAX / B || !mxfp8_size(B * S, N, z))
         return 0;
-    return rmsmod::mxfp8_activation_backward_workspace_bytes(B, S, N, true, 2);
+    return rmsmod::mxfp8_activation_backward_workspace_bytes(B, S, N, true, 2);  // any call's
 }
 
 RMSMOD_EXPORT int mxfp8_activation_backward(const void* z, const void* z_scales,
@@ -1552,7 +1554,9 @@ RMSMOD_EXPORT int mxfp8_activation_backward(const void* z, const void* z_scales,
         return RMSMOD_ERR_NULL;
     const bool sums = grad_bias || grad_gate;
     const size_t need =
-        rows && sums ? rmsmod::mxfp8_activation_backward_workspace_bytes(B, S, N, true, 2) : 0;
+        rows && sums ? rmsmod::mxfp8_activation_backward_workspace_bytes(
+                           B, S, N, gate && gate_bstride != 0, (grad_bias ? 1 : 0) + (grad_gate ? 1 : 0))
+                     : 0;
     if (need && !workspace)
         return RMSMOD_ERR_NULL;
     if (!aligned(z, 16) || !aligned(z_scales, 16) || !aligned(grad_out, 16) || !aligned(gate, 16) ||
