@@ -1548,7 +1548,7 @@ RMSMOD_EXPORT int mxfp8_activation_backward(const void* z, const void* z_scales,
     if ((st = check_bstride_span(B, gate_bstride)) != RMSMOD_OK)
         return st;
     const int64_t rows = B * S;
-    if (grad_gate && !gate)
+    if (rows != 0 && grad_gate && !gate)  // (no batches: an empty tensor's gate)
         return RMSMOD_ERR_UNSUPPORTED;
     if (rows != 0 && (!z || !z_scales || !grad_out || !grad_z || !grad_z_scales))
         return RMSMOD_ERR_NULL;
