@@ -146,8 +146,9 @@ __global__ void __launch_bounds__(kThreads) dequantize8_kernel(const Mxfp8RowsAr
 // bits.  Else (a column far below its rows' largest, scales 2^32 apart, NaN, the least scale)
 // turn_slowly() goes by whole numbers and fp32.
 //
-// Bound by its instructions as much as by HBM: 30 us at 4216 x 16384, whose bytes take 21 (six CTAs an SM;
-// five 33, seven 36, eight 39).
+// 30 us at 4216 x 16384, whose bytes take 21 (six CTAs an SM; five 33, seven 36, eight 39).  Neither its
+// instructions (56% of the issue slots) nor HBM (37%) bound it: a CTA loads, turns and stores one after
+// the other, which only the CTAs beside it on the SM hide.
 constexpr int kTurn = 128;
 
 __device__ __forceinline__ uint32_t byte_of(uint32_t w, int i) { return (w >> (8 * i)) & 0xFFu; }
@@ -372,10 +373,10 @@ __global__ void __launch_bounds__(kTurn, 6) transpose8_kernel(const Mxfp8Transpo
 // ends, and look them up; four rows of a warp with a block under any other scale work out their own.
 // Faster at all sizes: 5.1 against 6.0 us at 77 x 4096, 19.3 against 20.9 at 4216 x 4096, 57.7 against
 // 67.0 at 4096 x 16384.  With a gate whose gradient is taken as well there would be two values to look
-// up: 134 us, against 79 of working them out.
+// up: 134 us, against 80 of working them out.
 //
 // Now at 4216 x 16384: 56 us (GELU's tanh form; 54 the exact one; HBM's time 41), without an activation
-// 39 (z is not read: 31), with a gate and its gradient 60 (41), with both 79.  Some 18 instructions a
+// 39 (z is not read: 31), with a gate and its gradient 63 (41), with both 80.  Some 18 instructions a
 // value are issued, a fourth of them for an item's start and its sums.  Rows copied ahead to shared
 // memory: 76 us (tanh form), by TMA 78.
 constexpr int kRows = 20, kFirstByte = 127 - 16;

@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
         if (!extreme) {
             rstd = stored = rstd_fast(sum, n, inv_n, a.eps);
         } else {
-            // again over the power of two of the largest magnitude, joined in fp64; the next row's
+            // again over the power of two of the largest magnitude, mean and root in fp64; the next row's
             // place takes the largest, and then this row's, which every warp has read, the sums
             Parts& tops = part[odd][group];
             Parts& sums = part[odd ^ 1][group];
